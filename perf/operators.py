@@ -184,8 +184,12 @@ def prepare(case, seed):
         head = int(torch.randint(0, N, (1,), generator=g, device="cuda"))
         ids = torch.full((N,), -1, dtype=torch.int32, device="cuda")
         ids[(head + torch.arange(N - used, device="cuda")) % N] = order[used:]
+        empty = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device="cuda")  # noqa: E731
         s.update(new_lens=_ints(new), lens=_ints(held), table=table, free_ids=ids,
-                 pool=_ints([head, N - used, 0, 0]))
+                 pool=_ints([head, N - used, 0, 0]),
+                 # the buffers that a serving loop keeps for its step's maps
+                 maps=(empty(c["batch"]), empty(4), empty(c["batch"] + 1), empty(c["tokens"]),
+                       empty(c["tokens"]), empty(c["tokens"], torch.int64)))
         return s
     hd, Hk, H = c["head_dim"], c["kv_heads"], c["heads"]
     if c["op"] == "append":
@@ -235,7 +239,7 @@ def _own(c, s):
 
     if c["op"] == "plan":
         p = paged.paged_plan(s["new_lens"], s["lens"], s["pool"], s["free_ids"], s["table"],
-                             block_size=c["block"], max_tokens=c["tokens"])
+                             block_size=c["block"], max_tokens=c["tokens"], out=s["maps"])
         return {"table": s["table"], "free_ids": s["free_ids"], "lens": p.lens, "pool": p.pool,
                 "cu_tokens": p.cu_tokens, "requests": p.requests, "positions": p.positions,
                 "slots": p.slots}
