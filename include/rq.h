@@ -294,6 +294,146 @@ rq_status rq_attention_noalloc(int32_t batch, int32_t heads, int32_t head_dim,
                                const void *k, const void *v, const int32_t *positions,
                                float *out, void *cuda_stream);
 
+/* ---------------------------------------------------------------- paged K/V cache
+ * K/V memory as one pool of blocks that any number of requests share, in place of one
+ * `context`-slot array per session: a request holds the blocks its live positions need.
+ * Per step a caller enqueues rq_paged_plan once (blocks and token maps from the requests'
+ * lengths), then per layer rq_paged_append (norm, rotation, K/V stored by slot) and
+ * rq_paged_attention.  The pages have no counterpart; these are additions of this
+ * library.  None of the calls synchronizes, allocates or reads the device on the host, so
+ * all of them can be captured into a CUDA graph.  They run on the current device, which
+ * must be the one that holds the memory and the stream.  Different calls may run at the
+ * same time as long as they share no memory that one of them writes.
+ *
+ * Page p of a request holds its positions [p * block_size, (p + 1) * block_size) and is
+ * found in column p % max_blocks of the request's block table row.  A table at least as
+ * wide as the longest request is an ordinary one; a narrower table is a ring, in which
+ * page p takes over the block of page p - max_blocks (the paged form of the context
+ * window: a session of any length then holds max_blocks blocks).
+ *
+ * rq_paged_kv describes one layer's cache.  Position-in-block i of block n, head h, is at
+ * k + n * block_stride + i * row_stride + h * head_stride (elements; v alike), head_dim
+ * contiguous elements.  Strides are >= 0, k and v 16-byte aligned and every stride a
+ * multiple of 16 bytes.  head_dim must be 32, 64 or 128. */
+typedef struct {
+  void *k, *v;
+  int64_t block_stride, row_stride, head_stride;
+  int32_t dtype;      /* RQ_F32 or RQ_BF16 */
+  int32_t heads;      /* K/V heads */
+  int32_t head_dim;
+  int32_t block_size; /* positions per block, any size >= 1 */
+  int32_t n_blocks;
+} rq_paged_kv;
+
+/* Bits of pool[2] after rq_paged_plan: why the call changed nothing. */
+enum {
+  RQ_PAGED_BAD_INPUT = 1, /* a length or the pool's own words out of range */
+  RQ_PAGED_NO_TOKENS = 2, /* the new tokens exceed max_tokens */
+  RQ_PAGED_NO_BLOCKS = 4  /* the new pages exceed the free blocks */
+};
+
+/* The pool's free blocks: device pool [4] int32 {head, count, status, taken} and device
+ * free_ids [n_blocks] int32, a ring in which free_ids[(head + i) % n_blocks], i < count,
+ * are the free blocks, taken from the head and returned behind the tail.
+ * rq_paged_pool_init makes every block free: {0, n_blocks, 0, 0} and ids 0 .. n_blocks-1. */
+rq_status rq_paged_pool_init(int32_t n_blocks, int32_t *pool, int32_t *free_ids,
+                             void *cuda_stream);
+
+/* Block tables and token maps of one step, from the requests' lengths.  All memory is
+ * device memory.
+ *   new_lens     [batch] int32  tokens to add to request b (0: none); -1: the request has
+ *                ended, its blocks return to the pool and its length becomes 0
+ *   lens         [batch] int32  tokens request b has
+ *   pool, free_ids  the free blocks (above)
+ *   block_table  [batch][max_blocks] int32, updated in place: a request that grows gets a
+ *                block for each page that no column holds yet, in the ring's order,
+ *                request by request.  Other entries are left as they are, those of an
+ *                ended request too.  Blocks an ended request returns follow the free ones
+ *                in request and column order; this call does not hand them out again.
+ *   lens_out     [batch] int32  the lengths afterwards; may be lens itself
+ *   pool_out     [4] int32      the pool's words afterwards; may be pool itself.  taken is
+ *                the number of blocks handed out, or needed where there were too few
+ *   cu_tokens    [batch + 1] int32  request b's tokens are cu_tokens[b] .. cu_tokens[b+1]-1
+ *   requests, positions  [max_tokens] int32, slots [max_tokens] int64: for each token its
+ *                request, its position and its cache slot block * block_size + position %
+ *                block_size; the slot is -1 where a later token of the same call takes
+ *                over the page or the table's block is outside [0, n_blocks).  Entries
+ *                behind the last token are -1: padding that the other calls skip.
+ * All or nothing: pool_out[2] tells why a call did nothing (RQ_PAGED_*; 0 if it did); then
+ * lengths, table and free ring stay as they were, cu_tokens is all 0 and every token is
+ * padding.  Lengths from -1 (new_lens) or 0 (lens) up, sums up to 2^31 - 1.
+ * batch <= 8192 (RQ_ERR_UNSUPPORTED above). */
+rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t block_size,
+                        int32_t n_blocks, int32_t max_tokens, const int32_t *new_lens,
+                        const int32_t *lens, const int32_t *pool, int32_t *free_ids,
+                        int32_t *block_table, int32_t *lens_out, int32_t *pool_out,
+                        int32_t *cu_tokens, int32_t *requests, int32_t *positions,
+                        int64_t *slots, void *cuda_stream);
+
+/* Which pairs of a head's first rope_dim dimensions rotate together, by the angle
+ * position * rope_theta^(-2i / rope_dim): (2i, 2i+1), the frame's own pairing, or
+ * (i, i + rope_dim / 2). */
+enum { RQ_ROPE_INTERLEAVED = 0, RQ_ROPE_HALVES = 1 };
+
+/* The step between a qkv projection and its attention, in one pass over the rows: norm of
+ * each query and key head, position rotation, queries out, keys and values stored.
+ *   kv          the layer's cache
+ *   tokens      rows T (0: nothing is enqueued);  heads  query heads
+ *   qkv         device [T] rows, qkv_stride elements apart, in qkv_dtype (RQ_F32 /
+ *               RQ_BF16): heads * head_dim queries, then kv->heads * head_dim keys, then
+ *               as many values.  16-byte aligned, the stride a multiple of 16 bytes.
+ *   q_alpha, k_alpha  device [head_dim] f32 or NULL, 16-byte aligned: x * alpha /
+ *               sqrt(mean(x^2) + eps) over each head; NULL: no norm
+ *   rope_style  RQ_ROPE_*;  rope_dim  0 (no rotation) or a multiple of 8 up to head_dim
+ *   rope_theta  > 1
+ *   positions   device [T] int32; a row whose position is negative is padding: nothing of
+ *               it is read or written
+ *   slots       device [T] int64 (rq_paged_plan); the keys and values of a slot outside
+ *               [0, n_blocks * block_size) are not stored
+ *   q_out       device [T][heads * head_dim] in q_dtype, 16-byte aligned; must not overlap
+ *               qkv
+ * Norms and rotation are in f32 (angles exact to 2^-32 of a turn at any position); each
+ * stored value is rounded once.  Rows of one call must not share a slot (it would hold a
+ * mix of them). */
+rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
+                          int32_t qkv_dtype, const void *qkv, int64_t qkv_stride,
+                          const float *q_alpha, const float *k_alpha, float eps,
+                          int32_t rope_style, int32_t rope_dim, double rope_theta,
+                          const int32_t *positions, const int64_t *slots, int32_t q_dtype,
+                          void *q_out, void *cuda_stream);
+
+/* Attention of one query token per row over its request's blocks: for each query head,
+ * softmax(scale * q . k_j) weighted sum of v_j over the row's live positions j; query head
+ * i reads K/V head i / (heads / kv->heads).
+ *   rows        R (0: nothing is enqueued); several rows may be of one request (prompt
+ *               tokens, after all of them have been appended to a table that does not wrap)
+ *   heads       a multiple of kv->heads
+ *   batch, max_blocks, block_table  as rq_paged_plan
+ *   requests    device [R] int32 or NULL (row r is request r; R <= batch).  A row whose
+ *               request is outside [0, batch) is padding: its output is left as it was
+ *   positions   device [R] int32, the query's own position: its live positions are those
+ *               in [max(0, position - window + 1), position] that the table still holds
+ *               (the last max_blocks pages).  A block outside [0, n_blocks) is left out.
+ *               Negative: the request is empty.
+ *   window      positions, or 0 for no limit
+ *   scale       0 means 1 / sqrt(head_dim)
+ *   q           device [R][heads * head_dim] in q_dtype (RQ_F32 / RQ_BF16), 16-byte aligned
+ *   out         device [R][heads * head_dim] in q_dtype, 16-byte aligned
+ *   lse         device [R][heads] f32 or NULL: log of the sum of exp(scale * q . k_j)
+ *   workspace   device scratch of at least rq_paged_attention_workspace_size bytes, 16-byte
+ *               aligned, needing no initialisation; calls that may overlap need their own
+ * A row with no live position gives output 0 and lse -inf.  What lies in the cache outside
+ * the live positions is never used, NaN or not.  Scores, softmax and sums are f32; with
+ * f32 queries every product over a bf16 cache is exact (queries and weights enter as three
+ * bf16 parts), with bf16 queries the weights keep 16 significant bits. */
+size_t rq_paged_attention_workspace_size(int32_t heads, int32_t kv_heads, int32_t head_dim);
+rq_status rq_paged_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
+                             int32_t batch, int32_t max_blocks, const int32_t *block_table,
+                             const int32_t *requests, const int32_t *positions,
+                             int32_t window, float scale, int32_t q_dtype, const void *q,
+                             void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             void *cuda_stream);
+
 /* Token picks ("moshi_lm.rs", `Sampling`, `MoshiLm::set_sampling`, `pick`): every frame
  * picks the text token (temp_text, top_k_text) and then codebooks 0..7 (temp, top_k),
  * each session from its own xorshift64 state ("moshi_lm.rs", `xorshift_u01`):

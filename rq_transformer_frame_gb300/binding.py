@@ -35,6 +35,8 @@ _CFG_INT_FIELDS = ["batch", "dim", "layers", "heads", "head_dim", "hidden", "con
 
 
 RQ_SCHEDULE_AUTO, RQ_SCHEDULE_GRAPH, RQ_SCHEDULE_PERSISTENT, RQ_SCHEDULE_TENSOR = 0, 1, 2, 3
+RQ_ROPE_INTERLEAVED, RQ_ROPE_HALVES = 0, 1
+RQ_PAGED_BAD_INPUT, RQ_PAGED_NO_TOKENS, RQ_PAGED_NO_BLOCKS = 1, 2, 4
 RQ_PICK_GREEDY, RQ_PICK_TOPK, RQ_PICK_GUMBEL = 0, 1, 2
 RQ_F32, RQ_BF16, RQ_Q8, RQ_Q4 = 0, 1, 2, 3
 # stacked weight matrices (the weight bands quantize these; tables and alphas stay)
@@ -111,6 +113,18 @@ def load() -> C.CDLL:
     L.rq_attention_workspace_size.restype = C.c_size_t
     L.rq_attention.argtypes = [I32, I32, I32, I32, I32, P, P, P, P, P, P, C.c_size_t, P]
     L.rq_attention.restype = C.c_int
+    I64, F32 = C.c_int64, C.c_float
+    L.rq_paged_pool_init.argtypes = [I32, P, P, P]
+    L.rq_paged_plan.argtypes = [I32] * 5 + [P] * 12
+    # the rq_paged_kv struct is passed packed (paged.py)
+    L.rq_paged_append.argtypes = [C.c_char_p, I32, I32, I32, P, I64, P, P, F32, I32, I32,
+                                  C.c_double, P, P, I32, P, P]
+    L.rq_paged_attention_workspace_size.argtypes = [I32, I32, I32]
+    L.rq_paged_attention_workspace_size.restype = C.c_size_t
+    L.rq_paged_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, F32, I32,
+                                     P, P, P, P, C.c_size_t, P]
+    for f in ("rq_paged_pool_init", "rq_paged_plan", "rq_paged_append", "rq_paged_attention"):
+        getattr(L, f).restype = C.c_int
     for f in ("rq_create", "rq_reset", "rq_step", "rq_step_forced", "rq_step_device",
               "rq_sync", "rq_get_logits", "rq_get_trace", "rq_get_ring", "rq_set_kv",
               "rq_launch_op", "rq_set_sampling", "rq_get_rng", "rq_prime", "rq_replay",

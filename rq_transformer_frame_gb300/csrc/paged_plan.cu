@@ -1,0 +1,201 @@
+// paged_plan.cu -- block tables and token maps of the paged K/V cache, built on the GPU
+// from the requests' lengths (include/rq.h, rq_paged_plan).
+//
+// With pages(c) = min(ceil(c / P), W), request b needs pages(c_b + n_b) - pages(c_b) new
+// blocks, or gives back pages(c_b) if it has ended.  Three prefix sums over the requests
+// (tokens, blocks taken, blocks given back) place everything: taken block x is entry
+// head + x of the free ring, given block x goes to entry head + count + x, token t belongs
+// to the last request whose first token is <= t.  Every output element is then computed
+// from its index alone, by a binary search in the prefix sums in shared memory.
+//
+// What may alias needs no order of its own: taken entries of the ring are read at
+// [head, head + taken) and given ones written at [head + count, head + count + given), apart
+// because count + given <= N; table columns are written from pages(c_b) on and read below.
+// Only the lengths and the pool's words are read by all and written by some: those writes
+// follow a barrier.
+#include "paged.cuh"
+
+namespace rqk {
+namespace {
+
+constexpr int kPlanMaxBatch = 8192;  // four prefix arrays of this length fit shared memory
+constexpr int kPlanThreads = 1024;
+
+struct PlanParams {
+  int B, W, P, N, M;
+  const int32_t *new_lens, *lens, *pool;
+  int32_t *free_ids, *table, *lens_out, *pool_out, *cu, *requests, *positions;
+  int64_t* slots;
+};
+
+struct Sums {
+  long long tok, need, give;
+};
+
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return {a.tok + b.tok, a.need + b.need, a.give + b.give};
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums& a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.tok, o), __shfl_up_sync(0xffffffffu, a.need, o),
+          __shfl_up_sync(0xffffffffu, a.give, o)};
+}
+
+__device__ __forceinline__ int pages_of(int c, const PlanParams& p) {
+  const int n = c / p.P + (c % p.P != 0);
+  return n < p.W ? n : p.W;
+}
+
+// the last b with first[b] <= x, first[0] = 0
+__device__ __forceinline__ int last_at_most(const int* first, int B, int x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  extern __shared__ int s_mem[];
+  int* const s_cu = s_mem;               // [B + 1] first token
+  int* const s_take = s_cu + p.B + 1;    // [B] first taken block
+  int* const s_give = s_take + p.B;      // [B] first block given back
+  int* const s_held = s_give + p.B;      // [B] length before
+  __shared__ Sums s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int head = p.pool[0], count = p.pool[1];
+  Sums run{0, 0, 0};
+  int bad = head < 0 || head >= p.N || count < 0 || count > p.N;
+  for (int base = 0; base < p.B; base += nt) {
+    const int b = base + tid;
+    Sums own{0, 0, 0};
+    int c = 0;
+    if (b < p.B) {
+      const int n = p.new_lens[b];
+      c = p.lens[b];
+      if (n < -1 || c < 0 || (n > 0 && c > INT_MAX - n)) {
+        bad = 1;
+        c = 0;
+      } else if (n < 0) {
+        own.give = pages_of(c, p);
+      } else {
+        own.tok = n;
+        own.need = pages_of(c + n, p) - pages_of(c, p);
+      }
+    }
+    Sums inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums t = shfl_up(inc, o);
+      if (lane >= o) inc = inc + t;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    Sums before = run;
+    for (int w = 0; w < nt / 32; ++w) {
+      if (w < warp) before = before + s_warp[w];
+      run = run + s_warp[w];
+    }
+    if (b < p.B) {
+      // a sum past the limits fails the call below: the narrowed value is not used then
+      s_cu[b] = (int)(before.tok + inc.tok - own.tok);
+      s_take[b] = (int)(before.need + inc.need - own.need);
+      s_give[b] = (int)(before.give + inc.give - own.give);
+      s_held[b] = c;
+    }
+    __syncthreads();
+  }
+  bad = __syncthreads_or(bad);
+  int status = 0;
+  if (bad || (long long)count + run.give > p.N) status |= RQ_PAGED_BAD_INPUT;
+  if (run.tok > p.M) status |= RQ_PAGED_NO_TOKENS;
+  if (run.need > count) status |= RQ_PAGED_NO_BLOCKS;
+  const int T = status ? 0 : (int)run.tok;
+  const int taken = status ? 0 : (int)run.need, given = status ? 0 : (int)run.give;
+  if (tid == 0) s_cu[p.B] = T;
+  __syncthreads();
+
+  for (int b = tid; b < p.B; b += nt) {
+    const int n = status ? 0 : p.new_lens[b];
+    p.lens_out[b] = n < 0 ? 0 : p.lens[b] + n;
+    p.cu[b] = status ? 0 : s_cu[b];
+  }
+  if (tid == 0) {
+    p.cu[p.B] = T;
+    p.pool_out[0] = status ? head : (int)(((long long)head + taken) % p.N);
+    p.pool_out[1] = count - taken + given;
+    p.pool_out[2] = status;
+    p.pool_out[3] = (int)(run.need < INT_MAX ? run.need : INT_MAX);
+  }
+  for (int x = tid; x < taken; x += nt) {
+    const int b = last_at_most(s_take, p.B, x);
+    p.table[(size_t)b * p.W + pages_of(s_held[b], p) + (x - s_take[b])] =
+        p.free_ids[((long long)head + x) % p.N];
+  }
+  for (int x = tid; x < given; x += nt) {
+    const int b = last_at_most(s_give, p.B, x);
+    p.free_ids[((long long)head + count + x) % p.N] = p.table[(size_t)b * p.W + (x - s_give[b])];
+  }
+  for (int t = tid; t < p.M; t += nt) {
+    int b = -1, pos = -1;
+    long long slot = -1;
+    if (t < T) {
+      b = last_at_most(s_cu, p.B, t);
+      const int held = s_held[b], before = pages_of(held, p);
+      pos = held + (t - s_cu[b]);
+      const int page = pos / p.P, col = page % p.W;
+      const int last = (held + (s_cu[b + 1] - s_cu[b]) - 1) / p.P;
+      const int id = col < before
+                         ? p.table[(size_t)b * p.W + col]
+                         : p.free_ids[((long long)head + s_take[b] + (col - before)) % p.N];
+      if (last - page < p.W && id >= 0 && id < p.N) slot = (long long)id * p.P + pos % p.P;
+    }
+    p.requests[t] = b;
+    p.positions[t] = pos;
+    p.slots[t] = slot;
+  }
+}
+
+__global__ void pool_init_kernel(int n, int32_t* pool, int32_t* free_ids) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < n) free_ids[i] = i;
+  if (i < 4) pool[i] = i == 1 ? n : 0;
+}
+
+}  // namespace
+}  // namespace rqk
+
+extern "C" rq_status rq_paged_pool_init(int32_t n_blocks, int32_t* pool, int32_t* free_ids,
+                                        void* cuda_stream) {
+  if (n_blocks < 1 || !pool || !free_ids) return RQ_ERR_ARG;
+  const unsigned grid = (unsigned)(((long long)n_blocks + 4 + 255) / 256);
+  rqk::pool_init_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(n_blocks, pool,
+                                                                                  free_ids);
+  return cudaGetLastError() == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t block_size,
+                                   int32_t n_blocks, int32_t max_tokens, const int32_t* new_lens,
+                                   const int32_t* lens, const int32_t* pool, int32_t* free_ids,
+                                   int32_t* block_table, int32_t* lens_out, int32_t* pool_out,
+                                   int32_t* cu_tokens, int32_t* requests, int32_t* positions,
+                                   int64_t* slots, void* cuda_stream) {
+  using namespace rqk;
+  if (batch < 1 || max_blocks < 1 || block_size < 1 || n_blocks < 1 || max_tokens < 1)
+    return RQ_ERR_ARG;
+  if (batch > kPlanMaxBatch) return RQ_ERR_UNSUPPORTED;
+  if (!new_lens || !lens || !pool || !free_ids || !block_table || !lens_out || !pool_out ||
+      !cu_tokens || !requests || !positions || !slots)
+    return RQ_ERR_ARG;
+  PlanParams p{batch,       max_blocks, block_size, n_blocks,  max_tokens, new_lens,
+               lens,        pool,       free_ids,   block_table, lens_out, pool_out,
+               cu_tokens,   requests,   positions,  slots};
+  const size_t smem = ((size_t)4 * batch + 1) * sizeof(int);
+  if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)((4 * kPlanMaxBatch + 1) * sizeof(int))) != cudaSuccess)
+    return RQ_ERR_CUDA;
+  plan_kernel<<<1, kPlanThreads, smem, static_cast<cudaStream_t>(cuda_stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}

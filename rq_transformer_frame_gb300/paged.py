@@ -1,0 +1,238 @@
+"""The paged K/V cache: a pool of blocks that many requests share (include/rq.h, the
+rq_paged_* calls; argument marshalling only, like `binding`).
+
+  paged_plan       block tables and token maps of a step, from the requests' lengths
+  paged_append     per-head norm, position rotation, and K/V stored by slot
+  paged_attention  one query token per row over its request's blocks
+  PagedCache       the buffers of one cache, with the three as methods
+
+A layer's cache is a pair of tensors k, v [n_blocks][block_size][kv_heads][head_dim] (f32
+or bf16, of any strides that keep head_dim contiguous and every row 16-byte aligned).
+Nothing here synchronizes except PagedCache.status(), so a step can be captured into a CUDA
+graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace`.
+Every call runs on `stream` (a torch.cuda.Stream; default: the current one of the
+tensors' device); tensors it allocates belong to that stream.
+"""
+from __future__ import annotations
+
+import struct
+from collections import namedtuple
+from contextlib import contextmanager
+
+import torch
+
+from .binding import (RQ_BF16, RQ_F32, RQ_OK, RQ_PAGED_BAD_INPUT, RQ_PAGED_NO_BLOCKS,
+                      RQ_PAGED_NO_TOKENS, RQ_ROPE_HALVES, RQ_ROPE_INTERLEAVED, RQError, load)
+
+_KV = struct.Struct("@PPqqqiiiii4x")  # rq_paged_kv
+_TYPE = {torch.float32: RQ_F32, torch.bfloat16: RQ_BF16}
+_ROPE = {"interleaved": RQ_ROPE_INTERLEAVED, "halves": RQ_ROPE_HALVES}
+
+# What rq_paged_plan writes: lengths and pool words afterwards, and the step's maps.
+PagedPlan = namedtuple("PagedPlan", "lens pool cu_tokens requests positions slots")
+
+
+def _fail(what, rc):
+    raise RQError(rc, "%s failed" % what)
+
+
+@contextmanager
+def _on(device, stream):
+    """The tensors' device, and the stream the call runs on, made current."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            if stream.device != device:
+                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _ints(name, t, n, device, dtype=torch.int32):
+    """The address of a contiguous integer tensor of n elements (at least)."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s: a contiguous %s tensor of %d elements on %s is wanted" %
+                         (name, dtype, n, device))
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is wanted" %
+                         (name, dtype, shape, device))
+    return t.data_ptr()
+
+
+def _cache(k, v):
+    """(rq_paged_kv packed, heads, head_dim) of a layer's cache."""
+    if k.dim() != 4 or k.dtype not in _TYPE or not k.is_cuda:
+        raise ValueError("k, v: f32 or bf16 CUDA tensors [n_blocks][block_size][heads][head_dim]")
+    n, p, h, hd = k.shape
+    strides = k.stride()
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or v.stride() != strides:
+        raise ValueError("k and v differ in shape, strides, type or device")
+    if strides[3] != 1:
+        raise ValueError("k, v: the elements of a head must be contiguous")
+    return _KV.pack(k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2],
+                    _TYPE[k.dtype], h, hd, p, n), h, hd
+
+
+def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_tokens, out=None,
+               stream=None) -> PagedPlan:
+    """rq_paged_plan: new_lens, lens [B] int32, pool [4] int32, free_ids [n_blocks] int32 and
+    block_table [B][max_blocks] int32 (both updated in place).
+
+    out: a PagedPlan (or the same tuple) of tensors to write, lens [B], pool [4], cu_tokens
+    [B + 1], requests and positions [max_tokens] int32 and slots [max_tokens] int64; its lens
+    and pool may be the inputs themselves.  pool[2] says whether the call did anything
+    (RQ_PAGED_*)."""
+    L = load()
+    dev = lens.device
+    if not lens.is_cuda or block_table.dim() != 2:
+        raise ValueError("lens, block_table: CUDA tensors [B] and [B][max_blocks] are wanted")
+    B, W = block_table.shape
+    M = int(max_tokens)
+    with _on(dev, stream) as st:
+        if out is None:
+            e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
+            out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, torch.int64))
+        elif not isinstance(out, PagedPlan):
+            out = PagedPlan(*out)
+        if lens.numel() != B or new_lens.numel() != B:
+            raise ValueError("new_lens, lens and block_table differ in their requests")
+        rc = L.rq_paged_plan(
+            B, W, int(block_size), free_ids.numel(), M, _ints("new_lens", new_lens, B, dev),
+            _ints("lens", lens, B, dev), _ints("pool", pool, 4, dev),
+            _ints("free_ids", free_ids, 1, dev), _ints("block_table", block_table, B * W, dev),
+            _ints("out.lens", out.lens, B, dev), _ints("out.pool", out.pool, 4, dev),
+            _ints("out.cu_tokens", out.cu_tokens, B + 1, dev),
+            _ints("out.requests", out.requests, M, dev),
+            _ints("out.positions", out.positions, M, dev),
+            _ints("out.slots", out.slots, M, dev, torch.int64), st)
+    if rc != RQ_OK:
+        _fail("rq_paged_plan", rc)
+    return out
+
+
+def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e-8,
+                 rope="interleaved", rope_dim=None, rope_theta=10000.0, q_dtype=None, out=None,
+                 stream=None):
+    """rq_paged_append: rows qkv [T][(heads + 2 kv_heads) * head_dim] f32 or bf16 (rows may be
+    strided) -> queries [T][heads * head_dim] in q_dtype (default: qkv's, or out's), keys and
+    values stored in k, v at `slots` (int64 [T]).  rope: "interleaved" or "halves" over the
+    first rope_dim (default: all) dimensions; alphas: f32 [head_dim] or None for no norm."""
+    L = load()
+    kv, hk, hd = _cache(k, v)
+    dev = k.device
+    if qkv.dim() != 2 or qkv.dtype not in _TYPE or qkv.device != dev or \
+            (qkv.shape[1] > 1 and qkv.stride(1) != 1):
+        raise ValueError("qkv: an f32 or bf16 tensor [T][width] with contiguous rows on %s" % dev)
+    T, width = qkv.shape
+    heads = width // hd - 2 * hk
+    if heads < 1 or width % hd:
+        raise ValueError("qkv: %d columns are not queries, %d keys and %d values of %d" %
+                         (width, hk, hk, hd))
+    if rope not in _ROPE:
+        raise ValueError("rope: 'interleaved' or 'halves'")
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, heads * hd), dtype=q_dtype or qkv.dtype, device=dev)
+        elif out.dtype not in _TYPE or (q_dtype is not None and out.dtype != q_dtype):
+            raise ValueError("out: f32 or bf16, as q_dtype says")
+        rc = L.rq_paged_append(
+            kv, T, heads, _TYPE[qkv.dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
+            None if q_alpha is None else _rows("q_alpha", q_alpha, (hd,), torch.float32, dev),
+            None if k_alpha is None else _rows("k_alpha", k_alpha, (hd,), torch.float32, dev),
+            eps, _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta,
+            _ints("positions", positions, T, dev), _ints("slots", slots, T, dev, torch.int64),
+            _TYPE[out.dtype], _rows("out", out, (T, heads * hd), out.dtype, dev), st)
+    if rc != RQ_OK:
+        _fail("rq_paged_append", rc)
+    return out
+
+
+def paged_attention(q, k, v, block_table, positions, requests=None, window=0, scale=0.0, out=None,
+                    lse=None, workspace=None, stream=None):
+    """rq_paged_attention: q [R][heads * head_dim] f32 or bf16, block_table [B][max_blocks],
+    positions [R] (-1: an empty request), requests [R] (-1: padding, its output left as it
+    was; None: row r is request r), all int32 -> (out [R][heads * head_dim], lse [R][heads]
+    f32, None unless a tensor or True is passed for it)."""
+    L = load()
+    kv, hk, hd = _cache(k, v)
+    dev = k.device
+    if q.dim() != 2 or q.dtype not in _TYPE or q.shape[1] % hd:
+        raise ValueError("q: an f32 or bf16 tensor [R][heads * head_dim]")
+    R, heads = q.shape[0], q.shape[1] // hd
+    B, W = block_table.shape
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is True:
+            lse = torch.empty((R, heads), dtype=torch.float32, device=dev)
+        nbytes = L.rq_paged_attention_workspace_size(heads, hk, hd)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor on %s" % dev)
+        rc = L.rq_paged_attention(
+            kv, R, heads, B, W, _ints("block_table", block_table, B * W, dev),
+            None if requests is None else _ints("requests", requests, R, dev),
+            _ints("positions", positions, R, dev), window, scale, _TYPE[q.dtype],
+            _rows("q", q, (R, heads * hd), q.dtype, dev),
+            _rows("out", out, (R, heads * hd), q.dtype, dev),
+            None if lse is None else _rows("lse", lse, (R, heads), torch.float32, dev),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
+    if rc != RQ_OK:
+        _fail("rq_paged_attention", rc)
+    return out, lse
+
+
+class PagedCache:
+    """The buffers of one paged cache and its step's maps, at fixed addresses.
+
+    batch request rows, n_blocks blocks of block_size positions per layer, at most
+    max_blocks blocks a request (past that its table is a ring) and max_tokens new tokens a
+    step.  All layers share the block table; layer l's cache is k[l], v[l]."""
+
+    def __init__(self, batch, n_blocks, block_size, max_blocks, max_tokens, kv_heads, head_dim,
+                 layers=1, dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        shape = (layers, n_blocks, block_size, kv_heads, head_dim)
+        e = lambda n, dt=torch.int32: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731
+        self.block_size, self.max_tokens = int(block_size), int(max_tokens)
+        self.k = torch.zeros(shape, dtype=dtype, device=dev)
+        self.v = torch.zeros(shape, dtype=dtype, device=dev)
+        self.block_table = torch.full((batch, max_blocks), -1, dtype=torch.int32, device=dev)
+        self.free_ids = e(n_blocks)
+        self.maps = PagedPlan(e(batch), e(4), e(batch + 1), e(max_tokens), e(max_tokens),
+                              e(max_tokens, torch.int64))
+        with _on(self.k.device, None) as st:
+            rc = load().rq_paged_pool_init(n_blocks, self.maps.pool.data_ptr(),
+                                           self.free_ids.data_ptr(), st)
+        if rc != RQ_OK:
+            _fail("rq_paged_pool_init", rc)
+
+    def plan(self, new_lens, stream=None) -> PagedPlan:
+        """Add new_lens [batch] tokens (-1: the request has ended), in place."""
+        m = self.maps
+        return paged_plan(new_lens, m.lens, m.pool, self.free_ids, self.block_table,
+                          self.block_size, self.max_tokens, out=m, stream=stream)
+
+    def append(self, layer, qkv, **kw):
+        """The step's rows qkv [T][...], T <= max_tokens, into layer `layer` -> queries."""
+        T = qkv.shape[0]
+        return paged_append(qkv, self.k[layer], self.v[layer], self.maps.positions[:T],
+                            self.maps.slots[:T], **kw)
+
+    def attend(self, layer, q, **kw):
+        """Each of the step's tokens over its own request, q [T][heads * head_dim]."""
+        T = q.shape[0]
+        return paged_attention(q, self.k[layer], self.v[layer], self.block_table,
+                               self.maps.positions[:T], requests=self.maps.requests[:T], **kw)
+
+    def status(self):
+        """(why the last plan did nothing: RQ_PAGED_* bits, 0 if it did; free blocks).
+        Synchronizes."""
+        head, count, status, taken = self.maps.pool.tolist()
+        return status, count
