@@ -1,122 +1,20 @@
-// paged_attn.cu -- attention of one query token per row over a paged K/V cache
-// (include/rq.h, rq_paged_attention).
-//
-// For row r with position pos and query head h: s_j = scale q . k_j over the live positions
-// j, o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), m the running maximum.  One CTA per (row,
-// head), its warps taking every fourth key.
+// paged_attn.cu -- rq_paged_attention (include/rq.h): checks, workspace and launch of the
+// kernels in paged_attn.cuh.
 #include <cmath>
 
-#include "paged.cuh"
+#include "paged_attn.cuh"
 
-namespace rqk {
 namespace {
-
-constexpr int kWarps = 4;
-
-struct PagedAttnParams {
-  rq_paged_kv kv;
-  const void* q;
-  void* out;
-  float* lse;
-  const int32_t *table, *requests, *positions;
-  int rows, heads, batch, W, window;
-  float scale;
-};
-
-template <typename T>
-__device__ __forceinline__ float elem(const T* p, long long i);
-template <>
-__device__ __forceinline__ float elem<float>(const float* p, long long i) { return p[i]; }
-template <>
-__device__ __forceinline__ float elem<uint16_t>(const uint16_t* p, long long i) {
-  return bf16lo(p[i]);
+int heads_of_group(int heads, int kv_heads) {
+  const int g = heads / kv_heads;
+  return g < rqk::paged_attn::kHeads ? g : rqk::paged_attn::kHeads;
 }
-
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(uint16_t* p, float v) {
-  *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-template <typename QT, typename KT, int HD>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const PagedAttnParams p) {
-  constexpr int E = HD / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_acc[kWarps][HD];
-  const int h = blockIdx.x % p.heads, r = blockIdx.x / p.heads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = p.requests ? p.requests[r] : r, pos = p.positions[r];
-  if (b < 0 || b >= p.batch) return;
-  const int P = p.kv.block_size, kh = h / (p.heads / p.kv.heads);
-  const float ninf = -__int_as_float(0x7f800000);
-  const QT* q = static_cast<const QT*>(p.q) + ((long long)r * p.heads + h) * HD;
-  float qv[E], acc[E], m = ninf, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = elem<QT>(q, lane + 32 * e);
-    acc[e] = 0.f;
-  }
-  if (pos >= 0) {
-    const int first = pos / P - p.W + 1;
-    int lo = first > 0 ? first * P : 0;
-    if (p.window > 0 && pos - p.window + 1 > lo) lo = pos - p.window + 1;
-    const KT* kc = static_cast<const KT*>(p.kv.k) + kh * p.kv.head_stride;
-    const KT* vc = static_cast<const KT*>(p.kv.v) + kh * p.kv.head_stride;
-    for (long long j = (long long)lo + warp; j <= pos; j += kWarps) {
-      const int page = (int)(j / P);
-      const int id = p.table[(size_t)b * p.W + page % p.W];
-      if (id < 0 || id >= p.kv.n_blocks) continue;
-      const long long at = id * p.kv.block_stride + (j - (long long)page * P) * p.kv.row_stride;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(qv[e], elem<KT>(kc + at, lane + 32 * e), s);
-      s = warp_sum(s) * p.scale;
-      const float mn = fmaxf(m, s);
-      if (mn == ninf) continue;
-      const float c = expf(m - mn), w = expf(s - mn);
-      l = l * c + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + w * elem<KT>(vc + at, lane + 32 * e);
-      m = mn;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  float M = ninf, L = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) L += s_l[w] > 0.f ? s_l[w] * expf(s_m[w] - M) : 0.f;
-  QT* out = static_cast<QT*>(p.out) + ((long long)r * p.heads + h) * HD;
-  for (int d = threadIdx.x; d < HD; d += kWarps * 32) {
-    float a = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_l[w] > 0.f) a += s_acc[w][d] * expf(s_m[w] - M);
-    put(out + d, L > 0.f ? a / L : 0.f);
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[(long long)r * p.heads + h] = L > 0.f ? M + logf(L) : ninf;
-}
-
-template <typename QT, typename KT>
-cudaError_t launch(const PagedAttnParams& p, cudaStream_t s) {
-  const unsigned grid = (unsigned)p.rows * (unsigned)p.heads;
-  switch (p.kv.head_dim) {
-    case 32: paged_attn_kernel<QT, KT, 32><<<grid, kWarps * 32, 0, s>>>(p); break;
-    case 64: paged_attn_kernel<QT, KT, 64><<<grid, kWarps * 32, 0, s>>>(p); break;
-    default: paged_attn_kernel<QT, KT, 128><<<grid, kWarps * 32, 0, s>>>(p); break;
-  }
-  return cudaGetLastError();
-}
-
 }  // namespace
-}  // namespace rqk
 
 extern "C" size_t rq_paged_attention_workspace_size(int32_t heads, int32_t kv_heads,
                                                     int32_t head_dim) {
-  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1) return 0;
-  return 16;
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 || head_dim > 128) return 0;
+  return rqk::paged_attn::workspace_bytes(heads_of_group(heads, kv_heads), head_dim);
 }
 
 extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -140,7 +38,7 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
   if (workspace_bytes < rq_paged_attention_workspace_size(heads, kv->heads, kv->head_dim))
     return RQ_ERR_ARG;
-  PagedAttnParams p{};
+  paged_attn::Params p{};
   p.kv = *kv;
   p.q = q;
   p.out = out;
@@ -153,12 +51,19 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   p.batch = batch;
   p.W = max_blocks;
   p.window = window;
-  p.scale = scale != 0.f ? scale : 1.0f / sqrtf((float)kv->head_dim);
+  p.G = heads / kv->heads;
+  p.HG = (p.G + paged_attn::kHeads - 1) / paged_attn::kHeads;
+  p.GB = heads_of_group(heads, kv->heads);
+  p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)kv->head_dim)) *
+                    1.4426950408889634);
+  char* ws = static_cast<char*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(p.GB, kv->head_dim));
+  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(p.GB, kv->head_dim) +
+                                  paged_attn::ml_bytes(p.GB));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e;
-  if (q_dtype == RQ_BF16)
-    e = kv->dtype == RQ_BF16 ? launch<uint16_t, uint16_t>(p, s) : launch<uint16_t, float>(p, s);
-  else
-    e = kv->dtype == RQ_BF16 ? launch<float, uint16_t>(p, s) : launch<float, float>(p, s);
+  const bool qb = q_dtype == RQ_BF16;
+  const cudaError_t e = kv->dtype == RQ_BF16 ? paged_attn::launch_bf16(p, qb, s)
+                                             : paged_attn::launch_f32(p, qb, s);
   return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }
