@@ -5,16 +5,17 @@
 #include "paged_attn.cuh"
 
 namespace {
-int heads_of_group(int heads, int kv_heads) {
+// heads of a unit, at most (whatever the types)
+int heads_of_unit(int heads, int kv_heads) {
   const int g = heads / kv_heads;
-  return g < rqk::paged_attn::kHeads ? g : rqk::paged_attn::kHeads;
+  return g < rqk::paged_attn::kMaxHeads ? g : rqk::paged_attn::kMaxHeads;
 }
 }  // namespace
 
 extern "C" size_t rq_paged_attention_workspace_size(int32_t heads, int32_t kv_heads,
                                                     int32_t head_dim) {
   if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 || head_dim > 128) return 0;
-  return rqk::paged_attn::workspace_bytes(heads_of_group(heads, kv_heads), head_dim);
+  return rqk::paged_attn::workspace_bytes(heads_of_unit(heads, kv_heads), head_dim);
 }
 
 extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -52,15 +53,14 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   p.W = max_blocks;
   p.window = window;
   p.G = heads / kv->heads;
-  p.HG = (p.G + paged_attn::kHeads - 1) / paged_attn::kHeads;
-  p.GB = heads_of_group(heads, kv->heads);
+  const int unit = heads_of_unit(heads, kv->heads);
   p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)kv->head_dim)) *
                     1.4426950408889634);
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(p.GB, kv->head_dim));
-  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(p.GB, kv->head_dim) +
-                                  paged_attn::ml_bytes(p.GB));
+  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(unit, kv->head_dim));
+  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(unit, kv->head_dim) +
+                                  paged_attn::ml_bytes(unit));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool qb = q_dtype == RQ_BF16;
   const cudaError_t e = kv->dtype == RQ_BF16 ? paged_attn::launch_bf16(p, qb, s)

@@ -6,31 +6,39 @@
 // j, o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), in one pass with m the running maximum and
 // the sums rescaled when it moves (all in base 2: scale carries log2 e).
 //
-// Work. A unit is one (row, K/V head, group of up to 8 query heads that read it), a tile 64
-// consecutive positions of a unit. All units' tiles form one list, rows outermost; the grid
-// (a few CTAs per SM, all resident) cuts it into equal runs, one per CTA, whatever the rows'
-// lengths are. A unit that lies in one CTA is finished there; one that is cut leaves a
-// partial (m, l, acc) per CTA, joined in order by the merge kernel, so the result does not
-// depend on timing. A CTA has at most two cut units (its first and its last), which bounds
-// the workspace by the grid.
+// Work. A unit is one (row, K/V head, group of query heads that read it), a tile 2 KB of K
+// (and as much V) of a unit: 16 positions at head_dim 128 in bf16. All units' tiles form one
+// list, rows outermost, in which a unit also counts kUnitCost tiles for its start and end; the
+// resident warps cut it into equal runs, one each, whatever the rows' lengths are. Warps work
+// alone: each streams its own K and V rows with 16-byte cp.async into a ring of its own,
+// ahead across units, and writes what it finished. A unit that is cut leaves a partial
+// (m, l, acc) per run, joined in order by a second kernel, so the result does not depend on
+// timing. A run has at most two cut units (its first and its last), which bounds the
+// workspace by the grid.
 //
-// A tile is split over the CTA's 4 warps, 16 positions each. Every warp streams its own
-// K and V rows with 16-byte cp.async into a ring of its own, ahead across units, and meets the others
-// only at the end of a unit. Positions outside the live range or in a missing block are
-// filled with zeros by the copy and masked, so nothing that lies there is ever used.
+// Positions outside the live range or in a missing block are filled with zeros by the copy
+// and masked, so nothing that lies there is ever used.
 #pragma once
 
+#include <atomic>
+
 #include "paged.cuh"
+#include "tc_common.cuh"
 
 namespace rqk {
 namespace paged_attn {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kKeys = 16;                  // positions of a warp's part of a tile
-constexpr int kTile = kWarps * kKeys;      // positions of a tile
-constexpr int kHeads = 8;                  // query heads of a unit, at most
-constexpr int kMaxGrid = 608;              // CTAs of a launch, at most
-constexpr int kMinTiles = 1;               // tiles of a CTA's run, at least
+constexpr int kWarps = 4, kStages = 2;            // of a CTA of runs; stages of a warp's ring
+constexpr int kSplitWarps = 8;                    // of a CTA of one unit
+// its ring is deeper where the queries and weights do not need the shared memory
+template <typename KT>
+constexpr int split_stages = sizeof(KT) == 2 ? 3 : 2;
+constexpr int kMaxGrid = 304;              // CTAs of a launch, at most
+constexpr int kMaxRuns = kMaxGrid * kWarps;
+constexpr int kMinRun = 4;                 // tiles of a run, at least
+constexpr int kUnitCost = 2;               // what a unit's start and end count, in tiles
+constexpr int kMaxHeads = 16;              // query heads of a unit, at most
+constexpr int kMaxDevices = 64;
 
 struct Params {
   rq_paged_kv kv;
@@ -39,50 +47,61 @@ struct Params {
   float* lse;
   const int32_t *table, *requests, *positions;
   int rows, heads, batch, W, window;
-  int G, HG, GB;       // query heads per K/V head, groups of them, heads in a group
+  int G, GB, HG;       // query heads per K/V head, heads of a unit, units of a K/V head
+  int runs;            // runs (warps) of the launch
   float scale;         // times log2 e
-  float* part;         // [grid][2][GB][HD] partial sums
-  float2* part_ml;     // [grid][2][GB] (m, l)
-  int4* cut;           // [grid] (row, group, parts, 0) of the unit to join that starts there
+  float* part;         // [runs][2][GB][HD] partial sums
+  float2* part_ml;     // [runs][2][GB] (m, l)
+  int4* cut;           // [runs] (row, first head, heads, parts) of the unit that starts there and goes on
 };
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline size_t part_bytes(int gb, int hd) {
-  return align256((size_t)kMaxGrid * 2 * gb * hd * sizeof(float));
+  return align256((size_t)kMaxRuns * 2 * gb * hd * sizeof(float));
 }
-inline size_t ml_bytes(int gb) { return align256((size_t)kMaxGrid * 2 * gb * sizeof(float2)); }
+inline size_t ml_bytes(int gb) { return align256((size_t)kMaxRuns * 2 * gb * sizeof(float2)); }
 inline size_t workspace_bytes(int gb, int hd) {
-  return part_bytes(gb, hd) + ml_bytes(gb) + align256((size_t)kMaxGrid * sizeof(int4));
+  return part_bytes(gb, hd) + ml_bytes(gb) + align256((size_t)kMaxRuns * sizeof(int4));
 }
 
-// A unit's shared-memory ring and merge buffer, by element type and head size: the ring is
-// as deep as lets two or more CTAs share an SM (K rows of bf16 are padded by 16 bytes, so
-// the eight rows an ldmatrix reads fall into different banks).
+// A warp's ring, by element type and head size: stages of K and V rows. The 16-byte pieces of a
+// row are permuted by the row's number, so that one piece of eight rows -- what an ldmatrix
+// reads, and what eight lanes with a key each do -- falls into different banks.
 template <typename KT, int HD>
 struct Shape {
-  static constexpr int kPitch = sizeof(KT) == 2 ? HD * 2 + 16 : HD * 4;  // bytes of a row
-  static constexpr int kStage = 2 * kKeys * kPitch;                      // K rows, then V rows
-  static constexpr int kStages = HD == 128 ? 3 : 4;
-  static constexpr int kMergeDims = HD > 64 ? 64 : HD;  // dimensions joined at a time
-  static constexpr size_t kRing = (size_t)kWarps * kStages * kStage;
-  static constexpr size_t kSmem = kRing + (size_t)kWarps * kHeads * kMergeDims * sizeof(float);
+  static constexpr int kPitch = HD * (int)sizeof(KT);  // bytes of a row
+  // positions of a tile: 8 KB of K and V; 32 at most (a lane looks one up), 16 at least in
+  // bf16 (the second product's step)
+  static constexpr int kKeys = 4096 / kPitch < 32 ? 4096 / kPitch : 32;
+  static constexpr int kStage = 2 * kKeys * kPitch;    // K rows, then V rows
+  // where piece c of row r lies, in bytes from the tile's first row
+  static __device__ __forceinline__ int at(int r, int c) {
+    return r * kPitch + (c ^ (kPitch >= 128 ? r & 7 : (r >> 1) & 3)) * 16;
+  }
 };
 
 struct Row {
   int b, lo, pos, t0, nt;  // request, live positions [lo, pos], tiles [t0, t0 + nt)
 };
 
-__device__ __forceinline__ Row load_row(const Params& p, int r) {
+// row r's request and position as they stand; out of the list: no tiles
+__device__ __forceinline__ int2 row_words(const Params& p, int r) {
+  if (r >= p.rows) return make_int2(-1, -1);
+  return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
+}
+
+template <int kKeys>
+__device__ __forceinline__ Row row_of(const Params& p, int2 words) {
   Row x;
-  x.b = p.requests ? p.requests[r] : r;
-  x.pos = p.positions[r];
+  x.b = words.x;
+  x.pos = words.y;
   x.lo = x.t0 = x.nt = 0;
   if (x.b < 0 || x.b >= p.batch || x.pos < 0) return x;
   const int P = p.kv.block_size, first = x.pos / P - p.W + 1;
   if (first > 0) x.lo = first * P;
   if (p.window > 0) x.lo = max(x.lo, x.pos - p.window + 1);
-  x.t0 = x.lo / kTile;
-  x.nt = x.pos / kTile - x.t0 + 1;
+  x.t0 = x.lo / kKeys;
+  x.nt = x.pos / kKeys - x.t0 + 1;
   return x;
 }
 
@@ -113,6 +132,10 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) {
   *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
+// the log of the sum of e^s from the base-2 maximum and sum
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+}
 
 // ---------------------------------------------------------------- bf16 cache: tensor cores
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -140,6 +163,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void put2(uint16_t* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
+}
 // (lo, hi) as bf16 pairs: the rounded values, and what the rounding left
 __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
   const uint32_t u = pack_bf16(lo, hi);
@@ -148,23 +177,32 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
   return u;
 }
 
-// A warp's share of a unit over a bf16 cache. Decode is bound by reading the cache: the
-// tensor cores (mma.sync m16n8k16; a unit has at most 8 query rows, far below a tcgen05
-// tile) are there so that 8 queries a K/V head cost no more than one. The 16 rows of A hold
-// 8 heads twice: rows 0-7 a value's leading bf16 part, rows 8-15 the part that rounding
-// left, so both halves of a product come out of one instruction, in one thread (c0 + c2,
-// c1 + c3). f32 queries and their weights take a third part in a second instruction: 24
-// bits, every product exact. bf16 queries are exact in one part; their weights have two.
+// A warp's unit over a bf16 cache. Decode is bound by reading the cache: the tensor cores
+// (mma.sync m16n8k16; a unit has at most 16 query rows, far below a tcgen05 tile) are there so
+// that 8 queries a K/V head cost no more than one. The 16 rows of A hold 8 heads twice: rows
+// 0-7 a value's leading bf16 part, rows 8-15 the part that rounding left, so both halves of
+// a product come out of one instruction, in one thread (c0 + c2, c1 + c3). f32 queries and
+// their weights take a third part in a second instruction: 24 bits, every product exact.
+// bf16 queries are exact in one part; their weights have two.
 template <typename QT, int HD>
 struct MmaCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
+  static constexpr int kHeads = 8;
+  static constexpr int kScratch = 0;  // bytes of shared memory of a warp
   static constexpr int kSteps = HD / 16;
   using S = Shape<uint16_t, HD>;
+  static constexpr int K = S::kKeys, NT = K / 8;  // keys of a tile, in eights
   uint32_t q[kF32 ? 3 : 1][kSteps][2];
   float acc[HD / 8][2];
   float m, l;
 
-  __device__ __forceinline__ void begin(const Params& p, const QT* qrow, int live, int lane) {
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) acc[i][0] = acc[i][1] = 0.f;
+    m = neg_inf();
+    l = 0.f;
+  }
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
     const int g = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
@@ -181,260 +219,491 @@ struct MmaCore {
           q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)g * HD + d) : 0u;
         }
       }
-#pragma unroll
-    for (int i = 0; i < HD / 8; ++i) acc[i][0] = acc[i][1] = 0.f;
-    m = neg_inf();
-    l = 0.f;
   }
 
-  __device__ __forceinline__ void tile(const Params& p, uint32_t ks, uint32_t mask, int lane, float*) {
-    const uint32_t vs = ks + kKeys * S::kPitch;
-    float c[2][4] = {};
+  __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
+    const uint32_t vs = ks + K * S::kPitch;
+    float c[NT][4] = {};
     // B of the first product: K rows as they lie (8 keys x 8 dimensions a matrix)
-    const uint32_t kaddr = ks + ((lane >> 4) * 8 + (lane & 7)) * S::kPitch + ((lane >> 3) & 1) * 16;
+    const int krow = (lane >> 4) * 8 + (lane & 7), kpiece = (lane >> 3) & 1;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      uint32_t b[4];
-      ldmatrix4(kaddr + k * 32, b);
-      if constexpr (kF32) {
-        mma16816(c[0], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[0], b[1]);
-        mma16816(c[1], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[2], b[3]);
-      } else {
-        mma16816(c[0], q[0][k][0], 0u, q[0][k][1], 0u, b[0], b[1]);
-        mma16816(c[1], q[0][k][0], 0u, q[0][k][1], 0u, b[2], b[3]);
-      }
-    }
-    float e[2][4] = {};
-    if constexpr (kF32) {
+    for (int n = 0; n < NT; n += 2) {
+      float e[2][4] = {};
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         uint32_t b[4];
-        ldmatrix4(kaddr + k * 32, b);
-        mma16816(e[0], q[2][k][0], 0u, q[2][k][1], 0u, b[0], b[1]);
-        mma16816(e[1], q[2][k][0], 0u, q[2][k][1], 0u, b[2], b[3]);
+        ldmatrix4(ks + n * 8 * S::kPitch + S::at(krow, 2 * k + kpiece), b);
+        if constexpr (kF32) {
+          mma16816(c[n], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[0], b[1]);
+          mma16816(c[n + 1], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[2], b[3]);
+          mma16816(e[0], q[2][k][0], 0u, q[2][k][1], 0u, b[0], b[1]);
+          mma16816(e[1], q[2][k][0], 0u, q[2][k][1], 0u, b[2], b[3]);
+        } else {
+          mma16816(c[n], q[0][k][0], 0u, q[0][k][1], 0u, b[0], b[1]);
+          mma16816(c[n + 1], q[0][k][0], 0u, q[0][k][1], 0u, b[2], b[3]);
+        }
+      }
+      if constexpr (kF32) {
+        // an infinite key's product stands: the parts that are 0 would make it NaN
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (fabsf(c[n + j][i]) != -neg_inf()) c[n + j][i] += c[n + j][2 + i] + e[j][i];
       }
     }
     // this thread: head lane / 4, keys 8 n + 2 (lane % 4) + i
-    float s[2][2], mx = m;
+    float mx = m;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t bits = mask >> (n * 8 + (lane & 3) * 2);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x = c[n][i];
-        if constexpr (kF32) {
-          // an infinite key's product stands: the parts that are 0 would make it NaN
-          if (fabsf(x) != __int_as_float(0x7f800000)) x += c[n][2 + i] + e[n][i];
-        }
-        x *= p.scale;
-        s[n][i] = (mask >> (n * 8 + (lane & 3) * 2 + i)) & 1u ? x : neg_inf();
-        mx = fmaxf(mx, s[n][i]);
+        c[n][i] = (bits >> i) & 1u ? c[n][i] * scale_log2 : neg_inf();
+        mx = fmaxf(mx, c[n][i]);
       }
+    }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float ref = finite_or_zero(mx), scale = ex2(m - ref);
     m = mx;
-    float w[2][2];
+    l *= scale;
+    // A of the second product, 16 keys a step: the weights in their parts
+    uint32_t a[K / 16][4], e[K / 16][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int j = 0; j < K / 16; ++j)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) w[n][i] = ex2(s[n][i] - ref);
-    l = l * scale + ((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]));
-    const uint32_t a0 = split_bf16(w[0][0], w[0][1]), a2 = split_bf16(w[1][0], w[1][1]);
-    uint32_t a1, a3, e0 = 0, e2 = 0;
-    if constexpr (kF32) {
-      a1 = split_bf16(w[0][0], w[0][1]);
-      a3 = split_bf16(w[1][0], w[1][1]);
-      e0 = pack_bf16(w[0][0], w[0][1]);
-      e2 = pack_bf16(w[1][0], w[1][1]);
-    } else {
-      a1 = pack_bf16(w[0][0], w[0][1]);
-      a3 = pack_bf16(w[1][0], w[1][1]);
-    }
+      for (int i = 0; i < 2; ++i) {
+        float x = ex2(c[2 * j + i][0] - ref), y = ex2(c[2 * j + i][1] - ref);
+        l += x + y;
+        a[j][2 * i] = split_bf16(x, y);
+        if constexpr (kF32) {
+          a[j][2 * i + 1] = split_bf16(x, y);
+          e[j][i] = pack_bf16(x, y);
+        } else {
+          a[j][2 * i + 1] = pack_bf16(x, y);
+        }
+      }
     // B of the second product: V rows transposed on the way in
-    const uint32_t vaddr = vs + (((lane >> 3) & 1) * 8 + (lane & 7)) * S::kPitch + (lane >> 4) * 16;
+    const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vpiece = lane >> 4;
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) {
-      uint32_t b[4];
-      ldmatrix4_trans(vaddr + d * 32, b);
+      float o[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < K / 16; ++j) {
+        uint32_t b[4];
+        ldmatrix4_trans(vs + j * 16 * S::kPitch + S::at(vrow, 2 * d + vpiece), b);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma16816(o[n], a[j][0], a[j][1], a[j][2], a[j][3], b[2 * n], b[2 * n + 1]);
+          if constexpr (kF32) mma16816(o[n], e[j][0], 0u, e[j][1], 0u, b[2 * n], b[2 * n + 1]);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        float o[4] = {};
-        mma16816(o, a0, a1, a2, a3, b[2 * n], b[2 * n + 1]);
-        if constexpr (kF32) mma16816(o, e0, 0u, e2, 0u, b[2 * n], b[2 * n + 1]);
-        float* a = acc[2 * d + n];
-        a[0] = fmaf(a[0], scale, o[0] + o[2]);
-        a[1] = fmaf(a[1], scale, o[1] + o[3]);
+        acc[2 * d + n][0] = fmaf(acc[2 * d + n][0], scale, o[n][0] + o[n][2]);
+        acc[2 * d + n][1] = fmaf(acc[2 * d + n][1], scale, o[n][1] + o[n][3]);
       }
     }
   }
 
-  // this warp's (m, l) of each head, and its sums of dimensions [d0, d0 + n)
-  __device__ __forceinline__ void state(float2* ml, int lane) {
+  // the unit's outputs, or with PARTIAL its (m, l) and sums
+  template <bool PARTIAL, typename OT>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
     float t = l + __shfl_xor_sync(0xffffffffu, l, 1);
     t += __shfl_xor_sync(0xffffffffu, t, 2);
-    if ((lane & 3) == 0) ml[lane >> 2] = make_float2(m, t);
-  }
-  template <int N>
-  __device__ __forceinline__ void sums(float* dst, int d0, int lane) {
     const int g = lane >> 2, c = (lane & 3) * 2;
+    if (g >= live) return;
+    const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
 #pragma unroll
     for (int i = 0; i < HD / 8; ++i)
-      if (i * 8 >= d0 && i * 8 < d0 + N)
-        *reinterpret_cast<float2*>(dst + g * N + i * 8 - d0 + c) = make_float2(acc[i][0], acc[i][1]);
+      put2(out + (size_t)g * HD + i * 8 + c, acc[i][0] * inv, acc[i][1] * inv);
+    if ((lane & 3) != 0) return;
+    if (PARTIAL) ml[g] = make_float2(m, t);
+    else if (lse) lse[g] = log_sum(m, t);
+  }
+};
+
+// The same with 9 to 16 heads of a K/V head: the 16 rows of A are one head each, and each part
+// of a value is an instruction of its own. One pass over the cache instead of two.
+template <typename QT, int HD>
+struct WideCore {
+  static constexpr bool kF32 = sizeof(QT) == 4;
+  static constexpr int kHeads = 16;
+  static constexpr int kSteps = HD / 16, QP = kF32 ? 3 : 1, WP = kF32 ? 3 : 2;  // parts
+  static constexpr int kScratch = 0;
+  using S = Shape<uint16_t, HD>;
+  static constexpr int K = S::kKeys, NT = K / 8;
+  uint32_t q[QP][kSteps][4];
+  float acc[HD / 8][4];
+  float m[2], l[2];  // heads lane / 4, lane / 4 + 8
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    m[0] = m[1] = neg_inf();
+    l[0] = l[1] = 0.f;
+  }
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
+    const int c = (lane & 3) * 2;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int g = (lane >> 2) + (i & 1) * 8, d = k * 16 + c + (i >> 1) * 8;
+        if constexpr (kF32) {
+          float2 x = make_float2(0.f, 0.f);
+          if (g < live) x = *reinterpret_cast<const float2*>(qrow + (size_t)g * HD + d);
+#pragma unroll
+          for (int j = 0; j < QP; ++j) q[j][k][i] = split_bf16(x.x, x.y);
+        } else {
+          q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)g * HD + d) : 0u;
+        }
+      }
+  }
+
+  __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
+    const uint32_t vs = ks + K * S::kPitch;
+    float c[NT][4] = {};
+    const int krow = (lane >> 4) * 8 + (lane & 7), kpiece = (lane >> 3) & 1;
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      float e[2][4] = {};
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t b[4];
+        ldmatrix4(ks + n * 8 * S::kPitch + S::at(krow, 2 * k + kpiece), b);
+#pragma unroll
+        for (int j = 0; j < QP; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mma16816(j == 0 ? c[n + i] : e[i], q[j][k][0], q[j][k][1], q[j][k][2], q[j][k][3], b[2 * i],
+                     b[2 * i + 1]);
+      }
+      if constexpr (kF32) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (fabsf(c[n + j][i]) != -neg_inf()) c[n + j][i] += e[j][i];
+      }
+    }
+    float scale[2], ref[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = m[h];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t bits = mask >> (n * 8 + (lane & 3) * 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float& x = c[n][2 * h + i];
+          x = (bits >> i) & 1u ? x * scale_log2 : neg_inf();
+          mx = fmaxf(mx, x);
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      ref[h] = finite_or_zero(mx);
+      scale[h] = ex2(m[h] - ref[h]);
+      m[h] = mx;
+      l[h] *= scale[h];
+    }
+    uint32_t a[WP][K / 16][4];
+#pragma unroll
+    for (int j = 0; j < K / 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // A register i: head (i & 1), keys + 8 (i >> 1)
+        const int h = i & 1;
+        float x = ex2(c[2 * j + (i >> 1)][2 * h] - ref[h]);
+        float y = ex2(c[2 * j + (i >> 1)][2 * h + 1] - ref[h]);
+        l[h] += x + y;
+#pragma unroll
+        for (int w = 0; w < WP; ++w) a[w][j][i] = split_bf16(x, y);
+      }
+    const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vpiece = lane >> 4;
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) {
+      float o[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < K / 16; ++j) {
+        uint32_t b[4];
+        ldmatrix4_trans(vs + j * 16 * S::kPitch + S::at(vrow, 2 * d + vpiece), b);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int w = 0; w < WP; ++w)
+            mma16816(o[n], a[w][j][0], a[w][j][1], a[w][j][2], a[w][j][3], b[2 * n], b[2 * n + 1]);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[2 * d + n][i] = fmaf(acc[2 * d + n][i], scale[i >> 1], o[n][i]);
+    }
+  }
+
+  template <bool PARTIAL, typename OT>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+    const int c = (lane & 3) * 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t = l[h] + __shfl_xor_sync(0xffffffffu, l[h], 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      const int g = (lane >> 2) + h * 8;
+      if (g >= live) continue;
+      const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i)
+        put2(out + (size_t)g * HD + i * 8 + c, acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
+      if ((lane & 3) != 0) continue;
+      if (PARTIAL) ml[g] = make_float2(m[h], t);
+      else if (lse) lse[g] = log_sum(m[h], t);
+    }
   }
 };
 
 // ---------------------------------------------------------------- f32 cache: FMA
-// A lane holds HD / 32 consecutive dimensions of up to GP heads' queries and sums. Its part
-// of each score meets the other lanes' in a transposing butterfly (32 values in 31 shuffles,
-// one left per lane); the weights go round through shared memory.
+// packed pairs of f32: one instruction for two products
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {  // d += a * b
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ void lds2(uint32_t addr, f32x2& a, f32x2& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+
+// A tile is 1024 elements of K and of V whatever the head size. For the scores a lane takes 32
+// dimensions of one key (key lane % K, dimensions 32 (lane / K) ..) and all GP heads, the
+// queries read from shared memory, where all lanes of a slice read the same address. For
+// the sums a lane takes 4 dimensions and 8 of the keys, the weights through shared memory,
+// each stored twice (a packed pair).
+//
+// The reference that weights are taken against moves only when a score passes it by more
+// than 2^kSlack: sums keep 2^kSlack of headroom instead of finding each tile's maximum.
 template <typename QT, int HD, int GP>
 struct FmaCore {
-  static constexpr int E = HD / 32;
-  static constexpr int NV = kKeys * GP < 32 ? kKeys * GP : 32;  // scores of a butterfly
-  static constexpr int NB = kKeys * GP / NV;                     // butterflies of a tile
-  static constexpr int KB = NV / GP;                             // keys of a butterfly
+  static constexpr int kHeads = GP;
   using S = Shape<float, HD>;
-  float q[GP][E], acc[GP][E];
-  float m, l;  // of head index % GP, index = lane / (32 / NV)
+  static constexpr int K = S::kKeys;              // 8, 16, 32
+  static constexpr int SL = 32 / K;               // slices of 32 dimensions of a key
+  static constexpr int KS = 128 / HD;             // slices of 8 keys of a tile
+  static constexpr int kQPitch = 32 + 4;          // floats of a query slice: apart in banks
+  static constexpr int kWPitch = 8 * GP * 2 + 4;  // floats of a key slice's weights
+  static constexpr int kScratch = (GP * SL * kQPitch + KS * kWPitch) * 4;  // bytes of a warp
+  static constexpr float kSlack = 10.f;
+  f32x2 acc[GP][2];
+  float m[GP], l[GP];
 
   static __device__ __forceinline__ float one(const float* p) { return *p; }
   static __device__ __forceinline__ float one(const uint16_t* p) { return bf16lo(*p); }
 
-  static __device__ __forceinline__ void row(uint32_t addr, float (&v)[E]) {
-    if constexpr (E == 4)
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(addr) : "memory");
-    else if constexpr (E == 2)
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(addr) : "memory");
-    else
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0]) : "r"(addr) : "memory");
-  }
-
-  __device__ __forceinline__ void begin(const Params& p, const QT* qrow, int live, int lane) {
-#pragma unroll
-    for (int h = 0; h < GP; ++h)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        q[h][e] = h < live ? one(qrow + (size_t)h * HD + lane * E + e) : 0.f;
-        acc[h][e] = 0.f;
-      }
-    m = neg_inf();
-    l = 0.f;
-  }
-
-  __device__ __forceinline__ float max_over_keys(float x) const {
-#pragma unroll
-    for (int o = GP * (32 / NV); o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-  }
-
-  __device__ __forceinline__ void tile(const Params& p, uint32_t ks, uint32_t mask, int lane, float* sw) {
-    const uint32_t vs = ks + kKeys * S::kPitch;
-    const int vi = lane / (32 / NV);
-    float s[NB], mx = m;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float v[NV];
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        float x[E];
-        row(ks + (b * KB + k) * S::kPitch + lane * E * 4, x);
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          float d = q[h][0] * x[0];
-#pragma unroll
-          for (int e = 1; e < E; ++e) d = fmaf(q[h][e], x[e], d);
-          v[k * GP + h] = d;
-        }
-      }
-#pragma unroll
-      for (int o = 16, n = NV / 2; n >= 1; o >>= 1, n >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-      }
-      if (NV == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-      s[b] = (mask >> (b * KB + vi / GP)) & 1u ? v[0] * p.scale : neg_inf();
-      mx = fmaxf(mx, s[b]);
-    }
-    mx = max_over_keys(mx);
-    const float ref = finite_or_zero(mx), scale = ex2(m - ref);
-    m = mx;
-    l *= scale;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float w = ex2(s[b] - ref);
-      l += w;
-      sw[b * NV + vi] = w;
-    }
-    __syncwarp();
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
-      const float sc = __shfl_sync(0xffffffffu, scale, h * (32 / NV));
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[h][e] *= sc;
+      acc[h][0] = acc[h][1] = pair(0.f, 0.f);
+      m[h] = neg_inf();
+      l[h] = 0.f;
     }
+  }
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float* scratch) {
 #pragma unroll
-    for (int k = 0; k < kKeys; ++k) {
-      float x[E];
-      row(vs + k * S::kPitch + lane * E * 4, x);
+    for (int h = 0; h < GP; ++h)
+#pragma unroll
+      for (int sl = 0; sl < SL; ++sl)
+        scratch[(h * SL + sl) * kQPitch + lane] =
+            h < live ? one(qrow + (size_t)h * HD + sl * 32 + lane) : 0.f;
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane,
+                                       float* scratch) {
+    const uint32_t vs = ks + K * S::kPitch, qs = smem_u32(scratch);
+    float* const sw = scratch + GP * SL * kQPitch;
+    const int key = lane % K, sl = lane / K;
+    f32x2 d[GP];
+#pragma unroll
+    for (int h = 0; h < GP; ++h) d[h] = pair(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      f32x2 k0, k1;
+      lds2(ks + S::at(key, sl * 8 + c), k0, k1);
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        const float w = sw[k * GP + h];
+        f32x2 q0, q1;
+        lds2(qs + ((h * SL + sl) * kQPitch + c * 4) * 4, q0, q1);
+        fma2(d[h], q0, k0);
+        fma2(d[h], q1, k1);
+      }
+    }
+    const bool live = (mask >> key) & 1u;
+    float s[GP];
+    bool over = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[h][e] = fmaf(w, x[e], acc[h][e]);
+    for (int h = 0; h < GP; ++h) {
+      const float2 x = unpair(d[h]);
+      s[h] = x.x + x.y;
+#pragma unroll
+      for (int o = K; o < 32; o <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
+      s[h] = live ? s[h] * scale_log2 : neg_inf();
+      over |= s[h] > m[h] + kSlack;
+    }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        float mx = fmaxf(m[h], s[h]);
+#pragma unroll
+        for (int o = 1; o < K; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float f = ex2(m[h] - finite_or_zero(mx));
+        m[h] = mx;
+        l[h] *= f;
+        const f32x2 f2 = pair(f, f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f32x2 z = pair(0.f, 0.f);
+          fma2(z, acc[h][i], f2);
+          acc[h][i] = z;
+        }
+      }
+    }
+    // weights: slice key / 8, entry key % 8
+    if (sl == 0) {
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        const float w = ex2(s[h] - finite_or_zero(m[h]));
+        l[h] += w;
+        *reinterpret_cast<float2*>(sw + (key / 8) * kWPitch + ((key % 8) * GP + h) * 2) = make_float2(w, w);
+      }
+    }
+    __syncwarp();
+    const int piece = lane % (HD / 4), slice = lane / (HD / 4);
+    const uint32_t ws = smem_u32(sw + slice * kWPitch);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f32x2 v0, v1;
+      lds2(vs + S::at(slice * 8 + i, piece), v0, v1);
+      f32x2 w[GP];
+      if constexpr (GP == 1) {
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(w[0]) : "r"(ws + i * 8) : "memory");
+      } else {
+#pragma unroll
+        for (int h = 0; h < GP; h += 2) lds2(ws + (i * GP + h) * 8, w[h], w[h + 1]);
+      }
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        fma2(acc[h][0], w[h], v0);
+        fma2(acc[h][1], w[h], v1);
       }
     }
     __syncwarp();
   }
 
-  __device__ __forceinline__ void state(float2* ml, int lane) {
-    float t = l;
+  template <bool PARTIAL, typename OT>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
 #pragma unroll
-    for (int o = GP * (32 / NV); o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    const int h = lane / (32 / NV);
-    if (lane % (32 / NV) == 0 && h < GP) ml[h] = make_float2(m, t);
-    if (lane >= GP && lane < kHeads) ml[lane] = make_float2(neg_inf(), 0.f);
-  }
-  template <int N>
-  __device__ __forceinline__ void sums(float* dst, int d0, int lane) {
+    for (int h = 0; h < GP; ++h) {
+      float t = l[h];
 #pragma unroll
-    for (int h = 0; h < GP; ++h)
+      for (int o = 1; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      float2 a = unpair(acc[h][0]), b = unpair(acc[h][1]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e - d0;
-        if (d >= 0 && d < N) dst[h * N + d] = acc[h][e];
+      for (int o = HD / 4; o < 32; o <<= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+        b.x += __shfl_xor_sync(0xffffffffu, b.x, o);
+        b.y += __shfl_xor_sync(0xffffffffu, b.y, o);
       }
+      if (h >= live) continue;
+      const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
+      if (lane < HD / 4) {
+        put2(out + (size_t)h * HD + lane * 4, a.x * inv, a.y * inv);
+        put2(out + (size_t)h * HD + lane * 4 + 2, b.x * inv, b.y * inv);
+      }
+      if (lane != 0) continue;
+      if (PARTIAL) ml[h] = make_float2(m[h], t);
+      else if (lse) lse[h] = log_sum(m[h], t);
+    }
   }
 };
 
 // ---------------------------------------------------------------- the kernel
-enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };  // of the run's piece; of the unit
+// flags of a tile: begins / ends its run's piece of the unit; that piece has the unit's first
+// / last tile
+enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };
 
-template <typename QT, typename KT, int HD, typename Core>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ Params p) {
+// SPLIT: not a list of runs, but one unit for each cluster of gridDim.x CTAs, its tiles spread
+// evenly over their warps and joined through shared memory at the end: no join kernel and
+// no search, for few units.
+//
+// At least two CTAs an SM are asked for so that registers are not held back further: the
+// f32-query kernel takes 255 with the bound of two, 185 without one, and reads 64 sessions of
+// 3000 positions in 476 us against 563.
+template <typename QT, typename KT, int HD, typename Core, bool SPLIT>
+__global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT ? 1 : 2)
+    attend_kernel(const __grid_constant__ Params p) {
   using S = Shape<KT, HD>;
-  constexpr int NS = S::kStages;
+  constexpr int NW = SPLIT ? kSplitWarps : kWarps, NT = NW * 32;
+  constexpr int NS = SPLIT ? split_stages<KT> : kStages, K = S::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[kWarps];
-  __shared__ long long s_off;             // the run's first tile, counted from row s_row's first
-  __shared__ int s_row;
-  __shared__ int4 s_desc[kWarps][NS];     // row, group, key mask, flags of each stage's part
-  __shared__ float2 s_ml[kWarps][kHeads];
-  __shared__ __align__(16) float s_w[kWarps][kKeys * kHeads];
+  __shared__ int4 s_desc[NW][NS];  // each stage's tile: row, K/V head, group * 16 + flags, key mask
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int units = p.kv.heads * p.HG;    // units of a row
-  float* const s_acc = reinterpret_cast<float*>(smem + S::kRing);
-
-  // where this CTA's run starts: prefix sums of the rows' tiles, a slice of rows per thread
-  const int slice = (p.rows + kThreads - 1) / kThreads;
+  const int units = p.kv.heads * p.HG;  // units of a row
+  const int run = blockIdx.x * NW + warp;
+  const int P = p.kv.block_size;
+  auto empty_row = [&](int r, int h0, int h1, int i0, int step) {  // a row without a live position
+    QT* o = static_cast<QT*>(p.out) + (size_t)r * p.heads * HD;
+    for (int i = h0 * HD + i0; i < h1 * HD; i += step) put(o + i, 0.f);
+    if (p.lse)
+      for (int i = h0 + i0; i < h1; i += step) p.lse[(size_t)r * p.heads + i] = neg_inf();
+  };
+  int4 cut = make_int4(0, 0, 0, 0);
+  // the warp's tiles: the list's entries [at, stop), the first of them tile t of unit (kvh, hg)
+  // of row r; a run of the list is `per` entries
+  int r = 0, kvh = 0, hg = 0, t = 0;
+  long long at = 0, stop = 0, per = 1;
+  Row x;
+  int2 next_words = make_int2(-1, -1);
+  if constexpr (SPLIT) {
+    const int u = blockIdx.y % units;
+    r = blockIdx.y / units;
+    kvh = u / p.HG;
+    hg = u % p.HG;
+    const int2 words = row_words(p, r);
+    x = row_of<K>(p, words);
+    if (x.nt == 0) {  // the whole cluster's
+      const int h0 = kvh * p.G + hg * Core::kHeads;
+      if (blockIdx.x == 0 && words.x >= 0 && words.x < p.batch)
+        empty_row(r, h0, min(h0 + Core::kHeads, (kvh + 1) * p.G), tid, NT);
+      return;
+    }
+    const long long n = (long long)gridDim.x * NW;
+    t = (int)(x.nt * (long long)run / n);
+    at = t;
+    stop = x.nt * (long long)(run + 1) / n;
+  } else {
+    __shared__ long long s_scan[NW];
+    __shared__ long long s_off[NW];  // each run's start, counted from its row's start
+    __shared__ int s_row[NW];
+  // where each run starts: prefix sums of the rows' costs, a slice of rows per thread
+  auto cost = [&](int r) {
+    const int nt = row_of<K>(p, row_words(p, r)).nt;
+    return nt ? (long long)(nt + kUnitCost) * units : 0ll;
+  };
+  const int slice = (p.rows + NT - 1) / NT;
   const int r0 = min(tid * slice, p.rows), r1 = min(r0 + slice, p.rows);
   long long own = 0;
-  for (int r = r0; r < r1; ++r) own += (long long)load_row(p, r).nt * units;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) own += cost(r);
   long long inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -445,225 +714,408 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if (w < warp) inc += s_scan[w];
     total += s_scan[w];
   }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kMinTiles) per = kMinTiles;
-  const long long begin = min((long long)blockIdx.x * per, total);
-  const int n = (int)(min(begin + per, total) - begin);
-  if (n > 0 && inc - own <= begin && begin < inc) {
-    long long at = begin - (inc - own);
-    for (int r = r0; r < r1; ++r) {
-      const long long t = (long long)load_row(p, r).nt * units;
-      if (at < t) {
-        s_row = r;
-        s_off = at;
-        break;
+  per = (total + p.runs - 1) / p.runs;
+  if (per < kMinRun + kUnitCost) per = kMinRun + kUnitCost;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const long long begin = (blockIdx.x * NW + w) * per;
+    if (inc - own <= begin && begin < inc) {
+      long long at = begin - (inc - own);
+      for (int r = r0; r < r1; ++r) {
+        const long long t = cost(r);
+        if (at < t) {
+          s_row[w] = r;
+          s_off[w] = at;
+          break;
+        }
+        at -= t;
       }
-      at -= t;
     }
   }
   __syncthreads();
   pdl_trigger();
   // rows of empty requests
-  for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    const int b = p.requests ? p.requests[r] : r;
-    if (b < 0 || b >= p.batch || p.positions[r] >= 0) continue;
-    QT* o = static_cast<QT*>(p.out) + (size_t)r * p.heads * HD;
-    for (int i = tid; i < p.heads * HD; i += kThreads) put(o + i, 0.f);
-    if (p.lse)
-      for (int i = tid; i < p.heads; i += kThreads) p.lse[(size_t)r * p.heads + i] = neg_inf();
+  for (int r = run; r < p.rows; r += p.runs) {
+    const int2 words = row_words(p, r);
+    if (words.x < 0 || words.x >= p.batch || words.y >= 0) continue;
+    empty_row(r, 0, p.heads, lane, 32);
   }
-  int4 cut = make_int4(0, 0, 0, 0);
-  if (n > 0) {
-    // ---- the warp's stream of parts: a cursor over (row, group, tile), one table entry ahead
-    Row x = load_row(p, s_row);
-    int r = s_row, u = (int)(s_off / x.nt), t = (int)(s_off % x.nt);
-    int issued = 0;
-    const int P = p.kv.block_size;
-    const uint32_t ring = smem_u32(smem) + warp * NS * S::kStage;
-    int key = 0, page = 0, id = -1;  // lane i < 16: the i-th key of the cursor's part
-    auto look_up = [&]() {
-      key = (x.t0 + t) * kTile + warp * kKeys + (lane & 15);
-      page = key / P;
-      id = -1;
-      if (key >= x.lo && key <= x.pos && key >= 0)
-        id = p.table[(size_t)x.b * p.W + (page < p.W ? page : page % p.W)];
+    const long long begin = run * per;
+    stop = min(begin + per, total);
+    at = stop;
+    if (begin < total) {
+      r = s_row[warp];
+      x = row_of<K>(p, row_words(p, r));
+      next_words = row_words(p, r + 1);
+      const int unit_cost = x.nt + kUnitCost, u = (int)(s_off[warp] / unit_cost);
+      const int in = (int)(s_off[warp] % unit_cost);
+      kvh = u / p.HG;
+      hg = u % p.HG;
+      t = max(in - kUnitCost, 0);
+      at = begin + (t - (in - kUnitCost));
+    }
+  }
+  Core core;
+  core.clear();
+  if (at < stop) {
+    // ---- the cursor over the tiles. Table entries are read 32 pages at a time, a lane each,
+    // well ahead of their use: ids of pages [base, base + 32), then the 32 that follow, the
+    // first 32 of the row (every unit of it begins there) and of the next row.
+    auto ids_from = [&](const Row& y, int first) {
+      const int page = first + lane;  // past 2^31: a large unsigned number
+      if (y.nt == 0 || (unsigned)page > (unsigned)(y.pos / P)) return -1;
+      return p.table[(size_t)y.b * p.W + (page < p.W ? page : page % p.W)];
     };
-    look_up();
+    int base = (x.t0 + t) * K / P, ids = ids_from(x, base), ids_after = ids_from(x, base + 32);
+    int ids0 = SPLIT || t == 0 ? ids : ids_from(x, x.t0 * K / P), ids_next = -1;
+    bool next_known = SPLIT, more = true, start = true, first = false;
+    int issued = 0;
+    const uint32_t ring = smem_u32(smem) + warp * NS * S::kStage;
+    float* const scratch = reinterpret_cast<float*>(smem + NW * NS * S::kStage + warp * Core::kScratch);
     auto issue = [&]() {
-      const int s = issued % NS;
-      const bool ok = id >= 0 && id < p.kv.n_blocks;
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      const int kvh = u / p.HG;
+      const int s = issued % NS, key = (x.t0 + t) * K + (K < 32 ? lane % K : lane), page = key / P;
+      if (!next_known) {  // its words came with this row's: its first pages
+        const Row y = row_of<K>(p, next_words);
+        ids_next = ids_from(y, y.t0 * K / P);
+        next_known = true;
+      }
+      const int rel = page - base;
+      const int id0 = __shfl_sync(0xffffffffu, ids, rel & 31);
+      const int id1 = __shfl_sync(0xffffffffu, ids_after, rel & 31);
+      const int id = rel < 32 ? id0 : id1;
+      const bool ok = key >= x.lo && key <= x.pos && id >= 0 && id < p.kv.n_blocks;
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (K < 32 ? (1u << (K & 31)) - 1u : ~0u);
       const long long off = ok ? id * p.kv.block_stride + (key - page * P) * p.kv.row_stride +
                                      kvh * p.kv.head_stride
                                : 0;
-      if (lane == 0) {
-        int f = 0;
-        if (issued == 0 || t == 0) f |= kStart;
-        if (issued == n - 1 || t == x.nt - 1) f |= kEnd;
-        if (t == x.nt - 1) f |= kLast;
-        // the unit's first tile is in this run: t steps back are
-        if (t <= issued) f |= kFirst;
-        s_desc[warp][s] = make_int4(r, u, (int)mask, f);
-        if (issued == n - 1 && t < x.nt - 1) {  // the unit goes on in the runs that follow
-          const long long end = begin + n - 1 + (x.nt - t);
-          cut = make_int4(r, u, t <= issued ? (int)((end - 1) / per - blockIdx.x) + 1 : 0, 0);
-        }
+      if (t == 0) first = true;
+      const bool last = t == x.nt - 1, end = last || at + 1 >= stop;
+      if (lane == 0)
+        s_desc[warp][s] = make_int4(r, kvh, hg * 16 + ((start ? kStart : 0) | (end ? kEnd : 0) |
+                                                       (first ? kFirst : 0) | (last ? kLast : 0)),
+                                    (int)mask);
+      if (start) {  // the unit's queries will be wanted soon
+        const int g0 = hg * Core::kHeads, n = min(Core::kHeads, p.G - g0) * HD * (int)sizeof(QT);
+        const char* q = static_cast<const char*>(p.q) +
+                        ((size_t)r * p.heads + (size_t)kvh * p.G + g0) * HD * sizeof(QT);
+        if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
       }
+      if (end && !last && first)  // goes on in the runs that follow
+        cut = make_int4(r, kvh * p.G + hg * Core::kHeads, min(Core::kHeads, p.G - hg * Core::kHeads),
+                        (int)((at + (x.nt - t) - 1) / per - run) + 1);
       if (mask) {
         constexpr int CH = HD * sizeof(KT) / 16;  // 16-byte pieces of a row
-        constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;
+        constexpr int RPI = 32 / CH;              // rows of a warp's copy instruction
         const uint32_t dst = ring + s * S::kStage;
         const KT* kb = static_cast<const KT*>(p.kv.k);
         const KT* vb = static_cast<const KT*>(p.kv.v);
         const int c = lane % CH;
 #pragma unroll
-        for (int i = 0; i < kKeys / RPI; ++i) {
+        for (int i = 0; i < K / RPI; ++i) {
           const int row = i * RPI + lane / CH;
-          const long long o = __shfl_sync(0xffffffffu, off, row);
+          const long long e = __shfl_sync(0xffffffffu, off, row) + c * (16 / (int)sizeof(KT));
           const bool live = (mask >> row) & 1u;
-          const long long e = o + c * (16 / (int)sizeof(KT));
-          cp_async16(dst + row * S::kPitch + c * 16, kb + e, live);
-          cp_async16(dst + (kKeys + row) * S::kPitch + c * 16, vb + e, live);
+          cp_async16(dst + S::at(row, c), kb + e, live);
+          cp_async16(dst + K * S::kPitch + S::at(row, c), vb + e, live);
         }
       }
-      // on to the next part
+      // on to the next tile
       ++issued;
-      if (issued < n) {
-        if (++t == x.nt) {
-          t = 0;
-          if (++u == units) {
-            u = 0;
+      ++at;
+      start = last;
+      if (++t == x.nt) {
+        if (SPLIT) {
+          more = false;
+          return;
+        }
+        t = 0;
+        first = false;
+        at += kUnitCost;
+        const bool one_window = x.pos / P - x.t0 * K / P < 32;
+        if (++hg == p.HG) {
+          hg = 0;
+          if (++kvh == p.kv.heads) {
+            kvh = 0;
             do {
-              x = load_row(p, ++r);
-            } while (x.nt == 0 && r + 1 < p.rows);
+              x = row_of<K>(p, next_words);
+              ids0 = ids_next;
+              next_words = row_words(p, ++r + 1);
+              if (x.nt == 0) {  // an empty row between: the one after it is next
+                const Row y = row_of<K>(p, next_words);
+                ids_next = ids_from(y, y.t0 * K / P);
+              }
+              next_known = false;
+            } while (x.nt == 0 && r < p.rows);
           }
         }
-        look_up();
+        base = x.t0 * K / P;
+        ids = ids0;
+        if (!(one_window && kvh + hg > 0)) ids_after = ids_from(x, base + 32);
+      } else if ((x.t0 + t) * K / P - base >= 32) {
+        base += 32;
+        ids = ids_after;
+        ids_after = ids_from(x, base + 32);
       }
+      more = at < stop && x.nt > 0;
     };
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) {
-      if (issued < n) issue();
+      if (more) issue();
       cp_async_commit();
     }
-    Core core;
-    for (int i = 0; i < n; ++i) {
-      if (issued < n) issue();
+    for (int i = 0; i < issued; ++i) {
+      if (more) issue();
       cp_async_commit();
-      cp_async_wait<NS - 1>();
       __syncwarp();
       const int4 d = s_desc[warp][i % NS];
-      const int kvh = d.y / p.HG, g0 = (d.y % p.HG) * kHeads, live = min(kHeads, p.G - g0);
-      const size_t head = (size_t)d.x * p.heads + (size_t)kvh * p.G + g0;
-      if (d.w & kStart)
-        core.begin(p, static_cast<const QT*>(p.q) + head * HD, live, lane);
-      if (d.z) core.tile(p, ring + (i % NS) * S::kStage, (uint32_t)d.z, lane, s_w[warp]);
+      const int g0 = (d.z >> 4) * Core::kHeads, live = min(Core::kHeads, p.G - g0);
+      const size_t head = (size_t)d.x * p.heads + (size_t)d.y * p.G + g0;
+      if (d.z & kStart) {
+        core.clear();
+        core.load(static_cast<const QT*>(p.q) + head * HD, live, lane, scratch);
+      }
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      if (d.w) core.tile(p.scale, ring + (i % NS) * S::kStage, (uint32_t)d.w, lane, scratch);
       __syncwarp();  // the stage is free for the next copy
-      if (!(d.w & kEnd)) continue;
-      // ---- join the warps
-      constexpr int N = S::kMergeDims;
-      core.state(s_ml[warp], lane);
-      const bool whole = (d.w & kFirst) && (d.w & kLast);
-      const size_t slot = (size_t)blockIdx.x * 2 + ((d.w & kFirst) ? 1 : 0);
-#pragma unroll
-      for (int d0 = 0; d0 < HD; d0 += N) {
-        core.template sums<N>(s_acc + warp * kHeads * N, d0, lane);
-        __syncthreads();
-        for (int j = tid; j < live * N; j += kThreads) {
-          const int g = j / N, dd = j % N;
-          float M = neg_inf();
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][g].x);
-          const float ref = finite_or_zero(M);
-          float L = 0.f, A = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float c = ex2(s_ml[w][g].x - ref);
-            L += s_ml[w][g].y * c;
-            A += s_acc[(w * kHeads + g) * N + dd] * c;
-          }
-          if (whole) {
-            put(static_cast<QT*>(p.out) + (head + g) * HD + d0 + dd, L == 0.f ? 0.f : A / L);
-            if (p.lse && d0 + dd == 0)
-              p.lse[head + g] = L == 0.f ? neg_inf() : (M + log2f(L)) * 0.6931471805599453f;
-          } else {
-            p.part[(slot * p.GB + g) * HD + d0 + dd] = A;
-            if (d0 + dd == 0) p.part_ml[slot * p.GB + g] = make_float2(M, L);
-          }
-        }
-        __syncthreads();
+      if (SPLIT || !(d.z & kEnd)) continue;
+      if ((d.z & kFirst) && (d.z & kLast)) {
+        core.template end<false>(static_cast<QT*>(p.out) + head * HD, p.lse ? p.lse + head : nullptr,
+                                 nullptr, live, lane);
+      } else {
+        const size_t slot = ((size_t)run * 2 + ((d.z & kFirst) ? 1 : 0)) * p.GB;
+        core.template end<true>(p.part + slot * HD, nullptr, p.part_ml + slot, live, lane);
       }
     }
   }
-  if (tid == 0) p.cut[blockIdx.x] = cut;
-}
-
-// One CTA per (run, head of a group): if a unit starts in run blockIdx.x and goes on, its
-// partials -- the run's second slot, then the first slot of each run that follows -- are
-// summed in order.
-template <typename QT, int HD>
-__global__ void __launch_bounds__(HD) join_kernel(const __grid_constant__ Params p) {
-  pdl_wait();
-  const int4 cut = p.cut[blockIdx.x];
-  if (cut.z == 0) return;
-  const int kvh = cut.y / p.HG, g0 = (cut.y % p.HG) * kHeads, g = blockIdx.y;
-  if (g >= min(kHeads, p.G - g0)) return;
-  const size_t head = (size_t)cut.x * p.heads + (size_t)kvh * p.G + g0 + g;
-  const int d = threadIdx.x;
-  auto slot = [&](int i) { return (size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0); };
-  float M = neg_inf();
-  for (int i = 0; i < cut.z; ++i) M = fmaxf(M, p.part_ml[slot(i) * p.GB + g].x);
-  const float ref = finite_or_zero(M);
-  float L = 0.f, A = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < cut.z; ++i) {
-    const float2 ml = p.part_ml[slot(i) * p.GB + g];
-    const float a = p.part[(slot(i) * p.GB + g) * HD + d];
-    const float c = ex2(ml.x - ref);
-    L += ml.y * c;
-    A += a * c;
+  if constexpr (!SPLIT) {
+    if (lane == 0) p.cut[run] = cut;
+  } else {
+    // ---- join: the warps' sums in this CTA's shared memory (its ring is free), then each CTA
+    // of the cluster finishes a share of the outputs from every CTA's sums
+    const int live = min(Core::kHeads, p.G - hg * Core::kHeads), n = live * HD;
+    float* const s_sum = reinterpret_cast<float*>(smem);              // [NW][kHeads][HD]
+    float* const s_cta = s_sum + NW * Core::kHeads * HD;              // [kHeads][HD]
+    float2* const s_ml = reinterpret_cast<float2*>(s_cta + Core::kHeads * HD);  // [NW][kHeads]
+    float2* const s_cta_ml = s_ml + NW * Core::kHeads;                // [kHeads]
+    __syncthreads();
+    core.template end<true>(s_sum + warp * Core::kHeads * HD, nullptr, s_ml + warp * Core::kHeads, live, lane);
+    __syncthreads();
+    const size_t head = (size_t)r * p.heads + (size_t)kvh * p.G + hg * Core::kHeads;
+    const int ctas = gridDim.x;
+    for (int i = tid; i < n; i += NT) {
+      const int g = i / HD;
+      float m = neg_inf(), l = 0.f, a = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, s_ml[w * Core::kHeads + g].x);
+      const float ref = finite_or_zero(m);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = ex2(s_ml[w * Core::kHeads + g].x - ref);
+        l += s_ml[w * Core::kHeads + g].y * f;
+        a = fmaf(s_sum[w * Core::kHeads * HD + i], f, a);
+      }
+      if (ctas > 1) {
+        s_cta[i] = a;
+        if (i % HD == 0) s_cta_ml[g] = make_float2(m, l);
+      } else {
+        put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l);
+        if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
+      }
+    }
+    if (ctas == 1) return;
+    tc::cluster_sync();
+    const uint32_t sums = smem_u32(s_cta), mls = smem_u32(s_cta_ml);
+    for (int i = blockIdx.x * NT + tid; i < n; i += ctas * NT) {
+      const int g = i / HD;
+      float m = neg_inf(), l = 0.f, a = 0.f;
+      for (int c = 0; c < ctas; ++c) m = fmaxf(m, tc::ld_cluster(tc::mapa(mls + g * 8, c)));
+      const float ref = finite_or_zero(m);
+#pragma unroll 4
+      for (int c = 0; c < ctas; ++c) {
+        const float f = ex2(tc::ld_cluster(tc::mapa(mls + g * 8, c)) - ref);
+        l += tc::ld_cluster(tc::mapa(mls + g * 8 + 4, c)) * f;
+        a = fmaf(tc::ld_cluster(tc::mapa(sums + i * 4, c)), f, a);
+      }
+      put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l);
+      if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
+    }
+    tc::cluster_sync();  // no CTA leaves while another reads its sums
   }
-  put(static_cast<QT*>(p.out) + head * HD + d, L == 0.f ? 0.f : A / L);
-  if (p.lse && d == 0) p.lse[head] = L == 0.f ? neg_inf() : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// Launch one instantiation: as many CTAs as are resident at once, at most one per tile that
-// the largest rows could have.
+// Units that were cut: if a unit starts in run c and goes on, its partials -- run c's second
+// slot, then the first slot of each run that follows -- are summed in order. A CTA takes
+// kJoinWarps consecutive runs (blockIdx.x) and head blockIdx.y of their units. A unit of few
+// parts is a warp's, all eight at once; one of many parts (a long row over many runs, so
+// at most one or two among eight) is the whole CTA's: each warp sums a share of the parts.
+constexpr int kJoinWarps = 8, kJoinFew = 16;
+
+// (m, l, a) += the parts [i0, i1) of one head: m and l alike in every lane, a the lane's E
+// dimensions. `slot(i)`: where part i is.
+template <int E, typename Slot>
+__device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot slot, int lane, float& m,
+                                           float& l, float (&a)[E]) {
+  for (int b = i0; b < i1; b += 32) {
+    const int n = min(i1 - b, 32);
+    float2 ml = make_float2(neg_inf(), 0.f);
+    if (lane < n) ml = p.part_ml[slot(b + lane)];
+    const float mx = fmaxf(m, warp_max(ml.x)), ref = finite_or_zero(mx);
+    const float f = ex2(ml.x - ref), old = ex2(m - ref);
+    m = mx;
+    l = l * old + warp_sum(ml.y * f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] *= old;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      const float* src = p.part + slot(b + j) * (E * 32) + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = fmaf(src[e], fj, a[e]);
+    }
+  }
+}
+
+template <typename QT, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+  constexpr int E = HD / 32;
+  __shared__ int4 s_cut[kJoinWarps];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][HD];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = blockIdx.y;
+  const int run0 = blockIdx.x * kJoinWarps;
+  pdl_wait();
+  if (tid < kJoinWarps)
+    s_cut[tid] = run0 + tid < p.runs ? p.cut[run0 + tid] : make_int4(0, 0, 0, 0);
+  __syncthreads();
+  auto write = [&](const int4& cut, float m, float l, const float (&a)[E]) {
+    const size_t head = (size_t)cut.x * p.heads + cut.y + g;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) put(static_cast<QT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
+    if (p.lse && lane == 0) p.lse[head] = log_sum(m, l);
+  };
+  for (int c = 0; c < kJoinWarps; ++c) {
+    const int4 cut = s_cut[c];
+    if (g >= cut.z) continue;
+    auto slot = [&](int i) { return ((size_t)(run0 + c + i) * 2 + (i == 0 ? 1 : 0)) * p.GB + g; };
+    float m = neg_inf(), l = 0.f, a[E] = {};
+    if (cut.w <= kJoinFew) {
+      if (warp != c) continue;
+      join_parts<E>(p, 0, cut.w, slot, lane, m, l, a);
+      write(cut, m, l, a);
+      continue;
+    }
+    join_parts<E>(p, (int)((long long)cut.w * warp / kJoinWarps),
+                  (int)((long long)cut.w * (warp + 1) / kJoinWarps), slot, lane, m, l, a);
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
+    __syncthreads();
+    if (warp == 0) {
+      m = neg_inf();
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+      const float ref = finite_or_zero(m);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(s_m[w] - ref);
+        l += s_l[w] * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = fmaf(s_a[w][lane * E + e], f, a[e]);
+      }
+      write(cut, m, l, a);
+    }
+    __syncthreads();
+  }
+}
+
+// A split launch's CTAs per unit for `units` units of up to `tiles` tiles, or 0 for a launch of
+// runs. Measured (head_dim 128, bf16): one row of 8 K/V heads takes 5.8 / 6.6 / 9.9 / 23 us
+// split at 16 / 1000 / 4000 / 16000 positions against 9.4 / 16.0 / 16.2 / 23 us in runs, and
+// 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
+// of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
+// one row is split up to 32 tiles a warp, several rows up to 8 (1024 positions of one CTA).
+inline int split_ctas(long long units, long long tiles, int rows, int sms) {
+  if (units > sms) return 0;
+  int c = 1;
+  while (c < 8 && units * c * 2 <= sms) c *= 2;
+  // every warp of the cluster a tile at least
+  while (c > 1 && (long long)c * kSplitWarps > tiles * 2) c /= 2;
+  const long long most = tiles / (c * kSplitWarps);  // tiles of a warp, at most
+  return most <= (rows == 1 ? 32 : 8) ? c : 0;
+}
+
 template <typename QT, typename KT, int HD, typename Core>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+cudaError_t launch(Params p, cudaStream_t s) {
   using S = Shape<KT, HD>;
-  auto* kernel = attend_kernel<QT, KT, HD, Core>;
-  int dev = 0, sms = 0, per_sm = 0;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-  if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, S::kSmem);
   if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  static std::atomic<int> sm_count[kMaxDevices], resident[kMaxDevices];
+  int sms = dev < kMaxDevices ? sm_count[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if (dev < kMaxDevices) sm_count[dev].store(sms, std::memory_order_relaxed);
+  }
+  p.HG = (p.G + Core::kHeads - 1) / Core::kHeads;
+  p.GB = p.G < Core::kHeads ? p.G : Core::kHeads;
   long long keys = min((long long)p.W * p.kv.block_size, (long long)INT_MAX);
   if (p.window > 0 && p.window < keys) keys = p.window;
-  const long long most = (keys / kTile + 2) * p.rows * p.kv.heads * p.HG;
-  long long grid = (long long)sms * per_sm;
-  if (grid > kMaxGrid) grid = kMaxGrid;
-  if (grid > most) grid = most;
-  kernel<<<(unsigned)grid, kThreads, S::kSmem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const long long tiles = keys / S::kKeys + 2;  // of a unit, at most
+  const long long units = (long long)p.rows * p.kv.heads * p.HG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)p.GB, 1);
-  cfg.blockDim = dim3(HD, 1, 1);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (const int c = split_ctas(units, tiles, p.rows, sms)) {
+    auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
+    constexpr size_t ring = (size_t)kSplitWarps * (split_stages<KT> * S::kStage + Core::kScratch);
+    constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
+    constexpr size_t smem = ring > sums ? ring : sums;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)c, (unsigned)units, 1);
+    cfg.blockDim = dim3(kSplitWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
+  // as many CTAs as are resident at once, at most as many as the largest rows could fill
+  auto* kernel = attend_kernel<QT, KT, HD, Core, false>;
+  constexpr size_t smem = (size_t)kWarps * (kStages * S::kStage + Core::kScratch);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  int ctas = dev < kMaxDevices ? resident[dev].load(std::memory_order_relaxed) : 0;
+  if (ctas == 0) {
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    ctas = sms * per_sm < kMaxGrid ? sms * per_sm : kMaxGrid;
+    if (dev < kMaxDevices) resident[dev].store(ctas, std::memory_order_relaxed);
+  }
+  const long long most = (tiles * units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
+  const int grid = (int)(ctas < most ? ctas : most);
+  p.runs = grid * kWarps;
+  kernel<<<grid, kWarps * 32, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((p.runs + kJoinWarps - 1) / kJoinWarps), (unsigned)p.GB, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, join_kernel<QT, HD>, p);
 }
 

@@ -1,15 +1,21 @@
-// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore).
+// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore and WideCore).
 #include "paged_attn.cuh"
 
 namespace rqk {
 namespace paged_attn {
 
+template <typename QT, int HD>
+static cudaError_t by_heads(const Params& p, cudaStream_t s) {
+  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>>(p, s)
+                  : launch<QT, uint16_t, HD, WideCore<QT, HD>>(p, s);
+}
+
 template <typename QT>
 static cudaError_t by_head_dim(const Params& p, cudaStream_t s) {
   switch (p.kv.head_dim) {
-    case 32: return launch<QT, uint16_t, 32, MmaCore<QT, 32>>(p, s);
-    case 64: return launch<QT, uint16_t, 64, MmaCore<QT, 64>>(p, s);
-    default: return launch<QT, uint16_t, 128, MmaCore<QT, 128>>(p, s);
+    case 32: return by_heads<QT, 32>(p, s);
+    case 64: return by_heads<QT, 64>(p, s);
+    default: return by_heads<QT, 128>(p, s);
   }
 }
 

@@ -18,12 +18,18 @@ from __future__ import annotations
 import struct
 from collections import namedtuple
 from contextlib import contextmanager
+from functools import lru_cache
 
 import torch
 
 from .binding import (RQ_BF16, RQ_F32, RQ_OK, RQ_PAGED_BAD_INPUT, RQ_PAGED_NO_BLOCKS,
                       RQ_PAGED_NO_TOKENS, RQ_ROPE_HALVES, RQ_ROPE_INTERLEAVED, RQError, load)
 
+_F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+# the device and stream that a call finds current, without building the Python objects for them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _KV = struct.Struct("@PPqqqiiiii4x")  # rq_paged_kv
 _TYPE = {torch.float32: RQ_F32, torch.bfloat16: RQ_BF16}
 _ROPE = {"interleaved": RQ_ROPE_INTERLEAVED, "halves": RQ_ROPE_HALVES}
@@ -41,75 +47,84 @@ def _on(device, stream):
     """The tensors' device, and the stream the call runs on, made current."""
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
+            yield
         else:
             if stream.device != device:
                 raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                yield
 
 
-def _ints(name, t, n, device, dtype=torch.int32):
-    """The address of a contiguous integer tensor of n elements (at least)."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < n:
-        raise ValueError("%s: a contiguous %s tensor of %d elements on %s is wanted" %
-                         (name, dtype, n, device))
+def _ints(name, t, n, dev, dtype=_I32):
+    """The address of a contiguous integer tensor of (at least) n elements."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of %d elements on cuda:%d is wanted" %
+                         (name, dtype, n, dev))
     return t.data_ptr()
 
 
-def _rows(name, t, shape, dtype, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is wanted" %
-                         (name, dtype, shape, device))
+def _rows(name, t, shape, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s on cuda:%d is wanted" %
+                         (name, dtype, tuple(shape), dev))
     return t.data_ptr()
 
 
 def _cache(k, v):
-    """(rq_paged_kv packed, heads, head_dim) of a layer's cache."""
-    if k.dim() != 4 or k.dtype not in _TYPE or not k.is_cuda:
+    """(rq_paged_kv packed, heads, head_dim, device index) of a layer's cache."""
+    dev, dtype = k.get_device(), k.dtype
+    if dev < 0 or dtype not in _TYPE or k.dim() != 4:
         raise ValueError("k, v: f32 or bf16 CUDA tensors [n_blocks][block_size][heads][head_dim]")
-    n, p, h, hd = k.shape
+    n, p, h, hd = shape = k.shape
     strides = k.stride()
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or v.stride() != strides:
+    if v.shape != shape or v.dtype is not dtype or v.get_device() != dev or v.stride() != strides:
         raise ValueError("k and v differ in shape, strides, type or device")
     if strides[3] != 1:
         raise ValueError("k, v: the elements of a head must be contiguous")
-    return _KV.pack(k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2],
-                    _TYPE[k.dtype], h, hd, p, n), h, hd
+    return _KV.pack(k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], _TYPE[dtype],
+                    h, hd, p, n), h, hd, dev
 
+
+@lru_cache(maxsize=None)
+def _workspace_size(heads, kv_heads, head_dim):
+    return load().rq_paged_attention_workspace_size(heads, kv_heads, head_dim)
+
+
+# Each call below runs on the current stream of the tensors' device; a call on another
+# stream, or while another device is current, first makes those current.
 
 def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_tokens, out=None,
                stream=None) -> PagedPlan:
     """rq_paged_plan: new_lens, lens [B] int32, pool [4] int32, free_ids [n_blocks] int32 and
-    block_table [B][max_blocks] int32 (both updated in place).
+    block_table [B][max_blocks] int32 (the last two updated in place).
 
     out: a PagedPlan (or the same tuple) of tensors to write, lens [B], pool [4], cu_tokens
     [B + 1], requests and positions [max_tokens] int32 and slots [max_tokens] int64; its lens
     and pool may be the inputs themselves.  pool[2] says whether the call did anything
     (RQ_PAGED_*)."""
     L = load()
-    dev = lens.device
-    if not lens.is_cuda or block_table.dim() != 2:
+    dev = lens.get_device()
+    if dev < 0 or block_table.dim() != 2:
         raise ValueError("lens, block_table: CUDA tensors [B] and [B][max_blocks] are wanted")
+    if stream is not None or _current_device() != dev:
+        with _on(lens.device, stream):
+            return paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_tokens, out)
     B, W = block_table.shape
     M = int(max_tokens)
-    with _on(dev, stream) as st:
-        if out is None:
-            e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=dev)  # noqa: E731
-            out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, torch.int64))
-        elif not isinstance(out, PagedPlan):
-            out = PagedPlan(*out)
-        if lens.numel() != B or new_lens.numel() != B:
-            raise ValueError("new_lens, lens and block_table differ in their requests")
-        rc = L.rq_paged_plan(
-            B, W, int(block_size), free_ids.numel(), M, _ints("new_lens", new_lens, B, dev),
-            _ints("lens", lens, B, dev), _ints("pool", pool, 4, dev),
-            _ints("free_ids", free_ids, 1, dev), _ints("block_table", block_table, B * W, dev),
-            _ints("out.lens", out.lens, B, dev), _ints("out.pool", out.pool, 4, dev),
-            _ints("out.cu_tokens", out.cu_tokens, B + 1, dev),
-            _ints("out.requests", out.requests, M, dev),
-            _ints("out.positions", out.positions, M, dev),
-            _ints("out.slots", out.slots, M, dev, torch.int64), st)
+    if out is None:
+        e = lambda n, dt=_I32: torch.empty(n, dtype=dt, device=lens.device)  # noqa: E731
+        out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, _I64))
+    elif not isinstance(out, PagedPlan):
+        out = PagedPlan(*out)
+    if lens.numel() != B or new_lens.numel() != B:
+        raise ValueError("new_lens, lens and block_table differ in their requests")
+    rc = L.rq_paged_plan(
+        B, W, block_size, free_ids.numel(), M, _ints("new_lens", new_lens, B, dev),
+        _ints("lens", lens, B, dev), _ints("pool", pool, 4, dev), _ints("free_ids", free_ids, 1, dev),
+        _ints("block_table", block_table, B * W, dev), _ints("out.lens", out.lens, B, dev),
+        _ints("out.pool", out.pool, 4, dev), _ints("out.cu_tokens", out.cu_tokens, B + 1, dev),
+        _ints("out.requests", out.requests, M, dev), _ints("out.positions", out.positions, M, dev),
+        _ints("out.slots", out.slots, M, dev, _I64), _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_plan", rc)
     return out
@@ -123,11 +138,14 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
     values stored in k, v at `slots` (int64 [T]).  rope: "interleaved" or "halves" over the
     first rope_dim (default: all) dimensions; alphas: f32 [head_dim] or None for no norm."""
     L = load()
-    kv, hk, hd = _cache(k, v)
-    dev = k.device
-    if qkv.dim() != 2 or qkv.dtype not in _TYPE or qkv.device != dev or \
-            (qkv.shape[1] > 1 and qkv.stride(1) != 1):
-        raise ValueError("qkv: an f32 or bf16 tensor [T][width] with contiguous rows on %s" % dev)
+    kv, hk, hd, dev = _cache(k, v)
+    if stream is not None or _current_device() != dev:
+        with _on(k.device, stream):
+            return paged_append(qkv, k, v, positions, slots, q_alpha, k_alpha, eps, rope, rope_dim,
+                                rope_theta, q_dtype, out)
+    dtype = qkv.dtype
+    if qkv.dim() != 2 or dtype not in _TYPE or qkv.get_device() != dev or qkv.stride(1) != 1:
+        raise ValueError("qkv: an f32 or bf16 tensor [T][width], rows contiguous, on cuda:%d" % dev)
     T, width = qkv.shape
     heads = width // hd - 2 * hk
     if heads < 1 or width % hd:
@@ -135,18 +153,17 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
                          (width, hk, hk, hd))
     if rope not in _ROPE:
         raise ValueError("rope: 'interleaved' or 'halves'")
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, heads * hd), dtype=q_dtype or qkv.dtype, device=dev)
-        elif out.dtype not in _TYPE or (q_dtype is not None and out.dtype != q_dtype):
-            raise ValueError("out: f32 or bf16, as q_dtype says")
-        rc = L.rq_paged_append(
-            kv, T, heads, _TYPE[qkv.dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
-            None if q_alpha is None else _rows("q_alpha", q_alpha, (hd,), torch.float32, dev),
-            None if k_alpha is None else _rows("k_alpha", k_alpha, (hd,), torch.float32, dev),
-            eps, _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta,
-            _ints("positions", positions, T, dev), _ints("slots", slots, T, dev, torch.int64),
-            _TYPE[out.dtype], _rows("out", out, (T, heads * hd), out.dtype, dev), st)
+    if out is None:
+        out = torch.empty((T, heads * hd), dtype=q_dtype or dtype, device=k.device)
+    if out.dtype not in _TYPE or (q_dtype is not None and out.dtype is not q_dtype):
+        raise ValueError("out: f32 or bf16, as q_dtype says")
+    rc = L.rq_paged_append(
+        kv, T, heads, _TYPE[dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
+        None if q_alpha is None else _rows("q_alpha", q_alpha, (hd,), _F32, dev),
+        None if k_alpha is None else _rows("k_alpha", k_alpha, (hd,), _F32, dev),
+        eps, _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta,
+        _ints("positions", positions, T, dev), _ints("slots", slots, T, dev, _I64),
+        _TYPE[out.dtype], _rows("out", out, (T, heads * hd), out.dtype, dev), _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_append", rc)
     return out
@@ -159,30 +176,35 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     was; None: row r is request r), all int32 -> (out [R][heads * head_dim], lse [R][heads]
     f32, None unless a tensor or True is passed for it)."""
     L = load()
-    kv, hk, hd = _cache(k, v)
-    dev = k.device
-    if q.dim() != 2 or q.dtype not in _TYPE or q.shape[1] % hd:
-        raise ValueError("q: an f32 or bf16 tensor [R][heads * head_dim]")
-    R, heads = q.shape[0], q.shape[1] // hd
+    kv, hk, hd, dev = _cache(k, v)
+    if stream is not None or _current_device() != dev:
+        with _on(k.device, stream):
+            return paged_attention(q, k, v, block_table, positions, requests, window, scale, out, lse,
+                                   workspace)
+    dtype = q.dtype
+    if q.dim() != 2 or dtype not in _TYPE or q.shape[1] % hd or block_table.dim() != 2:
+        raise ValueError("q: an f32 or bf16 tensor [R][heads * head_dim]; block_table [B][max_blocks]")
+    shape = q.shape
+    R, heads = shape[0], shape[1] // hd
     B, W = block_table.shape
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is True:
-            lse = torch.empty((R, heads), dtype=torch.float32, device=dev)
-        nbytes = L.rq_paged_attention_workspace_size(heads, hk, hd)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous tensor on %s" % dev)
-        rc = L.rq_paged_attention(
-            kv, R, heads, B, W, _ints("block_table", block_table, B * W, dev),
-            None if requests is None else _ints("requests", requests, R, dev),
-            _ints("positions", positions, R, dev), window, scale, _TYPE[q.dtype],
-            _rows("q", q, (R, heads * hd), q.dtype, dev),
-            _rows("out", out, (R, heads * hd), q.dtype, dev),
-            None if lse is None else _rows("lse", lse, (R, heads), torch.float32, dev),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is True:
+        lse = torch.empty((R, heads), dtype=_F32, device=k.device)
+    if workspace is None:
+        nbytes = _workspace_size(heads, hk, hd)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = L.rq_paged_attention(
+        kv, R, heads, B, W, _ints("block_table", block_table, B * W, dev),
+        None if requests is None else _ints("requests", requests, R, dev),
+        _ints("positions", positions, R, dev), window, scale, _TYPE[dtype],
+        _rows("q", q, shape, dtype, dev), _rows("out", out, shape, dtype, dev),
+        None if lse is None else _rows("lse", lse, (R, heads), _F32, dev),
+        workspace.data_ptr(), nbytes, _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_attention", rc)
     return out, lse
@@ -207,9 +229,9 @@ class PagedCache:
         self.free_ids = e(n_blocks)
         self.maps = PagedPlan(e(batch), e(4), e(batch + 1), e(max_tokens), e(max_tokens),
                               e(max_tokens, torch.int64))
-        with _on(self.k.device, None) as st:
-            rc = load().rq_paged_pool_init(n_blocks, self.maps.pool.data_ptr(),
-                                           self.free_ids.data_ptr(), st)
+        with _on(self.k.device, None):
+            rc = load().rq_paged_pool_init(n_blocks, self.maps.pool.data_ptr(), self.free_ids.data_ptr(),
+                                           _current_stream(self.k.get_device()))
         if rc != RQ_OK:
             _fail("rq_paged_pool_init", rc)
 
