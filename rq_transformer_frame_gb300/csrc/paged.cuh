@@ -4,6 +4,8 @@
 
 #include <limits.h>
 
+#include <atomic>
+
 #include "../../include/rq.h"
 #include "common.cuh"
 
@@ -21,6 +23,26 @@ inline rq_status paged_kv_check(const rq_paged_kv* kv) {
   for (int64_t s : {kv->block_stride, kv->row_stride, kv->head_stride})
     if (s < 0 || s % unit != 0) return RQ_ERR_ARG;
   return RQ_OK;
+}
+
+constexpr int kMaxDevices = 64;
+
+// CTAs of `kernel` that are resident at once on the current device; `cache`: one entry a
+// device for this kernel and shared-memory size, 0 until looked up.
+template <typename K>
+inline cudaError_t resident_ctas(K* kernel, int threads, size_t smem, std::atomic<int>* cache, int* ctas) {
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *ctas = dev < kMaxDevices ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (*ctas != 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  *ctas = sms * per_sm;
+  if (dev < kMaxDevices) cache[dev].store(*ctas, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 }  // namespace rqk

@@ -8,7 +8,12 @@
 // F_i = theta^(-2i/rope_dim) / (2 pi) * 2^64 is exact in the position, so far positions
 // lose nothing (an f32 product pos * frequency is off by 0.06 rad at position 10^6).
 //
-// Each element is read once and written once: HBM-bound for many rows, latency for few.
+// Each element is read once and written once: HBM-bound for many rows, latency for few. A CTA
+// takes a row, or a slice of its heads where there are too few rows to fill the card: the
+// row's angles are computed once and shared. HD / 8 lanes share a head; a lane holds two pieces
+// of four dimensions such that both dimensions of each of its pairs are its own: 8
+// consecutive ones, or with the halves pairing 4 j and rope_dim / 2 + 4 j, so no value changes
+// lanes. Every warp's loads are issued at once, before the position is known.
 #include <cmath>
 
 #include "paged.cuh"
@@ -16,8 +21,12 @@
 namespace rqk {
 namespace {
 
-constexpr int kAppendThreads = 256;
+// Two warps a CTA: few wait for the angles together. 16384 rows of 48 heads of 128 (bf16) took
+// 70 us with two warps of up to 12 steps, 73 with four, 84 with eight; 3 steps in flight 70,
+// 4 70, 6 71 (two warps).
+constexpr int kAppendWarps = 2;
 constexpr int kMaxPairs = 64;
+constexpr int kAhead = 3;  // steps of a warp whose loads are in flight together
 
 struct AppendParams {
   rq_paged_kv kv;
@@ -25,127 +34,174 @@ struct AppendParams {
   long long qkv_stride;
   const float *q_alpha, *k_alpha;
   float eps;
-  int heads, style, rope_dim;
+  int heads, rope_dim;
+  int slices, steps;  // CTAs of a row, and steps (of 256 / HD heads) of each of their warps
   const int32_t* positions;
   const int64_t* slots;
   void* q_out;
   unsigned long long turns[kMaxPairs];  // F_i
 };
 
+// four values as they lie in memory
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
+struct Piece;
 template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
+struct Piece<float> {
+  float4 v;
+  __device__ __forceinline__ void widen(float* x) const { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+};
+template <>
+struct Piece<uint16_t> {
+  uint2 v;
+  __device__ __forceinline__ void widen(float* x) const {
+    x[0] = bf16lo(v.x), x[1] = bf16hi(v.x), x[2] = bf16lo(v.y), x[3] = bf16hi(v.y);
+  }
+};
+
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
-template <>
-__device__ __forceinline__ float4 load4<uint16_t>(const uint16_t* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+__device__ __forceinline__ void store4(uint16_t* p, const float* x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float4 v) {
-  *reinterpret_cast<float4*>(p) = v;
-}
-template <>
-__device__ __forceinline__ void store4<uint16_t>(uint16_t* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-}
-
-// One CTA per row; HD / 4 lanes share a head, four consecutive dimensions each.
-template <typename IT, typename OT, typename KT, int HD>
-__global__ void __launch_bounds__(kAppendThreads)
+template <typename IT, typename OT, typename KT, int HD, bool HALVES>
+__global__ void __launch_bounds__(kAppendWarps * 32)
     append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int LPH = HD / 4;                   // lanes per head
-  constexpr int HPS = kAppendThreads / LPH;     // heads per step of the CTA
-  __shared__ float2 s_cs[kMaxPairs];            // (cos, sin) of each pair's angle
-  const int tid = threadIdx.x, gl = tid % LPH;
-  const int t = blockIdx.x;
+  constexpr int LPH = HD / 8, HPS = 32 / LPH;  // lanes of a head, heads of a step
+  __shared__ float2 s_cs[kMaxPairs];
+  const int tid = threadIdx.x, lane = tid & 31, sub = lane / LPH, j = lane % LPH;
+  const int t = blockIdx.x / p.slices, slice = blockIdx.x - t * p.slices;
+  const int total = p.heads + 2 * p.kv.heads, half = p.rope_dim / 2;
+  const bool turned = j * 8 < p.rope_dim;
+  // this lane's dimensions: lo .. lo + 3 and hi .. hi + 3; its pairs are 4 j .. 4 j + 3
+  const int lo = HALVES && turned ? 4 * j : 8 * j, hi = HALVES && turned ? half + 4 * j : 8 * j + 4;
+  const IT* row = static_cast<const IT*>(p.qkv) + t * p.qkv_stride;
+  // the warp's heads: step i from h0 + i * HPS, this lane's head `sub` further, below h1
+  const int h0 = (slice * kAppendWarps + tid / 32) * p.steps * HPS, h1 = min(h0 + p.steps * HPS, total);
+  Piece<IT> in[kAhead][2];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b)
+      if (h + b * HPS + sub < h1) {
+        const IT* x = row + (long long)(h + b * HPS + sub) * HD;
+        in[b][0] = *reinterpret_cast<const Piece<IT>*>(x + lo);
+        in[b][1] = *reinterpret_cast<const Piece<IT>*>(x + hi);
+      }
+  };
+  load(h0);
   const int pos = p.positions[t];
+  const long long slot = p.slots[t];
   if (pos < 0) return;
-  if (tid < p.rope_dim / 2) {
-    const long long frac = (long long)((unsigned long long)pos * p.turns[tid]);
-    float s, c;
-    sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f /* 2^-63: half turns */, &s, &c);
-    s_cs[tid] = make_float2(c, s);
+  for (int i = tid; i < half; i += kAppendWarps * 32) {
+    const long long frac = (long long)((unsigned long long)pos * p.turns[i]);
+    float sn, cs;  // of half turns: 2^-63 of the fraction
+    sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &sn, &cs);
+    s_cs[i] = make_float2(cs, sn);
   }
   __syncthreads();
-  const long long slot = p.slots[t];
-  const bool stored = slot >= 0 && slot < (long long)p.kv.n_blocks * p.kv.block_size;
-  const long long block = stored ? slot / p.kv.block_size : 0;
-  const long long at = block * p.kv.block_stride + (slot - block * p.kv.block_size) * p.kv.row_stride;
-  const IT* row = static_cast<const IT*>(p.qkv) + (long long)t * p.qkv_stride;
-  const int Hk = p.kv.heads, total = p.heads + 2 * Hk, d = gl * 4;
-  const int half = p.rope_dim / 2;
-  // heads in steps of HPS over the CTA: every lane of a warp takes part in each shuffle
-  for (int base = 0; base < total; base += HPS) {
-    const int h = base + tid / LPH;
-    const bool live = h < total;
-    float4 x = live ? load4<IT>(row + (long long)h * HD + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool is_v = h >= p.heads + Hk;
-    const float* alpha = h < p.heads ? p.q_alpha : p.k_alpha;
-    float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w;
+  float c[4], s[4];
 #pragma unroll
-    for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!is_v && alpha) {
-      const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
-      const float4 a = *reinterpret_cast<const float4*>(alpha + d);
-      x = make_float4(x.x * r * a.x, x.y * r * a.y, x.z * r * a.z, x.w * r * a.w);
-    }
-    // the partner of dimension d in the halves pairing is rope_dim / 2 (half / 4 lanes) away
-    const int lane = tid & 31, src = p.style == RQ_ROPE_HALVES
-                                         ? (d < half ? lane + half / 4 : lane - half / 4) : lane;
-    float4 y;
-    y.x = __shfl_sync(0xffffffffu, x.x, src);
-    y.y = __shfl_sync(0xffffffffu, x.y, src);
-    y.z = __shfl_sync(0xffffffffu, x.z, src);
-    y.w = __shfl_sync(0xffffffffu, x.w, src);
-    if (!is_v && d < p.rope_dim) {
-      if (p.style == RQ_ROPE_INTERLEAVED) {
-        const float2 c0 = s_cs[d / 2], c1 = s_cs[d / 2 + 1];
-        x = make_float4(x.x * c0.x - x.y * c0.y, x.x * c0.y + x.y * c0.x,
-                        x.z * c1.x - x.w * c1.y, x.z * c1.y + x.w * c1.x);
-      } else {
-        const int i = d < half ? d : d - half;
-        const float g = d < half ? -1.f : 1.f;  // a cos - b sin, b cos + a sin
-        const float2 c0 = s_cs[i], c1 = s_cs[i + 1], c2 = s_cs[i + 2], c3 = s_cs[i + 3];
-        x = make_float4(x.x * c0.x + g * y.x * c0.y, x.y * c1.x + g * y.y * c1.y,
-                        x.z * c2.x + g * y.z * c2.y, x.w * c3.x + g * y.w * c3.y);
+  for (int i = 0; i < 4; ++i) {
+    const float2 cs = turned ? s_cs[4 * j + i] : make_float2(1.f, 0.f);
+    c[i] = cs.x;
+    s[i] = cs.y;
+  }
+  const bool stored = slot >= 0 && slot < (long long)p.kv.n_blocks * p.kv.block_size;
+  const long long block = !stored ? 0 : slot <= INT_MAX ? (int)slot / p.kv.block_size
+                                                        : slot / p.kv.block_size;
+  const long long at = block * p.kv.block_stride +
+                       (stored ? slot - block * p.kv.block_size : 0) * p.kv.row_stride;
+  for (int h = h0; h < h1; h += kAhead * HPS) {
+    if (h != h0) load(h);
+#pragma unroll
+    for (int b = 0; b < kAhead; ++b) {
+      if (h + b * HPS >= h1) break;  // the whole step is past the slice
+      const int head = h + b * HPS + sub;
+      const bool live = head < h1, is_q = head < p.heads, is_v = head >= p.heads + p.kv.heads;
+      float x[8] = {};
+      if (live) {
+        in[b][0].widen(x);
+        in[b][1].widen(x + 4);
       }
-    }
-    if (!live) continue;
-    if (h < p.heads) {
-      store4<OT>(static_cast<OT*>(p.q_out) + ((long long)t * p.heads + h) * HD + d, x);
-    } else if (stored) {
-      KT* base_kv = static_cast<KT*>(is_v ? p.kv.v : p.kv.k);
-      const int kh = h - p.heads - (is_v ? Hk : 0);
-      store4<KT>(base_kv + at + kh * p.kv.head_stride + d, x);
+      const float* alpha = is_q ? p.q_alpha : p.k_alpha;
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+      for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!is_v) {
+        if (alpha) {
+          const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
+          float a[8];
+          reinterpret_cast<const Piece<float>*>(alpha + lo)->widen(a);
+          reinterpret_cast<const Piece<float>*>(alpha + hi)->widen(a + 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= r * a[i];
+        }
+        if (turned) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float &u = x[HALVES ? i : 2 * i], &v = x[HALVES ? 4 + i : 2 * i + 1];
+            const float y = fmaf(u, c[i], -v * s[i]);
+            v = fmaf(u, s[i], v * c[i]);
+            u = y;
+          }
+        }
+      }
+      if (!live) continue;
+      if (is_q) {
+        OT* o = static_cast<OT*>(p.q_out) + ((long long)t * p.heads + head) * HD;
+        store4(o + lo, x);
+        store4(o + hi, x + 4);
+      } else if (stored) {
+        KT* o = static_cast<KT*>(is_v ? p.kv.v : p.kv.k) + at +
+                (head - p.heads - (is_v ? p.kv.heads : 0)) * p.kv.head_stride;
+        store4(o + lo, x);
+        store4(o + hi, x + 4);
+      }
     }
   }
 }
 
-template <typename IT, typename OT, typename KT>
-cudaError_t launch_append(const AppendParams& p, int tokens, cudaStream_t s) {
-  switch (p.kv.head_dim) {
-    case 32: append_kernel<IT, OT, KT, 32><<<tokens, kAppendThreads, 0, s>>>(p); break;
-    case 64: append_kernel<IT, OT, KT, 64><<<tokens, kAppendThreads, 0, s>>>(p); break;
-    default: append_kernel<IT, OT, KT, 128><<<tokens, kAppendThreads, 0, s>>>(p); break;
-  }
+template <typename IT, typename OT, typename KT, int HD, bool HALVES>
+cudaError_t launch_append(AppendParams& p, int tokens, cudaStream_t s) {
+  // A CTA per row once there are kRows of them (eight CTAs an SM); below that a row's steps
+  // are divided over more CTAs, down to one step a warp.
+  constexpr int HPS = 32 / (HD / 8), kRows = 152 * 8;
+  const int steps = (p.heads + 2 * p.kv.heads + HPS - 1) / HPS;
+  const int whole = (steps + kAppendWarps - 1) / kAppendWarps;  // of a warp, with one CTA a row
+  int slices = tokens >= kRows ? 1 : (kRows + tokens - 1) / tokens;
+  if (slices > whole) slices = whole;
+  p.steps = (whole + slices - 1) / slices;
+  p.slices = (steps + p.steps * kAppendWarps - 1) / (p.steps * kAppendWarps);
+  const long long grid = (long long)tokens * p.slices;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  append_kernel<IT, OT, KT, HD, HALVES><<<(unsigned)grid, kAppendWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
+template <typename IT, typename OT, typename KT, int HD>
+cudaError_t by_rope(AppendParams& p, int tokens, int style, cudaStream_t s) {
+  return style == RQ_ROPE_HALVES ? launch_append<IT, OT, KT, HD, true>(p, tokens, s)
+                                 : launch_append<IT, OT, KT, HD, false>(p, tokens, s);
+}
+
+template <typename IT, typename OT, typename KT>
+cudaError_t by_head_dim(AppendParams& p, int tokens, int style, cudaStream_t s) {
+  switch (p.kv.head_dim) {
+    case 32: return by_rope<IT, OT, KT, 32>(p, tokens, style, s);
+    case 64: return by_rope<IT, OT, KT, 64>(p, tokens, style, s);
+    default: return by_rope<IT, OT, KT, 128>(p, tokens, style, s);
+  }
+}
+
 template <typename IT, typename OT>
-cudaError_t launch_append_kv(const AppendParams& p, int tokens, cudaStream_t s) {
-  return p.kv.dtype == RQ_BF16 ? launch_append<IT, OT, uint16_t>(p, tokens, s)
-                               : launch_append<IT, OT, float>(p, tokens, s);
+cudaError_t by_cache(AppendParams& p, int tokens, int style, cudaStream_t s) {
+  return p.kv.dtype == RQ_BF16 ? by_head_dim<IT, OT, uint16_t>(p, tokens, style, s)
+                               : by_head_dim<IT, OT, float>(p, tokens, style, s);
 }
 
 // F_i = theta^(-2i/rd) / (2 pi) * 2^64 for i < rd / 2, each a product of at most six powers
@@ -196,7 +252,6 @@ extern "C" rq_status rq_paged_append(const rq_paged_kv* kv, int32_t tokens, int3
   p.k_alpha = k_alpha;
   p.eps = eps;
   p.heads = heads;
-  p.style = rope_style;
   p.rope_dim = rope_dim;
   p.positions = positions;
   p.slots = slots;
@@ -205,10 +260,10 @@ extern "C" rq_status rq_paged_append(const rq_paged_kv* kv, int32_t tokens, int3
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (qkv_dtype == RQ_BF16)
-    e = q_dtype == RQ_BF16 ? launch_append_kv<uint16_t, uint16_t>(p, tokens, s)
-                           : launch_append_kv<uint16_t, float>(p, tokens, s);
+    e = q_dtype == RQ_BF16 ? by_cache<uint16_t, uint16_t>(p, tokens, rope_style, s)
+                           : by_cache<uint16_t, float>(p, tokens, rope_style, s);
   else
-    e = q_dtype == RQ_BF16 ? launch_append_kv<float, uint16_t>(p, tokens, s)
-                           : launch_append_kv<float, float>(p, tokens, s);
+    e = q_dtype == RQ_BF16 ? by_cache<float, uint16_t>(p, tokens, rope_style, s)
+                           : by_cache<float, float>(p, tokens, rope_style, s);
   return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }

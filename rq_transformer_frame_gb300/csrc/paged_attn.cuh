@@ -20,8 +20,6 @@
 // and masked, so nothing that lies there is ever used.
 #pragma once
 
-#include <atomic>
-
 #include "paged.cuh"
 #include "tc_common.cuh"
 
@@ -35,10 +33,9 @@ template <typename KT>
 constexpr int split_stages = sizeof(KT) == 2 ? 3 : 2;
 constexpr int kMaxGrid = 304;              // CTAs of a launch, at most
 constexpr int kMaxRuns = kMaxGrid * kWarps;
-constexpr int kMinRun = 4;                 // tiles of a run, at least
-constexpr int kUnitCost = 2;               // what a unit's start and end count, in tiles
+constexpr int kMinRun = 1;                 // tiles of a run, at least
+constexpr int kUnitCost = 1;               // what a unit's start and end count, in tiles
 constexpr int kMaxHeads = 16;              // query heads of a unit, at most
-constexpr int kMaxDevices = 64;
 
 struct Params {
   rq_paged_kv kv;
@@ -951,9 +948,9 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
 // Units that were cut: if a unit starts in run c and goes on, its partials -- run c's second
 // slot, then the first slot of each run that follows -- are summed in order. A CTA takes
 // kJoinWarps consecutive runs (blockIdx.x) and head blockIdx.y of their units. A unit of few
-// parts is a warp's, all eight at once; one of many parts (a long row over many runs, so
-// at most one or two among eight) is the whole CTA's: each warp sums a share of the parts.
-constexpr int kJoinWarps = 8, kJoinFew = 16;
+// parts is a warp's, all sixteen at once; one of many parts (a long row over many runs, so
+// at most one or two among them) is the whole CTA's: each warp sums a share of the parts.
+constexpr int kJoinWarps = 16, kJoinFew = 12;
 
 // (m, l, a) += the parts [i0, i1) of one head: m and l alike in every lane, a the lane's E
 // dimensions. `slot(i)`: where part i is.
@@ -1098,15 +1095,9 @@ cudaError_t launch(Params p, cudaStream_t s) {
   constexpr size_t smem = (size_t)kWarps * (kStages * S::kStage + Core::kScratch);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  int ctas = dev < kMaxDevices ? resident[dev].load(std::memory_order_relaxed) : 0;
-  if (ctas == 0) {
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    ctas = sms * per_sm < kMaxGrid ? sms * per_sm : kMaxGrid;
-    if (dev < kMaxDevices) resident[dev].store(ctas, std::memory_order_relaxed);
-  }
+  int ctas = 0;
+  if ((e = resident_ctas(kernel, kWarps * 32, smem, resident, &ctas)) != cudaSuccess) return e;
+  if (ctas > kMaxGrid) ctas = kMaxGrid;
   const long long most = (tiles * units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
   const int grid = (int)(ctas < most ? ctas : most);
   p.runs = grid * kWarps;

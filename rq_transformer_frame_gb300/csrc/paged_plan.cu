@@ -8,7 +8,10 @@
 // to the last request whose first token is <= t.  Every output element is then computed
 // from its index alone, by a binary search in the prefix sums in shared memory.
 //
-// What may alias needs no order of its own: taken entries of the ring are read at
+// One CTA does the sums and whatever is written from them; many tokens are a second kernel's,
+// which finds everything it needs in the first one's outputs (a CTA of 1024 threads writes
+// 262144 tokens in 209 us, the two kernels take TOKENS_US). What may alias needs no order of
+// its own: taken entries of the ring are read at
 // [head, head + taken) and given ones written at [head + count, head + count + given), apart
 // because count + given <= N; table columns are written from pages(c_b) on and read below.
 // Only the lengths and the pool's words are read by all and written by some: those writes
@@ -19,7 +22,8 @@ namespace rqk {
 namespace {
 
 constexpr int kPlanMaxBatch = 8192;  // four prefix arrays of this length fit shared memory
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kTokenThreads = 256;
+constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens that the first kernel maps itself
 
 struct PlanParams {
   int B, W, P, N, M;
@@ -41,6 +45,11 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int o) {
           __shfl_up_sync(0xffffffffu, a.give, o)};
 }
 
+__device__ __forceinline__ Sums shfl(const Sums& a, int l) {
+  return {__shfl_sync(0xffffffffu, a.tok, l), __shfl_sync(0xffffffffu, a.need, l),
+          __shfl_sync(0xffffffffu, a.give, l)};
+}
+
 __device__ __forceinline__ int pages_of(int c, const PlanParams& p) {
   const int n = c / p.P + (c % p.P != 0);
   return n < p.W ? n : p.W;
@@ -57,6 +66,61 @@ __device__ __forceinline__ int last_at_most(const int* first, int B, int x) {
   return lo;
 }
 
+// Tokens [t0, t0 + 4) of T: request, position and slot, -1 behind the last. cu: first tokens
+// [B + 1]; held(b): the length before; block(b, col): the block in column col.
+template <typename Held, typename Block>
+__device__ __forceinline__ void map_tokens(const PlanParams& p, const int* cu, int t0, int T, bool wide,
+                                           Held held, Block block) {
+  int req[4], pos[4], b = 0, len = 0, page = -1, id = -1;
+  long long slot[4];
+  if (t0 < T) {
+    b = last_at_most(cu, p.B, t0);
+    len = held(b);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + i;
+    req[i] = pos[i] = -1;
+    slot[i] = -1;
+    if (t >= T) continue;
+    if (t >= cu[b + 1]) {
+      do ++b; while (t >= cu[b + 1]);
+      len = held(b);
+      page = -1;
+    }
+    req[i] = b;
+    pos[i] = len + (t - cu[b]);
+    const int pg = pos[i] / p.P;
+    if (pg != page) {
+      page = pg;
+      id = block(b, len, pg % p.W);
+      // a page that a later token of this call takes over, or a block that is none
+      const int last = (len + (cu[b + 1] - cu[b]) - 1) / p.P;
+      if (last - pg >= p.W || id >= p.N) id = -1;
+    }
+    if (id >= 0) slot[i] = (long long)id * p.P + (pos[i] - pg * p.P);
+  }
+  if (wide && t0 + 4 <= p.M) {
+    *reinterpret_cast<int4*>(p.requests + t0) = make_int4(req[0], req[1], req[2], req[3]);
+    *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    *reinterpret_cast<longlong2*>(p.slots + t0) = make_longlong2(slot[0], slot[1]);
+    *reinterpret_cast<longlong2*>(p.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t0 + i < p.M) {
+        p.requests[t0 + i] = req[i];
+        p.positions[t0 + i] = pos[i];
+        p.slots[t0 + i] = slot[i];
+      }
+  }
+}
+
+__device__ __forceinline__ bool wide_maps(const PlanParams& p) {
+  return ((reinterpret_cast<uintptr_t>(p.requests) | reinterpret_cast<uintptr_t>(p.positions) |
+           reinterpret_cast<uintptr_t>(p.slots)) & 15u) == 0;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   extern __shared__ int s_mem[];
   int* const s_cu = s_mem;               // [B + 1] first token
@@ -65,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int* const s_held = s_give + p.B;      // [B] length before
   __shared__ Sums s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  pdl_trigger();
   const int head = p.pool[0], count = p.pool[1];
   Sums run{0, 0, 0};
   int bad = head < 0 || head >= p.N || count < 0 || count > p.N;
@@ -93,18 +158,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    Sums before = run;
-    for (int w = 0; w < nt / 32; ++w) {
-      if (w < warp) before = before + s_warp[w];
-      run = run + s_warp[w];
+    // every warp scans the warps' sums
+    Sums w = lane < nt / 32 ? s_warp[lane] : Sums{0, 0, 0};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums t = shfl_up(w, o);
+      if (lane >= o) w = w + t;
     }
+    const Sums all = shfl(w, 31), below = shfl(w, (warp + 31) & 31);
     if (b < p.B) {
       // a sum past the limits fails the call below: the narrowed value is not used then
-      s_cu[b] = (int)(before.tok + inc.tok - own.tok);
-      s_take[b] = (int)(before.need + inc.need - own.need);
-      s_give[b] = (int)(before.give + inc.give - own.give);
+      const Sums at = run + (warp ? below : Sums{0, 0, 0}) + inc;
+      s_cu[b] = (int)(at.tok - own.tok);
+      s_take[b] = (int)(at.need - own.need);
+      s_give[b] = (int)(at.give - own.give);
       s_held[b] = c;
     }
+    run = run + all;
     __syncthreads();
   }
   bad = __syncthreads_or(bad);
@@ -138,24 +208,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     const int b = last_at_most(s_give, p.B, x);
     p.free_ids[((long long)head + count + x) % p.N] = p.table[(size_t)b * p.W + (x - s_give[b])];
   }
-  for (int t = tid; t < p.M; t += nt) {
-    int b = -1, pos = -1;
-    long long slot = -1;
-    if (t < T) {
-      b = last_at_most(s_cu, p.B, t);
-      const int held = s_held[b], before = pages_of(held, p);
-      pos = held + (t - s_cu[b]);
-      const int page = pos / p.P, col = page % p.W;
-      const int last = (held + (s_cu[b + 1] - s_cu[b]) - 1) / p.P;
-      const int id = col < before
-                         ? p.table[(size_t)b * p.W + col]
-                         : p.free_ids[((long long)head + s_take[b] + (col - before)) % p.N];
-      if (last - page < p.W && id >= 0 && id < p.N) slot = (long long)id * p.P + pos % p.P;
-    }
-    p.requests[t] = b;
-    p.positions[t] = pos;
-    p.slots[t] = slot;
-  }
+  if (p.M > kPlanTokens) return;  // the token kernel's
+  const bool wide = wide_maps(p);
+  for (int t0 = tid * 4; t0 < p.M; t0 += nt * 4)
+    map_tokens(p, s_cu, t0, T, wide, [&](int b) { return s_held[b]; },
+               [&](int b, int len, int col) {
+                 const int before = pages_of(len, p);
+                 return col < before
+                            ? p.table[(size_t)b * p.W + col]
+                            : p.free_ids[((long long)head + s_take[b] + (col - before)) % p.N];
+               });
+}
+
+// The maps of many tokens, from the first kernel's outputs.
+__global__ void __launch_bounds__(kTokenThreads) plan_tokens_kernel(const PlanParams p) {
+  extern __shared__ int s_cu[];  // [B + 1]
+  pdl_wait();
+  for (int b = threadIdx.x; b <= p.B; b += kTokenThreads) s_cu[b] = p.cu[b];
+  __syncthreads();
+  const int t0 = (blockIdx.x * kTokenThreads + threadIdx.x) * 4;
+  if (t0 >= p.M) return;
+  map_tokens(p, s_cu, t0, s_cu[p.B], wide_maps(p),
+             [&](int b) { return p.lens_out[b] - (s_cu[b + 1] - s_cu[b]); },
+             [&](int b, int, int col) { return p.table[(size_t)b * p.W + col]; });
 }
 
 __global__ void pool_init_kernel(int n, int32_t* pool, int32_t* free_ids) {
@@ -192,10 +267,25 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
   PlanParams p{batch,       max_blocks, block_size, n_blocks,  max_tokens, new_lens,
                lens,        pool,       free_ids,   block_table, lens_out, pool_out,
                cu_tokens,   requests,   positions,  slots};
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const size_t smem = ((size_t)4 * batch + 1) * sizeof(int);
   if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)((4 * kPlanMaxBatch + 1) * sizeof(int))) != cudaSuccess)
     return RQ_ERR_CUDA;
-  plan_kernel<<<1, kPlanThreads, smem, static_cast<cudaStream_t>(cuda_stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+  // few requests and tokens: fewer warps to wait for one another (64 tokens SMALL_US)
+  const int threads = batch <= 256 && max_tokens <= 1024 ? 256 : kPlanThreads;
+  plan_kernel<<<1, threads, smem, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return RQ_ERR_CUDA;
+  if (max_tokens <= kPlanTokens) return RQ_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)max_tokens + kTokenThreads * 4 - 1) / (kTokenThreads * 4)), 1, 1);
+  cfg.blockDim = dim3(kTokenThreads, 1, 1);
+  cfg.dynamicSmemBytes = ((size_t)batch + 1) * sizeof(int);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_tokens_kernel, p) == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }
