@@ -421,12 +421,15 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
  *   out         device [R][heads * head_dim] in q_dtype, 16-byte aligned
  *   lse         device [R][heads] f32 or NULL: log of the sum of exp(scale * q . k_j)
  *   workspace   device scratch of at least rq_paged_attention_workspace_size bytes, 16-byte
- *               aligned, needing no initialisation; calls that may overlap need their own
+ *               aligned, needing no initialisation; calls that may overlap need their own.
+ *               May be NULL where that is 0 (few rows or short ones: the size depends on the
+ *               arguments it is asked with and on the current device)
  * A row with no live position gives output 0 and lse -inf.  What lies in the cache outside
  * the live positions is never used, NaN or not.  Scores, softmax and sums are f32; with
  * f32 queries every product over a bf16 cache is exact (queries and weights enter as three
  * bf16 parts), with bf16 queries the weights keep 16 significant bits. */
-size_t rq_paged_attention_workspace_size(int32_t heads, int32_t kv_heads, int32_t head_dim);
+size_t rq_paged_attention_workspace_size(const rq_paged_kv *kv, int32_t rows, int32_t heads,
+                                         int32_t max_blocks, int32_t window);
 rq_status rq_paged_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
                              int32_t batch, int32_t max_blocks, const int32_t *block_table,
                              const int32_t *requests, const int32_t *positions,

@@ -119,7 +119,7 @@ def load() -> C.CDLL:
     # the rq_paged_kv struct is passed packed (paged.py)
     L.rq_paged_append.argtypes = [C.c_char_p, I32, I32, I32, P, I64, P, P, F32, I32, I32,
                                   C.c_double, P, P, I32, P, P]
-    L.rq_paged_attention_workspace_size.argtypes = [I32, I32, I32]
+    L.rq_paged_attention_workspace_size.argtypes = [C.c_char_p, I32, I32, I32, I32]
     L.rq_paged_attention_workspace_size.restype = C.c_size_t
     L.rq_paged_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, F32, I32,
                                      P, P, P, P, C.c_size_t, P]

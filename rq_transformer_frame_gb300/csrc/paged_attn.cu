@@ -12,10 +12,18 @@ int heads_of_unit(int heads, int kv_heads) {
 }
 }  // namespace
 
-extern "C" size_t rq_paged_attention_workspace_size(int32_t heads, int32_t kv_heads,
-                                                    int32_t head_dim) {
-  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 || head_dim > 128) return 0;
-  return rqk::paged_attn::workspace_bytes(heads_of_unit(heads, kv_heads), head_dim);
+extern "C" size_t rq_paged_attention_workspace_size(const rq_paged_kv* kv, int32_t rows,
+                                                    int32_t heads, int32_t max_blocks,
+                                                    int32_t window) {
+  using namespace rqk;
+  if (paged_kv_check(kv) != RQ_OK || rows < 1 || heads < 1 || heads % kv->heads != 0 ||
+      max_blocks < 1 || window < 0)
+    return 0;
+  const paged_attn::Extent x =
+      paged_attn::extent(rows, heads, kv->heads, kv->head_dim, kv->dtype == RQ_BF16, kv->block_size,
+                         max_blocks, window);
+  if (paged_attn::split_ctas(x.units, x.tiles, rows, paged_attn::sm_count())) return 0;
+  return paged_attn::workspace_bytes(heads_of_unit(heads, kv->heads), kv->head_dim);
 }
 
 extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -35,10 +43,10 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   if ((long long)rows * heads > INT_MAX) return RQ_ERR_UNSUPPORTED;
   if (rows == 0) return RQ_OK;
   if (!requests && rows > batch) return RQ_ERR_ARG;
-  if (!block_table || !positions || !q || !out || !workspace) return RQ_ERR_ARG;
+  if (!block_table || !positions || !q || !out) return RQ_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
-  if (workspace_bytes < rq_paged_attention_workspace_size(heads, kv->heads, kv->head_dim))
-    return RQ_ERR_ARG;
+  const size_t need = rq_paged_attention_workspace_size(kv, rows, heads, max_blocks, window);
+  if (workspace_bytes < need || (need && !workspace)) return RQ_ERR_ARG;
   paged_attn::Params p{};
   p.kv = *kv;
   p.q = q;

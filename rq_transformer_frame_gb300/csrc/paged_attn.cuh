@@ -28,9 +28,10 @@ namespace paged_attn {
 
 constexpr int kWarps = 4, kStages = 2;            // of a CTA of runs; stages of a warp's ring
 constexpr int kSplitWarps = 8;                    // of a CTA of one unit
-// its ring is deeper where the queries and weights do not need the shared memory
-template <typename KT>
-constexpr int split_stages = sizeof(KT) == 2 ? 3 : 2;
+// stages of a split warp's ring, with SCRATCH bytes of a warp beside it: as the CTA's 227 KB
+// allow
+template <int STAGE, int SCRATCH>
+constexpr int split_stages = kSplitWarps * (3 * STAGE + SCRATCH) <= 224 * 1024 ? 3 : 2;
 constexpr int kMaxGrid = 304;              // CTAs of a launch, at most
 constexpr int kMaxRuns = kMaxGrid * kWarps;
 constexpr int kMinRun = 1;                 // tiles of a run, at least
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     attend_kernel(const __grid_constant__ Params p) {
   using S = Shape<KT, HD>;
   constexpr int NW = SPLIT ? kSplitWarps : kWarps, NT = NW * 32;
-  constexpr int NS = SPLIT ? split_stages<KT> : kStages, K = S::kKeys;
+  constexpr int NS = SPLIT ? split_stages<S::kStage, Core::kScratch> : kStages, K = S::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int4 s_desc[NW][NS];  // each stage's tile: row, K/V head, group * 16 + flags, key mask
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1052,37 +1053,54 @@ inline int split_ctas(long long units, long long tiles, int rows, int sms) {
   return most <= (rows == 1 ? 32 : 8) ? c : 0;
 }
 
+// What a call's launch is decided by: units of all rows and tiles of a unit, at most.
+struct Extent {
+  long long units, tiles;
+};
+inline Extent extent(long long rows, int heads, int kv_heads, int head_dim, bool kv_bf16, int block_size,
+                     int max_blocks, int window) {
+  const int g = heads / kv_heads, most = kv_bf16 ? 16 : 8;  // heads of a unit
+  long long keys = (long long)max_blocks * block_size;
+  if (keys > INT_MAX) keys = INT_MAX;
+  if (window > 0 && window < keys) keys = window;
+  int tile = 4096 / (head_dim * (kv_bf16 ? 2 : 4));
+  if (tile > 32) tile = 32;
+  return {rows * kv_heads * ((g + most - 1) / most), keys / tile + 2};
+}
+
+// multiprocessors of the current device, looked up once (0 if there is none)
+inline int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) != 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 template <typename QT, typename KT, int HD, typename Core>
 cudaError_t launch(Params p, cudaStream_t s) {
   using S = Shape<KT, HD>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static std::atomic<int> sm_count[kMaxDevices], resident[kMaxDevices];
-  int sms = dev < kMaxDevices ? sm_count[dev].load(std::memory_order_relaxed) : 0;
-  if (sms == 0) {
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if (dev < kMaxDevices) sm_count[dev].store(sms, std::memory_order_relaxed);
-  }
+  static_assert(S::kKeys == (4096 / S::kPitch < 32 ? 4096 / S::kPitch : 32), "as in extent()");
+  cudaError_t e;
   p.HG = (p.G + Core::kHeads - 1) / Core::kHeads;
   p.GB = p.G < Core::kHeads ? p.G : Core::kHeads;
-  long long keys = min((long long)p.W * p.kv.block_size, (long long)INT_MAX);
-  if (p.window > 0 && p.window < keys) keys = p.window;
-  const long long tiles = keys / S::kKeys + 2;  // of a unit, at most
-  const long long units = (long long)p.rows * p.kv.heads * p.HG;
+  const Extent x = extent(p.rows, p.heads, p.kv.heads, HD, sizeof(KT) == 2, p.kv.block_size, p.W, p.window);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (const int c = split_ctas(units, tiles, p.rows, sms)) {
+  if (const int c = split_ctas(x.units, x.tiles, p.rows, sm_count())) {
     auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
-    constexpr size_t ring = (size_t)kSplitWarps * (split_stages<KT> * S::kStage + Core::kScratch);
+    constexpr size_t ring = (size_t)kSplitWarps *
+                            (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
     constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
     constexpr size_t smem = ring > sums ? ring : sums;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)c, (unsigned)units, 1);
+    cfg.gridDim = dim3((unsigned)c, (unsigned)x.units, 1);
     cfg.blockDim = dim3(kSplitWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = smem;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1095,10 +1113,11 @@ cudaError_t launch(Params p, cudaStream_t s) {
   constexpr size_t smem = (size_t)kWarps * (kStages * S::kStage + Core::kScratch);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  static std::atomic<int> resident[kMaxDevices];
   int ctas = 0;
   if ((e = resident_ctas(kernel, kWarps * 32, smem, resident, &ctas)) != cudaSuccess) return e;
   if (ctas > kMaxGrid) ctas = kMaxGrid;
-  const long long most = (tiles * units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
+  const long long most = (x.tiles * x.units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
   const int grid = (int)(ctas < most ? ctas : most);
   p.runs = grid * kWarps;
   kernel<<<grid, kWarps * 32, smem, s>>>(p);

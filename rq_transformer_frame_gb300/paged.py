@@ -4,12 +4,13 @@ rq_paged_* calls; argument marshalling only, like `binding`).
   paged_plan       block tables and token maps of a step, from the requests' lengths
   paged_append     per-head norm, position rotation, and K/V stored by slot
   paged_attention  one query token per row over its request's blocks
+  paged_attention_workspace  scratch for it, where a call's addresses must stay
   PagedCache       the buffers of one cache, with the three as methods
 
 A layer's cache is a pair of tensors k, v [n_blocks][block_size][kv_heads][head_dim] (f32
 or bf16, of any strides that keep head_dim contiguous and every row 16-byte aligned).
 Nothing here synchronizes except PagedCache.status(), so a step can be captured into a CUDA
-graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace`.
+graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace` (paged_attention_workspace).
 Every call runs on `stream` (a torch.cuda.Stream; default: the current one of the
 tensors' device); tensors it allocates belong to that stream.
 """
@@ -85,9 +86,21 @@ def _cache(k, v):
                     h, hd, p, n), h, hd, dev
 
 
-@lru_cache(maxsize=None)
-def _workspace_size(heads, kv_heads, head_dim):
-    return load().rq_paged_attention_workspace_size(heads, kv_heads, head_dim)
+@lru_cache(maxsize=1024)
+def _workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, block_size, max_blocks, window):
+    # the size goes by these alone: any pointer and strides that are valid stand for a cache
+    kv = _KV.pack(16, 16, 0, 0, 0, dtype, kv_heads, head_dim, block_size, 1)
+    return load().rq_paged_attention_workspace_size(kv, rows, heads, max_blocks, window)
+
+
+def paged_attention_workspace(q, k, block_table, window=0):
+    """Scratch for paged_attention with these shapes, for calls whose addresses must stay (a
+    captured graph), or None where the call needs none."""
+    n, p, hk, hd = k.shape
+    with _on(k.device, None):
+        size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd, p,
+                               block_table.shape[1], window)
+    return torch.empty(size, dtype=torch.uint8, device=k.device) if size else None
 
 
 # Each call below runs on the current stream of the tensors' device; a call on another
@@ -192,8 +205,9 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     if lse is True:
         lse = torch.empty((R, heads), dtype=_F32, device=k.device)
     if workspace is None:
-        nbytes = _workspace_size(heads, hk, hd)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
+        nbytes = _workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.shape[1], W, window)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
     else:
@@ -204,7 +218,7 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
         _ints("positions", positions, R, dev), window, scale, _TYPE[dtype],
         _rows("q", q, shape, dtype, dev), _rows("out", out, shape, dtype, dev),
         None if lse is None else _rows("lse", lse, (R, heads), _F32, dev),
-        workspace.data_ptr(), nbytes, _current_stream(dev))
+        None if workspace is None else workspace.data_ptr(), nbytes, _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_attention", rc)
     return out, lse

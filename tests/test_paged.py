@@ -94,8 +94,8 @@ def test_append_refusals(lib, kw):
     (dict(rows=-1), 1), (dict(heads=0), 1), (dict(heads=6), 1), (dict(batch=0), 1), (dict(W=0), 1),
     (dict(window=-1), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(qdt=2), 1), (dict(table=None), 1), (dict(pos=None), 1), (dict(q=None), 1),
-    (dict(out=None), 1), (dict(ws=None), 1), (dict(q=A + 8), 1), (dict(out=B_ + 4), 1),
-    (dict(ws=C_ + 8), 1), (dict(rows=4), 1), (dict(wsb=15), 1),
+    (dict(out=None), 1), (dict(q=A + 8), 1), (dict(out=B_ + 4), 1),
+    (dict(ws=C_ + 8), 1), (dict(rows=4), 1),
     (dict(rows=2**30, batch=2**30), 6),
 ])
 def test_attention_refusals(lib, kw, status):
@@ -103,10 +103,17 @@ def test_attention_refusals(lib, kw, status):
 
 
 def test_attention_wants_its_whole_workspace(lib):
-    need = lib.rq_paged_attention_workspace_size(8, 4, 128)
-    assert need > 0 and _attend(lib, wsb=need - 1) == binding.RQ_ERR_ARG
-    assert lib.rq_paged_attention_workspace_size(6, 4, 128) == 0
-    assert lib.rq_paged_attention_workspace_size(0, 4, 128) == 0
+    """Rows that may be long are cut over the card and need scratch for their pieces."""
+    many = dict(rows=300, batch=300, W=400)
+    need = lib.rq_paged_attention_workspace_size(_kv(), 300, 8, 400, 0)
+    assert need > 0
+    assert _attend(lib, **many, wsb=need - 1) == binding.RQ_ERR_ARG
+    assert _attend(lib, **many, ws=None) == binding.RQ_ERR_ARG
+    size = lambda **kw: lib.rq_paged_attention_workspace_size(  # noqa: E731
+        kw.get("kv", _kv()), kw.get("rows", 300), kw.get("heads", 8), kw.get("W", 400), kw.get("window", 0))
+    assert size() == need
+    assert [size(**kw) for kw in (dict(kv=_kv(hd=48)), dict(rows=0), dict(heads=6), dict(W=0),
+                                  dict(window=-1))] == [0] * 5
 
 
 def test_no_rows_is_not_an_error(lib):

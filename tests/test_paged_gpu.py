@@ -19,7 +19,7 @@ import pytest
 import torch
 
 import paged_ref
-from rq_transformer_frame_gb300 import binding, paged
+from rq_transformer_frame_gb300 import paged
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -327,12 +327,13 @@ def run_attend(lens, heads, hk, hd, io, cache, P, W=None, window=0, scale=0.0, s
     was_out = torch.randn(R + pad, heads * hd, generator=g).to(io)
     was_lse = torch.randn(R + pad, heads, generator=g)
     out.copy_(was_out), lse.copy_(was_lse)
-    need = binding.load().rq_paged_attention_workspace_size(heads, hk, hd)
-    ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = paged.paged_attention_workspace(q, k.cuda(), table, window)
+    need = 0 if ws is None else ws.numel()
+    guarded = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
     paged.paged_attention(q.cuda(), to_gpu(k), to_gpu(v), table.cuda(), ints(pos),
                           requests=None if req is None else ints(req), window=window, scale=scale, out=out,
-                          lse=lse, workspace=ws[:need])
-    assert (ws[need:] == 0xff).all()
+                          lse=lse, workspace=guarded[:need] if need else None)
+    assert (guarded[need:] == 0xff).all()
     check_rows(out.cpu(), lse.cpu(), q, k, v, table, req, pos, window, scale or hd ** -0.5, was_out, was_lse)
 
 
@@ -480,8 +481,7 @@ def test_streams_and_graphs():
     for o, l in outs:
         assert torch.equal(o, want) and torch.equal(l, want_lse)
     out, lse = torch.empty_like(q), torch.empty(R, heads, device="cuda")
-    ws = torch.empty(binding.load().rq_paged_attention_workspace_size(heads, hk, hd), dtype=torch.uint8,
-                     device="cuda")
+    ws = paged.paged_attention_workspace(q, k, table)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         paged.paged_attention(q, k, v, table, pos, out=out, lse=lse, workspace=ws)
@@ -512,8 +512,7 @@ def test_decode_steps(captured, io, cache, heads, hk, hd, P, W, window):
     qs = torch.zeros(layers, M, heads * hd, dtype=io, device="cuda")
     outs = torch.full((layers, M, heads * hd), 7.0, dtype=io, device="cuda")
     lses = torch.full((layers, M, heads), 7.0, device="cuda")
-    ws = torch.empty(binding.load().rq_paged_attention_workspace_size(heads, hk, hd), dtype=torch.uint8,
-                     device="cuda")
+    ws = paged.paged_attention_workspace(qs[0], c.k[0], c.block_table, window)
 
     def step():
         c.plan(new)
