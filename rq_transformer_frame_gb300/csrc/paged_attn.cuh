@@ -1042,15 +1042,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 // split at 16 / 1000 / 4000 / 16000 positions against 9.4 / 16.0 / 16.2 / 23 us in runs, and
 // 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
 // of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
-// one row is split up to 32 tiles a warp, several rows up to 8 (1024 positions of one CTA).
+// several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 32, or
+// up to 128 where the clusters fill three quarters of the card (32 K/V heads: 5.5 / 7.9 / 19 /
+// 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768 positions against 8.5 / 13 / 23 / 53 / 92).
 inline int split_ctas(long long units, long long tiles, int rows, int sms) {
   if (units > sms) return 0;
   int c = 1;
-  while (c < 8 && units * c * 2 <= sms) c *= 2;
+  // clusters that are all resident: with one CTA an SM 15 clusters of eight fit this card at
+  // once, 36 of four, 76 of two; a sixteenth cluster of eight waits for the others (16 units
+  // of 16 positions took 8.8 us in eights, 5.6 in fours)
+  while (c < 8 && (units + 4) * c * 2 <= sms) c *= 2;
   // every warp of the cluster a tile at least
   while (c > 1 && (long long)c * kSplitWarps > tiles * 2) c /= 2;
   const long long most = tiles / (c * kSplitWarps);  // tiles of a warp, at most
-  return most <= (rows == 1 ? 32 : 8) ? c : 0;
+  const bool full = 4 * units * c >= 3 * sms;        // the clusters fill the card
+  return most <= (rows > 1 ? 8 : full ? 128 : 32) ? c : 0;
 }
 
 // What a call's launch is decided by: units of all rows and tiles of a unit, at most.
