@@ -362,7 +362,7 @@ rq_status rq_paged_pool_init(int32_t n_blocks, int32_t *pool, int32_t *free_ids,
  * All or nothing: pool_out[2] tells why a call did nothing (RQ_PAGED_*; 0 if it did); then
  * lengths, table and free ring stay as they were, cu_tokens is all 0 and every token is
  * padding.  Lengths from -1 (new_lens) or 0 (lens) up, sums up to 2^31 - 1.
- * batch <= 8192 (RQ_ERR_UNSUPPORTED above). */
+ * batch <= 8192, max_tokens <= 2^30 (RQ_ERR_UNSUPPORTED above). */
 rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t block_size,
                         int32_t n_blocks, int32_t max_tokens, const int32_t *new_lens,
                         const int32_t *lens, const int32_t *pool, int32_t *free_ids,
@@ -386,8 +386,8 @@ enum { RQ_ROPE_INTERLEAVED = 0, RQ_ROPE_HALVES = 1 };
  *               sqrt(mean(x^2) + eps) over each head; NULL: no norm
  *   rope_style  RQ_ROPE_*;  rope_dim  0 (no rotation) or a multiple of 8 up to head_dim
  *   rope_theta  > 1
- *   positions   device [T] int32; a row whose position is negative is padding: nothing of
- *               it is read or written
+ *   positions   device [T] int32; a row whose position is negative is padding: nothing is
+ *               written for it
  *   slots       device [T] int64 (rq_paged_plan); the keys and values of a slot outside
  *               [0, n_blocks * block_size) are not stored
  *   q_out       device [T][heads * head_dim] in q_dtype, 16-byte aligned; must not overlap

@@ -45,4 +45,26 @@ inline cudaError_t resident_ctas(K* kernel, int threads, size_t smem, std::atomi
   return cudaSuccess;
 }
 
+// Launch with a programmatic dependency on the kernel before it in the stream: the CTAs start
+// while that one ends, and wait (pdl_wait, the first thing every kernel here does) until its
+// writes are there.  cluster: CTAs of a cluster along x, 0 for none.
+template <typename P>
+inline cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, size_t smem, int cluster,
+                                    cudaStream_t s, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace rqk

@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const IT* row = static_cast<const IT*>(p.qkv) + t * p.qkv_stride;
   // the warp's heads: step i from h0 + i * HPS, this lane's head `sub` further, below h1
   const int h0 = (slice * kAppendWarps + tid / 32) * p.steps * HPS, h1 = min(h0 + p.steps * HPS, total);
+  pdl_wait();
+  pdl_trigger();
   Piece<IT> in[kAhead][2];
   auto load = [&](int h) {
 #pragma unroll
@@ -179,8 +181,8 @@ cudaError_t launch_append(AppendParams& p, int tokens, cudaStream_t s) {
   p.slices = (steps + p.steps * kAppendWarps - 1) / (p.steps * kAppendWarps);
   const long long grid = (long long)tokens * p.slices;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  append_kernel<IT, OT, KT, HD, HALVES><<<(unsigned)grid, kAppendWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(append_kernel<IT, OT, KT, HD, HALVES>, dim3((unsigned)grid), kAppendWarps * 32, 0, 0,
+                          s, p);
 }
 
 template <typename IT, typename OT, typename KT, int HD>

@@ -664,6 +664,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     if (p.lse)
       for (int i = h0 + i0; i < h1; i += step) p.lse[(size_t)r * p.heads + i] = neg_inf();
   };
+  pdl_wait();
+  pdl_trigger();
   int4 cut = make_int4(0, 0, 0, 0);
   // the warp's tiles: the list's entries [at, stop), the first of them tile t of unit (kvh, hg)
   // of row r; a run of the list is `per` entries
@@ -735,7 +737,6 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     }
   }
   __syncthreads();
-  pdl_trigger();
   // rows of empty requests
   for (int r = run; r < p.rows; r += p.runs) {
     const int2 words = row_words(p, r);
@@ -951,29 +952,48 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
 // kJoinWarps consecutive runs (blockIdx.x) and head blockIdx.y of their units. A unit of few
 // parts is a warp's, all sixteen at once; one of many parts (a long row over many runs, so
 // at most one or two among them) is the whole CTA's: each warp sums a share of the parts.
+// All of it is latency: a chain of reads in L2 behind the main kernel's end.
 constexpr int kJoinWarps = 16, kJoinFew = 12;
+
+template <int E>
+struct alignas(4 * E) Floats {
+  float v[E];
+};
 
 // (m, l, a) += the parts [i0, i1) of one head: m and l alike in every lane, a the lane's E
 // dimensions. `slot(i)`: where part i is.
 template <int E, typename Slot>
 __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot slot, int lane, float& m,
                                            float& l, float (&a)[E]) {
+  auto part = [&](int i) { return *reinterpret_cast<const Floats<E>*>(p.part + slot(i) * (E * 32) + lane * E); };
+  constexpr int U = 12;  // sums in flight, the first of them beside their (m, l)
   for (int b = i0; b < i1; b += 32) {
     const int n = min(i1 - b, 32);
     float2 ml = make_float2(neg_inf(), 0.f);
     if (lane < n) ml = p.part_ml[slot(b + lane)];
+    Floats<E> x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (j < n) x[j] = part(b + j);
     const float mx = fmaxf(m, warp_max(ml.x)), ref = finite_or_zero(mx);
     const float f = ex2(ml.x - ref), old = ex2(m - ref);
     m = mx;
     l = l * old + warp_sum(ml.y * f);
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] *= old;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      const float* src = p.part + slot(b + j) * (E * 32) + lane * E;
+    for (int j0 = 0; j0 < n; j0 += U) {
+      if (j0 > 0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = fmaf(src[e], fj, a[e]);
+        for (int j = 0; j < U; ++j)
+          if (j0 + j < n) x[j] = part(b + j0 + j);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        if (j0 + j >= n) break;
+        const float fj = __shfl_sync(0xffffffffu, f, j0 + j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = fmaf(x[j].v[e], fj, a[e]);
+      }
     }
   }
 }
@@ -986,9 +1006,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = blockIdx.y;
   const int run0 = blockIdx.x * kJoinWarps;
   pdl_wait();
-  if (tid < kJoinWarps)
-    s_cut[tid] = run0 + tid < p.runs ? p.cut[run0 + tid] : make_int4(0, 0, 0, 0);
-  __syncthreads();
+  pdl_trigger();
   auto write = [&](const int4& cut, float m, float l, const float (&a)[E]) {
     const size_t head = (size_t)cut.x * p.heads + cut.y + g;
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -996,19 +1014,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     for (int e = 0; e < E; ++e) put(static_cast<QT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
     if (p.lse && lane == 0) p.lse[head] = log_sum(m, l);
   };
+  auto slots_of = [&](int run) {
+    return [=](int i) { return ((size_t)(run + i) * 2 + (i == 0 ? 1 : 0)) * p.GB + g; };
+  };
+  int4 own = make_int4(0, 0, 0, 0);
+  if (run0 + warp < p.runs) own = p.cut[run0 + warp];
+  const bool many = g < own.z && own.w > kJoinFew;
+  if (g < own.z && !many) {
+    float m = neg_inf(), l = 0.f, a[E] = {};
+    join_parts<E>(p, 0, own.w, slots_of(run0 + warp), lane, m, l, a);
+    write(own, m, l, a);
+  }
+  if (lane == 0) s_cut[warp] = many ? own : make_int4(0, 0, 0, 0);
+  if (!__syncthreads_or(many)) return;
   for (int c = 0; c < kJoinWarps; ++c) {
     const int4 cut = s_cut[c];
-    if (g >= cut.z) continue;
-    auto slot = [&](int i) { return ((size_t)(run0 + c + i) * 2 + (i == 0 ? 1 : 0)) * p.GB + g; };
+    if (cut.w == 0) continue;
     float m = neg_inf(), l = 0.f, a[E] = {};
-    if (cut.w <= kJoinFew) {
-      if (warp != c) continue;
-      join_parts<E>(p, 0, cut.w, slot, lane, m, l, a);
-      write(cut, m, l, a);
-      continue;
-    }
     join_parts<E>(p, (int)((long long)cut.w * warp / kJoinWarps),
-                  (int)((long long)cut.w * (warp + 1) / kJoinWarps), slot, lane, m, l, a);
+                  (int)((long long)cut.w * (warp + 1) / kJoinWarps), slots_of(run0 + c), lane, m, l, a);
     if (lane == 0) {
       s_m[warp] = m;
       s_l[warp] = l;
@@ -1093,11 +1117,6 @@ cudaError_t launch(Params p, cudaStream_t s) {
   p.HG = (p.G + Core::kHeads - 1) / Core::kHeads;
   p.GB = p.G < Core::kHeads ? p.G : Core::kHeads;
   const Extent x = extent(p.rows, p.heads, p.kv.heads, HD, sizeof(KT) == 2, p.kv.block_size, p.W, p.window);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (const int c = split_ctas(x.units, x.tiles, p.rows, sm_count())) {
     auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
     constexpr size_t ring = (size_t)kSplitWarps *
@@ -1106,13 +1125,7 @@ cudaError_t launch(Params p, cudaStream_t s) {
     constexpr size_t smem = ring > sums ? ring : sums;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)c, (unsigned)x.units, 1);
-    cfg.blockDim = dim3(kSplitWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return launch_dependent(kernel, dim3((unsigned)c, (unsigned)x.units, 1), kSplitWarps * 32, smem, c, s, p);
   }
   // as many CTAs as are resident at once, at most as many as the largest rows could fill
   auto* kernel = attend_kernel<QT, KT, HD, Core, false>;
@@ -1126,13 +1139,9 @@ cudaError_t launch(Params p, cudaStream_t s) {
   const long long most = (x.tiles * x.units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
   const int grid = (int)(ctas < most ? ctas : most);
   p.runs = grid * kWarps;
-  kernel<<<grid, kWarps * 32, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((p.runs + kJoinWarps - 1) / kJoinWarps), (unsigned)p.GB, 1);
-  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<QT, HD>, p);
+  if ((e = launch_dependent(kernel, dim3((unsigned)grid), kWarps * 32, smem, 0, s, p)) != cudaSuccess) return e;
+  const dim3 joins((unsigned)((p.runs + kJoinWarps - 1) / kJoinWarps), (unsigned)p.GB, 1);
+  return launch_dependent(join_kernel<QT, HD>, joins, kJoinWarps * 32, 0, 0, s, p);
 }
 
 cudaError_t launch_bf16(const Params& p, bool q_bf16, cudaStream_t s);  // over a bf16 cache

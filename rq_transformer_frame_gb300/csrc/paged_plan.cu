@@ -10,7 +10,7 @@
 //
 // One CTA does the sums and whatever is written from them; many tokens are a second kernel's,
 // which finds everything it needs in the first one's outputs (a CTA of 1024 threads writes
-// 262144 tokens in 209 us, the two kernels take TOKENS_US). What may alias needs no order of
+// 262144 tokens in 209 us, the two kernels take 8.2 us). What may alias needs no order of
 // its own: taken entries of the ring are read at
 // [head, head + taken) and given ones written at [head + count, head + count + given), apart
 // because count + given <= N; table columns are written from pages(c_b) on and read below.
@@ -22,6 +22,7 @@ namespace rqk {
 namespace {
 
 constexpr int kPlanMaxBatch = 8192;  // four prefix arrays of this length fit shared memory
+constexpr int kPlanMaxTokens = 1 << 30;  // token numbers and a thread's four stay in 32 bits
 constexpr int kPlanThreads = 1024, kTokenThreads = 256;
 constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens that the first kernel maps itself
 
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int* const s_held = s_give + p.B;      // [B] length before
   __shared__ Sums s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  pdl_wait();
   pdl_trigger();
   const int head = p.pool[0], count = p.pool[1];
   Sums run{0, 0, 0};
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 __global__ void __launch_bounds__(kTokenThreads) plan_tokens_kernel(const PlanParams p) {
   extern __shared__ int s_cu[];  // [B + 1]
   pdl_wait();
+  pdl_trigger();
   for (int b = threadIdx.x; b <= p.B; b += kTokenThreads) s_cu[b] = p.cu[b];
   __syncthreads();
   const int t0 = (blockIdx.x * kTokenThreads + threadIdx.x) * 4;
@@ -260,7 +263,7 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
   using namespace rqk;
   if (batch < 1 || max_blocks < 1 || block_size < 1 || n_blocks < 1 || max_tokens < 1)
     return RQ_ERR_ARG;
-  if (batch > kPlanMaxBatch) return RQ_ERR_UNSUPPORTED;
+  if (batch > kPlanMaxBatch || max_tokens > kPlanMaxTokens) return RQ_ERR_UNSUPPORTED;
   if (!new_lens || !lens || !pool || !free_ids || !block_table || !lens_out || !pool_out ||
       !cu_tokens || !requests || !positions || !slots)
     return RQ_ERR_ARG;
@@ -269,23 +272,15 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
                cu_tokens,   requests,   positions,  slots};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const size_t smem = ((size_t)4 * batch + 1) * sizeof(int);
-  if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)((4 * kPlanMaxBatch + 1) * sizeof(int))) != cudaSuccess)
     return RQ_ERR_CUDA;
-  // few requests and tokens: fewer warps to wait for one another (64 tokens SMALL_US)
+  // few requests and tokens: fewer warps to wait for one another (64 tokens take 5.6 us; with 1024 threads 5.5)
   const int threads = batch <= 256 && max_tokens <= 1024 ? 256 : kPlanThreads;
-  plan_kernel<<<1, threads, smem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return RQ_ERR_CUDA;
+  if (launch_dependent(plan_kernel, dim3(1), threads, smem, 0, s, p) != cudaSuccess) return RQ_ERR_CUDA;
   if (max_tokens <= kPlanTokens) return RQ_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)max_tokens + kTokenThreads * 4 - 1) / (kTokenThreads * 4)), 1, 1);
-  cfg.blockDim = dim3(kTokenThreads, 1, 1);
-  cfg.dynamicSmemBytes = ((size_t)batch + 1) * sizeof(int);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_tokens_kernel, p) == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+  const unsigned grid = (unsigned)(((long long)max_tokens + kTokenThreads * 4 - 1) / (kTokenThreads * 4));
+  return launch_dependent(plan_tokens_kernel, dim3(grid), kTokenThreads, ((size_t)batch + 1) * sizeof(int), 0, s,
+                          p) == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }

@@ -129,7 +129,7 @@ def _plan(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [(dict(B=0), 1), (dict(W=0), 1), (dict(P=0), 1), (dict(N=0), 1),
-                                       (dict(M=0), 1), (dict(B=8193), 6)] +
+                                       (dict(M=0), 1), (dict(B=8193), 6), (dict(M=2**30 + 1), 6)] +
                          [(dict(ptrs=[A] * i + [None] + [A] * (10 - i)), 1) for i in range(11)])
 def test_plan_refusals(lib, kw, status):
     assert _plan(lib, **kw) == status
