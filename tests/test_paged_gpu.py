@@ -19,7 +19,7 @@ import pytest
 import torch
 
 import paged_ref
-from rq_transformer_frame_gb300 import paged
+from rq_transformer_frame_gb300 import binding, paged
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -68,6 +68,7 @@ def check_plan(new, lens, pool, ids, table, P, M, alias):
 @pytest.mark.parametrize("B,W,P,N,M,alias", [
     (1, 1, 1, 1, 1, True), (1, 3, 16, 8, 40, False), (5, 2, 4, 40, 64, True), (33, 9, 5, 400, 257, True),
     (300, 12, 16, 2000, 1023, False), (1025, 4, 3, 6000, 2048, True), (2500, 3, 7, 9000, 4099, False),
+    (8192, 2, 16, 20000, 30000, True),
 ])
 def test_plan_steps(B, W, P, N, M, alias):
     """Twelve steps in a row of arrivals, growth past the table's width, and ends."""
@@ -125,6 +126,25 @@ def test_plan_long_prompts():
                    np.r_[np.arange(56), [-1] * 4, np.arange(56, 60)].astype(np.int32),
                    np.array([[61, 62, -1, -1, -1]] + [[-1] * 5] * 3, np.int32), P, M, alias=True)
     assert o["pool"][2] == 0 and (o["slot"] >= 0).sum() > 0
+
+
+def test_plan_maps_at_any_address():
+    """Maps that start at any element: no wide stores there, and nothing around them."""
+    B, W, P, N, M = 3, 4, 4, 20, 4103
+    lens, new = ints([3, 0, 9]), ints([5, 7, 1])
+    table, ids = torch.full((B, W), -1, dtype=torch.int32, device="cuda"), torch.arange(N, dtype=torch.int32).cuda()
+    pool = ints([6, 14, 0, 0])
+    table[0, 0], table[2, :3] = 0, ints([1, 2, 3])
+    for m in (M, 37):
+        req, pos = (torch.full((m + 2,), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+        slot = torch.full((m + 2,), 77, dtype=torch.int64, device="cuda")
+        out = paged.PagedPlan(torch.empty_like(lens), torch.empty_like(pool), torch.empty(B + 1).int().cuda(),
+                              req[1:-1], pos[1:-1], slot[1:-1])
+        paged.paged_plan(new, lens, pool, ids, table.clone(), P, m, out=out)
+        want = paged_ref.plan(new.tolist(), lens.tolist(), pool.tolist(), ids.cpu().numpy(), table.cpu().numpy(), P, m)
+        for got, w in ((req, want["req"]), (pos, want["pos"]), (slot, want["slot"])):
+            np.testing.assert_array_equal(got[1:-1].cpu().numpy(), w)
+            assert got[0] == 77 and got[-1] == 77
 
 
 def test_plan_leaves_bad_blocks_out():
@@ -203,7 +223,8 @@ def test_append_rotations(hd, rd, style, norm):
 
 
 @pytest.mark.parametrize("T,heads,hk,hd", [(1, 1, 1, 32), (1, 32, 32, 128), (2, 40, 8, 128),
-                                           (65, 7, 7, 64), (130, 5, 1, 32), (333, 24, 4, 64)])
+                                           (65, 7, 7, 64), (130, 5, 1, 32), (333, 24, 4, 64),
+                                           (1300, 3, 1, 32), (2, 130, 20, 128)])
 def test_append_sizes(T, heads, hk, hd):
     run_append(T, heads, hk, hd, BF16, BF16, BF16, "halves", hd, True, 16, pad=T // 4, seed=T)
 
@@ -337,41 +358,69 @@ def run_attend(lens, heads, hk, hd, io, cache, P, W=None, window=0, scale=0.0, s
     check_rows(out.cpu(), lse.cpu(), q, k, v, table, req, pos, window, scale or hd ** -0.5, was_out, was_lse)
 
 
+# A table of many columns, most of them never used: rows that may be long are cut over the card
+# instead of being one thread block's (or cluster's) each.
+CUT = 6000
+
+
 EDGES = [0, 1, 2, 7, 8, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 300]
 
 
+@pytest.mark.parametrize("W", [None, CUT])
 @pytest.mark.parametrize("hd", [32, 64, 128])
 @pytest.mark.parametrize("io", [F32, BF16])
 @pytest.mark.parametrize("cache", [F32, BF16])
-def test_attend_lengths(hd, io, cache):
+def test_attend_lengths(hd, io, cache, W):
     """Empty, one key, and both sides of every tile's edge, in one ragged batch."""
-    run_attend(EDGES, 4, 2, hd, io, cache, 16, pad=3, seed=hd)
+    run_attend(EDGES, 4, 2, hd, io, cache, 16, W=W, pad=3, seed=hd)
+
+
+@pytest.mark.parametrize("W", [None, CUT])
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("n", [1, 16, 17, 300, 2000])
+def test_attend_one_row(io, cache, n, W):
+    """A single request, over a cluster or over the card."""
+    run_attend([n], 6, 2, 64, io, cache, 16, W=W, seed=n)
 
 
 @pytest.mark.parametrize("heads,hk", [(1, 1), (5, 5), (2, 1), (6, 2), (8, 2), (5, 1), (14, 2), (8, 1), (9, 1),
-                                      (12, 1), (16, 1), (34, 2)])
+                                      (12, 1), (16, 1), (34, 2), (40, 1)])
+@pytest.mark.parametrize("W", [None, CUT])
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
-def test_attend_heads(heads, hk, io, cache):
-    """Queries a K/V head from one to seventeen."""
-    run_attend([0, 1, 40, 77, 130], heads, hk, 64, io, cache, 8, seed=heads)
+def test_attend_heads(heads, hk, io, cache, W):
+    """Queries a K/V head from one to forty."""
+    run_attend([0, 1, 40, 77, 130], heads, hk, 64, io, cache, 8, W=W, seed=heads)
+
+
+@pytest.mark.parametrize("hd", [32, 128])
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("W", [None, CUT])
+def test_attend_sixteen_heads(hd, io, cache, W):
+    run_attend([0, 1, 40, 77, 130], 32, 2, hd, io, cache, 16, W=W, seed=hd)
 
 
 @pytest.mark.parametrize("P", [1, 3, 5, 8, 24, 32, 100, 128, 1000])
 @pytest.mark.parametrize("cache", [F32, BF16])
-def test_attend_block_sizes(P, cache):
-    """Blocks smaller and larger than a tile, of sizes that end inside one."""
-    run_attend([1, 64, 99, 250, 3, 0, 511], 4, 2, 64, F32, cache, P, seed=P)
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("W", [None, 20000])
+def test_attend_block_sizes(P, cache, hd, W):
+    """Blocks smaller and larger than a tile, of sizes that end inside one; with blocks of one
+    position a tile's table entries are as many as are read ahead at a time."""
+    run_attend([1, 64, 99, 250, 3, 0, 511], 4, 2, hd, F32, cache, P, W=W, seed=P)
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 33, 64, 100, 1000])
-def test_attend_window(window):
-    run_attend([0, 1, 16, 33, 65, 130, 400, 999, 1500], 4, 4, 64, F32, BF16, 16, window=window, seed=window)
+@pytest.mark.parametrize("rows", [9, 90])
+def test_attend_window(window, rows):
+    lens = [0, 1, 16, 33, 65, 130, 400, 999, 1500]
+    run_attend([lens[i % 9] + i // 9 for i in range(rows)], 4, 4, 64, F32, BF16, 16, window=window, seed=window)
 
 
 @pytest.mark.parametrize("W,P", [(1, 1), (1, 16), (3, 5), (5, 16), (2, 64)])
 @pytest.mark.parametrize("window", [0, 40])
 def test_attend_ring_table(W, P, window):
     """Requests longer than their table: the last W pages are live."""
+    run_attend([0, 1, 16, 81, 313, 17, 80, 1000] * 20, 4, 2, 64, BF16, BF16, P, W=W, window=window, seed=W)
     run_attend([0, 1, 15, 16, 17, 80, 81, 100, 313, 1000], 4, 2, 32, BF16, BF16, P, W=W, window=window, seed=W)
     run_attend([0, 1, 16, 81, 313], 4, 2, 32, F32, F32, P, W=W, window=window, seed=W)
 
@@ -391,10 +440,13 @@ def test_attend_scale(scale):
 
 @pytest.mark.parametrize("io,cache,hd,lens,heads,hk", [
     (F32, BF16, 128, [9000], 2, 1), (BF16, BF16, 64, [20011, 3], 3, 1), (F32, F32, 32, [7001, 0, 513], 4, 2),
-    (BF16, BF16, 128, [4097, 1, 0, 2048, 700], 16, 2)])
+    (BF16, BF16, 128, [4097, 1, 0, 2048, 700], 16, 2), (F32, BF16, 64, [12001, 1, 3000], 4, 4),
+    (F32, F32, 128, [9001, 0, 40], 2, 2), (BF16, F32, 64, [9001, 0, 40], 8, 1),
+    (BF16, BF16, 32, [1, 30011, 3], 12, 1)])
 def test_attend_long(io, cache, hd, lens, heads, hk):
     """Rows long enough to be split over many thread blocks."""
     run_attend(lens, heads, hk, hd, io, cache, 16, seed=7, poison=False)
+    run_attend(lens, heads, hk, hd, io, cache, 16, W=20000, seed=7, poison=False)
 
 
 def test_attend_many_rows():
@@ -414,13 +466,15 @@ def test_attend_one_key_is_its_value():
 
 
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
-def test_attend_bad_blocks(io, cache):
+@pytest.mark.parametrize("columns", [4, CUT])
+def test_attend_bad_blocks(io, cache, columns):
     """Blocks outside the pool are left out; a row with no other has no live position."""
     g = torch.Generator().manual_seed(11)
     N, P, hk, hd, heads = 6, 16, 2, 64, 4
     k, v = make_cache(N, P, hk, hd, cache, g)
     table = torch.tensor([[0, -1, 2, 1], [N, 3, 2**31 - 1, -2**31], [-1, -5, N, N + 1], [5, 4, 3, 2]],
                          dtype=torch.int32)
+    table = torch.cat([table, torch.full((4, columns - 4), -1, dtype=torch.int32)], 1)
     pos = [63, 60, 50, 37]
     q = torch.randn(4, heads * hd, generator=g).to(io)
     lse = torch.zeros(4, heads, device="cuda")
@@ -491,6 +545,86 @@ def test_streams_and_graphs():
         graph.replay()
         want, want_lse = paged.paged_attention(q, k, v, table, pos, lse=True)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs of different shapes over one workspace, replayed in turn: each finds what it
+    needs whatever the other left there."""
+    g = torch.Generator().manual_seed(14)
+    N, P, hd = 400, 16, 64
+    graphs = []
+    ws = None
+    for heads, hk, lens in ((8, 4, [900, 3, 2500, 40]), (32, 2, [1, 2700, 0, 600, 1800])):
+        k, v = (x.cuda() for x in make_cache(N, P, hk, hd, BF16, g))
+        table = torch.stack([torch.randperm(N, generator=g)[:200] for _ in lens]).int().cuda()
+        table = torch.cat([table, torch.full((len(lens), CUT), -1, dtype=torch.int32, device="cuda")], 1)
+        q = torch.randn(len(lens), heads * hd, generator=g).cuda()
+        graphs.append([q, k, v, table, ints([n - 1 for n in lens])])
+        need = paged.paged_attention_workspace(q, k, table)
+        ws = need if ws is None or need.numel() > ws.numel() else ws
+    want = [paged.paged_attention(*a, lse=True) for a in graphs]
+    captured = []
+    for a in graphs:
+        out, lse = torch.empty_like(a[0]), torch.empty(a[0].shape[0], a[0].shape[1] // hd, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            paged.paged_attention(*a, out=out, lse=lse, workspace=ws)
+        captured.append((graph, out, lse))
+    ws.fill_(0xff)
+    for _ in range(3):
+        for (graph, out, lse), (o, l) in zip(captured, want):
+            out.zero_(), lse.zero_()
+            graph.replay()
+            assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_python_refusals():
+    """What the binding refuses before the library is called, and what the library refuses."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.zeros(4, 16, 2, 64, device="cuda")
+    q, table = torch.zeros(3, 256, device="cuda"), i(3, 4)
+    bad = [
+        dict(q=q.half()), dict(q=q[:, :100]), dict(q=q.t()), dict(k=k.half(), v=k.half()), dict(v=k.bfloat16()),
+        dict(v=k[:2]), dict(k=k[..., :32], v=k[..., :32].contiguous()), dict(k=k.permute(0, 1, 3, 2)),
+        dict(block_table=table.long()), dict(block_table=table.t()), dict(positions=i(2)),
+        dict(positions=i(3).long()), dict(positions=i(3).cpu()), dict(requests=i(2)), dict(out=q.bfloat16()),
+        dict(out=q[:2]), dict(lse=torch.zeros(3, 3, device="cuda")), dict(lse=torch.zeros(3, 4)),
+        dict(workspace=torch.zeros(8, dtype=torch.uint8)),
+    ]
+    ok = dict(q=q, k=k, v=k, block_table=table, positions=i(3))
+    for b in bad:
+        with pytest.raises(ValueError):
+            paged.paged_attention(**{**ok, **b})
+    for b in (dict(window=-1), dict(scale=float("inf")), dict(block_table=i(2, 4)), dict(q=torch.zeros(3, 192, device="cuda"))):
+        with pytest.raises(binding.RQError):
+            paged.paged_attention(**{**ok, **b})
+    out, lse = paged.paged_attention(**ok)
+    assert lse is None and out.shape == q.shape
+    qkv, slots = torch.zeros(3, 6 * 64, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    ok = dict(qkv=qkv, k=k, v=k.clone(), positions=i(3), slots=slots)
+    for b in (dict(qkv=qkv.half()), dict(qkv=qkv[:, :256]), dict(qkv=qkv.t()), dict(slots=i(3)), dict(slots=slots[:2]),
+              dict(q_alpha=torch.ones(64)), dict(q_alpha=torch.ones(32, device="cuda")), dict(rope="other"),
+              dict(out=torch.zeros(3, 128, device="cuda", dtype=torch.half)), dict(out=torch.zeros(3, 64, device="cuda"))):
+        with pytest.raises(ValueError):
+            paged.paged_append(**{**ok, **b})
+    for b in (dict(rope_dim=12), dict(rope_dim=72), dict(rope_theta=1.0), dict(eps=-1.0)):
+        with pytest.raises(binding.RQError):
+            paged.paged_append(**{**ok, **b})
+    with pytest.raises(ValueError):
+        paged.paged_plan(i(3), i(2), i(4), i(8), i(2, 4), 16, 8)
+    with pytest.raises(ValueError):
+        paged.paged_plan(i(2), i(2), i(3), i(8), i(2, 4), 16, 8)
+    with pytest.raises(binding.RQError):
+        paged.paged_plan(i(2), i(2), i(4), i(8), i(2, 4), 0, 8)
+
+
+def test_no_rows():
+    k = torch.zeros(4, 16, 2, 64, device="cuda")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q = paged.paged_append(torch.zeros(0, 6 * 64, device="cuda"), k, k, none, none.long())
+    assert q.shape == (0, 128)
+    out, lse = paged.paged_attention(q, k, k, torch.zeros(1, 4, dtype=torch.int32, device="cuda"), none, lse=True)
+    assert out.shape == (0, 128) and lse.shape == (0, 2)
 
 
 # ---------------------------------------------------------------- all of them, as they are used
