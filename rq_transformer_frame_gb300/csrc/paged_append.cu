@@ -21,12 +21,11 @@
 namespace rqk {
 namespace {
 
-// Two warps a CTA: few wait for the angles together. 16384 rows of 48 heads of 128 (bf16) took
-// 70 us with two warps of up to 12 steps, 73 with four, 84 with eight; 3 steps in flight 70,
-// 4 70, 6 71 (two warps).
-constexpr int kAppendWarps = 2;
+constexpr int kMaxWarps = 4;  // of a CTA
 constexpr int kMaxPairs = 64;
-constexpr int kAhead = 3;  // steps of a warp whose loads are in flight together
+// steps of a warp whose loads are in flight, always
+template <typename IT>
+constexpr int kAheadOf = sizeof(IT) == 2 ? 4 : 3;
 
 struct AppendParams {
   rq_paged_kv kv;
@@ -67,10 +66,32 @@ __device__ __forceinline__ void store4(uint16_t* p, const float* x) {
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// A lane's eight values of a head as the first and second members of its four pairs, packed by
+// two: one instruction works on two values (the kernel issues more than it waits otherwise).
+// HALVES: the first members are the piece at lo; else every second value from there.
+struct Pairs {
+  f32x2 u[2], v[2];
+};
+template <bool HALVES>
+__device__ __forceinline__ Pairs pairs_of(const float (&x)[8]) {
+  if (HALVES) return {{pack2(x[0], x[1]), pack2(x[2], x[3])}, {pack2(x[4], x[5]), pack2(x[6], x[7])}};
+  return {{pack2(x[0], x[2]), pack2(x[4], x[6])}, {pack2(x[1], x[3]), pack2(x[5], x[7])}};
+}
+template <bool HALVES>
+__device__ __forceinline__ void values_of(const Pairs& p, float (&x)[8]) {
+  const float2 a = unpack2(p.u[0]), b = unpack2(p.u[1]), c = unpack2(p.v[0]), d = unpack2(p.v[1]);
+  if (HALVES) {
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+  } else {
+    x[0] = a.x, x[2] = a.y, x[4] = b.x, x[6] = b.y, x[1] = c.x, x[3] = c.y, x[5] = d.x, x[7] = d.y;
+  }
+}
+
 template <typename IT, typename OT, typename KT, int HD, bool HALVES>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+__global__ void __launch_bounds__(kMaxWarps * 32, 28 / kMaxWarps)
     append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPH = HD / 8, HPS = 32 / LPH;  // lanes of a head, heads of a step
+  constexpr int kAhead = kAheadOf<IT>;
   __shared__ float2 s_cs[kMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31, sub = lane / LPH, j = lane % LPH;
   const int t = blockIdx.x / p.slices, slice = blockIdx.x - t * p.slices;
@@ -78,46 +99,52 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const bool turned = j * 8 < p.rope_dim;
   // this lane's dimensions: lo .. lo + 3 and hi .. hi + 3; its pairs are 4 j .. 4 j + 3
   const int lo = HALVES && turned ? 4 * j : 8 * j, hi = HALVES && turned ? half + 4 * j : 8 * j + 4;
-  const IT* row = static_cast<const IT*>(p.qkv) + t * p.qkv_stride;
   // the warp's heads: step i from h0 + i * HPS, this lane's head `sub` further, below h1
-  const int h0 = (slice * kAppendWarps + tid / 32) * p.steps * HPS, h1 = min(h0 + p.steps * HPS, total);
+  const int h0 = (slice * ((int)blockDim.x / 32) + tid / 32) * p.steps * HPS, h1 = min(h0 + p.steps * HPS, total);
   pdl_wait();
   pdl_trigger();
+  const IT* const row = static_cast<const IT*>(p.qkv) + t * p.qkv_stride + (long long)sub * HD;
   Piece<IT> in[kAhead][2];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b)
-      if (h + b * HPS + sub < h1) {
-        const IT* x = row + (long long)(h + b * HPS + sub) * HD;
-        in[b][0] = *reinterpret_cast<const Piece<IT>*>(x + lo);
-        in[b][1] = *reinterpret_cast<const Piece<IT>*>(x + hi);
-      }
+  auto load = [&](Piece<IT> (&d)[2], int h) {
+    if (h + sub >= h1) return;
+    const IT* x = row + (long long)h * HD;
+    d[0] = *reinterpret_cast<const Piece<IT>*>(x + lo);
+    d[1] = *reinterpret_cast<const Piece<IT>*>(x + hi);
   };
-  load(h0);
+#pragma unroll
+  for (int b = 0; b < kAhead; ++b) load(in[b], h0 + b * HPS);
   const int pos = p.positions[t];
   const long long slot = p.slots[t];
   if (pos < 0) return;
-  for (int i = tid; i < half; i += kAppendWarps * 32) {
+  auto alpha_of = [&](const float* alpha) {
+    float a[8];
+    reinterpret_cast<const Piece<float>*>(alpha + lo)->widen(a);
+    reinterpret_cast<const Piece<float>*>(alpha + hi)->widen(a + 4);
+    return pairs_of<HALVES>(a);
+  };
+  for (int i = tid; i < half; i += blockDim.x) {
     const long long frac = (long long)((unsigned long long)pos * p.turns[i]);
     float sn, cs;  // of half turns: 2^-63 of the fraction
     sincospif(__ll2float_rn(frac) * 1.0842021724855044e-19f, &sn, &cs);
     s_cs[i] = make_float2(cs, sn);
   }
   __syncthreads();
-  float c[4], s[4];
+  f32x2 c[2], s[2], ns[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 cs = turned ? s_cs[4 * j + i] : make_float2(1.f, 0.f);
-    c[i] = cs.x;
-    s[i] = cs.y;
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = turned ? s_cs[4 * j + 2 * i] : make_float2(1.f, 0.f);
+    const float2 b = turned ? s_cs[4 * j + 2 * i + 1] : make_float2(1.f, 0.f);
+    c[i] = pack2(a.x, b.x);
+    s[i] = pack2(a.y, b.y);
+    ns[i] = pack2(-a.y, -b.y);
   }
   const bool stored = slot >= 0 && slot < (long long)p.kv.n_blocks * p.kv.block_size;
   const long long block = !stored ? 0 : slot <= INT_MAX ? (int)slot / p.kv.block_size
                                                         : slot / p.kv.block_size;
   const long long at = block * p.kv.block_stride +
                        (stored ? slot - block * p.kv.block_size : 0) * p.kv.row_stride;
+  OT* const out = static_cast<OT*>(p.q_out) + (long long)t * p.heads * HD;
   for (int h = h0; h < h1; h += kAhead * HPS) {
-    if (h != h0) load(h);
 #pragma unroll
     for (int b = 0; b < kAhead; ++b) {
       if (h + b * HPS >= h1) break;  // the whole step is past the slice
@@ -128,34 +155,39 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
         in[b][0].widen(x);
         in[b][1].widen(x + 4);
       }
-      const float* alpha = is_q ? p.q_alpha : p.k_alpha;
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+      load(in[b], h + (b + kAhead) * HPS);
+      Pairs y = pairs_of<HALVES>(x);
+      f32x2 sq = mul2(y.u[0], y.u[0]);
+      sq = fma2(y.u[1], y.u[1], sq);
+      sq = fma2(y.v[0], y.v[0], sq);
+      sq = fma2(y.v[1], y.v[1], sq);
+      float ss = unpack2(sq).x + unpack2(sq).y;
 #pragma unroll
       for (int o = LPH / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (!is_v) {
-        if (alpha) {
+        if (const float* alpha = is_q ? p.q_alpha : p.k_alpha) {
+          const Pairs a = alpha_of(alpha);
           const float r = rsqrtf(ss * (1.0f / HD) + p.eps);
-          float a[8];
-          reinterpret_cast<const Piece<float>*>(alpha + lo)->widen(a);
-          reinterpret_cast<const Piece<float>*>(alpha + hi)->widen(a + 4);
+          const f32x2 r2 = pack2(r, r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= r * a[i];
+          for (int i = 0; i < 2; ++i) {
+            y.u[i] = mul2(y.u[i], mul2(r2, a.u[i]));
+            y.v[i] = mul2(y.v[i], mul2(r2, a.v[i]));
+          }
         }
         if (turned) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float &u = x[HALVES ? i : 2 * i], &v = x[HALVES ? 4 + i : 2 * i + 1];
-            const float y = fmaf(u, c[i], -v * s[i]);
-            v = fmaf(u, s[i], v * c[i]);
-            u = y;
+          for (int i = 0; i < 2; ++i) {
+            const f32x2 u = y.u[i];
+            y.u[i] = fma2(u, c[i], mul2(y.v[i], ns[i]));
+            y.v[i] = fma2(u, s[i], mul2(y.v[i], c[i]));
           }
         }
+        values_of<HALVES>(y, x);
       }
       if (!live) continue;
       if (is_q) {
-        OT* o = static_cast<OT*>(p.q_out) + ((long long)t * p.heads + head) * HD;
+        OT* o = out + (long long)head * HD;
         store4(o + lo, x);
         store4(o + hi, x + 4);
       } else if (stored) {
@@ -170,19 +202,20 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
 
 template <typename IT, typename OT, typename KT, int HD, bool HALVES>
 cudaError_t launch_append(AppendParams& p, int tokens, cudaStream_t s) {
-  // A CTA per row once there are kRows of them (eight CTAs an SM); below that a row's steps
-  // are divided over more CTAs, down to one step a warp.
-  constexpr int HPS = 32 / (HD / 8), kRows = 152 * 8;
-  const int steps = (p.heads + 2 * p.kv.heads + HPS - 1) / HPS;
-  const int whole = (steps + kAppendWarps - 1) / kAppendWarps;  // of a warp, with one CTA a row
-  int slices = tokens >= kRows ? 1 : (kRows + tokens - 1) / tokens;
+  // Rows in plenty are a CTA of one warp each: no warp waits for another's angles (16384 rows
+  // of 48 heads of 128 in bf16: 67 us; 69 with two warps a row, 73 with four; 4300 rows 26
+  // and 23). Fewer rows are CTAs of two warps, and below kCtas rows each is divided over
+  // several, down to one step a warp (64 such rows: 2.7 us, with CTAs of one warp 3.2).
+  constexpr int HPS = 32 / (HD / 8), kRows = 152 * 48, kCtas = 152 * 8;
+  const int steps = (p.heads + 2 * p.kv.heads + HPS - 1) / HPS, warps = tokens >= kRows ? 1 : 2;
+  const int whole = (steps + warps - 1) / warps;  // of a warp, with one CTA a row
+  int slices = tokens >= kCtas ? 1 : (kCtas + tokens - 1) / tokens;
   if (slices > whole) slices = whole;
   p.steps = (whole + slices - 1) / slices;
-  p.slices = (steps + p.steps * kAppendWarps - 1) / (p.steps * kAppendWarps);
+  p.slices = (steps + p.steps * warps - 1) / (p.steps * warps);
   const long long grid = (long long)tokens * p.slices;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  return launch_dependent(append_kernel<IT, OT, KT, HD, HALVES>, dim3((unsigned)grid), kAppendWarps * 32, 0, 0,
-                          s, p);
+  return launch_dependent(append_kernel<IT, OT, KT, HD, HALVES>, dim3((unsigned)grid), warps * 32, 0, 0, s, p);
 }
 
 template <typename IT, typename OT, typename KT, int HD>

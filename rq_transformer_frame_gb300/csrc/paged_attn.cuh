@@ -462,21 +462,6 @@ struct WideCore {
 };
 
 // ---------------------------------------------------------------- f32 cache: FMA
-// packed pairs of f32: one instruction for two products
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {  // d += a * b
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
 __device__ __forceinline__ void lds2(uint32_t addr, f32x2& a, f32x2& b) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
@@ -509,7 +494,7 @@ struct FmaCore {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
-      acc[h][0] = acc[h][1] = pair(0.f, 0.f);
+      acc[h][0] = acc[h][1] = pack2(0.f, 0.f);
       m[h] = neg_inf();
       l[h] = 0.f;
     }
@@ -531,7 +516,7 @@ struct FmaCore {
     const int key = lane % K, sl = lane / K;
     f32x2 d[GP];
 #pragma unroll
-    for (int h = 0; h < GP; ++h) d[h] = pair(0.f, 0.f);
+    for (int h = 0; h < GP; ++h) d[h] = pack2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       f32x2 k0, k1;
@@ -540,8 +525,8 @@ struct FmaCore {
       for (int h = 0; h < GP; ++h) {
         f32x2 q0, q1;
         lds2(qs + ((h * SL + sl) * kQPitch + c * 4) * 4, q0, q1);
-        fma2(d[h], q0, k0);
-        fma2(d[h], q1, k1);
+        d[h] = fma2(q0, k0, d[h]);
+        d[h] = fma2(q1, k1, d[h]);
       }
     }
     const bool live = (mask >> key) & 1u;
@@ -549,7 +534,7 @@ struct FmaCore {
     bool over = false;
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
-      const float2 x = unpair(d[h]);
+      const float2 x = unpack2(d[h]);
       s[h] = x.x + x.y;
 #pragma unroll
       for (int o = K; o < 32; o <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
@@ -565,13 +550,9 @@ struct FmaCore {
         const float f = ex2(m[h] - finite_or_zero(mx));
         m[h] = mx;
         l[h] *= f;
-        const f32x2 f2 = pair(f, f);
+        const f32x2 f2 = pack2(f, f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f32x2 z = pair(0.f, 0.f);
-          fma2(z, acc[h][i], f2);
-          acc[h][i] = z;
-        }
+        for (int i = 0; i < 2; ++i) acc[h][i] = mul2(acc[h][i], f2);
       }
     }
     // weights: slice key / 8, entry key % 8
@@ -599,8 +580,8 @@ struct FmaCore {
       }
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        fma2(acc[h][0], w[h], v0);
-        fma2(acc[h][1], w[h], v1);
+        acc[h][0] = fma2(w[h], v0, acc[h][0]);
+        acc[h][1] = fma2(w[h], v1, acc[h][1]);
       }
     }
     __syncwarp();
@@ -613,7 +594,7 @@ struct FmaCore {
       float t = l[h];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      float2 a = unpair(acc[h][0]), b = unpair(acc[h][1]);
+      float2 a = unpack2(acc[h][0]), b = unpack2(acc[h][1]);
 #pragma unroll
       for (int o = HD / 4; o < 32; o <<= 1) {
         a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
