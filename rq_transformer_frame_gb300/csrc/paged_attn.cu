@@ -4,14 +4,6 @@
 
 #include "paged_attn.cuh"
 
-namespace {
-// heads of a unit, at most (whatever the types)
-int heads_of_unit(int heads, int kv_heads) {
-  const int g = heads / kv_heads;
-  return g < rqk::paged_attn::kMaxHeads ? g : rqk::paged_attn::kMaxHeads;
-}
-}  // namespace
-
 extern "C" size_t rq_paged_attention_workspace_size(const rq_paged_kv* kv, int32_t rows,
                                                     int32_t heads, int32_t max_blocks,
                                                     int32_t window) {
@@ -19,11 +11,7 @@ extern "C" size_t rq_paged_attention_workspace_size(const rq_paged_kv* kv, int32
   if (paged_kv_check(kv) != RQ_OK || rows < 1 || heads < 1 || heads % kv->heads != 0 ||
       max_blocks < 1 || window < 0)
     return 0;
-  const paged_attn::Extent x =
-      paged_attn::extent(rows, heads, kv->heads, kv->head_dim, kv->dtype == RQ_BF16, kv->block_size,
-                         max_blocks, window);
-  if (paged_attn::split_ctas(x.units, x.tiles, rows, paged_attn::sm_count())) return 0;
-  return paged_attn::workspace_bytes(heads_of_unit(heads, kv->heads), kv->head_dim);
+  return paged_attn::choose(*kv, rows, heads, max_blocks, window).workspace;
 }
 
 extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -45,8 +33,8 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   if (!requests && rows > batch) return RQ_ERR_ARG;
   if (!block_table || !positions || !q || !out) return RQ_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
-  const size_t need = rq_paged_attention_workspace_size(kv, rows, heads, max_blocks, window);
-  if (workspace_bytes < need || (need && !workspace)) return RQ_ERR_ARG;
+  const paged_attn::Choice x = paged_attn::choose(*kv, rows, heads, max_blocks, window);
+  if (workspace_bytes < x.workspace || (x.workspace && !workspace)) return RQ_ERR_ARG;
   paged_attn::Params p{};
   p.kv = *kv;
   p.q = q;
@@ -61,17 +49,16 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   p.W = max_blocks;
   p.window = window;
   p.G = heads / kv->heads;
-  const int unit = heads_of_unit(heads, kv->heads);
   p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)kv->head_dim)) *
                     1.4426950408889634);
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(unit, kv->head_dim));
-  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(unit, kv->head_dim) +
-                                  paged_attn::ml_bytes(unit));
+  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(x.unit_heads, kv->head_dim));
+  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(x.unit_heads, kv->head_dim) +
+                                  paged_attn::ml_bytes(x.unit_heads));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool qb = q_dtype == RQ_BF16;
-  const cudaError_t e = kv->dtype == RQ_BF16 ? paged_attn::launch_bf16(p, qb, s)
-                                             : paged_attn::launch_f32(p, qb, s);
+  const cudaError_t e = kv->dtype == RQ_BF16 ? paged_attn::launch_bf16(p, x, qb, s)
+                                             : paged_attn::launch_f32(p, x, qb, s);
   return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }

@@ -14,7 +14,8 @@
 // ahead across units, and writes what it finished. A unit that is cut leaves a partial
 // (m, l, acc) per run, joined in order by a second kernel, so the result does not depend on
 // timing. A run has at most two cut units (its first and its last), which bounds the
-// workspace by the grid.
+// workspace by the grid. Where no row can be long, runs are of whole units instead: nothing
+// to search and nothing to join.
 //
 // Positions outside the live range or in a missing block are filled with zeros by the copy
 // and masked, so nothing that lies there is ever used.
@@ -45,8 +46,9 @@ struct Params {
   float* lse;
   const int32_t *table, *requests, *positions;
   int rows, heads, batch, W, window;
-  int G, GB, HG;       // query heads per K/V head, heads of a unit, units of a K/V head
+  int G, GB, HG;       // query heads per K/V head (or pair), of a unit; units of a K/V head (or pair)
   int runs;            // runs (warps) of the launch
+  int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
   float2* part_ml;     // [runs][2][GB] (m, l)
@@ -182,13 +184,16 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
 // a product come out of one instruction, in one thread (c0 + c2, c1 + c3). f32 queries and
 // their weights take a third part in a second instruction: 24 bits, every product exact.
 // bf16 queries are exact in one part; their weights have two.
-template <typename QT, int HD>
+// The rows in shared memory may hold more than this head (PairCore): SHAPE is theirs, FIRST the
+// head's first 16-byte piece.
+template <typename QT, int HD, typename SHAPE = Shape<uint16_t, HD>, int FIRST = 0>
 struct MmaCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
   static constexpr int kHeads = 8;
+  static constexpr int kLoad = HD;    // dimensions of a row in the ring
   static constexpr int kScratch = 0;  // bytes of shared memory of a warp
   static constexpr int kSteps = HD / 16;
-  using S = Shape<uint16_t, HD>;
+  using S = SHAPE;
   static constexpr int K = S::kKeys, NT = K / 8;  // keys of a tile, in eights
   uint32_t q[kF32 ? 3 : 1][kSteps][2];
   float acc[HD / 8][2];
@@ -230,7 +235,7 @@ struct MmaCore {
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         uint32_t b[4];
-        ldmatrix4(ks + n * 8 * S::kPitch + S::at(krow, 2 * k + kpiece), b);
+        ldmatrix4(ks + n * 8 * S::kPitch + S::at(krow, FIRST + 2 * k + kpiece), b);
         if constexpr (kF32) {
           mma16816(c[n], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[0], b[1]);
           mma16816(c[n + 1], q[0][k][0], q[1][k][0], q[0][k][1], q[1][k][1], b[2], b[3]);
@@ -290,7 +295,7 @@ struct MmaCore {
 #pragma unroll
       for (int j = 0; j < K / 16; ++j) {
         uint32_t b[4];
-        ldmatrix4_trans(vs + j * 16 * S::kPitch + S::at(vrow, 2 * d + vpiece), b);
+        ldmatrix4_trans(vs + j * 16 * S::kPitch + S::at(vrow, FIRST + 2 * d + vpiece), b);
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           mma16816(o[n], a[j][0], a[j][1], a[j][2], a[j][3], b[2 * n], b[2 * n + 1]);
@@ -328,6 +333,7 @@ template <typename QT, int HD>
 struct WideCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
   static constexpr int kHeads = 16;
+  static constexpr int kLoad = HD;
   static constexpr int kSteps = HD / 16, QP = kF32 ? 3 : 1, WP = kF32 ? 3 : 2;  // parts
   static constexpr int kScratch = 0;
   using S = Shape<uint16_t, HD>;
@@ -461,6 +467,39 @@ struct WideCore {
   }
 };
 
+// Two neighbouring K/V heads of 32 dimensions in bf16, up to 8 query heads each, as one unit: a
+// head's row is 64 bytes, half of what the memory hands over at a time, and by the time
+// another warp wants the other half it has left the L2 (128 rows of 3000 positions, 8 heads:
+// 703 MB read for 393). Rows of both heads fill whole lines.
+template <typename QT>
+struct PairCore {
+  static constexpr int kHeads = 16;
+  static constexpr int kLoad = 64;
+  static constexpr int kScratch = 0;
+  using S = Shape<uint16_t, 64>;
+  MmaCore<QT, 32, S, 0> a;
+  MmaCore<QT, 32, S, 4> b;
+
+  __device__ __forceinline__ void clear() {
+    a.clear();
+    b.clear();
+  }
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
+    a.load(qrow, live / 2, lane, nullptr);
+    b.load(qrow + (size_t)(live / 2) * 32, live / 2, lane, nullptr);
+  }
+  __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
+    a.tile(scale_log2, ks, mask, lane, nullptr);
+    b.tile(scale_log2, ks, mask, lane, nullptr);
+  }
+  template <bool PARTIAL, typename OT>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+    const int g = live / 2;
+    a.template end<PARTIAL>(out, lse, ml, g, lane);
+    b.template end<PARTIAL>(out + (size_t)g * 32, lse ? lse + g : nullptr, ml ? ml + g : nullptr, g, lane);
+  }
+};
+
 // ---------------------------------------------------------------- f32 cache: FMA
 __device__ __forceinline__ void lds2(uint32_t addr, f32x2& a, f32x2& b) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
@@ -477,6 +516,7 @@ __device__ __forceinline__ void lds2(uint32_t addr, f32x2& a, f32x2& b) {
 template <typename QT, int HD, int GP>
 struct FmaCore {
   static constexpr int kHeads = GP;
+  static constexpr int kLoad = HD;
   using S = Shape<float, HD>;
   static constexpr int K = S::kKeys;              // 8, 16, 32
   static constexpr int SL = 32 / K;               // slices of 32 dimensions of a key
@@ -630,7 +670,7 @@ enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };
 template <typename QT, typename KT, int HD, typename Core, bool SPLIT>
 __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT ? 1 : 2)
     attend_kernel(const __grid_constant__ Params p) {
-  using S = Shape<KT, HD>;
+  using S = Shape<KT, Core::kLoad>;
   constexpr int NW = SPLIT ? kSplitWarps : kWarps, NT = NW * 32;
   constexpr int NS = SPLIT ? split_stages<S::kStage, Core::kScratch> : kStages, K = S::kKeys;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -651,7 +691,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   // the warp's tiles: the list's entries [at, stop), the first of them tile t of unit (kvh, hg)
   // of row r; a run of the list is `per` entries
   int r = 0, kvh = 0, hg = 0, t = 0;
-  long long at = 0, stop = 0, per = 1;
+  long long at = 0, stop = 0, per = 1, unit_end = LLONG_MAX;
   Row x;
   int2 next_words = make_int2(-1, -1);
   if constexpr (SPLIT) {
@@ -672,71 +712,90 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     at = t;
     stop = x.nt * (long long)(run + 1) / n;
   } else {
-    __shared__ long long s_scan[NW];
-    __shared__ long long s_off[NW];  // each run's start, counted from its row's start
-    __shared__ int s_row[NW];
-  // where each run starts: prefix sums of the rows' costs, a slice of rows per thread
-  auto cost = [&](int r) {
-    const int nt = row_of<K>(p, row_words(p, r)).nt;
-    return nt ? (long long)(nt + kUnitCost) * units : 0ll;
-  };
-  const int slice = (p.rows + NT - 1) / NT;
-  const int r0 = min(tid * slice, p.rows), r1 = min(r0 + slice, p.rows);
-  long long own = 0;
-#pragma unroll 4
-  for (int r = r0; r < r1; ++r) own += cost(r);
-  long long inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
-  }
-  if (lane == 31) s_scan[warp] = inc;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) inc += s_scan[w];
-    total += s_scan[w];
-  }
-  per = (total + p.runs - 1) / p.runs;
-  if (per < kMinRun + kUnitCost) per = kMinRun + kUnitCost;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const long long begin = (blockIdx.x * NW + w) * per;
-    if (inc - own <= begin && begin < inc) {
-      long long at = begin - (inc - own);
-      for (int r = r0; r < r1; ++r) {
-        const long long t = cost(r);
-        if (at < t) {
-          s_row[w] = r;
-          s_off[w] = at;
-          break;
+    if (p.whole) {
+      // units [first, last): rows without tiles have units too, of no work
+      const long long all = (long long)p.rows * units, from = min((long long)run * p.whole, all);
+      unit_end = min(from + p.whole, all);
+      if (from < unit_end) {
+        r = (int)(from / units);
+        int u = (int)(from % units);
+        x = row_of<K>(p, row_words(p, r));
+        while (x.nt == 0 && (long long)(r + 1) * units < unit_end) {
+          x = row_of<K>(p, row_words(p, ++r));
+          u = 0;
         }
-        at -= t;
+        next_words = row_words(p, r + 1);
+        kvh = u / p.HG;
+        hg = u % p.HG;
+        stop = x.nt ? LLONG_MAX : 0;  // ends by unit_end
+      }
+    } else {
+      __shared__ long long s_scan[NW];
+      __shared__ long long s_off[NW];  // each run's start, counted from its row's start
+      __shared__ int s_row[NW];
+      // where each run starts: prefix sums of the rows' costs, a slice of rows per thread
+      auto cost = [&](int r) {
+        const int nt = row_of<K>(p, row_words(p, r)).nt;
+        return nt ? (long long)(nt + kUnitCost) * units : 0ll;
+      };
+      const int slice = (p.rows + NT - 1) / NT;
+      const int r0 = min(tid * slice, p.rows), r1 = min(r0 + slice, p.rows);
+      long long own = 0;
+#pragma unroll 4
+      for (int i = r0; i < r1; ++i) own += cost(i);
+      long long inc = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      if (lane == 31) s_scan[warp] = inc;
+      __syncthreads();
+      long long total = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        if (w < warp) inc += s_scan[w];
+        total += s_scan[w];
+      }
+      per = (total + p.runs - 1) / p.runs;
+      if (per < kMinRun + kUnitCost) per = kMinRun + kUnitCost;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const long long begin = (blockIdx.x * NW + w) * per;
+        if (inc - own <= begin && begin < inc) {
+          long long at = begin - (inc - own);
+          for (int i = r0; i < r1; ++i) {
+            const long long c = cost(i);
+            if (at < c) {
+              s_row[w] = i;
+              s_off[w] = at;
+              break;
+            }
+            at -= c;
+          }
+        }
+      }
+      __syncthreads();
+      const long long begin = run * per;
+      stop = min(begin + per, total);
+      at = stop;
+      if (begin < total) {
+        r = s_row[warp];
+        x = row_of<K>(p, row_words(p, r));
+        next_words = row_words(p, r + 1);
+        const int unit_cost = x.nt + kUnitCost, u = (int)(s_off[warp] / unit_cost);
+        const int in = (int)(s_off[warp] % unit_cost);
+        kvh = u / p.HG;
+        hg = u % p.HG;
+        t = max(in - kUnitCost, 0);
+        at = begin + (t - (in - kUnitCost));
       }
     }
-  }
-  __syncthreads();
-  // rows of empty requests
-  for (int r = run; r < p.rows; r += p.runs) {
-    const int2 words = row_words(p, r);
-    if (words.x < 0 || words.x >= p.batch || words.y >= 0) continue;
-    empty_row(r, 0, p.heads, lane, 32);
-  }
-    const long long begin = run * per;
-    stop = min(begin + per, total);
-    at = stop;
-    if (begin < total) {
-      r = s_row[warp];
-      x = row_of<K>(p, row_words(p, r));
-      next_words = row_words(p, r + 1);
-      const int unit_cost = x.nt + kUnitCost, u = (int)(s_off[warp] / unit_cost);
-      const int in = (int)(s_off[warp] % unit_cost);
-      kvh = u / p.HG;
-      hg = u % p.HG;
-      t = max(in - kUnitCost, 0);
-      at = begin + (t - (in - kUnitCost));
+    // rows of empty requests
+    for (int i = run; i < p.rows; i += p.runs) {
+      const int2 words = row_words(p, i);
+      if (words.x < 0 || words.x >= p.batch || words.y >= 0) continue;
+      empty_row(i, 0, p.heads, lane, 32);
     }
   }
   Core core;
@@ -788,7 +847,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         cut = make_int4(r, kvh * p.G + hg * Core::kHeads, min(Core::kHeads, p.G - hg * Core::kHeads),
                         (int)((at + (x.nt - t) - 1) / per - run) + 1);
       if (mask) {
-        constexpr int CH = HD * sizeof(KT) / 16;  // 16-byte pieces of a row
+        constexpr int CH = S::kPitch / 16;        // 16-byte pieces of a row
         constexpr int RPI = 32 / CH;              // rows of a warp's copy instruction
         const uint32_t dst = ring + s * S::kStage;
         const KT* kb = static_cast<const KT*>(p.kv.k);
@@ -840,7 +899,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         ids = ids_after;
         ids_after = ids_from(x, base + 32);
       }
-      more = at < stop && x.nt > 0;
+      more = at < stop && x.nt > 0 &&
+             (!p.whole || (long long)r * units + kvh * p.HG + hg < unit_end);
     };
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) {
@@ -873,7 +933,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     }
   }
   if constexpr (!SPLIT) {
-    if (lane == 0) p.cut[run] = cut;
+    if (lane == 0 && !p.whole) p.cut[run] = cut;
   } else {
     // ---- join: the warps' sums in this CTA's shared memory (its ring is free), then each CTA
     // of the cluster finishes a share of the outputs from every CTA's sums
@@ -1042,43 +1102,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   }
 }
 
-// A split launch's CTAs per unit for `units` units of up to `tiles` tiles, or 0 for a launch of
-// runs. Measured (head_dim 128, bf16): one row of 8 K/V heads takes 5.8 / 6.6 / 9.9 / 23 us
-// split at 16 / 1000 / 4000 / 16000 positions against 9.4 / 16.0 / 16.2 / 23 us in runs, and
-// 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
-// of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
-// several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 32, or
-// up to 128 where the clusters fill three quarters of the card (32 K/V heads: 5.5 / 7.9 / 19 /
-// 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768 positions against 8.5 / 13 / 23 / 53 / 92).
-inline int split_ctas(long long units, long long tiles, int rows, int sms) {
-  if (units > sms) return 0;
-  int c = 1;
-  // clusters that are all resident: with one CTA an SM 15 clusters of eight fit this card at
-  // once, 36 of four, 76 of two; a sixteenth cluster of eight waits for the others (16 units
-  // of 16 positions took 8.8 us in eights, 5.6 in fours)
-  while (c < 8 && (units + 4) * c * 2 <= sms) c *= 2;
-  // every warp of the cluster a tile at least
-  while (c > 1 && (long long)c * kSplitWarps > tiles * 2) c /= 2;
-  const long long most = tiles / (c * kSplitWarps);  // tiles of a warp, at most
-  const bool full = 4 * units * c >= 3 * sms;        // the clusters fill the card
-  return most <= (rows > 1 ? 8 : full ? 128 : 32) ? c : 0;
-}
-
-// What a call's launch is decided by: units of all rows and tiles of a unit, at most.
-struct Extent {
-  long long units, tiles;
-};
-inline Extent extent(long long rows, int heads, int kv_heads, int head_dim, bool kv_bf16, int block_size,
-                     int max_blocks, int window) {
-  const int g = heads / kv_heads, most = kv_bf16 ? 16 : 8;  // heads of a unit
-  long long keys = (long long)max_blocks * block_size;
-  if (keys > INT_MAX) keys = INT_MAX;
-  if (window > 0 && window < keys) keys = window;
-  int tile = 4096 / (head_dim * (kv_bf16 ? 2 : 4));
-  if (tile > 32) tile = 32;
-  return {rows * kv_heads * ((g + most - 1) / most), keys / tile + 2};
-}
-
 // multiprocessors of the current device, looked up once (0 if there is none)
 inline int sm_count() {
   static std::atomic<int> known[kMaxDevices];
@@ -1090,15 +1113,71 @@ inline int sm_count() {
   return sms;
 }
 
+// How a call is launched, from what the host knows: the shapes, and how long a row may be.
+struct Choice {
+  bool pair;               // units of two K/V heads (PairCore)
+  int unit_heads;          // query heads of a unit, at most
+  int units_of_kv;         // units of a K/V head (or pair)
+  long long units, tiles;  // units of all rows, tiles of a unit, at most
+  int split;               // CTAs of a unit in a split launch, or 0
+  bool whole;              // runs of whole units
+  size_t workspace;
+};
+
+// A split launch's CTAs per unit for `units` units of up to `tiles` tiles, or 0 for a launch of
+// runs. Measured (head_dim 128, bf16): one row of 8 K/V heads takes 5.8 / 6.6 / 9.9 / 23 us
+// split at 16 / 1000 / 4000 / 16000 positions against 9.4 / 16.0 / 16.2 / 23 us in runs, and
+// 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
+// of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
+// several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 32 (f32,
+// whose tiles take longer: 8), or up to 128 where the clusters fill three quarters of the card
+// (32 K/V heads: 5.5 / 7.9 / 19 / 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768 positions
+// against 8.5 / 13 / 23 / 53 / 92).
+inline int split_ctas(long long units, long long tiles, int rows, bool bf16, int sms) {
+  if (units > sms) return 0;
+  int c = 1;
+  // clusters that are all resident: with one CTA an SM 15 clusters of eight fit this card at
+  // once, 36 of four, 76 of two; a sixteenth cluster of eight waits for the others (16 units
+  // of 16 positions took 8.8 us in eights, 5.6 in fours)
+  while (c < 8 && (units + 4) * c * 2 <= sms) c *= 2;
+  // every warp of the cluster a tile at least
+  while (c > 1 && (long long)c * kSplitWarps > tiles * 2) c /= 2;
+  const long long most = tiles / (c * kSplitWarps);  // tiles of a warp, at most
+  const bool full = 4 * units * c >= 3 * sms;        // the clusters fill the card
+  return most <= (rows > 1 ? 8 : full ? 128 : bf16 ? 32 : 8) ? c : 0;
+}
+
+inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int window) {
+  Choice x{};
+  const int g = heads / kv.heads;
+  const bool bf16 = kv.dtype == RQ_BF16;
+  x.pair = bf16 && kv.head_dim == 32 && kv.head_stride == 32 && kv.heads % 2 == 0 && g <= 8;
+  const int most = bf16 ? 16 : 8, wanted = x.pair ? 2 * g : g;
+  x.unit_heads = wanted < most ? wanted : most;
+  x.units_of_kv = (wanted + most - 1) / most;
+  int tile = 4096 / ((x.pair ? 64 : kv.head_dim) * (bf16 ? 2 : 4));
+  if (tile > 32) tile = 32;
+  long long keys = (long long)max_blocks * kv.block_size;
+  if (keys > INT_MAX) keys = INT_MAX;
+  if (window > 0 && window < keys) keys = window;
+  x.units = (long long)rows * (x.pair ? kv.heads / 2 : kv.heads) * x.units_of_kv;
+  x.tiles = keys / tile + 2;
+  x.split = split_ctas(x.units, x.tiles, rows, bf16, sm_count());
+  // rows of at most eight whole tiles: no search and no join (182 rows of up to 192 positions,
+  // head_dim 64, 12.9 us with them and 8.4 without; longer units would be uneven shares)
+  x.whole = !x.split && x.tiles <= 10;
+  x.workspace = x.split || x.whole ? 0 : workspace_bytes(x.unit_heads, kv.head_dim);
+  return x;
+}
+
 template <typename QT, typename KT, int HD, typename Core>
-cudaError_t launch(Params p, cudaStream_t s) {
-  using S = Shape<KT, HD>;
-  static_assert(S::kKeys == (4096 / S::kPitch < 32 ? 4096 / S::kPitch : 32), "as in extent()");
+cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
+  using S = Shape<KT, Core::kLoad>;
   cudaError_t e;
-  p.HG = (p.G + Core::kHeads - 1) / Core::kHeads;
-  p.GB = p.G < Core::kHeads ? p.G : Core::kHeads;
-  const Extent x = extent(p.rows, p.heads, p.kv.heads, HD, sizeof(KT) == 2, p.kv.block_size, p.W, p.window);
-  if (const int c = split_ctas(x.units, x.tiles, p.rows, sm_count())) {
+  if (x.unit_heads > Core::kHeads) return cudaErrorInvalidValue;
+  p.HG = x.units_of_kv;
+  p.GB = x.unit_heads;
+  if (x.split) {
     auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
     constexpr size_t ring = (size_t)kSplitWarps *
                             (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
@@ -1106,7 +1185,8 @@ cudaError_t launch(Params p, cudaStream_t s) {
     constexpr size_t smem = ring > sums ? ring : sums;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3((unsigned)c, (unsigned)x.units, 1), kSplitWarps * 32, smem, c, s, p);
+    return launch_dependent(kernel, dim3((unsigned)x.split, (unsigned)x.units, 1), kSplitWarps * 32, smem, x.split,
+                            s, p);
   }
   // as many CTAs as are resident at once, at most as many as the largest rows could fill
   auto* kernel = attend_kernel<QT, KT, HD, Core, false>;
@@ -1117,6 +1197,15 @@ cudaError_t launch(Params p, cudaStream_t s) {
   int ctas = 0;
   if ((e = resident_ctas(kernel, kWarps * 32, smem, resident, &ctas)) != cudaSuccess) return e;
   if (ctas > kMaxGrid) ctas = kMaxGrid;
+  if (x.whole) {
+    const long long runs = (long long)ctas * kWarps, share = (x.units + runs - 1) / runs;
+    if (share > INT_MAX) return cudaErrorInvalidValue;
+    p.whole = (int)share;
+    p.runs = (int)((x.units + share - 1) / share);
+    const int grid = (p.runs + kWarps - 1) / kWarps;
+    p.runs = grid * kWarps;
+    return launch_dependent(kernel, dim3((unsigned)grid), kWarps * 32, smem, 0, s, p);
+  }
   const long long most = (x.tiles * x.units + kWarps * kMinRun - 1) / (kWarps * kMinRun);
   const int grid = (int)(ctas < most ? ctas : most);
   p.runs = grid * kWarps;
@@ -1125,8 +1214,9 @@ cudaError_t launch(Params p, cudaStream_t s) {
   return launch_dependent(join_kernel<QT, HD>, joins, kJoinWarps * 32, 0, 0, s, p);
 }
 
-cudaError_t launch_bf16(const Params& p, bool q_bf16, cudaStream_t s);  // over a bf16 cache
-cudaError_t launch_f32(const Params& p, bool q_bf16, cudaStream_t s);   // over an f32 cache
+// over a bf16 cache, over an f32 cache
+cudaError_t launch_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 
 }  // namespace paged_attn
 }  // namespace rqk

@@ -1,26 +1,33 @@
-// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore and WideCore).
+// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore, WideCore and PairCore).
 #include "paged_attn.cuh"
 
 namespace rqk {
 namespace paged_attn {
 
 template <typename QT, int HD>
-static cudaError_t by_heads(const Params& p, cudaStream_t s) {
-  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>>(p, s)
-                  : launch<QT, uint16_t, HD, WideCore<QT, HD>>(p, s);
+static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
+  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>>(p, x, s)
+                  : launch<QT, uint16_t, HD, WideCore<QT, HD>>(p, x, s);
 }
 
 template <typename QT>
-static cudaError_t by_head_dim(const Params& p, cudaStream_t s) {
+static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s) {
+  if (x.pair) {
+    Params pairs = p;
+    pairs.kv.heads /= 2;
+    pairs.kv.head_stride = 64;
+    pairs.G *= 2;
+    return launch<QT, uint16_t, 32, PairCore<QT>>(pairs, x, s);
+  }
   switch (p.kv.head_dim) {
-    case 32: return by_heads<QT, 32>(p, s);
-    case 64: return by_heads<QT, 64>(p, s);
-    default: return by_heads<QT, 128>(p, s);
+    case 32: return by_heads<QT, 32>(p, x, s);
+    case 64: return by_heads<QT, 64>(p, x, s);
+    default: return by_heads<QT, 128>(p, x, s);
   }
 }
 
-cudaError_t launch_bf16(const Params& p, bool q_bf16, cudaStream_t s) {
-  return q_bf16 ? by_head_dim<uint16_t>(p, s) : by_head_dim<float>(p, s);
+cudaError_t launch_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s) {
+  return q_bf16 ? by_head_dim<uint16_t>(p, x, s) : by_head_dim<float>(p, x, s);
 }
 
 }  // namespace paged_attn

@@ -87,9 +87,10 @@ def _cache(k, v):
 
 
 @lru_cache(maxsize=1024)
-def _workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, block_size, max_blocks, window):
-    # the size goes by these alone: any pointer and strides that are valid stand for a cache
-    kv = _KV.pack(16, 16, 0, 0, 0, dtype, kv_heads, head_dim, block_size, 1)
+def _workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, head_stride, block_size, max_blocks,
+                    window):
+    # the size goes by these alone: any pointer and other strides stand for a cache
+    kv = _KV.pack(16, 16, 0, 0, head_stride, dtype, kv_heads, head_dim, block_size, 1)
     return load().rq_paged_attention_workspace_size(kv, rows, heads, max_blocks, window)
 
 
@@ -98,8 +99,8 @@ def paged_attention_workspace(q, k, block_table, window=0):
     captured graph), or None where the call needs none."""
     n, p, hk, hd = k.shape
     with _on(k.device, None):
-        size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd, p,
-                               block_table.shape[1], window)
+        size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
+                               k.stride(2), p, block_table.shape[1], window)
     return torch.empty(size, dtype=torch.uint8, device=k.device) if size else None
 
 
@@ -205,7 +206,7 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     if lse is True:
         lse = torch.empty((R, heads), dtype=_F32, device=k.device)
     if workspace is None:
-        nbytes = _workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.shape[1], W, window)
+        nbytes = _workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.stride(2), k.shape[1], W, window)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():

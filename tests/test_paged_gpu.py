@@ -431,6 +431,27 @@ def test_attend_layouts(layout, cache):
     run_attend([0, 1, 40, 130, 77], 8, 2, 64, F32, cache, 16, layout=layout, poison=layout == "nhd", seed=3)
 
 
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_attend_short_rows(io, cache, hd):
+    """Many rows of a few blocks, empty ones among them, first and last: whole units a warp."""
+    r = random.Random(hd)
+    lens = [0, 0, 0] + [r.choice([0, 0, 1, 2, 5, 16, 17, 31, 40, 63]) for _ in range(400)] + [0, 0]
+    run_attend(lens, 4, 2, hd, io, cache, 8, W=8, pad=2, seed=hd)
+    run_attend([0] * 300 + [3], 4, 2, hd, io, cache, 8, W=8, seed=hd)
+
+
+@pytest.mark.parametrize("heads,hk", [(4, 4), (16, 2), (14, 2), (34, 2), (3, 3), (2, 1)])
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("W", [None, CUT])
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+def test_attend_heads_of_32(heads, hk, io, W, layout):
+    """Heads of 32 dimensions: two neighbours as one unit, or where they do not lie side by side,
+    are odd in number or have many queries, one by one."""
+    run_attend([0, 1, 40, 77, 130, 300], heads, hk, 32, io, BF16, 16, W=W, layout=layout, poison=layout == "nhd",
+               seed=heads)
+
+
 @pytest.mark.parametrize("scale", [0.5, 3.0, -0.7])
 def test_attend_scale(scale):
     """Sharp and negative scales: large scores of both signs."""
