@@ -993,7 +993,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
 // kJoinWarps consecutive runs (blockIdx.x) and head blockIdx.y of their units. A unit of few
 // parts is a warp's, all sixteen at once; one of many parts (a long row over many runs, so
 // at most one or two among them) is the whole CTA's: each warp sums a share of the parts.
-// All of it is latency: a chain of reads in L2 behind the main kernel's end.
+// All of it is latency, a chain of reads in L2 behind the main kernel's end, so the CTAs are
+// held to 64 registers: 1216 cut units of 8 heads want all their warps resident at once.
 constexpr int kJoinWarps = 16, kJoinFew = 12;
 
 template <int E>
@@ -1002,12 +1003,12 @@ struct alignas(4 * E) Floats {
 };
 
 // (m, l, a) += the parts [i0, i1) of one head: m and l alike in every lane, a the lane's E
-// dimensions. `slot(i)`: where part i is.
-template <int E, typename Slot>
+// dimensions. `slot(i)`: where part i is. U sums are in flight, the first of them beside their
+// (m, l).
+template <int E, int U, typename Slot>
 __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot slot, int lane, float& m,
                                            float& l, float (&a)[E]) {
   auto part = [&](int i) { return *reinterpret_cast<const Floats<E>*>(p.part + slot(i) * (E * 32) + lane * E); };
-  constexpr int U = 12;  // sums in flight, the first of them beside their (m, l)
   for (int b = i0; b < i1; b += 32) {
     const int n = min(i1 - b, 32);
     float2 ml = make_float2(neg_inf(), 0.f);
@@ -1022,6 +1023,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot
     l = l * old + warp_sum(ml.y * f);
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] *= old;
+#pragma unroll 1
     for (int j0 = 0; j0 < n; j0 += U) {
       if (j0 > 0) {
 #pragma unroll
@@ -1040,7 +1042,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot
 }
 
 template <typename QT, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_constant__ Params p) {
   constexpr int E = HD / 32;
   __shared__ int4 s_cut[kJoinWarps];
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][HD];
@@ -1063,7 +1065,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const bool many = g < own.z && own.w > kJoinFew;
   if (g < own.z && !many) {
     float m = neg_inf(), l = 0.f, a[E] = {};
-    join_parts<E>(p, 0, own.w, slots_of(run0 + warp), lane, m, l, a);
+    join_parts<E, 4>(p, 0, own.w, slots_of(run0 + warp), lane, m, l, a);
     write(own, m, l, a);
   }
   if (lane == 0) s_cut[warp] = many ? own : make_int4(0, 0, 0, 0);
@@ -1072,8 +1074,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const int4 cut = s_cut[c];
     if (cut.w == 0) continue;
     float m = neg_inf(), l = 0.f, a[E] = {};
-    join_parts<E>(p, (int)((long long)cut.w * warp / kJoinWarps),
-                  (int)((long long)cut.w * (warp + 1) / kJoinWarps), slots_of(run0 + c), lane, m, l, a);
+    join_parts<E, 6>(p, (int)((long long)cut.w * warp / kJoinWarps),
+                     (int)((long long)cut.w * (warp + 1) / kJoinWarps), slots_of(run0 + c), lane, m, l, a);
     if (lane == 0) {
       s_m[warp] = m;
       s_l[warp] = l;
