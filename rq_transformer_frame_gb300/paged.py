@@ -56,19 +56,15 @@ def _on(device, stream):
                 yield
 
 
-def _ints(name, t, n, dev, dtype=_I32):
-    """The address of a contiguous integer tensor of (at least) n elements."""
-    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of %d elements on cuda:%d is wanted" %
-                         (name, dtype, n, dev))
-    return t.data_ptr()
+# The checks stand in line in the calls below (a Python call costs as much as the check); these
+# two say what was wrong.
+def _bad_ints(name, n, dev, dtype=_I32):
+    raise ValueError("%s: a contiguous %s tensor of %d elements on cuda:%d is wanted" % (name, dtype, n, dev))
 
 
-def _rows(name, t, shape, dtype, dev):
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of shape %s on cuda:%d is wanted" %
-                         (name, dtype, tuple(shape), dev))
-    return t.data_ptr()
+def _bad_rows(name, shape, dtype, dev):
+    raise ValueError("%s: a contiguous %s tensor of shape %s on cuda:%d is wanted" %
+                     (name, dtype, tuple(shape), dev))
 
 
 def _cache(k, v):
@@ -116,7 +112,6 @@ def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_toke
     [B + 1], requests and positions [max_tokens] int32 and slots [max_tokens] int64; its lens
     and pool may be the inputs themselves.  pool[2] says whether the call did anything
     (RQ_PAGED_*)."""
-    L = load()
     dev = lens.get_device()
     if dev < 0 or block_table.dim() != 2:
         raise ValueError("lens, block_table: CUDA tensors [B] and [B][max_blocks] are wanted")
@@ -128,17 +123,22 @@ def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_toke
     if out is None:
         e = lambda n, dt=_I32: torch.empty(n, dtype=dt, device=lens.device)  # noqa: E731
         out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, _I64))
-    elif not isinstance(out, PagedPlan):
+    elif type(out) is not PagedPlan:
         out = PagedPlan(*out)
     if lens.numel() != B or new_lens.numel() != B:
         raise ValueError("new_lens, lens and block_table differ in their requests")
-    rc = L.rq_paged_plan(
-        B, W, block_size, free_ids.numel(), M, _ints("new_lens", new_lens, B, dev),
-        _ints("lens", lens, B, dev), _ints("pool", pool, 4, dev), _ints("free_ids", free_ids, 1, dev),
-        _ints("block_table", block_table, B * W, dev), _ints("out.lens", out.lens, B, dev),
-        _ints("out.pool", out.pool, 4, dev), _ints("out.cu_tokens", out.cu_tokens, B + 1, dev),
-        _ints("out.requests", out.requests, M, dev), _ints("out.positions", out.positions, M, dev),
-        _ints("out.slots", out.slots, M, dev, _I64), _current_stream(dev))
+    o_lens, o_pool, cu, req, pos, slots = out
+    for name, t, n in (("new_lens", new_lens, B), ("lens", lens, B), ("pool", pool, 4), ("free_ids", free_ids, 1),
+                       ("block_table", block_table, B * W), ("out.lens", o_lens, B), ("out.pool", o_pool, 4),
+                       ("out.cu_tokens", cu, B + 1), ("out.requests", req, M), ("out.positions", pos, M)):
+        if t.dtype is not _I32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+            _bad_ints(name, n, dev)
+    if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < M or not slots.is_contiguous():
+        _bad_ints("out.slots", M, dev, _I64)
+    rc = load().rq_paged_plan(
+        B, W, block_size, free_ids.numel(), M, new_lens.data_ptr(), lens.data_ptr(), pool.data_ptr(),
+        free_ids.data_ptr(), block_table.data_ptr(), o_lens.data_ptr(), o_pool.data_ptr(), cu.data_ptr(),
+        req.data_ptr(), pos.data_ptr(), slots.data_ptr(), _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_plan", rc)
     return out
@@ -151,7 +151,6 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
     strided) -> queries [T][heads * head_dim] in q_dtype (default: qkv's, or out's), keys and
     values stored in k, v at `slots` (int64 [T]).  rope: "interleaved" or "halves" over the
     first rope_dim (default: all) dimensions; alphas: f32 [head_dim] or None for no norm."""
-    L = load()
     kv, hk, hd, dev = _cache(k, v)
     if stream is not None or _current_device() != dev:
         with _on(k.device, stream):
@@ -169,15 +168,25 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
         raise ValueError("rope: 'interleaved' or 'halves'")
     if out is None:
         out = torch.empty((T, heads * hd), dtype=q_dtype or dtype, device=k.device)
-    if out.dtype not in _TYPE or (q_dtype is not None and out.dtype is not q_dtype):
+    o_dtype = out.dtype
+    if o_dtype not in _TYPE or (q_dtype is not None and o_dtype is not q_dtype):
         raise ValueError("out: f32 or bf16, as q_dtype says")
-    rc = L.rq_paged_append(
+    if out.shape != (T, heads * hd) or out.get_device() != dev or not out.is_contiguous():
+        _bad_rows("out", (T, heads * hd), o_dtype, dev)
+    for alpha in (q_alpha, k_alpha):
+        if alpha is not None and (alpha.dtype is not _F32 or alpha.get_device() != dev or alpha.shape != (hd,) or
+                                  not alpha.is_contiguous()):
+            _bad_rows("q_alpha, k_alpha", (hd,), _F32, dev)
+    if positions.dtype is not _I32 or positions.get_device() != dev or positions.numel() < T or \
+            not positions.is_contiguous():
+        _bad_ints("positions", T, dev)
+    if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < T or not slots.is_contiguous():
+        _bad_ints("slots", T, dev, _I64)
+    rc = load().rq_paged_append(
         kv, T, heads, _TYPE[dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
-        None if q_alpha is None else _rows("q_alpha", q_alpha, (hd,), _F32, dev),
-        None if k_alpha is None else _rows("k_alpha", k_alpha, (hd,), _F32, dev),
-        eps, _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta,
-        _ints("positions", positions, T, dev), _ints("slots", slots, T, dev, _I64),
-        _TYPE[out.dtype], _rows("out", out, (T, heads * hd), out.dtype, dev), _current_stream(dev))
+        None if q_alpha is None else q_alpha.data_ptr(), None if k_alpha is None else k_alpha.data_ptr(), eps,
+        _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta, positions.data_ptr(), slots.data_ptr(),
+        _TYPE[o_dtype], out.data_ptr(), _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_append", rc)
     return out
@@ -189,7 +198,6 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     positions [R] (-1: an empty request), requests [R] (-1: padding, its output left as it
     was; None: row r is request r), all int32 -> (out [R][heads * head_dim], lse [R][heads]
     f32, None unless a tensor or True is passed for it)."""
-    L = load()
     kv, hk, hd, dev = _cache(k, v)
     if stream is not None or _current_device() != dev:
         with _on(k.device, stream):
@@ -205,6 +213,21 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
         out = torch.empty_like(q)
     if lse is True:
         lse = torch.empty((R, heads), dtype=_F32, device=k.device)
+    if q.get_device() != dev or not q.is_contiguous():
+        _bad_rows("q", shape, dtype, dev)
+    if out.dtype is not dtype or out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _bad_rows("out", shape, dtype, dev)
+    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != (R, heads) or
+                            not lse.is_contiguous()):
+        _bad_rows("lse", (R, heads), _F32, dev)
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        _bad_ints("block_table", B * W, dev)
+    if positions.dtype is not _I32 or positions.get_device() != dev or positions.numel() < R or \
+            not positions.is_contiguous():
+        _bad_ints("positions", R, dev)
+    if requests is not None and (requests.dtype is not _I32 or requests.get_device() != dev or
+                                 requests.numel() < R or not requests.is_contiguous()):
+        _bad_ints("requests", R, dev)
     if workspace is None:
         nbytes = _workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.stride(2), k.shape[1], W, window)
         if nbytes:
@@ -213,13 +236,11 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
         raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
     else:
         nbytes = workspace.numel() * workspace.element_size()
-    rc = L.rq_paged_attention(
-        kv, R, heads, B, W, _ints("block_table", block_table, B * W, dev),
-        None if requests is None else _ints("requests", requests, R, dev),
-        _ints("positions", positions, R, dev), window, scale, _TYPE[dtype],
-        _rows("q", q, shape, dtype, dev), _rows("out", out, shape, dtype, dev),
-        None if lse is None else _rows("lse", lse, (R, heads), _F32, dev),
-        None if workspace is None else workspace.data_ptr(), nbytes, _current_stream(dev))
+    rc = load().rq_paged_attention(
+        kv, R, heads, B, W, block_table.data_ptr(), None if requests is None else requests.data_ptr(),
+        positions.data_ptr(), window, scale, _TYPE[dtype], q.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes,
+        _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_attention", rc)
     return out, lse

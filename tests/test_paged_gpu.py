@@ -147,6 +147,16 @@ def test_plan_maps_at_any_address():
             assert got[0] == 77 and got[-1] == 77
 
 
+def test_plan_far_lengths():
+    """Lengths up to 2^31 - 1: tables that have wrapped many times."""
+    table = np.array([[3, 1, 2], [4, 0, 5]], np.int32)
+    ids = np.array([6, 7, -1, -1, -1, -1, -1, -1], np.int32)
+    for P in (1, 5, 16):
+        o = check_plan([4, 1], [2**31 - 5, 2**31 - 2], [0, 2, 0, 0], ids, table, P, 8, alias=False)
+        assert o["pool"][2] == 0 and o["pos"][3] == 2**31 - 2 and (o["slot"][2:5] >= 0).all()
+        assert check_plan([5, 1], [2**31 - 5, 0], [0, 2, 0, 0], ids, table, P, 8, alias=True)["pool"][2] == 1
+
+
 def test_plan_leaves_bad_blocks_out():
     """A table or ring that holds ids outside the pool gives slots of -1, not addresses."""
     table = np.array([[1000000, 2], [3, -7]], np.int32)
@@ -474,6 +484,31 @@ def test_attend_many_rows():
     """More rows than the grid has blocks, most of them short, some empty."""
     r = random.Random(3)
     run_attend([r.choice([0, 1, 3, 17, 40, 90]) for _ in range(700)], 2, 1, 32, BF16, BF16, 8, seed=8, pad=4)
+
+
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("P", [1, 5, 16])
+@pytest.mark.parametrize("rows", [1, 3, 200])
+def test_attend_far_positions(io, cache, P, rows):
+    """Positions up to 2^31 - 1 over a ring of blocks: nothing in between overflows."""
+    far = [2**31 - 1, 2**31 - 2, 2**31 - 17, 2**30 + 3]
+    run_attend([far[i % 4] + (1 if i % 4 else 0) for i in range(rows)], 4, 2, 64, io, cache, P, W=33 if P == 1 else 7,
+               seed=P)
+    run_attend([2**31 - 1 - i for i in range(rows)], 2, 2, 32, io, cache, P, W=70, window=50, seed=P)
+
+
+@pytest.mark.parametrize("cache", [F32, BF16])
+def test_attend_very_many_rows(cache):
+    """More rows than threads look at once: one live key each, so its value."""
+    R, hd = 70001, 32
+    k, v = (torch.randn(50, 4, 1, hd, device="cuda").to(cache) for _ in range(2))
+    table = torch.randint(0, 50, (R, 600), device="cuda", dtype=torch.int32)
+    pos = torch.randint(-1, 4, (R,), device="cuda", dtype=torch.int32)
+    q = torch.randn(R, 2 * hd, device="cuda")
+    out, lse = paged.paged_attention(q, k, v, table, pos, window=1, lse=True)
+    want = v[table[:, 0].long(), pos.clamp(min=0).long(), 0].float().repeat(1, 2)
+    assert torch.equal(out, torch.where(pos[:, None] >= 0, want, 0.0))
+    assert torch.equal(lse == -math.inf, (pos < 0)[:, None].expand(R, 2))
 
 
 def test_attend_one_key_is_its_value():
