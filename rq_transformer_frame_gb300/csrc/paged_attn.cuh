@@ -37,7 +37,6 @@ constexpr int kMaxGrid = 304;              // CTAs of a launch, at most
 constexpr int kMaxRuns = kMaxGrid * kWarps;
 constexpr int kMinRun = 1;                 // tiles of a run, at least
 constexpr int kUnitCost = 1;               // what a unit's start and end count, in tiles
-constexpr int kMaxHeads = 16;              // query heads of a unit, at most
 
 struct Params {
   rq_paged_kv kv;
@@ -46,7 +45,7 @@ struct Params {
   float* lse;
   const int32_t *table, *requests, *positions;
   int rows, heads, batch, W, window;
-  int G, GB, HG;       // query heads per K/V head (or pair), of a unit; units of a K/V head (or pair)
+  int G, GB, HG;       // query heads per K/V head (of all a unit reads), of a unit; units of a K/V head
   int runs;            // runs (warps) of the launch
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
   float scale;         // times log2 e
@@ -184,9 +183,9 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
 // a product come out of one instruction, in one thread (c0 + c2, c1 + c3). f32 queries and
 // their weights take a third part in a second instruction: 24 bits, every product exact.
 // bf16 queries are exact in one part; their weights have two.
-// The rows in shared memory may hold more than this head (PairCore): SHAPE is theirs, FIRST the
-// head's first 16-byte piece.
-template <typename QT, int HD, typename SHAPE = Shape<uint16_t, HD>, int FIRST = 0>
+// The rows in shared memory may hold more than this head (SideCore): SHAPE is theirs, a tile's
+// FIRST the head's first 16-byte piece.
+template <typename QT, int HD, typename SHAPE = Shape<uint16_t, HD>>
 struct MmaCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
   static constexpr int kHeads = 8;
@@ -224,6 +223,7 @@ struct MmaCore {
       }
   }
 
+  template <int FIRST = 0>
   __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
     const uint32_t vs = ks + K * S::kPitch;
     float c[NT][4] = {};
@@ -467,36 +467,40 @@ struct WideCore {
   }
 };
 
-// Two neighbouring K/V heads of 32 dimensions in bf16, up to 8 query heads each, as one unit: a
-// head's row is 64 bytes, half of what the memory hands over at a time, and by the time
+// N neighbouring K/V heads of 32 or 64 dimensions in bf16, up to 8 query heads each, as one unit
+// whose rows hold them all. A head of 32 dimensions alone is half of a line, and by the time
 // another warp wants the other half it has left the L2 (128 rows of 3000 positions, 8 heads:
-// 703 MB read for 393). Rows of both heads fill whole lines.
-template <typename QT>
-struct PairCore {
-  static constexpr int kHeads = 16;
-  static constexpr int kLoad = 64;
+// 703 MB read for 393; 256 rows 237 us, in twos 137, in fours 140 and with f32 queries 10 to
+// 25% longer); one of 64 is a line, but short pieces of a DRAM page cost more than their bytes
+// (256 rows of 3000 positions, 8 heads: 280 us, in twos 251).
+template <typename QT, int HD, int N>
+struct SideCore {
+  static constexpr int kHeads = 8 * N;
+  static constexpr int kLoad = N * HD;
   static constexpr int kScratch = 0;
-  using S = Shape<uint16_t, 64>;
-  MmaCore<QT, 32, S, 0> a;
-  MmaCore<QT, 32, S, 4> b;
+  using S = Shape<uint16_t, kLoad>;
+  MmaCore<QT, HD, S> core[N];
 
   __device__ __forceinline__ void clear() {
-    a.clear();
-    b.clear();
+#pragma unroll
+    for (int i = 0; i < N; ++i) core[i].clear();
   }
   __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
-    a.load(qrow, live / 2, lane, nullptr);
-    b.load(qrow + (size_t)(live / 2) * 32, live / 2, lane, nullptr);
+#pragma unroll
+    for (int i = 0; i < N; ++i) core[i].load(qrow + (size_t)i * (live / N) * HD, live / N, lane, nullptr);
   }
+  template <int I = 0>
   __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
-    a.tile(scale_log2, ks, mask, lane, nullptr);
-    b.tile(scale_log2, ks, mask, lane, nullptr);
+    core[I].template tile<I * HD / 8>(scale_log2, ks, mask, lane, nullptr);
+    if constexpr (I + 1 < N) tile<I + 1>(scale_log2, ks, mask, lane, nullptr);
   }
   template <bool PARTIAL, typename OT>
   __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
-    const int g = live / 2;
-    a.template end<PARTIAL>(out, lse, ml, g, lane);
-    b.template end<PARTIAL>(out + (size_t)g * 32, lse ? lse + g : nullptr, ml ? ml + g : nullptr, g, lane);
+    const int g = live / N;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      core[i].template end<PARTIAL>(out + (size_t)i * g * HD, lse ? lse + i * g : nullptr,
+                                    ml ? ml + i * g : nullptr, g, lane);
   }
 };
 
@@ -1117,9 +1121,9 @@ inline int sm_count() {
 
 // How a call is launched, from what the host knows: the shapes, and how long a row may be.
 struct Choice {
-  bool pair;               // units of two K/V heads (PairCore)
+  int side;                // K/V heads of a unit (SideCore), or 1
   int unit_heads;          // query heads of a unit, at most
-  int units_of_kv;         // units of a K/V head (or pair)
+  int units_of_kv;         // units of a K/V head (or of `side` of them)
   long long units, tiles;  // units of all rows, tiles of a unit, at most
   int split;               // CTAs of a unit in a split launch, or 0
   bool whole;              // runs of whole units
@@ -1153,22 +1157,30 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
   Choice x{};
   const int g = heads / kv.heads;
   const bool bf16 = kv.dtype == RQ_BF16;
-  x.pair = bf16 && kv.head_dim == 32 && kv.head_stride == 32 && kv.heads % 2 == 0 && g <= 8;
-  const int most = bf16 ? 16 : 8, wanted = x.pair ? 2 * g : g;
-  x.unit_heads = wanted < most ? wanted : most;
-  x.units_of_kv = (wanted + most - 1) / most;
-  int tile = 4096 / ((x.pair ? 64 : kv.head_dim) * (bf16 ? 2 : 4));
-  if (tile > 32) tile = 32;
+  const int most = bf16 ? 16 : 8;  // query heads of a unit
   long long keys = (long long)max_blocks * kv.block_size;
   if (keys > INT_MAX) keys = INT_MAX;
   if (window > 0 && window < keys) keys = window;
-  x.units = (long long)rows * (x.pair ? kv.heads / 2 : kv.heads) * x.units_of_kv;
+  const int row_bytes = kv.head_dim * (bf16 ? 2 : 4), tile = 4096 / row_bytes < 32 ? 4096 / row_bytes : 32;
+  x.side = 1;
+  x.unit_heads = g < most ? g : most;
+  x.units_of_kv = (g + most - 1) / most;
+  x.units = (long long)rows * kv.heads * x.units_of_kv;
   x.tiles = keys / tile + 2;
   x.split = split_ctas(x.units, x.tiles, rows, bf16, sm_count());
   // rows of at most eight whole tiles: no search and no join (182 rows of up to 192 positions,
   // head_dim 64, 12.9 us with them and 8.4 without; longer units would be uneven shares)
   x.whole = !x.split && x.tiles <= 10;
-  x.workspace = x.split || x.whole ? 0 : workspace_bytes(x.unit_heads, kv.head_dim);
+  x.workspace = 0;
+  if (x.split || x.whole) return x;
+  // runs that the memory bounds: two heads at a time where they lie side by side
+  if (bf16 && kv.head_dim < 128 && g <= 8 && kv.head_stride == kv.head_dim && kv.heads % 2 == 0) {
+    x.side = 2;
+    x.unit_heads = 2 * g;
+    x.units /= 2;
+    x.tiles = keys / (2048 / (2 * kv.head_dim)) + 2;
+  }
+  x.workspace = workspace_bytes(x.unit_heads, kv.head_dim);
   return x;
 }
 
@@ -1179,16 +1191,18 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   if (x.unit_heads > Core::kHeads) return cudaErrorInvalidValue;
   p.HG = x.units_of_kv;
   p.GB = x.unit_heads;
-  if (x.split) {
-    auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
-    constexpr size_t ring = (size_t)kSplitWarps *
-                            (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
-    constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
-    constexpr size_t smem = ring > sums ? ring : sums;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3((unsigned)x.split, (unsigned)x.units, 1), kSplitWarps * 32, smem, x.split,
-                            s, p);
+  if constexpr (Core::kLoad == HD) {  // units of one K/V head
+    if (x.split) {
+      auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
+      constexpr size_t ring = (size_t)kSplitWarps *
+                              (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
+      constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
+      constexpr size_t smem = ring > sums ? ring : sums;
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      return launch_dependent(kernel, dim3((unsigned)x.split, (unsigned)x.units, 1), kSplitWarps * 32, smem, x.split,
+                              s, p);
+    }
   }
   // as many CTAs as are resident at once, at most as many as the largest rows could fill
   auto* kernel = attend_kernel<QT, KT, HD, Core, false>;

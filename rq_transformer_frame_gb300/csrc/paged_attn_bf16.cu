@@ -1,4 +1,4 @@
-// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore, WideCore and PairCore).
+// paged_attn_bf16.cu -- paged attention over a bf16 cache (paged_attn.cuh, MmaCore, WideCore and SideCore).
 #include "paged_attn.cuh"
 
 namespace rqk {
@@ -6,19 +6,21 @@ namespace paged_attn {
 
 template <typename QT, int HD>
 static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
+  if constexpr (HD < 128)
+    if (x.side > 1) {
+      constexpr int N = 2;
+      Params side = p;
+      side.kv.heads /= N;
+      side.kv.head_stride *= N;
+      side.G *= N;
+      return launch<QT, uint16_t, HD, SideCore<QT, HD, N>>(side, x, s);
+    }
   return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>>(p, x, s)
                   : launch<QT, uint16_t, HD, WideCore<QT, HD>>(p, x, s);
 }
 
 template <typename QT>
 static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s) {
-  if (x.pair) {
-    Params pairs = p;
-    pairs.kv.heads /= 2;
-    pairs.kv.head_stride = 64;
-    pairs.G *= 2;
-    return launch<QT, uint16_t, 32, PairCore<QT>>(pairs, x, s);
-  }
   switch (p.kv.head_dim) {
     case 32: return by_heads<QT, 32>(p, x, s);
     case 64: return by_heads<QT, 64>(p, x, s);

@@ -451,14 +451,15 @@ def test_attend_short_rows(io, cache, hd):
     run_attend([0] * 300 + [3], 4, 2, hd, io, cache, 8, W=8, seed=hd)
 
 
-@pytest.mark.parametrize("heads,hk", [(4, 4), (16, 2), (14, 2), (34, 2), (3, 3), (2, 1)])
+@pytest.mark.parametrize("heads,hk", [(4, 4), (32, 4), (24, 8), (16, 2), (14, 2), (34, 2), (40, 4), (3, 3), (2, 1)])
 @pytest.mark.parametrize("io", [F32, BF16])
 @pytest.mark.parametrize("W", [None, CUT])
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])
-def test_attend_heads_of_32(heads, hk, io, W, layout):
-    """Heads of 32 dimensions: two neighbours as one unit, or where they do not lie side by side,
-    are odd in number or have many queries, one by one."""
-    run_attend([0, 1, 40, 77, 130, 300], heads, hk, 32, io, BF16, 16, W=W, layout=layout, poison=layout == "nhd",
+@pytest.mark.parametrize("hd", [32, 64])
+def test_attend_heads_side_by_side(heads, hk, io, W, layout, hd):
+    """Heads of 32 and 64 dimensions: two neighbours as one unit, or where they do not lie side by
+    side, are odd in number or have many queries, one by one."""
+    run_attend([0, 1, 40, 77, 130, 300], heads, hk, hd, io, BF16, 16, W=W, layout=layout, poison=layout == "nhd",
                seed=heads)
 
 
