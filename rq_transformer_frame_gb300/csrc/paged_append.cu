@@ -13,7 +13,8 @@
 // row's angles are computed once and shared. HD / 8 lanes share a head; a lane holds two pieces
 // of four dimensions such that both dimensions of each of its pairs are its own: 8
 // consecutive ones, or with the halves pairing 4 j and rope_dim / 2 + 4 j, so no value changes
-// lanes. Every warp's loads are issued at once, before the position is known.
+// lanes. The loads of a few steps (a step is a head for each HD / 8 lanes) are always in flight,
+// the first of them before the position is known.
 #include <cmath>
 
 #include "paged.cuh"
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kMaxWarps = 4;  // of a CTA
 constexpr int kMaxPairs = 64;
-// steps of a warp whose loads are in flight, always
+// steps of a warp whose loads are in flight: 16 registers of bf16, 24 of f32
 template <typename IT>
 constexpr int kAheadOf = sizeof(IT) == 2 ? 4 : 3;
 

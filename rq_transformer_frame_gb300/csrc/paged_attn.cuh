@@ -6,7 +6,7 @@
 // j, o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), in one pass with m the running maximum and
 // the sums rescaled when it moves (all in base 2: scale carries log2 e).
 //
-// Work. A unit is one (row, K/V head, group of query heads that read it), a tile 2 KB of K
+// Work. A unit is one (row, K/V head, group of query heads that read it), a tile 4 KB of K
 // (and as much V) of a unit: 16 positions at head_dim 128 in bf16. All units' tiles form one
 // list, rows outermost, in which a unit also counts kUnitCost tiles for its start and end; the
 // resident warps cut it into equal runs, one each, whatever the rows' lengths are. Warps work

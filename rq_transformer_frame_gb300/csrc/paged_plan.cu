@@ -10,12 +10,13 @@
 //
 // One CTA does the sums and whatever is written from them; many tokens are a second kernel's,
 // which finds everything it needs in the first one's outputs (a CTA of 1024 threads writes
-// 262144 tokens in 209 us, the two kernels take 8.2 us). What may alias needs no order of
-// its own: taken entries of the ring are read at
-// [head, head + taken) and given ones written at [head + count, head + count + given), apart
-// because count + given <= N; table columns are written from pages(c_b) on and read below.
-// Only the lengths and the pool's words are read by all and written by some: those writes
-// follow a barrier.
+// 262144 tokens in 209 us, the two kernels take 8.2 us).
+//
+// What may alias needs no order of its own: taken entries of the ring are read at [head,
+// head + taken) and given ones written at [head + count, head + count + given), apart because
+// count + given <= N; table columns are written from pages(c_b) on and read below. Only the
+// lengths and the pool's words are read by all and written by some: those writes follow a
+// barrier.
 #include "paged.cuh"
 
 namespace rqk {
@@ -54,6 +55,12 @@ __device__ __forceinline__ Sums shfl(const Sums& a, int l) {
 __device__ __forceinline__ int pages_of(int c, const PlanParams& p) {
   const int n = c / p.P + (c % p.P != 0);
   return n < p.W ? n : p.W;
+}
+
+// entry i behind entry `from` of the ring of N, both in [0, N] (from < N)
+__device__ __forceinline__ int ring_at(int N, int from, int i) {
+  const unsigned x = (unsigned)from + (unsigned)i;
+  return (int)(x >= (unsigned)N ? x - (unsigned)N : x);
 }
 
 // the last b with first[b] <= x, first[0] = 0
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   }
   if (tid == 0) {
     p.cu[p.B] = T;
-    p.pool_out[0] = status ? head : (int)(((long long)head + taken) % p.N);
+    p.pool_out[0] = status ? head : ring_at(p.N, head, taken);
     p.pool_out[1] = count - taken + given;
     p.pool_out[2] = status;
     p.pool_out[3] = (int)(run.need < INT_MAX ? run.need : INT_MAX);
@@ -204,11 +211,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   for (int x = tid; x < taken; x += nt) {
     const int b = last_at_most(s_take, p.B, x);
     p.table[(size_t)b * p.W + pages_of(s_held[b], p) + (x - s_take[b])] =
-        p.free_ids[((long long)head + x) % p.N];
+        p.free_ids[ring_at(p.N, head, x)];
   }
+  const int tail = given ? ring_at(p.N, head, count) : 0;
   for (int x = tid; x < given; x += nt) {
     const int b = last_at_most(s_give, p.B, x);
-    p.free_ids[((long long)head + count + x) % p.N] = p.table[(size_t)b * p.W + (x - s_give[b])];
+    p.free_ids[ring_at(p.N, tail, x)] = p.table[(size_t)b * p.W + (x - s_give[b])];
   }
   if (p.M > kPlanTokens) return;  // the token kernel's
   const bool wide = wide_maps(p);
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
                  const int before = pages_of(len, p);
                  return col < before
                             ? p.table[(size_t)b * p.W + col]
-                            : p.free_ids[((long long)head + s_take[b] + (col - before)) % p.N];
+                            : p.free_ids[ring_at(p.N, head, s_take[b] + (col - before))];
                });
 }
 
@@ -276,7 +284,7 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)((4 * kPlanMaxBatch + 1) * sizeof(int))) != cudaSuccess)
     return RQ_ERR_CUDA;
-  // few requests and tokens: fewer warps to wait for one another (64 tokens take 5.6 us; with 1024 threads 5.5)
+  // few requests and tokens: fewer warps to wait for one another (64 tokens: 5.6 us, with 1024 threads 6.4)
   const int threads = batch <= 256 && max_tokens <= 1024 ? 256 : kPlanThreads;
   if (launch_dependent(plan_kernel, dim3(1), threads, smem, 0, s, p) != cudaSuccess) return RQ_ERR_CUDA;
   if (max_tokens <= kPlanTokens) return RQ_OK;
