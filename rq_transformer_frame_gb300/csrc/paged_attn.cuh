@@ -1135,8 +1135,9 @@ struct Choice {
 // split at 16 / 1000 / 4000 / 16000 positions against 9.4 / 16.0 / 16.2 / 23 us in runs, and
 // 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
 // of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
-// several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 32 (f32,
-// whose tiles take longer: 8), or up to 128 where the clusters fill three quarters of the card
+// several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 24, half
+// more than where the two meet, as a row is seldom as long as its table allows (f32, whose tiles
+// take longer: 8), or up to 128 where the clusters fill three quarters of the card
 // (32 K/V heads: 5.5 / 7.9 / 19 / 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768 positions
 // against 8.5 / 13 / 23 / 53 / 92).
 inline int split_ctas(long long units, long long tiles, int rows, bool bf16, int sms) {
@@ -1150,7 +1151,7 @@ inline int split_ctas(long long units, long long tiles, int rows, bool bf16, int
   while (c > 1 && (long long)c * kSplitWarps > tiles * 2) c /= 2;
   const long long most = tiles / (c * kSplitWarps);  // tiles of a warp, at most
   const bool full = 4 * units * c >= 3 * sms;        // the clusters fill the card
-  return most <= (rows > 1 ? 8 : full ? 128 : bf16 ? 32 : 8) ? c : 0;
+  return most <= (rows > 1 ? 8 : full ? 128 : bf16 ? 24 : 8) ? c : 0;
 }
 
 inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int window) {
