@@ -1136,10 +1136,11 @@ struct Choice {
 // 136 against 92 us at 131071; 16 rows of 1000 positions 15.4 against 21.2 us. But 16 rows
 // of 1 to 16000 take 132 against 46 us: a split launch lasts as long as its longest unit. So
 // several rows are split up to 8 tiles a warp (1024 positions of one CTA), one row up to 24, half
-// more than where the two meet, as a row is seldom as long as its table allows (f32, whose tiles
-// take longer: 8), or up to 128 where the clusters fill three quarters of the card
-// (32 K/V heads: 5.5 / 7.9 / 19 / 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768 positions
-// against 8.5 / 13 / 23 / 53 / 92).
+// more than where the two meet, as a row is seldom as long as its table allows (3 K/V heads whose
+// table allows 25000 positions: 8.6 us split and 12.3 in runs at 3000, 31.1 and 20.9 at 24951;
+// f32, whose tiles take longer: 8), or up to 128 where the clusters fill three quarters of the
+// card (32 K/V heads: 5.5 / 7.9 / 19 / 53 / 99 us at 16 / 1000 / 4000 / 16000 / 32768
+// positions against 8.5 / 13 / 23 / 53 / 92).
 inline int split_ctas(long long units, long long tiles, int rows, bool bf16, int sms) {
   if (units > sms) return 0;
   int c = 1;
