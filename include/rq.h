@@ -405,8 +405,10 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
 /* Attention of one query token per row over its request's blocks: for each query head,
  * softmax(scale * q . k_j) weighted sum of v_j over the row's live positions j; query head
  * i reads K/V head i / (heads / kv->heads).
- *   rows        R (0: nothing is enqueued); several rows may be of one request (prompt
- *               tokens, after all of them have been appended to a table that does not wrap)
+ *   rows        R (0: nothing is enqueued).  Several rows may be of one request, as a prompt's
+ *               tokens are once all of them have been appended; a table that is a ring must
+ *               then be wide enough that the last of the n tokens took over no page that the
+ *               first one reads: (max_blocks - 1) * block_size + 1 >= window + n - 1
  *   heads       a multiple of kv->heads
  *   batch, max_blocks, block_table  as rq_paged_plan
  *   requests    device [R] int32 or NULL (row r is request r; R <= batch).  A row whose

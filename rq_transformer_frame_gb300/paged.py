@@ -197,7 +197,8 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     """rq_paged_attention: q [R][heads * head_dim] f32 or bf16, block_table [B][max_blocks],
     positions [R] (-1: an empty request), requests [R] (-1: padding, its output left as it
     was; None: row r is request r), all int32 -> (out [R][heads * head_dim], lse [R][heads]
-    f32, None unless a tensor or True is passed for it)."""
+    f32, None unless a tensor or True is passed for it).  workspace: what
+    paged_attention_workspace gives for these shapes (allocated here if None)."""
     kv, hk, hd, dev = _cache(k, v)
     if stream is not None or _current_device() != dev:
         with _on(k.device, stream):
@@ -284,7 +285,9 @@ class PagedCache:
                             self.maps.slots[:T], **kw)
 
     def attend(self, layer, q, **kw):
-        """Each of the step's tokens over its own request, q [T][heads * head_dim]."""
+        """Each of the step's tokens over its own request, q [T][heads * head_dim].  With n new
+        tokens of a request in the step and a table that is a ring, the window has to leave
+        them room: (max_blocks - 1) * block_size + 1 >= window + n - 1."""
         T = q.shape[0]
         return paged_attention(q, self.k[layer], self.v[layer], self.block_table,
                                self.maps.positions[:T], requests=self.maps.requests[:T], **kw)

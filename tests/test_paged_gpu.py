@@ -684,6 +684,31 @@ def test_no_rows():
     assert out.shape == (0, 128) and lse.shape == (0, 2)
 
 
+def test_prompt_rows_over_a_ring():
+    """A prompt longer than the ring, in steps of n tokens: with window + n - 1 positions held,
+    every token of a step finds its whole window."""
+    g = torch.Generator().manual_seed(31)
+    P, W, window, n, hd, heads = 4, 7, 18, 8, 32, 2
+    assert (W - 1) * P + 1 >= window + n - 1
+    c = paged.PagedCache(1, W, P, W, n, 1, hd, dtype=F32)
+    keys, values = [], []
+    for step in range(9):
+        c.plan(ints([n]))
+        qkv = torch.randn(n, (heads + 2) * hd, generator=g)
+        q = c.append(0, qkv.cuda(), rope_dim=0)
+        out, _ = c.attend(0, q, window=window)
+        keys += list(qkv[:, heads * hd:(heads + 1) * hd].double())
+        values += list(qkv[:, (heads + 1) * hd:].double())
+        for i in range(n):
+            p = step * n + i
+            k, v = (torch.stack(x[max(0, p - window + 1):p + 1]) for x in (keys, values))
+            for h in range(heads):
+                w = torch.softmax(k @ qkv[i, h * hd:(h + 1) * hd].double() / math.sqrt(hd), 0) @ v
+                got = out[i, h * hd:(h + 1) * hd].double().cpu()
+                assert (got - w).abs().max() <= 64 * U * 32, (step, i)
+    assert c.status() == (0, 0)
+
+
 # ---------------------------------------------------------------- all of them, as they are used
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("io,cache,heads,hk,hd,P,W,window", [
