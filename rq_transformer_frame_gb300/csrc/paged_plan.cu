@@ -25,6 +25,7 @@ namespace {
 constexpr int kPlanMaxBatch = 8192;  // four prefix arrays of this length fit shared memory
 constexpr int kPlanMaxTokens = 1 << 30;  // token numbers and a thread's four stay in 32 bits
 constexpr int kPlanThreads = 1024, kTokenThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens that the first kernel maps itself
 
 struct PlanParams {
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int* const s_take = s_cu + p.B + 1;    // [B] first taken block
   int* const s_give = s_take + p.B;      // [B] first block given back
   int* const s_held = s_give + p.B;      // [B] length before
-  __shared__ Sums s_warp[32];
+  __shared__ Sums s_warp[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   pdl_wait();
   pdl_trigger();
@@ -280,7 +281,8 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
                cu_tokens,   requests,   positions,  slots};
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const size_t smem = ((size_t)4 * batch + 1) * sizeof(int);
-  if (smem > 48 * 1024 &&
+  // a block has 48 KB unasked, for these sums and what the kernel declares itself (its warps' sums)
+  if (smem + kPlanWarps * sizeof(Sums) > 48 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)((4 * kPlanMaxBatch + 1) * sizeof(int))) != cudaSuccess)
     return RQ_ERR_CUDA;

@@ -12,7 +12,10 @@ Tolerances, with u = 2^-24 (half an f32 step) and e = half a step of the output'
   by 2 ds, their sums over n keys by 4 sqrt(n) + 16 u, and bf16 queries' weights keep 16 bits
   (2^-17): each times sum p |v|. The store adds e |o|."""
 import math
+import os
 import random
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -789,3 +792,18 @@ def test_decode_steps(captured, io, cache, heads, hk, hd, P, W, window):
                     err = (got[l, i, h * hd:(h + 1) * hd].double() - o).abs()
                     assert (err <= tol).all(), (t, b, p, l, h, float((err / tol).max()))
                     assert abs(float(lse[l, i, h]) - float(torch.logsumexp(s, 0))) <= e * S + 1e-5
+
+
+# ---------------------------------------------------------------- edges of the calls
+def test_plan_batches_around_48_kb():
+    """Batches whose sums take more shared memory than a block has without asking, in a process
+    that has planned no larger one before."""
+    code = ("import sys; sys.path[:0] = %r\n"
+            "import numpy as np, test_paged_gpu as t\n"
+            "for B in (3023, 3024, 3050, 3071, 3072):\n"
+            "    t.check_plan([1] * B, [0] * B, [0, B, 0, 0], np.arange(B, dtype=np.int32),\n"
+            "                 np.full((B, 1), -1, np.int32), 16, B, True)\n"
+            % [os.path.dirname(os.path.dirname(os.path.abspath(paged.__file__))),
+               os.path.dirname(os.path.abspath(paged_ref.__file__))])
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
