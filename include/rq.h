@@ -335,7 +335,8 @@ enum {
 /* The pool's free blocks: device pool [4] int32 {head, count, status, taken} and device
  * free_ids [n_blocks] int32, a ring in which free_ids[(head + i) % n_blocks], i < count,
  * are the free blocks, taken from the head and returned behind the tail.
- * rq_paged_pool_init makes every block free: {0, n_blocks, 0, 0} and ids 0 .. n_blocks-1. */
+ * rq_paged_pool_init makes every block free: {0, n_blocks, 0, 0} and ids 0 .. n_blocks-1.
+ * n_blocks <= 2^30 here and in rq_paged_plan (RQ_ERR_UNSUPPORTED above). */
 rq_status rq_paged_pool_init(int32_t n_blocks, int32_t *pool, int32_t *free_ids,
                              void *cuda_stream);
 

@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kPlanMaxBatch = 8192;  // four prefix arrays of this length fit shared memory
 constexpr int kPlanMaxTokens = 1 << 30;  // token numbers and a thread's four stay in 32 bits
+constexpr int kPlanMaxBlocks = 1 << 30;  // and so do ring entries and a thread's next one
 constexpr int kPlanThreads = 1024, kTokenThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanTokens = 4 * kPlanThreads;  // tokens that the first kernel maps itself
@@ -257,7 +258,8 @@ __global__ void pool_init_kernel(int n, int32_t* pool, int32_t* free_ids) {
 extern "C" rq_status rq_paged_pool_init(int32_t n_blocks, int32_t* pool, int32_t* free_ids,
                                         void* cuda_stream) {
   if (n_blocks < 1 || !pool || !free_ids) return RQ_ERR_ARG;
-  const unsigned grid = (unsigned)(((long long)n_blocks + 4 + 255) / 256);
+  if (n_blocks > rqk::kPlanMaxBlocks) return RQ_ERR_UNSUPPORTED;
+  const unsigned grid = ((unsigned)n_blocks + 4 + 255) / 256;
   rqk::pool_init_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(n_blocks, pool,
                                                                                   free_ids);
   return cudaGetLastError() == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
@@ -272,7 +274,8 @@ extern "C" rq_status rq_paged_plan(int32_t batch, int32_t max_blocks, int32_t bl
   using namespace rqk;
   if (batch < 1 || max_blocks < 1 || block_size < 1 || n_blocks < 1 || max_tokens < 1)
     return RQ_ERR_ARG;
-  if (batch > kPlanMaxBatch || max_tokens > kPlanMaxTokens) return RQ_ERR_UNSUPPORTED;
+  if (batch > kPlanMaxBatch || max_tokens > kPlanMaxTokens || n_blocks > kPlanMaxBlocks)
+    return RQ_ERR_UNSUPPORTED;
   if (!new_lens || !lens || !pool || !free_ids || !block_table || !lens_out || !pool_out ||
       !cu_tokens || !requests || !positions || !slots)
     return RQ_ERR_ARG;

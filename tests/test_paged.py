@@ -173,3 +173,10 @@ def test_plain_plan_keeps_the_ledger(seed):
         assert sorted(held + free) == list(range(N))
         slots = o["slot"][o["slot"] >= 0]
         assert len(set(slots.tolist())) == len(slots)
+
+
+@pytest.mark.parametrize("n", [2**30 + 1, 2**31 - 300, 2**31 - 1])
+def test_pools_past_32_bit_counting_are_refused(lib, n):
+    """A thread's next ring entry, up to 1024 past the last, has to stay below 2^31."""
+    assert lib.rq_paged_pool_init(n, A, B_, None) == binding.RQ_ERR_UNSUPPORTED
+    assert _plan(lib, N=n) == binding.RQ_ERR_UNSUPPORTED
