@@ -175,6 +175,25 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
   hi -= bf16hi(u);
   return u;
 }
+// A pair of weights' leading bf16 parts, and in lo and hi what is left, both above 0 where the weight is:
+// cut just below the weight instead of rounded to nearest. An infinite value times any part of a
+// weight then has its own sign; times 0 or a negative part it would make the sum NaN. Three such
+// parts are a weight's 24 bits exactly: the first leaves at most 2^-7 of it, 17 bits, the second
+// 8 of them or a power of two.
+__device__ __forceinline__ uint32_t cut_bf16(float& lo, float& hi) {
+  const uint32_t a = (uint32_t)__viaddmax_s32(__float_as_int(lo), -1, 0);
+  const uint32_t b = (uint32_t)__viaddmax_s32(__float_as_int(hi), -1, 0);
+  lo -= __uint_as_float(a & 0xffff0000u);
+  hi -= __uint_as_float(b & 0xffff0000u);
+  return __byte_perm(a, b, 0x7632);
+}
+constexpr uint32_t kTiny = 0x00010001u;  // a pair of bf16's smallest number above 0
+// x within the finite numbers: infinities and NaN become the largest one, of either sign
+__device__ __forceinline__ float finite(float x) {
+  float y;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(3.4028234663852886e38f));
+  return y;
+}
 
 // A warp's unit over a bf16 cache. Decode is bound by reading the cache: the tensor cores
 // (mma.sync m16n8k16; a unit has at most 16 query rows, far below a tcgen05 tile) are there so
@@ -182,7 +201,9 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
 // 0-7 a value's leading bf16 part, rows 8-15 the part that rounding left, so both halves of
 // a product come out of one instruction, in one thread (c0 + c2, c1 + c3). f32 queries and
 // their weights take a third part in a second instruction: 24 bits, every product exact.
-// bf16 queries are exact in one part; their weights have two.
+// bf16 queries are exact in one part; their weights have two. The weights of f32 queries are cut
+// into parts that are all above 0 (cut_bf16): rounded to nearest, with infinite values guarded as
+// those of bf16 queries are, 64 rows of 3000 positions took 551 us against 480.
 // The rows in shared memory may hold more than this head (SideCore): SHAPE is theirs, a tile's
 // FIRST the head's first 16-byte piece.
 template <typename QT, int HD, typename SHAPE = Shape<uint16_t, HD>>
@@ -195,12 +216,12 @@ struct MmaCore {
   using S = SHAPE;
   static constexpr int K = S::kKeys, NT = K / 8;  // keys of a tile, in eights
   uint32_t q[kF32 ? 3 : 1][kSteps][2];
-  float acc[HD / 8][2];
+  f32x2 acc[HD / 8];
   float m, l;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < HD / 8; ++i) acc[i][0] = acc[i][1] = 0.f;
+    for (int i = 0; i < HD / 8; ++i) acc[i] = pack2(0.f, 0.f);
     m = neg_inf();
     l = 0.f;
   }
@@ -279,16 +300,18 @@ struct MmaCore {
       for (int i = 0; i < 2; ++i) {
         float x = ex2(c[2 * j + i][0] - ref), y = ex2(c[2 * j + i][1] - ref);
         l += x + y;
-        a[j][2 * i] = split_bf16(x, y);
         if constexpr (kF32) {
-          a[j][2 * i + 1] = split_bf16(x, y);
+          a[j][2 * i] = cut_bf16(x, y);
+          a[j][2 * i + 1] = cut_bf16(x, y);
           e[j][i] = pack_bf16(x, y);
         } else {
+          a[j][2 * i] = split_bf16(x, y);
           a[j][2 * i + 1] = pack_bf16(x, y);
         }
       }
     // B of the second product: V rows transposed on the way in
     const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vpiece = lane >> 4;
+    const f32x2 scale2 = pack2(scale, scale);
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) {
       float o[2][4] = {};
@@ -299,13 +322,17 @@ struct MmaCore {
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           mma16816(o[n], a[j][0], a[j][1], a[j][2], a[j][3], b[2 * n], b[2 * n + 1]);
-          if constexpr (kF32) mma16816(o[n], e[j][0], 0u, e[j][1], 0u, b[2 * n], b[2 * n + 1]);
+          // the rows beside the third parts: 2^-133, of whose products nothing comes but an infinite
+          // value's own sign (with zeros there NaN); 2^-126 of a value is what ex2 may drop anyway
+          if constexpr (kF32) mma16816(o[n], e[j][0], kTiny, e[j][1], kTiny, b[2 * n], b[2 * n + 1]);
         }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        acc[2 * d + n][0] = fmaf(acc[2 * d + n][0], scale, o[n][0] + o[n][2]);
-        acc[2 * d + n][1] = fmaf(acc[2 * d + n][1], scale, o[n][1] + o[n][3]);
+        // of two parts rounded to nearest (16 bits and a sign) the second may be 0 or negative: where
+        // a value is infinite its product with the first one stands
+        const f32x2 rest = kF32 ? pack2(o[n][2], o[n][3]) : pack2(finite(o[n][2]), finite(o[n][3]));
+        acc[2 * d + n] = fma2(acc[2 * d + n], scale2, add2(pack2(o[n][0], o[n][1]), rest));
       }
     }
   }
@@ -319,8 +346,10 @@ struct MmaCore {
     if (g >= live) return;
     const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
 #pragma unroll
-    for (int i = 0; i < HD / 8; ++i)
-      put2(out + (size_t)g * HD + i * 8 + c, acc[i][0] * inv, acc[i][1] * inv);
+    for (int i = 0; i < HD / 8; ++i) {
+      const float2 x = unpack2(acc[i]);
+      put2(out + (size_t)g * HD + i * 8 + c, x.x * inv, x.y * inv);
+    }
     if ((lane & 3) != 0) return;
     if (PARTIAL) ml[g] = make_float2(m, t);
     else if (lse) lse[g] = log_sum(m, t);
@@ -328,7 +357,10 @@ struct MmaCore {
 };
 
 // The same with 9 to 16 heads of a K/V head: the 16 rows of A are one head each, and each part
-// of a value is an instruction of its own. One pass over the cache instead of two.
+// of a value is an instruction of its own, into the same sums. One pass over the cache instead of
+// two. All weights are in parts above 0, so two parts (bf16 queries) are within 2^-16 of them; rounded
+// to nearest, 2^-17, the second part wants sums of its own against infinite values (512 rows of 3000
+// positions, 16 heads of 128: 145 us against 139; outputs are rounded to 2^-9).
 template <typename QT, int HD>
 struct WideCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
@@ -423,7 +455,8 @@ struct WideCore {
         float y = ex2(c[2 * j + (i >> 1)][2 * h + 1] - ref[h]);
         l[h] += x + y;
 #pragma unroll
-        for (int w = 0; w < WP; ++w) a[w][j][i] = split_bf16(x, y);
+        for (int w = 0; w < WP - 1; ++w) a[w][j][i] = cut_bf16(x, y);
+        a[WP - 1][j][i] = pack_bf16(x, y);
       }
     const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vpiece = lane >> 4;
 #pragma unroll

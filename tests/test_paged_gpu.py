@@ -807,3 +807,38 @@ def test_plan_batches_around_48_kb():
                os.path.dirname(os.path.abspath(paged_ref.__file__))])
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("heads,hk", [(2, 1), (16, 1), (4, 2)])
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("W", [None, CUT])
+def test_attend_infinite_values(heads, hk, io, cache, hd, W):
+    """A live value of +-inf gives +-inf in its dimension, both of them or a NaN give NaN, and
+    every other element is as without them."""
+    g = torch.Generator().manual_seed(hd + heads)
+    P, lens = 16, [1, 40, 300]
+    pages = [-(-n // P) for n in lens]
+    N = sum(pages)
+    k, v = make_cache(N, P, hk, hd, cache, g)
+    table, at = torch.full((3, W or max(pages)), -1, dtype=torch.int32), 0
+    for b, n in enumerate(pages):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+        for d, j, x in ((0, 0, math.inf), (5, lens[b] - 1, -math.inf), (hd - 1, lens[b] // 2, math.inf),
+                        (9, 0, math.inf), (9, lens[b] - 1, -math.inf), (18, lens[b] // 3, math.nan)):
+            v[int(table[b, j // P]), j % P, :, d] = x
+    q = torch.randn(3, heads * hd, generator=g).to(io)
+    out, lse = paged.paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ints([n - 1 for n in lens]), lse=True)
+    e = half_step(io)
+    for r, n in enumerate(lens):
+        w = paged_ref.attend_row(q[r].double().view(heads, hd), k, v, table[r].tolist(), n - 1, 0, hd ** -0.5)
+        got, want = out[r].double().cpu().view(heads, hd), w["out"]
+        odd = ~torch.isfinite(want)
+        assert odd.any() and torch.equal(odd, ~torch.isfinite(got)), r
+        np.testing.assert_array_equal(got[odd].numpy(), want[odd].numpy())
+        ds = U * (8 * math.sqrt(hd) * w["norm"] + 8 * w["smax"])
+        sums = U * (4 * math.sqrt(n) + 16)
+        tol = (2 * ds + sums + (2.0 ** -17 if io == BF16 else 0.0)) * w["mass"] * (1 + e) + e * want.abs() + 1e-30
+        assert ((got - want).abs() <= tol)[~odd].all(), r
+        assert ((lse[r].double().cpu() - w["lse"]).abs() <= ds + sums + 4 * U * w["lse"].abs()).all()
