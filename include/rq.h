@@ -429,7 +429,8 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
  *               arguments it is asked with and on the current device)
  * A row with no live position gives output 0 and lse -inf.  What lies in the cache outside
  * the live positions is never used, NaN or not; an infinite or NaN value at a live one
- * reaches its own dimension of the output only, as in the formula.  Scores, softmax and sums are f32; with
+ * reaches its own dimension of the output only, as in the formula.  Scores, softmax and sums are f32 (the
+ * number of live positions times the largest |value| has to stay in f32's range); with
  * f32 queries every product over a bf16 cache is exact (queries and weights enter as three
  * bf16 parts), with bf16 queries the weights keep 16 significant bits. */
 size_t rq_paged_attention_workspace_size(const rq_paged_kv *kv, int32_t rows, int32_t heads,

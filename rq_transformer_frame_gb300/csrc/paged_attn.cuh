@@ -50,6 +50,7 @@ struct Params {
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
+  float unit;          // what the sums of values are in (a core's kUnit)
   float2* part_ml;     // [runs][2][GB] (m, l)
   int4* cut;           // [runs] (row, first head, heads, parts) of the unit that starts there and goes on
 };
@@ -210,6 +211,7 @@ template <typename QT, int HD, typename SHAPE = Shape<uint16_t, HD>>
 struct MmaCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
   static constexpr int kHeads = 8;
+  static constexpr float kUnit = 1.f;  // what the sums of values are in
   static constexpr int kLoad = HD;    // dimensions of a row in the ring
   static constexpr int kScratch = 0;  // bytes of shared memory of a warp
   static constexpr int kSteps = HD / 16;
@@ -365,6 +367,7 @@ template <typename QT, int HD>
 struct WideCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
   static constexpr int kHeads = 16;
+  static constexpr float kUnit = 1.f;
   static constexpr int kLoad = HD;
   static constexpr int kSteps = HD / 16, QP = kF32 ? 3 : 1, WP = kF32 ? 3 : 2;  // parts
   static constexpr int kScratch = 0;
@@ -509,6 +512,7 @@ struct WideCore {
 template <typename QT, int HD, int N>
 struct SideCore {
   static constexpr int kHeads = 8 * N;
+  static constexpr float kUnit = 1.f;
   static constexpr int kLoad = N * HD;
   static constexpr int kScratch = 0;
   using S = Shape<uint16_t, kLoad>;
@@ -548,8 +552,10 @@ __device__ __forceinline__ void lds2(uint32_t addr, f32x2& a, f32x2& b) {
 // the sums a lane takes 4 dimensions and 8 of the keys, the weights through shared memory,
 // each stored twice (a packed pair).
 //
-// The reference that weights are taken against moves only when a score passes it by more
-// than 2^kSlack: sums keep 2^kSlack of headroom instead of finding each tile's maximum.
+// The reference that weights are taken against moves only when a score passes it by more than kSlack,
+// instead of by finding each tile's maximum. A weight may be up to 2^kSlack then; it enters the sums
+// of values divided by that (exactly), so they stay in range wherever a softmax's own would, and
+// what is written is multiplied by it again.
 template <typename QT, int HD, int GP>
 struct FmaCore {
   static constexpr int kHeads = GP;
@@ -561,7 +567,7 @@ struct FmaCore {
   static constexpr int kQPitch = 32 + 4;          // floats of a query slice: apart in banks
   static constexpr int kWPitch = 8 * GP * 2 + 4;  // floats of a key slice's weights
   static constexpr int kScratch = (GP * SL * kQPitch + KS * kWPitch) * 4;  // bytes of a warp
-  static constexpr float kSlack = 10.f;
+  static constexpr float kSlack = 10.f, kUnit = 1024.f;  // 2^kSlack
   f32x2 acc[GP][2];
   float m[GP], l[GP];
 
@@ -638,7 +644,7 @@ struct FmaCore {
       for (int h = 0; h < GP; ++h) {
         const float w = ex2(s[h] - finite_or_zero(m[h]));
         l[h] += w;
-        *reinterpret_cast<float2*>(sw + (key / 8) * kWPitch + ((key % 8) * GP + h) * 2) = make_float2(w, w);
+        *reinterpret_cast<float2*>(sw + (key / 8) * kWPitch + ((key % 8) * GP + h) * 2) = make_float2(w * (1.f / kUnit), w * (1.f / kUnit));
       }
     }
     __syncwarp();
@@ -680,7 +686,7 @@ struct FmaCore {
         b.y += __shfl_xor_sync(0xffffffffu, b.y, o);
       }
       if (h >= live) continue;
-      const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
+      const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : kUnit / t;
       if (lane < HD / 4) {
         put2(out + (size_t)h * HD + lane * 4, a.x * inv, a.y * inv);
         put2(out + (size_t)h * HD + lane * 4 + 2, b.x * inv, b.y * inv);
@@ -1000,7 +1006,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         s_cta[i] = a;
         if (i % HD == 0) s_cta_ml[g] = make_float2(m, l);
       } else {
-        put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l);
+        put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
         if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
       }
     }
@@ -1018,7 +1024,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         l += tc::ld_cluster(tc::mapa(mls + g * 8 + 4, c)) * f;
         a = fmaf(tc::ld_cluster(tc::mapa(sums + i * 4, c)), f, a);
       }
-      put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l);
+      put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
       if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
     }
     tc::cluster_sync();  // no CTA leaves while another reads its sums
@@ -1089,7 +1095,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_c
   pdl_trigger();
   auto write = [&](const int4& cut, float m, float l, const float (&a)[E]) {
     const size_t head = (size_t)cut.x * p.heads + cut.y + g;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : p.unit / l;
 #pragma unroll
     for (int e = 0; e < E; ++e) put(static_cast<QT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
     if (p.lse && lane == 0) p.lse[head] = log_sum(m, l);
@@ -1226,6 +1232,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   if (x.unit_heads > Core::kHeads) return cudaErrorInvalidValue;
   p.HG = x.units_of_kv;
   p.GB = x.unit_heads;
+  p.unit = Core::kUnit;
   if constexpr (Core::kLoad == HD) {  // units of one K/V head
     if (x.split) {
       auto* kernel = attend_kernel<QT, KT, HD, Core, true>;

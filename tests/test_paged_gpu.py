@@ -842,3 +842,24 @@ def test_attend_infinite_values(heads, hk, io, cache, hd, W):
         tol = (2 * ds + sums + (2.0 ** -17 if io == BF16 else 0.0)) * w["mass"] * (1 + e) + e * want.abs() + 1e-30
         assert ((got - want).abs() <= tol)[~odd].all(), r
         assert ((lse[r].double().cpu() - w["lse"]).abs() <= ds + sums + 4 * U * w["lse"].abs()).all()
+
+
+@pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("hk,W", [(1, None), (4, CUT)])
+def test_attend_large_values(io, cache, hd, hk, W):
+    """Values near the top of f32's range, and one key late in the row whose weight is 2^9.9 times
+    the others': what is summed stays in range where the result does."""
+    g = torch.Generator().manual_seed(hd)
+    P, heads, n, R = 16, 2 * hk, 300, 100
+    N = -(-n // P)
+    k = torch.zeros(N, P, hk, hd)
+    k[-1, (n - 1) % P, :, 0] = 6.875  # 9.92 in base 2; every other key scores 0
+    v = 5e35 * (0.7 + 0.3 * torch.rand(N, P, hk, hd, generator=g))
+    k, v = k.to(cache), v.to(cache)
+    q = torch.zeros(R, heads * hd).to(io)
+    q[:, ::hd] = 1
+    table = torch.cat([torch.arange(N), torch.full(((W or N) - N,), -1)]).int().view(1, -1)
+    out, lse = paged.paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ints([n - 1] * R),
+                                     requests=ints([0] * R), scale=1.0, lse=True)
+    check_rows(out.cpu(), lse.cpu(), q, k, v, table, [0] * R, [n - 1] * R, 0, 1.0, None, None)
