@@ -863,3 +863,45 @@ def test_attend_large_values(io, cache, hd, hk, W):
     out, lse = paged.paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ints([n - 1] * R),
                                      requests=ints([0] * R), scale=1.0, lse=True)
     check_rows(out.cpu(), lse.cpu(), q, k, v, table, [0] * R, [n - 1] * R, 0, 1.0, None, None)
+
+
+@pytest.mark.parametrize("W,hd", [(CUT, 128), (8, 64)])
+def test_attend_padding_behind_costs_no_more_than_in_front(W, hd):
+    """Rows of padding behind the last request are not walked one after another."""
+    P, hk, heads, live, pad = 16, 2, 4, 300, 30000
+    k, v = (torch.randn(live * 4, P, hk, hd, device="cuda").to(BF16) for _ in range(2))
+    table = torch.full((live, W), -1, dtype=torch.int32, device="cuda")
+    table[:, :4] = torch.arange(live * 4, dtype=torch.int32, device="cuda").view(live, 4)
+    q = torch.randn(live + pad, heads * hd, device="cuda").to(BF16)
+    out = torch.zeros_like(q)
+    ws = paged.paged_attention_workspace(q, k, table)
+    times = []
+    for front in (True, False):
+        req = torch.full((live + pad,), -1, dtype=torch.int32, device="cuda")
+        rows = slice(pad, pad + live) if front else slice(0, live)
+        req[rows] = torch.arange(live, dtype=torch.int32, device="cuda")
+        pos = torch.full_like(req, 63)
+        call = lambda: paged.paged_attention(q, k, v, table, pos, requests=req, out=out, workspace=ws)  # noqa: E731
+        call()
+        best = math.inf
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(4):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b) / 4)
+        times.append(best)
+    assert times[1] <= 3 * times[0], times
+
+
+@pytest.mark.parametrize("W,P,longest", [(2000, 16, 300), (8, 8, 64)])
+@pytest.mark.parametrize("cache", [F32, BF16])
+def test_attend_gaps_between_rows(W, P, longest, cache):
+    """Runs that cross empty rows: fewer and more of them than are looked at together."""
+    r = random.Random(5)
+    lens = [0] * 40
+    for _ in range(60):
+        lens += [r.randint(longest // 2, longest)] + [0] * r.choice([0, 1, 2, 30, 31, 32, 33, 63, 64, 65, 130])
+    run_attend(lens + [0] * 70, 4, 4, 64, BF16, cache, P, W=W, pad=4, seed=W)
