@@ -393,8 +393,9 @@ enum { RQ_ROPE_INTERLEAVED = 0, RQ_ROPE_HALVES = 1 };
  *               [0, n_blocks * block_size) are not stored
  *   q_out       device [T][heads * head_dim] in q_dtype, 16-byte aligned; must not overlap
  *               qkv
- * Norms and rotation are in f32 (angles exact to 2^-32 of a turn at any position); each
- * stored value is rounded once.  Rows of one call must not share a slot (it would hold a
+ * Norms and rotation are in f32; angles are within 2^-31 of a turn at any position before
+ * they are rounded to f32 for their sine and cosine (2^-26 of a turn).  Each stored value is
+ * rounded once.  Rows of one call must not share a slot (it would hold a
  * mix of them). */
 rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
                           int32_t qkv_dtype, const void *qkv, int64_t qkv_stride,

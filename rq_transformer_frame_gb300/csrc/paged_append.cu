@@ -5,8 +5,9 @@
 // Per head y = x * alpha / sqrt(mean(x^2) + eps); a pair (a, b) of y's first rope_dim
 // dimensions becomes (a cos w - b sin w, a sin w + b cos w), w = pos * theta^(-2i/rope_dim).
 // The angle is formed in turns, as a 64-bit fixed-point fraction: pos * F_i mod 2^64 with
-// F_i = theta^(-2i/rope_dim) / (2 pi) * 2^64 is exact in the position, so far positions
-// lose nothing (an f32 product pos * frequency is off by 0.06 rad at position 10^6).
+// F_i = theta^(-2i/rope_dim) / (2 pi) * 2^64 to 2^-62, so it is within 2^-31 of a turn at any
+// position (an f32 product pos * frequency is off by 0.06 rad at position 10^6). It is rounded
+// once, to the f32 half turns that sine and cosine are taken of (2^-26 of a turn).
 //
 // Each element is read once and written once: HBM-bound for many rows, latency for few. A CTA
 // takes a row, or a slice of its heads where there are too few rows to fill the card: the
@@ -240,17 +241,47 @@ cudaError_t by_cache(AppendParams& p, int tokens, int style, cudaStream_t s) {
                                : by_head_dim<IT, OT, float>(p, tokens, style, s);
 }
 
-// F_i = theta^(-2i/rd) / (2 pi) * 2^64 for i < rd / 2, each a product of at most six powers
-// g^(2^k), g = theta^(-2/rd) (one call of pow), so within 2^-49 of its value.
+// hi + lo: a number in two doubles, 100 bits and more of it
+struct Double2 {
+  double hi, lo;
+};
+// The product's rounding error comes from a fused multiply-add, the sum's from T. J. Dekker, "A
+// floating-point technique for extending the available precision" (1971).
+Double2 times(const Double2& a, const Double2& b) {
+  const double p = a.hi * b.hi;
+  const double e = std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi);
+  const double s = p + e;
+  return {s, e - (s - p)};
+}
+// v in (0, 1) times 2^64, to nearest (hi may be 1 already, lo is below 0 then)
+unsigned long long fixed64(const Double2& v) {
+  const double h = v.hi * 18446744073709551616.0;
+  const unsigned long long whole = v.hi < 1.0 ? (unsigned long long)h : 0;
+  const double rest = (v.hi < 1.0 ? h - (double)whole : 0.0) + v.lo * 18446744073709551616.0;
+  return whole + (unsigned long long)std::llround(rest);
+}
+
+// F_i = theta^(-2i/rd) / (2 pi) * 2^64 for i < n = rd / 2, within 4 (2^-62 of a turn): F_0 times
+// powers g^(2^k) of g = theta^(-2/rd), at most six of them, each and each product to nearest in
+// 64 bits. A double's g would be off by 2^-53 and its powers by n times that, which position 2^31
+// makes 2^-21 of a turn; but g^n theta = 1 in exact arithmetic, so what it is in two doubles says
+// by how much g, and each of its powers, is off.
 void rope_turns(unsigned long long* turns, int rd, double theta) {
-  double power[6];
-  power[0] = std::pow(theta, -2.0 / rd);
-  for (int k = 1; k < 6; ++k) power[k] = power[k - 1] * power[k - 1];
-  for (int i = 0; i < rd / 2; ++i) {
-    double f = 0.15915494309189535;  // 1 / (2 pi)
-    for (int k = 0; k < 6; ++k)
-      if (i >> k & 1) f *= power[k];
-    turns[i] = (unsigned long long)(f * 18446744073709551616.0);  // f < 1/6: in range
+  const int n = rd / 2;  // 64 at most
+  Double2 power[7], all{1.0, 0.0};
+  power[0] = {std::pow(theta, -2.0 / rd), 0.0};
+  for (int k = 1; n >> k; ++k) power[k] = times(power[k - 1], power[k - 1]);
+  for (int k = 0; n >> k; ++k)
+    if (n >> k & 1) all = times(all, power[k]);
+  all = times(all, {theta, 0.0});
+  const double off = ((all.hi - 1.0) + all.lo) / n;  // of g, relative
+  turns[0] = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+  for (int k = 0; 1 << k < n; ++k) {
+    power[k].lo -= power[k].hi * off * (1 << k);
+    const unsigned long long g = fixed64(power[k]);
+    for (int i = 0; i < 1 << k && i + (1 << k) < n; ++i)
+      turns[i + (1 << k)] =
+          (unsigned long long)(((unsigned __int128)turns[i] * g + (1ull << 63)) >> 64);
   }
 }
 

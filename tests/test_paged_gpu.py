@@ -16,6 +16,7 @@ import os
 import random
 import subprocess
 import sys
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -905,3 +906,36 @@ def test_attend_gaps_between_rows(W, P, longest, cache):
     for _ in range(60):
         lens += [r.randint(longest // 2, longest)] + [0] * r.choice([0, 1, 2, 30, 31, 32, 33, 63, 64, 65, 130])
     run_attend(lens + [0] * 70, 4, 4, 64, BF16, cache, P, W=W, pad=4, seed=W)
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803")
+
+
+def exact_turn(pos, theta, i, rd):
+    """The angle pos * theta^(-2i/rd) as a fraction of a turn, in [0, 1), in 70 digits."""
+    with localcontext() as c:
+        c.prec = 70
+        return float(pos * (Decimal(theta) ** (Decimal(-2 * i) / rd)) / (2 * PI) % 1)
+
+
+@pytest.mark.parametrize("theta", [1.001, 2.0, 10000.0, 1000000.0])
+@pytest.mark.parametrize("style", ["interleaved", "halves"])
+@pytest.mark.parametrize("rd", [8, 24, 128])
+def test_append_angles(theta, style, rd):
+    """cos and sin of every pair, read off the pair (1, 0), against angles in 70 digits. Half a step
+    of the f32 half turns is pi 2^-25 = 1.6 u of angle, the functions are within 2 steps of u, and
+    2^-31 of a turn is 0.05 u."""
+    far = [0, 1, 4097, 131071, 2**24 + 1, 2**30 + 12345, 2**31 - 1]
+    hd, T = 128, 7
+    qkv = torch.zeros(T, 3 * hd)
+    pairs = [(2 * i, 2 * i + 1) if style == "interleaved" else (i, i + rd // 2) for i in range(rd // 2)]
+    qkv[:, [a for a, _ in pairs]] = 1
+    k, v = (torch.zeros(T, 1, 1, hd, device="cuda") for _ in range(2))
+    q = paged.paged_append(qkv.cuda(), k, v, ints(far), torch.arange(T, device="cuda"), rope=style, rope_dim=rd,
+                           rope_theta=theta).double().cpu()
+    worst = 0.0
+    for t, pos in enumerate(far):
+        for i, (a, b) in enumerate(pairs):
+            w = 2 * math.pi * exact_turn(pos, theta, i, rd)
+            worst = max(worst, abs(float(q[t, a]) - math.cos(w)), abs(float(q[t, b]) - math.sin(w)))
+    assert worst <= 4 * U, worst / U
