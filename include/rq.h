@@ -420,7 +420,7 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
  *               (the last max_blocks pages).  A block outside [0, n_blocks) is left out.
  *               Negative: the request is empty.
  *   window      positions, or 0 for no limit
- *   scale       0 means 1 / sqrt(head_dim)
+ *   scale       0 means 1 / sqrt(head_dim); scale * log2(e) must be in f32's range
  *   q           device [R][heads * head_dim] in q_dtype (RQ_F32 / RQ_BF16), 16-byte aligned
  *   out         device [R][heads * head_dim] in q_dtype, 16-byte aligned
  *   lse         device [R][heads] f32 or NULL: log of the sum of exp(scale * q . k_j)

@@ -24,8 +24,10 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   using namespace rqk;
   const rq_status st = paged_kv_check(kv);
   if (st != RQ_OK) return st;
+  const float scale_log2 =
+      (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)kv->head_dim)) * 1.4426950408889634);
   if (rows < 0 || heads < 1 || heads % kv->heads != 0 || batch < 1 || max_blocks < 1 ||
-      window < 0 || !std::isfinite(scale))
+      window < 0 || !std::isfinite(scale_log2))
     return RQ_ERR_ARG;
   if (q_dtype != RQ_F32 && q_dtype != RQ_BF16) return RQ_ERR_ARG;
   if ((long long)rows * heads > INT_MAX) return RQ_ERR_UNSUPPORTED;
@@ -49,8 +51,7 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   p.W = max_blocks;
   p.window = window;
   p.G = heads / kv->heads;
-  p.scale = (float)((scale != 0.f ? (double)scale : 1.0 / std::sqrt((double)kv->head_dim)) *
-                    1.4426950408889634);
+  p.scale = scale_log2;
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(x.unit_heads, kv->head_dim));

@@ -39,6 +39,11 @@ _ROPE = {"interleaved": RQ_ROPE_INTERLEAVED, "halves": RQ_ROPE_HALVES}
 PagedPlan = namedtuple("PagedPlan", "lens pool cu_tokens requests positions slots")
 
 
+# ctypes takes an int32 argument modulo 2^32, and the smallest scales as the 0 that means the default;
+# an `or` of sizes leaves 32 bits where one of them does (a negative one is the library's to refuse)
+_TOP, _TINY = 2 ** 31 - 1, torch.finfo(torch.float32).tiny
+
+
 def _fail(what, rc):
     raise RQError(rc, "%s failed" % what)
 
@@ -65,6 +70,10 @@ def _bad_ints(name, n, dev, dtype=_I32):
 def _bad_rows(name, shape, dtype, dev):
     raise ValueError("%s: a contiguous %s tensor of shape %s on cuda:%d is wanted" %
                      (name, dtype, tuple(shape), dev))
+
+
+def _past_int32(what):
+    raise ValueError("%s: past 32 bits" % what)
 
 
 def _cache(k, v):
@@ -94,6 +103,8 @@ def paged_attention_workspace(q, k, block_table, window=0):
     """Scratch for paged_attention with these shapes, for calls whose addresses must stay (a
     captured graph), or None where the call needs none."""
     n, p, hk, hd = k.shape
+    if not -_TOP <= window | block_table.shape[1] <= _TOP:
+        _past_int32("window, block_table")
     with _on(k.device, None):
         size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
                                k.stride(2), p, block_table.shape[1], window)
@@ -120,6 +131,9 @@ def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_toke
             return paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_tokens, out)
     B, W = block_table.shape
     M = int(max_tokens)
+    N = free_ids.numel()
+    if not -_TOP <= block_size | M | B | W | N <= _TOP:
+        _past_int32("block_size, max_tokens, block_table, free_ids")
     if out is None:
         e = lambda n, dt=_I32: torch.empty(n, dtype=dt, device=lens.device)  # noqa: E731
         out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, _I64))
@@ -136,7 +150,7 @@ def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_toke
     if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < M or not slots.is_contiguous():
         _bad_ints("out.slots", M, dev, _I64)
     rc = load().rq_paged_plan(
-        B, W, block_size, free_ids.numel(), M, new_lens.data_ptr(), lens.data_ptr(), pool.data_ptr(),
+        B, W, block_size, N, M, new_lens.data_ptr(), lens.data_ptr(), pool.data_ptr(),
         free_ids.data_ptr(), block_table.data_ptr(), o_lens.data_ptr(), o_pool.data_ptr(), cu.data_ptr(),
         req.data_ptr(), pos.data_ptr(), slots.data_ptr(), _current_stream(dev))
     if rc != RQ_OK:
@@ -182,10 +196,13 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
         _bad_ints("positions", T, dev)
     if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < T or not slots.is_contiguous():
         _bad_ints("slots", T, dev, _I64)
+    rope_dim = hd if rope_dim is None else rope_dim
+    if not -_TOP <= rope_dim <= _TOP:
+        _past_int32("rope_dim")
     rc = load().rq_paged_append(
         kv, T, heads, _TYPE[dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
         None if q_alpha is None else q_alpha.data_ptr(), None if k_alpha is None else k_alpha.data_ptr(), eps,
-        _ROPE[rope], hd if rope_dim is None else rope_dim, rope_theta, positions.data_ptr(), slots.data_ptr(),
+        _ROPE[rope], rope_dim, rope_theta, positions.data_ptr(), slots.data_ptr(),
         _TYPE[o_dtype], out.data_ptr(), _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_append", rc)
@@ -210,6 +227,10 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     shape = q.shape
     R, heads = shape[0], shape[1] // hd
     B, W = block_table.shape
+    if not -_TOP <= window | B | W <= _TOP:
+        _past_int32("window, block_table")
+    if scale and -_TINY < scale < _TINY:
+        raise ValueError("scale: 0 for 1 / sqrt(head_dim), or at least %g" % _TINY)
     if out is None:
         out = torch.empty_like(q)
     if lse is True:

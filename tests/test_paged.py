@@ -180,3 +180,9 @@ def test_pools_past_32_bit_counting_are_refused(lib, n):
     """A thread's next ring entry, up to 1024 past the last, has to stay below 2^31."""
     assert lib.rq_paged_pool_init(n, A, B_, None) == binding.RQ_ERR_UNSUPPORTED
     assert _plan(lib, N=n) == binding.RQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38])
+def test_scales_past_f32_are_refused(lib, scale):
+    """Finite themselves, but not times log2(e), as the kernels take them: 0 times that is NaN."""
+    assert _attend(lib, scale=scale) == binding.RQ_ERR_ARG

@@ -939,3 +939,24 @@ def test_append_angles(theta, style, rd):
             w = 2 * math.pi * exact_turn(pos, theta, i, rd)
             worst = max(worst, abs(float(q[t, a]) - math.cos(w)), abs(float(q[t, b]) - math.sin(w)))
     assert worst <= 4 * U, worst / U
+
+
+def test_binding_refuses_what_does_not_fit():
+    """Sizes that modulo 2^32 are others, and scales that f32 takes for 0: a size is never cut."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.zeros(4, 16, 2, 64, device="cuda")
+    q, table, big = torch.zeros(3, 256, device="cuda"), i(3, 4), 2**32
+    for kw in (dict(window=big), dict(window=big + 5), dict(window=5 - big), dict(scale=1e-60), dict(scale=-1e-39)):
+        with pytest.raises(ValueError):
+            paged.paged_attention(q, k, k, table, i(3), **kw)
+    for scale in (1e300, 3e38, -3e38):
+        with pytest.raises(binding.RQError):
+            paged.paged_attention(q, k, k, table, i(3), scale=scale)
+    with pytest.raises(ValueError):
+        paged.paged_attention_workspace(q, k, table, big)
+    for rope_dim in (big, big + 64, 64 - big):
+        with pytest.raises(ValueError):
+            paged.paged_append(torch.zeros(3, 6 * 64, device="cuda"), k, k, i(3), i(3).long(), rope_dim=rope_dim)
+    for block_size, max_tokens in ((big + 16, 8), (16 - big, 8), (16, big + 8), (16, 8 - big)):
+        with pytest.raises(ValueError):
+            paged.paged_plan(i(2), i(2), i(4), i(8), i(2, 4), block_size, max_tokens)
