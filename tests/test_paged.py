@@ -186,3 +186,9 @@ def test_pools_past_32_bit_counting_are_refused(lib, n):
 def test_scales_past_f32_are_refused(lib, scale):
     """Finite themselves, but not times log2(e), as the kernels take them: 0 times that is NaN."""
     assert _attend(lib, scale=scale) == binding.RQ_ERR_ARG
+
+
+def test_rows_past_32_bit_counting_are_refused(lib):
+    """A row's elements are counted in 32 bits: 2^24 heads of 128 dimensions are 2^31."""
+    assert _attend(lib, rows=1, heads=2**24) == binding.RQ_ERR_UNSUPPORTED
+    assert _attend(lib, rows=3, heads=2**26, req=A) == binding.RQ_ERR_UNSUPPORTED
