@@ -27,6 +27,17 @@ inline rq_status paged_kv_check(const rq_paged_kv* kv) {
 
 constexpr int kMaxDevices = 64;
 
+// multiprocessors of the current device, looked up once (0 if there is none)
+inline int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) != 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 // CTAs of `kernel` that are resident at once on the current device; `cache`: one entry a
 // device for this kernel and shared-memory size, 0 until looked up.
 template <typename K>

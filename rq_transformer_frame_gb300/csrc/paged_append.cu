@@ -23,7 +23,7 @@
 namespace rqk {
 namespace {
 
-constexpr int kMaxWarps = 4;  // of a CTA
+constexpr int kMaxWarps = 2;  // of a CTA
 constexpr int kMaxPairs = 64;
 // steps of a warp whose loads are in flight: 16 registers of bf16, 24 of f32
 template <typename IT>
@@ -206,12 +206,14 @@ template <typename IT, typename OT, typename KT, int HD, bool HALVES>
 cudaError_t launch_append(AppendParams& p, int tokens, cudaStream_t s) {
   // Rows in plenty are a CTA of one warp each: no warp waits for another's angles (16384 rows
   // of 48 heads of 128 in bf16: 67 us; 69 with two warps a row, 73 with four; 4300 rows 26
-  // and 23). Fewer rows are CTAs of two warps, and below kCtas rows each is divided over
-  // several, down to one step a warp (64 such rows: 2.7 us, with CTAs of one warp 3.2).
-  constexpr int HPS = 32 / (HD / 8), kRows = 152 * 48, kCtas = 152 * 8;
-  const int steps = (p.heads + 2 * p.kv.heads + HPS - 1) / HPS, warps = tokens >= kRows ? 1 : 2;
+  // and 23). Fewer rows are CTAs of two warps, and below eight rows a multiprocessor each is divided
+  // over several, down to one step a warp (64 such rows: 2.7 us, with CTAs of one warp 3.2).
+  constexpr int HPS = 32 / (HD / 8);
+  const int sms = sm_count();
+  if (sms == 0) return cudaErrorInvalidDevice;
+  const int steps = (p.heads + 2 * p.kv.heads + HPS - 1) / HPS, warps = tokens >= sms * 48 ? 1 : 2;
   const int whole = (steps + warps - 1) / warps;  // of a warp, with one CTA a row
-  int slices = tokens >= kCtas ? 1 : (kCtas + tokens - 1) / tokens;
+  int slices = tokens >= sms * 8 ? 1 : (sms * 8 + tokens - 1) / tokens;
   if (slices > whole) slices = whole;
   p.steps = (whole + slices - 1) / slices;
   p.slices = (steps + p.steps * warps - 1) / (p.steps * warps);

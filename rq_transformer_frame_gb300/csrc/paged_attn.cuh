@@ -1158,17 +1158,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_c
   }
 }
 
-// multiprocessors of the current device, looked up once (0 if there is none)
-inline int sm_count() {
-  static std::atomic<int> known[kMaxDevices];
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev < kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) != 0) return sms;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
 // How a call is launched, from what the host knows: the shapes, and how long a row may be.
 struct Choice {
   int side;                // K/V heads of a unit (SideCore), or 1
