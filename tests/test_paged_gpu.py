@@ -801,7 +801,7 @@ def test_plan_batches_around_48_kb():
     that has planned no larger one before."""
     code = ("import sys; sys.path[:0] = %r\n"
             "import numpy as np, test_paged_gpu as t\n"
-            "for B in (3023, 3024, 3050, 3071, 3072):\n"
+            "for B in (3023, 3024, 3050, 3071, 3080):\n"
             "    t.check_plan([1] * B, [0] * B, [0, B, 0, 0], np.arange(B, dtype=np.int32),\n"
             "                 np.full((B, 1), -1, np.int32), 16, B, True)\n"
             % [os.path.dirname(os.path.dirname(os.path.abspath(paged.__file__))),
