@@ -12,7 +12,9 @@ or bf16, of any strides that keep head_dim contiguous and every row 16-byte alig
 Nothing here synchronizes except PagedCache.status(), so a step can be captured into a CUDA
 graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace` (paged_attention_workspace).
 Every call runs on `stream` (a torch.cuda.Stream; default: the current one of the
-tensors' device); tensors it allocates belong to that stream.
+tensors' device); tensors it allocates belong to that stream. As with any work on a side
+stream, a tensor of another one has to be ready there and to live until the call has run
+(wait_stream, record_stream).
 """
 from __future__ import annotations
 
