@@ -411,8 +411,8 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
  *               tokens are once all of them have been appended; a table that is a ring must
  *               then be wide enough that the last of the n tokens took over no page that the
  *               first one reads: (max_blocks - 1) * block_size + 1 >= window + n - 1
- *   heads       a multiple of kv->heads, below 2^24, and rows * heads below 2^31
- *               (RQ_ERR_UNSUPPORTED above)
+ *   heads       a multiple of kv->heads, at most 2^23; rows at most 2^30 and rows * heads
+ *               below 2^31 (RQ_ERR_UNSUPPORTED above)
  *   batch, max_blocks, block_table  as rq_paged_plan
  *   requests    device [R] int32 or NULL (row r is request r; R <= batch).  A row whose
  *               request is outside [0, batch) is padding: its output is left as it was

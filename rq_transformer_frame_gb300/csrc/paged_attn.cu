@@ -30,8 +30,8 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
       window < 0 || !std::isfinite(scale_log2))
     return RQ_ERR_ARG;
   if (q_dtype != RQ_F32 && q_dtype != RQ_BF16) return RQ_ERR_ARG;
-  // (row, head) pairs, and a row's elements, are counted in 32 bits
-  if ((long long)rows * heads > INT_MAX || heads > INT_MAX / 128) return RQ_ERR_UNSUPPORTED;
+  // rows, a row's elements and (row, head) pairs are counted in 32 bits, a thread's next one too
+  if (rows > 1 << 30 || heads > 1 << 23 || (long long)rows * heads > INT_MAX) return RQ_ERR_UNSUPPORTED;
   if (rows == 0) return RQ_OK;
   if (!requests && rows > batch) return RQ_ERR_ARG;
   if (!block_table || !positions || !q || !out) return RQ_ERR_ARG;

@@ -192,3 +192,12 @@ def test_rows_past_32_bit_counting_are_refused(lib):
     """A row's elements are counted in 32 bits: 2^24 heads of 128 dimensions are 2^31."""
     assert _attend(lib, rows=1, heads=2**24) == binding.RQ_ERR_UNSUPPORTED
     assert _attend(lib, rows=3, heads=2**26, req=A) == binding.RQ_ERR_UNSUPPORTED
+
+
+def test_a_threads_next_row_and_element_stay_in_32_bits(lib):
+    """A warp steps over all rows by up to 1216, a block over a row's elements by 256."""
+    one = _kv(heads=1)
+    assert _attend(lib, one, rows=2**31 - 1, heads=1, batch=2**31 - 1) == binding.RQ_ERR_UNSUPPORTED
+    assert _attend(lib, one, rows=2**30 + 1, heads=1, batch=2**31 - 1) == binding.RQ_ERR_UNSUPPORTED
+    assert _attend(lib, one, rows=1, heads=2**24 - 1) == binding.RQ_ERR_UNSUPPORTED
+    assert _attend(lib, rows=1, heads=2**23 + 4) == binding.RQ_ERR_UNSUPPORTED
