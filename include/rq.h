@@ -395,8 +395,7 @@ enum { RQ_ROPE_INTERLEAVED = 0, RQ_ROPE_HALVES = 1 };
  *               qkv
  * Norms and rotation are in f32; angles are within 2^-31 of a turn at any position before
  * they are rounded to f32 for their sine and cosine (2^-26 of a turn).  Each stored value is
- * rounded once.  Rows of one call must not share a slot (it would hold a
- * mix of them). */
+ * rounded once.  Rows of one call must not share a slot (it would hold a mix of them). */
 rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
                           int32_t qkv_dtype, const void *qkv, int64_t qkv_stride,
                           const float *q_alpha, const float *k_alpha, float eps,
@@ -431,10 +430,10 @@ rq_status rq_paged_append(const rq_paged_kv *kv, int32_t tokens, int32_t heads,
  *               arguments it is asked with and on the current device)
  * A row with no live position gives output 0 and lse -inf.  What lies in the cache outside
  * the live positions is never used, NaN or not; an infinite or NaN value at a live one
- * reaches its own dimension of the output only, as in the formula.  Scores, softmax and sums are f32 (the
- * number of live positions times the largest |value| has to stay in f32's range); with
- * f32 queries every product over a bf16 cache is exact (queries and weights enter as three
- * bf16 parts), with bf16 queries the weights keep 16 significant bits. */
+ * reaches its own dimension of the output only, as in the formula.  Scores, softmax and sums
+ * are f32 (the number of live positions times the largest |value| has to stay in f32's
+ * range); with f32 queries every product over a bf16 cache is exact (queries and weights
+ * enter as three bf16 parts), with bf16 queries the weights keep 16 significant bits. */
 size_t rq_paged_attention_workspace_size(const rq_paged_kv *kv, int32_t rows, int32_t heads,
                                          int32_t max_blocks, int32_t window);
 rq_status rq_paged_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,

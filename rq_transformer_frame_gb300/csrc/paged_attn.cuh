@@ -176,11 +176,11 @@ __device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
   hi -= bf16hi(u);
   return u;
 }
-// A pair of weights' leading bf16 parts, and in lo and hi what is left, both above 0 where the weight is:
-// cut just below the weight instead of rounded to nearest. An infinite value times any part of a
-// weight then has its own sign; times 0 or a negative part it would make the sum NaN. Three such
-// parts are a weight's 24 bits exactly: the first leaves at most 2^-7 of it, 17 bits, the second
-// 8 of them or a power of two.
+// A pair of weights' leading bf16 parts, and in lo and hi what is left, all above 0 where the weight
+// is: cut just below the weight instead of rounded to nearest. An infinite value times any part of
+// a weight then has its own sign; times 0 or a negative part it would make the sum NaN. Three such
+// parts are a weight's 24 bits exactly: the first leaves at most 2^-7 of it, 17 bits, the second 8
+// of them or a power of two.
 __device__ __forceinline__ uint32_t cut_bf16(float& lo, float& hi) {
   const uint32_t a = (uint32_t)__viaddmax_s32(__float_as_int(lo), -1, 0);
   const uint32_t b = (uint32_t)__viaddmax_s32(__float_as_int(hi), -1, 0);
@@ -361,9 +361,10 @@ struct MmaCore {
 // The same with 9 to 16 heads of a K/V head: the 16 rows of A are one head each, and each part
 // of a value is an instruction of its own, into the same sums. One pass over the cache instead of
 // two: 512 rows of 3000 positions, 16 heads of 128, take 139 us (84% of the measured copy rate), 256
-// rows of 4 x 12 heads 255 (91%), 256 rows of 2 x 16 f32 heads 178 (65%). All weights are in parts above 0, so two parts (bf16 queries) are within 2^-16 of them; rounded
-// to nearest, 2^-17, the second part wants sums of its own against infinite values (512 rows of 3000
-// positions, 16 heads of 128: 145 us against 139; outputs are rounded to 2^-9).
+// rows of 4 x 12 heads 255 (91%), 256 rows of 2 x 16 heads with f32 queries 178 (65%). All weights
+// are in parts above 0, so two parts (bf16 queries) are within 2^-16 of them. Rounded to nearest
+// they would be within 2^-17, but the second part wants sums of its own against infinite values (the
+// first case above: 145 us), and these outputs are rounded to 2^-9.
 template <typename QT, int HD>
 struct WideCore {
   static constexpr bool kF32 = sizeof(QT) == 4;
@@ -645,7 +646,8 @@ struct FmaCore {
       for (int h = 0; h < GP; ++h) {
         const float w = ex2(s[h] - finite_or_zero(m[h]));
         l[h] += w;
-        *reinterpret_cast<float2*>(sw + (key / 8) * kWPitch + ((key % 8) * GP + h) * 2) = make_float2(w * (1.f / kUnit), w * (1.f / kUnit));
+        const float u = w * (1.f / kUnit);
+        *reinterpret_cast<float2*>(sw + (key / 8) * kWPitch + ((key % 8) * GP + h) * 2) = make_float2(u, u);
       }
     }
     __syncwarp();
