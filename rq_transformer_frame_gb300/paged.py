@@ -41,9 +41,8 @@ _ROPE = {"interleaved": RQ_ROPE_INTERLEAVED, "halves": RQ_ROPE_HALVES}
 PagedPlan = namedtuple("PagedPlan", "lens pool cu_tokens requests positions slots")
 
 
-# ctypes takes an int32 argument modulo 2^32, and the smallest scales as the 0 that means the default;
-# an `or` of sizes leaves 32 bits where one of them does (a negative one is the library's to refuse)
-_TOP, _TINY = 2 ** 31 - 1, torch.finfo(torch.float32).tiny
+# ctypes takes an int32 argument modulo 2^32, and the smallest scales as the 0 that means the default
+_TINY = torch.finfo(torch.float32).tiny
 
 
 def _fail(what, rc):
@@ -74,8 +73,12 @@ def _bad_rows(name, shape, dtype, dev):
                      (name, dtype, tuple(shape), dev))
 
 
-def _past_int32(what):
-    raise ValueError("%s: past 32 bits" % what)
+def _past_int32(*sizes):
+    """What the calls ask where an `or` of their sizes is negative or past 31 bits: a negative size
+    alone is the library's to refuse."""
+    for x in sizes:
+        if x >> 31 not in (0, -1):
+            raise ValueError("a size of %d does not fit 32 bits" % x)
 
 
 def _cache(k, v):
@@ -105,8 +108,8 @@ def paged_attention_workspace(q, k, block_table, window=0):
     """Scratch for paged_attention with these shapes, for calls whose addresses must stay (a
     captured graph), or None where the call needs none."""
     n, p, hk, hd = k.shape
-    if not -_TOP <= window | block_table.shape[1] <= _TOP:
-        _past_int32("window, block_table")
+    if (window | block_table.shape[1]) >> 31:
+        _past_int32(window, block_table.shape[1])
     with _on(k.device, None):
         size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
                                k.stride(2), p, block_table.shape[1], window)
@@ -134,8 +137,8 @@ def paged_plan(new_lens, lens, pool, free_ids, block_table, block_size, max_toke
     B, W = block_table.shape
     M = int(max_tokens)
     N = free_ids.numel()
-    if not -_TOP <= block_size | M | B | W | N <= _TOP:
-        _past_int32("block_size, max_tokens, block_table, free_ids")
+    if (block_size | M | B | W | N) >> 31:
+        _past_int32(block_size, M, B, W, N)
     if out is None:
         e = lambda n, dt=_I32: torch.empty(n, dtype=dt, device=lens.device)  # noqa: E731
         out = PagedPlan(e(B), e(4), e(B + 1), e(M), e(M), e(M, _I64))
@@ -199,8 +202,8 @@ def paged_append(qkv, k, v, positions, slots, q_alpha=None, k_alpha=None, eps=1e
     if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < T or not slots.is_contiguous():
         _bad_ints("slots", T, dev, _I64)
     rope_dim = hd if rope_dim is None else rope_dim
-    if not -_TOP <= rope_dim <= _TOP:
-        _past_int32("rope_dim")
+    if rope_dim >> 31:
+        _past_int32(rope_dim)
     rc = load().rq_paged_append(
         kv, T, heads, _TYPE[dtype], qkv.data_ptr(), qkv.stride(0) if T > 1 else width,
         None if q_alpha is None else q_alpha.data_ptr(), None if k_alpha is None else k_alpha.data_ptr(), eps,
@@ -229,8 +232,8 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     shape = q.shape
     R, heads = shape[0], shape[1] // hd
     B, W = block_table.shape
-    if not -_TOP <= window | B | W <= _TOP:
-        _past_int32("window, block_table")
+    if (window | B | W) >> 31:
+        _past_int32(window, B, W)
     if scale and -_TINY < scale < _TINY:
         raise ValueError("scale: 0 for 1 / sqrt(head_dim), or at least %g" % _TINY)
     if out is None:
