@@ -443,6 +443,102 @@ rq_status rq_paged_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
                              void *out, float *lse, void *workspace, size_t workspace_bytes,
                              void *cuda_stream);
 
+/* ---- Long contexts over the paged cache.  Beside rq_paged_attention, which reads all of a
+ * row's positions, two ways of reading less: pages that a cheap score selects for each row
+ * (rq_paged_bounds, rq_paged_select, rq_paged_sparse_attention), and a prefix that many rows
+ * share, read once for all of them (rq_paged_prefix_attention).  Rows, requests, positions,
+ * block tables (rings too) and types are as there, and so are padding rows (a request outside
+ * [0, batch): outputs left as they were) and empty ones (a negative position). */
+
+/* The smallest and the largest key of a block by dimension, for the blocks that a step's
+ * tokens lie in; to be called after rq_paged_append stored the tokens.
+ *   kv          the layer's cache; its keys are read
+ *   bounds      device [n_blocks][heads][2][head_dim] in kv->dtype, 16-byte aligned: the smallest
+ *               values of a block's keys, then the largest ones.  A block is written if one of the
+ *               tokens lies in it, from its rows up to the last such token's, so rows behind
+ *               (of a request that had the block before) do not count
+ *   tokens      T (0: nothing is enqueued), at most 2^30 (RQ_ERR_UNSUPPORTED above)
+ *   positions, slots  device [T], as rq_paged_append takes them; tokens it does not store are
+ *               skipped.  Tokens of one block must stand in rising order with no others among
+ *               them, as rq_paged_plan writes them (else the bounds are some of theirs)
+ * Values are chosen, not computed: a block's bounds do not depend on how its tokens came in
+ * steps.  A NaN key makes its dimension's bounds NaN. */
+rq_status rq_paged_bounds(const rq_paged_kv *kv, void *bounds, int32_t tokens,
+                          const int32_t *positions, const int64_t *slots, void *cuda_stream);
+
+/* For each row and K/V head, `top` pages of the row's request to attend to:
+ *   - the `first` lowest and the `last` highest of its live pages (those that hold its live
+ *     positions: the last max_blocks pages up to its own), and
+ *   - of the others whose block lies in [0, n_blocks) the top - first - last best (or all) by
+ *     score = sum over dimensions d of max_d sum_h max(q_hd, 0) + min_d sum_h min(q_hd, 0),
+ *     h over the K/V head's queries: no sum of their scores with a key of the page is larger.
+ *     Of equal scores the lowest page is taken; a NaN score is lower than all others.
+ *   kv          the cache's sizes and type (its addresses and strides are not used)
+ *   bounds      rq_paged_bounds of the layer; the live blocks' must be there
+ *   top, first, last  pages; last >= 1 (the row's own page is always taken), first >= 0,
+ *               first + last <= top
+ *   q           device [R][heads * head_dim] in q_dtype, 16-byte aligned
+ *   pages       device [R][kv->heads][top] int32: page numbers (position / block_size) in
+ *               rising order, then -1
+ *   workspace   device scratch of at least rq_paged_select_workspace_size bytes, 16-byte aligned,
+ *               needing no initialisation; calls that may overlap need their own
+ * rows, heads and rows * heads as rq_paged_attention; rows * kv->heads * max_blocks at most 2^40,
+ * max_blocks at most 2^30 (RQ_ERR_UNSUPPORTED above).  Pages are compared by scores in f64
+ * wherever f32 could order them wrongly. */
+size_t rq_paged_select_workspace_size(const rq_paged_kv *kv, int32_t rows, int32_t max_blocks);
+rq_status rq_paged_select(const rq_paged_kv *kv, const void *bounds, int32_t rows, int32_t heads,
+                          int32_t batch, int32_t max_blocks, const int32_t *block_table,
+                          const int32_t *requests, const int32_t *positions, int32_t top,
+                          int32_t first, int32_t last, int32_t q_dtype, const void *q,
+                          int32_t *pages, void *workspace, size_t workspace_bytes,
+                          void *cuda_stream);
+
+/* rq_paged_attention over the pages of a list: row r's queries of K/V head h read the
+ * positions up to the row's own of the pages pages[r][h][0 .. list - 1].
+ *   list        entries of a list, at least 1; rows * kv->heads below 2^30 and
+ *               list * block_size below 2^31 - 64 (RQ_ERR_UNSUPPORTED above)
+ *   pages       device [R][kv->heads][list] int32, in any order; an entry that is negative, behind
+ *               the row's own page or no longer in the table is left out, one that stands
+ *               twice counts twice
+ * The rest, results and workspace too, as rq_paged_attention; a row without a live position in
+ * its lists gives output 0 and lse -inf for that K/V head. */
+size_t rq_paged_sparse_attention_workspace_size(const rq_paged_kv *kv, int32_t rows,
+                                                int32_t heads, int32_t list);
+rq_status rq_paged_sparse_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
+                                    int32_t batch, int32_t max_blocks,
+                                    const int32_t *block_table, const int32_t *requests,
+                                    const int32_t *positions, int32_t list, const int32_t *pages,
+                                    float scale, int32_t q_dtype, const void *q, void *out,
+                                    float *lse, void *workspace, size_t workspace_bytes,
+                                    void *cuda_stream);
+
+/* rq_paged_attention with a prefix that rows share: a row of group g attends to the positions
+ * of request prefix_requests[g] below prefix_lens[g], then to those of its own request up to its
+ * own position, as one softmax.  The prefix is a request of the pool like any other (its tokens
+ * were appended once); the rows' own requests hold what follows, at positions of their own
+ * from 0.  (Rotations are rq_paged_append's: its positions count from the prefix's start.)
+ *   groups      G >= 0, at most 2^20 (RQ_ERR_UNSUPPORTED above)
+ *   cu_rows     device [G + 1] int32, rising: rows cu_rows[g] .. cu_rows[g+1]-1 are group g's; rows
+ *               outside all groups attend to their own request alone.  Entries outside [0, R]
+ *               count as its ends
+ *   prefix_requests, prefix_lens  device [G] int32; a request outside [0, batch) or a length
+ *               below 1 is no prefix.  Of a prefix longer than its table row the last
+ *               max_blocks pages are read, as of a row's own request
+ *   positions   device [R] int32, the row's position in its own request; negative: it holds
+ *               nothing there, the prefix alone is read
+ * The rest, results and workspace too, as rq_paged_attention (no window). */
+size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv *kv, int32_t rows,
+                                                int32_t heads, int32_t max_blocks,
+                                                int32_t groups);
+rq_status rq_paged_prefix_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
+                                    int32_t batch, int32_t max_blocks,
+                                    const int32_t *block_table, const int32_t *requests,
+                                    const int32_t *positions, int32_t groups,
+                                    const int32_t *cu_rows, const int32_t *prefix_requests,
+                                    const int32_t *prefix_lens, float scale, int32_t q_dtype,
+                                    const void *q, void *out, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *cuda_stream);
+
 /* Token picks ("moshi_lm.rs", `Sampling`, `MoshiLm::set_sampling`, `pick`): every frame
  * picks the text token (temp_text, top_k_text) and then codebooks 0..7 (temp, top_k),
  * each session from its own xorshift64 state ("moshi_lm.rs", `xorshift_u01`):

@@ -123,7 +123,21 @@ def load() -> C.CDLL:
     L.rq_paged_attention_workspace_size.restype = C.c_size_t
     L.rq_paged_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, F32, I32,
                                      P, P, P, P, C.c_size_t, P]
-    for f in ("rq_paged_pool_init", "rq_paged_plan", "rq_paged_append", "rq_paged_attention"):
+    L.rq_paged_bounds.argtypes = [C.c_char_p, P, I32, P, P, P]
+    L.rq_paged_select_workspace_size.argtypes = [C.c_char_p, I32, I32]
+    L.rq_paged_select.argtypes = [C.c_char_p, P, I32, I32, I32, I32, P, P, P, I32, I32, I32, I32,
+                                  P, P, P, C.c_size_t, P]
+    L.rq_paged_sparse_attention_workspace_size.argtypes = [C.c_char_p, I32, I32, I32]
+    L.rq_paged_sparse_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, P, F32,
+                                            I32, P, P, P, P, C.c_size_t, P]
+    L.rq_paged_prefix_attention_workspace_size.argtypes = [C.c_char_p, I32, I32, I32, I32]
+    L.rq_paged_prefix_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, P, P, P,
+                                            F32, I32, P, P, P, P, C.c_size_t, P]
+    for f in ("rq_paged_select", "rq_paged_sparse_attention", "rq_paged_prefix_attention"):
+        getattr(L, f + "_workspace_size").restype = C.c_size_t
+    for f in ("rq_paged_pool_init", "rq_paged_plan", "rq_paged_append", "rq_paged_attention",
+              "rq_paged_bounds", "rq_paged_select", "rq_paged_sparse_attention",
+              "rq_paged_prefix_attention"):
         getattr(L, f).restype = C.c_int
     for f in ("rq_create", "rq_reset", "rq_step", "rq_step_forced", "rq_step_device",
               "rq_sync", "rq_get_logits", "rq_get_trace", "rq_get_ring", "rq_set_kv",

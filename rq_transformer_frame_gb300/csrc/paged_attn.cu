@@ -53,11 +53,7 @@ extern "C" rq_status rq_paged_attention(const rq_paged_kv* kv, int32_t rows, int
   p.window = window;
   p.G = heads / kv->heads;
   p.scale = scale_log2;
-  char* ws = static_cast<char*>(workspace);
-  p.part = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(ws + paged_attn::part_bytes(x.unit_heads, kv->head_dim));
-  p.cut = reinterpret_cast<int4*>(ws + paged_attn::part_bytes(x.unit_heads, kv->head_dim) +
-                                  paged_attn::ml_bytes(x.unit_heads));
+  paged_attn::place(p, x, workspace);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool qb = q_dtype == RQ_BF16;
   const cudaError_t e = kv->dtype == RQ_BF16 ? paged_attn::launch_bf16(p, x, qb, s)

@@ -1,6 +1,7 @@
 // paged_attn.cuh -- attention of one query token per row over a paged K/V cache: the kernel
 // template (include/rq.h, rq_paged_attention; instantiated by paged_attn_bf16.cu and
-// paged_attn_f32.cu, launched by paged_attn.cu).
+// paged_attn_f32.cu, launched by paged_attn.cu; with lists of pages rq_paged_sparse_attention,
+// paged_sparse.cu; with f32 outputs part of rq_paged_prefix_attention, paged_prefix.cu).
 //
 // For row r with position pos and query head h: s_j = scale q . k_j over the live positions
 // j, o = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m), in one pass with m the running maximum and
@@ -19,6 +20,10 @@
 //
 // Positions outside the live range or in a missing block are filled with zeros by the copy
 // and masked, so nothing that lies there is ever used.
+//
+// Lists. With LISTS a row's positions are not a range but those of the pages that a list names,
+// another list for each K/V head: every (row, K/V head) is then a row of its own, of one K/V head
+// and its queries, and its key j is position j % block_size of the list's entry j / block_size.
 #pragma once
 
 #include "paged.cuh"
@@ -48,6 +53,8 @@ struct Params {
   int G, GB, HG;       // query heads per K/V head (of all a unit reads), of a unit; units of a K/V head
   int runs;            // runs (warps) of the launch
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
+  const int32_t* pages;  // LISTS: [rows][list] pages, -1 in empty entries
+  int list, kv_heads;    // LISTS: entries of a list; rows of one query token
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
   float unit;          // what the sums of values are in (a core's kUnit)
@@ -81,22 +88,30 @@ struct Shape {
 };
 
 struct Row {
+  int r;                   // LISTS: its number
   int b, lo, pos, t0, nt;  // request, live positions [lo, pos], tiles [t0, t0 + nt)
 };
 
 // row r's request and position as they stand; out of the list: no tiles
+template <bool LISTS>
 __device__ __forceinline__ int2 row_words(const Params& p, int r) {
   if ((unsigned)r >= (unsigned)p.rows) return make_int2(-1, -1);
+  if (LISTS) r /= p.kv_heads;
   return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
 }
 
-template <int kKeys>
-__device__ __forceinline__ Row row_of(const Params& p, int2 words) {
+template <int kKeys, bool LISTS>
+__device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
   Row x;
+  x.r = r;
   x.b = words.x;
   x.pos = words.y;
   x.lo = x.t0 = x.nt = 0;
   if (x.b < 0 || x.b >= p.batch || x.pos < 0) return x;
+  if constexpr (LISTS) {
+    x.nt = (p.list * p.kv.block_size - 1) / kKeys + 1;
+    return x;
+  }
   const int P = p.kv.block_size, first = x.pos / P - p.W + 1;
   if (first > 0) x.lo = first * P;
   if (p.window > 0) x.lo = max(x.lo, x.pos - p.window + 1);
@@ -713,7 +728,9 @@ enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };
 // At least two CTAs an SM are asked for so that registers are not held back further: the
 // f32-query kernel takes 255 with the bound of two, 185 without one, and reads 64 sessions of
 // 3000 positions in 476 us against 563.
-template <typename QT, typename KT, int HD, typename Core, bool SPLIT>
+//
+// OT: the outputs' type, QT but for sums that are joined with others.
+template <typename QT, typename KT, int HD, typename Core, bool SPLIT, bool LISTS, typename OT>
 __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT ? 1 : 2)
     attend_kernel(const __grid_constant__ Params p) {
   using S = Shape<KT, Core::kLoad>;
@@ -726,7 +743,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   const int run = blockIdx.x * NW + warp;
   const int P = p.kv.block_size;
   auto empty_row = [&](int r, int h0, int h1, int i0, int step) {  // a row without a live position
-    QT* o = static_cast<QT*>(p.out) + (size_t)r * p.heads * HD;
+    OT* o = static_cast<OT*>(p.out) + (size_t)r * p.heads * HD;
     for (int i = h0 * HD + i0; i < h1 * HD; i += step) put(o + i, 0.f);
     if (p.lse)
       for (int i = h0 + i0; i < h1; i += step) p.lse[(size_t)r * p.heads + i] = neg_inf();
@@ -745,8 +762,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     r = blockIdx.y / units;
     kvh = u / p.HG;
     hg = u % p.HG;
-    const int2 words = row_words(p, r);
-    x = row_of<K>(p, words);
+    const int2 words = row_words<LISTS>(p, r);
+    x = row_of<K, LISTS>(p, r, words);
     if (x.nt == 0) {  // the whole cluster's
       const int h0 = kvh * p.G + hg * Core::kHeads;
       if (blockIdx.x == 0 && words.x >= 0 && words.x < p.batch)
@@ -765,12 +782,13 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (from < unit_end) {
         r = (int)(from / units);
         int u = (int)(from % units);
-        x = row_of<K>(p, row_words(p, r));
+        x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
         while (x.nt == 0 && (long long)(r + 1) * units < unit_end) {
-          x = row_of<K>(p, row_words(p, ++r));
+          ++r;
+          x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
           u = 0;
         }
-        next_words = row_words(p, r + 1);
+        next_words = row_words<LISTS>(p, r + 1);
         kvh = u / p.HG;
         hg = u % p.HG;
         stop = x.nt ? LLONG_MAX : 0;  // ends by unit_end
@@ -781,7 +799,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       __shared__ int s_row[NW];
       // where each run starts: prefix sums of the rows' costs, a slice of rows per thread
       auto cost = [&](int r) {
-        const int nt = row_of<K>(p, row_words(p, r)).nt;
+        const int nt = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r)).nt;
         return nt ? (long long)(nt + kUnitCost) * units : 0ll;
       };
       const int slice = (p.rows + NT - 1) / NT;
@@ -827,8 +845,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       at = stop;
       if (begin < total) {
         r = s_row[warp];
-        x = row_of<K>(p, row_words(p, r));
-        next_words = row_words(p, r + 1);
+        x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
+        next_words = row_words<LISTS>(p, r + 1);
         const int unit_cost = x.nt + kUnitCost, u = (int)(s_off[warp] / unit_cost);
         const int in = (int)(s_off[warp] % unit_cost);
         kvh = u / p.HG;
@@ -839,7 +857,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     }
     // rows of empty requests
     for (int i = run; i < p.rows; i += p.runs) {
-      const int2 words = row_words(p, i);
+      const int2 words = row_words<LISTS>(p, i);
       if (words.x < 0 || words.x >= p.batch || words.y >= 0) continue;
       empty_row(i, 0, p.heads, lane, 32);
     }
@@ -850,8 +868,18 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     // ---- the cursor over the tiles. Table entries are read 32 pages at a time, a lane each,
     // well ahead of their use: ids of pages [base, base + 32), then the 32 that follow, the
     // first 32 of the row (every unit of it begins there) and of the next row.
+    //
+    // Of a list, entries stand for pages: an id's complement is that of the row's own, newest page,
+    // which holds positions behind the row's, and INT_MIN, the complement of no block, that of none.
     auto ids_from = [&](const Row& y, int first) {
       const int page = first + lane;  // past 2^31: a large unsigned number
+      if constexpr (LISTS) {
+        if (y.nt == 0 || (unsigned)page >= (unsigned)p.list) return INT_MIN;
+        const int at = p.pages[(size_t)y.r * p.list + page], newest = y.pos / P;
+        if (at < 0 || at > newest || at <= newest - p.W) return INT_MIN;
+        const int id = p.table[(size_t)y.b * p.W + (at < p.W ? at : at % p.W)];
+        return id < 0 ? INT_MIN : at == newest ? ~id : id;
+      }
       if (y.nt == 0 || (unsigned)page > (unsigned)(y.pos / P)) return -1;
       return p.table[(size_t)y.b * p.W + (page < p.W ? page : page % p.W)];
     };
@@ -864,18 +892,25 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     auto issue = [&]() {
       const int s = issued % NS, key = (x.t0 + t) * K + (K < 32 ? lane % K : lane), page = key / P;
       if (!next_known) {  // its words came with this row's: its first pages
-        const Row y = row_of<K>(p, next_words);
+        const Row y = row_of<K, LISTS>(p, r + 1, next_words);
         ids_next = ids_from(y, y.t0 * K / P);
         next_known = true;
       }
       const int rel = page - base;
       const int id0 = __shfl_sync(0xffffffffu, ids, rel & 31);
       const int id1 = __shfl_sync(0xffffffffu, ids_after, rel & 31);
-      const int id = rel < 32 ? id0 : id1;
-      const bool ok = key >= x.lo && key <= x.pos && id >= 0 && id < p.kv.n_blocks;
+      int id = rel < 32 ? id0 : id1;
+      bool ok;
+      if constexpr (LISTS) {
+        ok = id >= 0 || key - page * P <= x.pos % P;
+        if (id < 0) id = ~id;
+        ok = ok && id < p.kv.n_blocks && page < p.list;
+      } else {
+        ok = key >= x.lo && key <= x.pos && id >= 0 && id < p.kv.n_blocks;
+      }
       const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (K < 32 ? (1u << (K & 31)) - 1u : ~0u);
       const long long off = ok ? id * p.kv.block_stride + (key - page * P) * p.kv.row_stride +
-                                     kvh * p.kv.head_stride
+                                     (LISTS ? r % p.kv_heads : kvh) * p.kv.head_stride
                                : 0;
       if (t == 0) first = true;
       const bool last = t == x.nt - 1, end = last || at + 1 >= stop;
@@ -920,7 +955,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         t = 0;
         first = false;
         at += kUnitCost;
-        const bool one_window = x.pos / P - x.t0 * K / P < 32;
+        const bool one_window = LISTS ? p.list <= 32 : x.pos / P - x.t0 * K / P < 32;
         if (++hg == p.HG) {
           hg = 0;
           if (++kvh == p.kv.heads) {
@@ -931,20 +966,20 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
               more = false;
               return;
             }
-            x = row_of<K>(p, next_words);
-            ids0 = ids_next;
             ++r;
+            x = row_of<K, LISTS>(p, r, next_words);
+            ids0 = ids_next;
             // empty rows between, 32 at a time (of a run that is not whole units a row follows)
             while (x.nt == 0 && r < p.rows - 1 && (!p.whole || (long long)(r + 1) * units < unit_end)) {
-              const int2 words = row_words(p, r + 1 + lane);
-              const uint32_t some = __ballot_sync(0xffffffffu, row_of<K>(p, words).nt > 0);
+              const int2 words = row_words<LISTS>(p, r + 1 + lane);
+              const uint32_t some = __ballot_sync(0xffffffffu, row_of<K, LISTS>(p, 0, words).nt > 0);
               const int n = some ? __ffs(some) : min(32, p.rows - 1 - r);
               r += n;
-              x = row_of<K>(p, make_int2(__shfl_sync(0xffffffffu, words.x, n - 1),
-                                         __shfl_sync(0xffffffffu, words.y, n - 1)));
+              x = row_of<K, LISTS>(p, r, make_int2(__shfl_sync(0xffffffffu, words.x, n - 1),
+                                                   __shfl_sync(0xffffffffu, words.y, n - 1)));
               ids0 = ids_from(x, x.t0 * K / P);
             }
-            next_words = row_words(p, r + 1);
+            next_words = row_words<LISTS>(p, r + 1);
             next_known = false;
           }
         }
@@ -981,7 +1016,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       __syncwarp();  // the stage is free for the next copy
       if (SPLIT || !(d.z & kEnd)) continue;
       if ((d.z & kFirst) && (d.z & kLast)) {
-        core.template end<false>(static_cast<QT*>(p.out) + head * HD, p.lse ? p.lse + head : nullptr,
+        core.template end<false>(static_cast<OT*>(p.out) + head * HD, p.lse ? p.lse + head : nullptr,
                                  nullptr, live, lane);
       } else {
         const size_t slot = ((size_t)run * 2 + ((d.z & kFirst) ? 1 : 0)) * p.GB;
@@ -1020,7 +1055,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         s_cta[i] = a;
         if (i % HD == 0) s_cta_ml[g] = make_float2(m, l);
       } else {
-        put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
+        put(static_cast<OT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
         if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
       }
     }
@@ -1038,7 +1073,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         l += tc::ld_cluster(tc::mapa(mls + g * 8 + 4, c)) * f;
         a = fmaf(tc::ld_cluster(tc::mapa(sums + i * 4, c)), f, a);
       }
-      put(static_cast<QT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
+      put(static_cast<OT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
       if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
     }
     tc::cluster_sync();  // no CTA leaves while another reads its sums
@@ -1098,7 +1133,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot
   }
 }
 
-template <typename QT, int HD>
+template <typename OT, int HD>
 __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_constant__ Params p) {
   constexpr int E = HD / 32;
   __shared__ int4 s_cut[kJoinWarps];
@@ -1111,7 +1146,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_c
     const size_t head = (size_t)cut.x * p.heads + cut.y + g;
     const float inv = l == 0.f ? 0.f : p.unit / l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) put(static_cast<QT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
+    for (int e = 0; e < E; ++e) put(static_cast<OT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
     if (p.lse && lane == 0) p.lse[head] = log_sum(m, l);
   };
   auto slots_of = [&](int run) {
@@ -1228,7 +1263,7 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
   return x;
 }
 
-template <typename QT, typename KT, int HD, typename Core>
+template <typename QT, typename KT, int HD, typename Core, bool LISTS = false, typename OT = QT>
 cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   using S = Shape<KT, Core::kLoad>;
   cudaError_t e;
@@ -1238,7 +1273,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   p.unit = Core::kUnit;
   if constexpr (Core::kLoad == HD) {  // units of one K/V head
     if (x.split) {
-      auto* kernel = attend_kernel<QT, KT, HD, Core, true>;
+      auto* kernel = attend_kernel<QT, KT, HD, Core, true, LISTS, OT>;
       constexpr size_t ring = (size_t)kSplitWarps *
                               (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
       constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
@@ -1250,7 +1285,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
     }
   }
   // as many CTAs as are resident at once, at most as many as the largest rows could fill
-  auto* kernel = attend_kernel<QT, KT, HD, Core, false>;
+  auto* kernel = attend_kernel<QT, KT, HD, Core, false, LISTS, OT>;
   constexpr size_t smem = (size_t)kWarps * (kStages * S::kStage + Core::kScratch);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1272,12 +1307,24 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   p.runs = grid * kWarps;
   if ((e = launch_dependent(kernel, dim3((unsigned)grid), kWarps * 32, smem, 0, s, p)) != cudaSuccess) return e;
   const dim3 joins((unsigned)((p.runs + kJoinWarps - 1) / kJoinWarps), (unsigned)p.GB, 1);
-  return launch_dependent(join_kernel<QT, HD>, joins, kJoinWarps * 32, 0, 0, s, p);
+  return launch_dependent(join_kernel<OT, HD>, joins, kJoinWarps * 32, 0, 0, s, p);
 }
 
-// over a bf16 cache, over an f32 cache
+// a launch's scratch in its workspace
+inline void place(Params& p, const Choice& x, void* workspace) {
+  char* ws = static_cast<char*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + part_bytes(x.unit_heads, p.kv.head_dim));
+  p.cut = reinterpret_cast<int4*>(ws + part_bytes(x.unit_heads, p.kv.head_dim) + ml_bytes(x.unit_heads));
+}
+
+// over a bf16 cache, over an f32 cache; with lists; with f32 outputs whatever the queries are
 cudaError_t launch_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_lists_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_lists_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_sums_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_sums_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 
 }  // namespace paged_attn
 }  // namespace rqk

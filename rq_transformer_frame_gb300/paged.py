@@ -5,12 +5,17 @@ rq_paged_* calls; argument marshalling only, like `binding`).
   paged_append     per-head norm, position rotation, and K/V stored by slot
   paged_attention  one query token per row over its request's blocks
   paged_attention_workspace  scratch for it, where a call's addresses must stay
-  PagedCache       the buffers of one cache, with the three as methods
+  paged_bounds     smallest and largest keys of the blocks a step's tokens lie in
+  paged_select     the pages each row and K/V head should read, by those bounds
+  paged_sparse_attention  paged_attention over such lists of pages
+  paged_prefix_attention  paged_attention behind a prefix that groups of rows share
+  PagedCache       the buffers of one cache, with all of them as methods
 
 A layer's cache is a pair of tensors k, v [n_blocks][block_size][kv_heads][head_dim] (f32
 or bf16, of any strides that keep head_dim contiguous and every row 16-byte aligned).
 Nothing here synchronizes except PagedCache.status(), so a step can be captured into a CUDA
-graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace` (paged_attention_workspace).
+graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace` (the
+paged_*_workspace functions).
 Every call runs on `stream` (a torch.cuda.Stream; default: the current one of the
 tensors' device); tensors it allocates belong to that stream. As with any work on a side
 stream, a tensor of another one has to be ready there and to live until the call has run
@@ -273,21 +278,253 @@ def paged_attention(q, k, v, block_table, positions, requests=None, window=0, sc
     return out, lse
 
 
+def paged_bounds(k, bounds, positions, slots, stream=None):
+    """rq_paged_bounds: bounds [n_blocks][heads][2][head_dim] (smallest keys, then largest) of the
+    blocks of keys k that the tokens lie in, updated in place and returned; positions [T] int32,
+    slots [T] int64, as paged_append had them."""
+    kv, hk, hd, dev = _cache(k, k)
+    if stream is not None or _current_device() != dev:
+        with _on(k.device, stream):
+            return paged_bounds(k, bounds, positions, slots)
+    shape = (k.shape[0], hk, 2, hd)
+    if bounds.dtype is not k.dtype or bounds.get_device() != dev or bounds.shape != shape or \
+            not bounds.is_contiguous():
+        _bad_rows("bounds", shape, k.dtype, dev)
+    T = positions.numel()
+    if positions.dtype is not _I32 or positions.get_device() != dev or not positions.is_contiguous():
+        _bad_ints("positions", T, dev)
+    if slots.dtype is not _I64 or slots.get_device() != dev or slots.numel() < T or not slots.is_contiguous():
+        _bad_ints("slots", T, dev, _I64)
+    if T >> 31:
+        _past_int32(T)
+    rc = load().rq_paged_bounds(kv, bounds.data_ptr(), T, positions.data_ptr(), slots.data_ptr(),
+                                _current_stream(dev))
+    if rc != RQ_OK:
+        _fail("rq_paged_bounds", rc)
+    return bounds
+
+
+def _geometry(bounds, block_size):
+    """(rq_paged_kv packed, heads, head_dim, device index) of the cache that bounds belong to."""
+    dev, dtype = bounds.get_device(), bounds.dtype
+    if dev < 0 or dtype not in _TYPE or bounds.dim() != 4 or bounds.shape[2] != 2 or not bounds.is_contiguous():
+        raise ValueError("bounds: a contiguous f32 or bf16 CUDA tensor [n_blocks][heads][2][head_dim]")
+    n, h, _, hd = bounds.shape
+    if (n | block_size) >> 31:
+        _past_int32(n, block_size)
+    at = bounds.data_ptr()
+    return _KV.pack(at, at, 0, 0, 0, _TYPE[dtype], h, hd, block_size, n), h, hd, dev
+
+
+def paged_select_workspace(q, bounds, block_table, block_size):
+    """Scratch for paged_select with these shapes."""
+    kv, _, _, _ = _geometry(bounds, block_size)
+    if (q.shape[0] | block_table.shape[1]) >> 31:
+        _past_int32(q.shape[0], block_table.shape[1])
+    with _on(bounds.device, None):
+        size = load().rq_paged_select_workspace_size(kv, q.shape[0], block_table.shape[1])
+    return torch.empty(size, dtype=torch.uint8, device=bounds.device)
+
+
+def paged_select(q, bounds, block_table, positions, block_size, top, first=1, last=1, requests=None,
+                 pages=None, workspace=None, stream=None):
+    """rq_paged_select: for each row of q [R][heads * head_dim] and each K/V head `top` pages of
+    the row's request -- its `first` and `last` ones and the best of the others by paged_bounds'
+    bounds -- -> pages [R][kv_heads][top] int32, in rising order, -1 behind the last.  The rest as
+    paged_attention; block_size: the cache's."""
+    kv, hk, hd, dev = _geometry(bounds, block_size)
+    if stream is not None or _current_device() != dev:
+        with _on(bounds.device, stream):
+            return paged_select(q, bounds, block_table, positions, block_size, top, first, last,
+                                requests, pages, workspace)
+    dtype = q.dtype
+    if q.dim() != 2 or dtype not in _TYPE or q.shape[1] % hd or block_table.dim() != 2:
+        raise ValueError("q: an f32 or bf16 tensor [R][heads * head_dim]; block_table [B][max_blocks]")
+    R, heads = q.shape[0], q.shape[1] // hd
+    B, W = block_table.shape
+    if (top | first | last | B | W) >> 31:
+        _past_int32(top, first, last, B, W)
+    if q.get_device() != dev or not q.is_contiguous():
+        _bad_rows("q", q.shape, dtype, dev)
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        _bad_ints("block_table", B * W, dev)
+    if positions.dtype is not _I32 or positions.get_device() != dev or positions.numel() < R or \
+            not positions.is_contiguous():
+        _bad_ints("positions", R, dev)
+    if requests is not None and (requests.dtype is not _I32 or requests.get_device() != dev or
+                                 requests.numel() < R or not requests.is_contiguous()):
+        _bad_ints("requests", R, dev)
+    if pages is None:
+        pages = torch.empty((R, hk, max(top, 0)), dtype=_I32, device=bounds.device)
+    if pages.dtype is not _I32 or pages.get_device() != dev or pages.shape != (R, hk, top) or \
+            not pages.is_contiguous():
+        _bad_rows("pages", (R, hk, top), _I32, dev)
+    if workspace is None:
+        workspace = torch.empty(load().rq_paged_select_workspace_size(kv, R, W), dtype=torch.uint8,
+                                device=bounds.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    rc = load().rq_paged_select(
+        kv, bounds.data_ptr(), R, heads, B, W, block_table.data_ptr(),
+        None if requests is None else requests.data_ptr(), positions.data_ptr(), top, first, last,
+        _TYPE[dtype], q.data_ptr(), pages.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _current_stream(dev))
+    if rc != RQ_OK:
+        _fail("rq_paged_select", rc)
+    return pages
+
+
+@lru_cache(maxsize=1024)
+def _sparse_workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, block_size, list_):
+    kv = _KV.pack(16, 16, 0, 0, 0, dtype, kv_heads, head_dim, block_size, 1)
+    return load().rq_paged_sparse_attention_workspace_size(kv, rows, heads, list_)
+
+
+def paged_sparse_attention_workspace(q, k, pages):
+    """Scratch for paged_sparse_attention with these shapes, or None where the call needs none."""
+    hk, hd = k.shape[2:]
+    with _on(k.device, None):
+        size = _sparse_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
+                                      k.shape[1], pages.shape[2])
+    return torch.empty(size, dtype=torch.uint8, device=k.device) if size else None
+
+
+@lru_cache(maxsize=1024)
+def _prefix_workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, head_stride, block_size, max_blocks,
+                           groups):
+    kv = _KV.pack(16, 16, 0, 0, head_stride, dtype, kv_heads, head_dim, block_size, 1)
+    return load().rq_paged_prefix_attention_workspace_size(kv, rows, heads, max_blocks, groups)
+
+
+def paged_prefix_attention_workspace(q, k, block_table, prefix_lens):
+    """Scratch for paged_prefix_attention with these shapes."""
+    n, p, hk, hd = k.shape
+    with _on(k.device, None):
+        size = _prefix_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
+                                      k.stride(2), p, block_table.shape[1], prefix_lens.numel())
+    return torch.empty(size, dtype=torch.uint8, device=k.device)
+
+
+def _rows(q, k, hd, dev, block_table, positions, requests, out, lse, scale):
+    """Checks that both attentions below share -> (R, heads, B, W, out, lse)."""
+    dtype = q.dtype
+    if q.dim() != 2 or dtype not in _TYPE or q.shape[1] % hd or block_table.dim() != 2:
+        raise ValueError("q: an f32 or bf16 tensor [R][heads * head_dim]; block_table [B][max_blocks]")
+    shape = q.shape
+    R, heads = shape[0], shape[1] // hd
+    B, W = block_table.shape
+    if (B | W) >> 31:
+        _past_int32(B, W)
+    if scale and -_TINY < scale < _TINY:
+        raise ValueError("scale: 0 for 1 / sqrt(head_dim), or at least %g" % _TINY)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is True:
+        lse = torch.empty((R, heads), dtype=_F32, device=k.device)
+    if q.get_device() != dev or not q.is_contiguous():
+        _bad_rows("q", shape, dtype, dev)
+    if out.dtype is not dtype or out.get_device() != dev or out.shape != shape or not out.is_contiguous():
+        _bad_rows("out", shape, dtype, dev)
+    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != (R, heads) or
+                            not lse.is_contiguous()):
+        _bad_rows("lse", (R, heads), _F32, dev)
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        _bad_ints("block_table", B * W, dev)
+    if positions.dtype is not _I32 or positions.get_device() != dev or positions.numel() < R or \
+            not positions.is_contiguous():
+        _bad_ints("positions", R, dev)
+    if requests is not None and (requests.dtype is not _I32 or requests.get_device() != dev or
+                                 requests.numel() < R or not requests.is_contiguous()):
+        _bad_ints("requests", R, dev)
+    return R, heads, B, W, out, lse
+
+
+def _scratch(workspace, nbytes, k, dev):
+    """(workspace, its bytes), allocated where the caller passed none."""
+    if workspace is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=k.device) if nbytes else None), nbytes
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def paged_sparse_attention(q, k, v, block_table, positions, pages, requests=None, scale=0.0, out=None,
+                           lse=None, workspace=None, stream=None):
+    """rq_paged_sparse_attention: paged_attention in which row r's queries of K/V head h read the
+    pages pages[r][h] ([R][kv_heads][list] int32, as paged_select gives them; -1: none)."""
+    kv, hk, hd, dev = _cache(k, v)
+    if stream is not None or _current_device() != dev:
+        with _on(k.device, stream):
+            return paged_sparse_attention(q, k, v, block_table, positions, pages, requests, scale, out,
+                                          lse, workspace)
+    R, heads, B, W, out, lse = _rows(q, k, hd, dev, block_table, positions, requests, out, lse, scale)
+    if pages.dtype is not _I32 or pages.get_device() != dev or pages.dim() != 3 or \
+            pages.shape[:2] != (R, hk) or not pages.is_contiguous():
+        _bad_rows("pages", (R, hk, "list"), _I32, dev)
+    n = pages.shape[2]
+    if n >> 31:
+        _past_int32(n)
+    workspace, nbytes = _scratch(workspace, 0 if workspace is not None else _sparse_workspace_size(
+        dev, _TYPE[k.dtype], R, heads, hk, hd, k.shape[1], n), k, dev)
+    rc = load().rq_paged_sparse_attention(
+        kv, R, heads, B, W, block_table.data_ptr(), None if requests is None else requests.data_ptr(),
+        positions.data_ptr(), n, pages.data_ptr(), scale, _TYPE[q.dtype], q.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(), nbytes,
+        _current_stream(dev))
+    if rc != RQ_OK:
+        _fail("rq_paged_sparse_attention", rc)
+    return out, lse
+
+
+def paged_prefix_attention(q, k, v, block_table, positions, cu_rows, prefix_requests, prefix_lens,
+                           requests=None, scale=0.0, out=None, lse=None, workspace=None, stream=None):
+    """rq_paged_prefix_attention: paged_attention in which rows cu_rows[g] .. cu_rows[g + 1] - 1 also
+    read the first prefix_lens[g] positions of request prefix_requests[g], once for all of them
+    (cu_rows [G + 1], prefix_requests, prefix_lens [G] int32).  positions are the rows' own, in
+    their own requests."""
+    kv, hk, hd, dev = _cache(k, v)
+    if stream is not None or _current_device() != dev:
+        with _on(k.device, stream):
+            return paged_prefix_attention(q, k, v, block_table, positions, cu_rows, prefix_requests,
+                                          prefix_lens, requests, scale, out, lse, workspace)
+    R, heads, B, W, out, lse = _rows(q, k, hd, dev, block_table, positions, requests, out, lse, scale)
+    G = prefix_lens.numel()
+    if G >> 31:
+        _past_int32(G)
+    for name, t, n in (("cu_rows", cu_rows, G + 1), ("prefix_requests", prefix_requests, G),
+                       ("prefix_lens", prefix_lens, G)):
+        if t.dtype is not _I32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+            _bad_ints(name, n, dev)
+    workspace, nbytes = _scratch(workspace, 0 if workspace is not None else _prefix_workspace_size(
+        dev, _TYPE[k.dtype], R, heads, hk, hd, k.stride(2), k.shape[1], W, G), k, dev)
+    rc = load().rq_paged_prefix_attention(
+        kv, R, heads, B, W, block_table.data_ptr(), None if requests is None else requests.data_ptr(),
+        positions.data_ptr(), G, cu_rows.data_ptr(), prefix_requests.data_ptr(), prefix_lens.data_ptr(),
+        scale, _TYPE[q.dtype], q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), nbytes, _current_stream(dev))
+    if rc != RQ_OK:
+        _fail("rq_paged_prefix_attention", rc)
+    return out, lse
+
+
 class PagedCache:
     """The buffers of one paged cache and its step's maps, at fixed addresses.
 
     batch request rows, n_blocks blocks of block_size positions per layer, at most
     max_blocks blocks a request (past that its table is a ring) and max_tokens new tokens a
-    step.  All layers share the block table; layer l's cache is k[l], v[l]."""
+    step.  All layers share the block table; layer l's cache is k[l], v[l].  bounds: keep the
+    blocks' smallest and largest keys too, for bound, select and attend_pages."""
 
     def __init__(self, batch, n_blocks, block_size, max_blocks, max_tokens, kv_heads, head_dim,
-                 layers=1, dtype=torch.bfloat16, device="cuda"):
+                 layers=1, dtype=torch.bfloat16, device="cuda", bounds=False):
         dev = torch.device(device)
         shape = (layers, n_blocks, block_size, kv_heads, head_dim)
         e = lambda n, dt=torch.int32: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731
         self.block_size, self.max_tokens = int(block_size), int(max_tokens)
         self.k = torch.zeros(shape, dtype=dtype, device=dev)
         self.v = torch.zeros(shape, dtype=dtype, device=dev)
+        self.bounds = torch.zeros((layers, n_blocks, kv_heads, 2, head_dim), dtype=dtype, device=dev) \
+            if bounds else None
         self.block_table = torch.full((batch, max_blocks), -1, dtype=torch.int32, device=dev)
         self.free_ids = e(n_blocks)
         self.maps = PagedPlan(e(batch), e(4), e(batch + 1), e(max_tokens), e(max_tokens),
@@ -317,6 +554,31 @@ class PagedCache:
         T = q.shape[0]
         return paged_attention(q, self.k[layer], self.v[layer], self.block_table,
                                self.maps.positions[:T], requests=self.maps.requests[:T], **kw)
+
+    def bound(self, layer, T, **kw):
+        """The bounds of the blocks that the step's first T tokens lie in, once they are appended
+        (a cache made with bounds=True)."""
+        return paged_bounds(self.k[layer], self.bounds[layer], self.maps.positions[:T], self.maps.slots[:T], **kw)
+
+    def select(self, layer, q, top, **kw):
+        """`top` pages of its own request for each of the step's tokens and K/V heads."""
+        T = q.shape[0]
+        return paged_select(q, self.bounds[layer], self.block_table, self.maps.positions[:T],
+                            self.block_size, top, requests=self.maps.requests[:T], **kw)
+
+    def attend_pages(self, layer, q, pages, **kw):
+        """Each of the step's tokens over the pages that select gave it."""
+        T = q.shape[0]
+        return paged_sparse_attention(q, self.k[layer], self.v[layer], self.block_table,
+                                      self.maps.positions[:T], pages, requests=self.maps.requests[:T], **kw)
+
+    def attend_prefix(self, layer, q, cu_rows, prefix_requests, prefix_lens, **kw):
+        """Each of the step's tokens over its group's prefix, a request of this cache, and then
+        over its own request."""
+        T = q.shape[0]
+        return paged_prefix_attention(q, self.k[layer], self.v[layer], self.block_table,
+                                      self.maps.positions[:T], cu_rows, prefix_requests, prefix_lens,
+                                      requests=self.maps.requests[:T], **kw)
 
     def status(self):
         """(why the last plan did nothing: RQ_PAGED_* bits, 0 if it did; free blocks).
