@@ -1,13 +1,15 @@
 // paged_prefix.cu -- attention over a prefix that a group of rows shares and over each row's own
 // request (include/rq.h, rq_paged_prefix_attention).
 //
-// Softmax over two sets of positions from the two apart: with o_i, lse_i of set i,
-// lse = log(e^lse_1 + e^lse_2) and o = e^(lse_1 - lse) o_1 + e^(lse_2 - lse) o_2. Both parts are f32;
-// the output is rounded once.
+// The rows' own requests are paged_attn.cuh's work, with f32 outputs. The prefixes are paged_prefix.cuh's,
+// all rows of a group at once, where the cache is bf16 and there are queries enough for a matrix
+// product; else paged_attn.cuh's too, a row at a time. Then all parts of a row are joined: with o_i, lse_i
+// of a part, lse = log sum e^lse_i and o = sum e^(lse_i - lse) o_i. All parts are f32, the output is
+// rounded once.
 #include <algorithm>
 #include <cmath>
 
-#include "paged_attn.cuh"
+#include "paged_prefix.cuh"
 
 namespace rqk {
 namespace {
@@ -74,18 +76,121 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Pref
   }
 }
 
-struct Layout {
-  paged_attn::Choice x;
-  size_t o, lse, map, bytes;
+// The prefix kernel's pieces and the own request's part of each query. A lane has one query -- those of
+// a K/V head one after another, as they lie in the pieces -- and a warp some of its dimensions.
+struct JoinParams {
+  prefix::Params t;
+  const int32_t* requests;
+  const float *own, *own_lse;
+  void* out;
+  float* lse;
 };
 
-Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks) {
+constexpr int kJoinWarps = 8;
+
+template <typename OT, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ JoinParams p) {
+  constexpr int E = HD / 4 / kJoinWarps;  // fours of dimensions of a thread
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long of_head = (long long)p.t.rows * p.t.G, all = of_head * p.t.kv.heads;
+  const long long idx = (long long)blockIdx.x * 32 + lane;
+  if (idx >= all) return;
+  const int h = (int)(idx / of_head), in = (int)(idx % of_head), r = in / p.t.G, g = in % p.t.G;
+  const int b = p.requests ? p.requests[r] : r;
+  if (b < 0 || b >= p.t.batch) return;
+  const size_t head = (size_t)r * p.t.heads + (size_t)h * p.t.G + g;
+  // the query's pieces: none, one in row order, or those of runs [c0, c1]
+  long long c0 = 0, c1 = -1;
+  size_t at = 0;  // in a piece
+  int unit = 0;
+  bool whole = false;
+  {
+    int lo = 0, hi = p.t.groups;  // the last group that starts at the row or before
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (p.t.cu_rows[mid] <= r) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo > 0 && r < p.t.cu_rows[lo]) {
+      const prefix::Group x = p.t.group[lo - 1];
+      if (x.tiles > 0) {
+        unit = x.unit_rows;
+        const int i = (r - x.row0) * p.t.G + g, u = i / unit;
+        const prefix::Costs c = unit == 256 ? prefix::costs_of<256>(x.queries, x.tiles)
+                                            : prefix::costs_of<128>(x.queries, x.tiles);
+        const long long per = *p.t.per, first = x.list0 + h * c.head + u * c.full + prefix::kUnitCost;
+        const int w = u == c.units - 1 ? c.last_weight : unit / prefix::kRows;
+        c0 = first / per;
+        c1 = (first + (long long)(x.tiles - 1) * w) / per;
+        whole = c0 == c1;
+        at = i % unit;
+      }
+    }
+  }
+  auto slot_of = [&](long long c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * unit; };
+  auto ml_of = [&](long long c) { return whole ? p.t.whole_ml[head] : p.t.part_ml[slot_of(c) + at]; };
+  const float own = p.own_lse[head] * 1.4426950408889634f;
+  float m = own;
+#pragma unroll 4
+  for (long long c = c0; c <= c1; ++c) m = fmaxf(m, ml_of(c).x);
+  const float ref = finite_or_zero(m);
+  float sum = 0.f, o[E][4] = {};
+  auto add = [&](const float* from, size_t step, float f) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (warp * E + e) * step);
+      o[e][0] = fmaf(v.x, f, o[e][0]), o[e][1] = fmaf(v.y, f, o[e][1]);
+      o[e][2] = fmaf(v.z, f, o[e][2]), o[e][3] = fmaf(v.w, f, o[e][3]);
+    }
+  };
+#pragma unroll 4
+  for (long long c = c0; c <= c1; ++c) {
+    const float2 ml = ml_of(c);
+    const float f = exp2f(ml.x - ref);
+    sum = fmaf(ml.y, f, sum);
+    if (whole) add(p.t.whole + head * HD, 4, f);
+    else add(p.t.part + (slot_of(c) + at / prefix::kRows * prefix::kRows) * HD + (at % prefix::kRows) * 4,
+             prefix::kRows * 4, f);
+  }
+  if (own != neg_inf()) {
+    const float f = exp2f(own - ref);
+    sum += f;
+    add(p.own + head * HD, 4, f);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    OT* out = static_cast<OT*>(p.out) + head * HD + (warp * E + e) * 4;
+    paged_attn::put2(out, o[e][0] * inv, o[e][1] * inv);
+    paged_attn::put2(out + 2, o[e][2] * inv, o[e][3] * inv);
+  }
+  if (p.lse && warp == 0) p.lse[head] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+struct Layout {
+  paged_attn::Choice x;
+  bool tc;         // prefixes by matrix products
+  int ctas, unit;  // of the prefix kernel
+  size_t o, lse, map, part, part_ml, group, bytes;
+};
+
+Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int groups, bool q_bf16) {
+  using paged_attn::align256;
   Layout l{};
+  const size_t hd = kv.head_dim;
   l.x = paged_attn::choose(kv, rows, heads, max_blocks, 0);
-  l.o = paged_attn::align256((size_t)rows * heads * kv.head_dim * sizeof(float));
-  l.lse = paged_attn::align256((size_t)rows * heads * sizeof(float));
-  l.map = paged_attn::align256((size_t)rows * sizeof(int32_t));
-  l.bytes = 2 * (l.o + l.lse + l.map) + l.x.workspace;
+  l.o = align256((size_t)rows * heads * hd * sizeof(float));
+  l.lse = align256((size_t)rows * heads * sizeof(float2));
+  l.map = align256((size_t)rows * sizeof(int32_t));
+  l.tc = groups > 0 && kv.dtype == RQ_BF16;
+  l.ctas = std::max(sm_count(), 1);
+  l.unit = prefix::unit_queries(q_bf16);
+  l.part = align256((size_t)l.ctas * 2 * l.unit * hd * sizeof(float));
+  l.part_ml = align256((size_t)l.ctas * 2 * l.unit * sizeof(float2));
+  l.group = align256((size_t)groups * sizeof(prefix::Group)) + 256;
+  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : 2 * l.map);
   return l;
 }
 
@@ -106,7 +211,8 @@ extern "C" size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv* kv
                                                            int32_t groups) {
   using namespace rqk;
   if (check(kv, rows, heads, max_blocks, groups) != RQ_OK || rows < 1) return 0;
-  return layout_of(*kv, rows, heads, max_blocks).bytes;
+  return std::max(layout_of(*kv, rows, heads, max_blocks, groups, true).bytes,
+                  layout_of(*kv, rows, heads, max_blocks, groups, false).bytes);
 }
 
 extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -131,20 +237,20 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   if (!block_table || !positions || !q || !out || !workspace) return RQ_ERR_ARG;
   if (groups > 0 && (!cu_rows || !prefix_requests || !prefix_lens)) return RQ_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
-  const Layout l = layout_of(*kv, rows, heads, max_blocks);
+  const bool qb = q_dtype == RQ_BF16;
+  const Layout l = layout_of(*kv, rows, heads, max_blocks, groups, qb);
   if (workspace_bytes < l.bytes) return RQ_ERR_ARG;
   char* ws = static_cast<char*>(workspace);
-  float* o[2] = {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.o)};
-  ws += 2 * l.o;
-  float* ls[2] = {reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.lse)};
-  ws += 2 * l.lse;
-  int32_t* map[2] = {reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + l.map)};
-  ws += 2 * l.map;
-  PrefixParams pp{requests, cu_rows, prefix_requests, prefix_lens, rows, heads, batch, groups, kv->head_dim,
-                  map[0], map[1], o[0], o[1], ls[0], ls[1], out, lse};
+  auto take = [&](size_t n) {
+    char* at = ws;
+    ws += n;
+    return at;
+  };
+  float* const o1 = reinterpret_cast<float*>(take(l.o));
+  float* const o2 = reinterpret_cast<float*>(take(l.o));
+  float* const lse1 = reinterpret_cast<float*>(take(l.lse));
+  float* const lse2 = reinterpret_cast<float*>(take(l.lse));
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = launch_dependent(rows_kernel, dim3((unsigned)((rows + 255) / 256)), 256, 0, 0, s, pp);
-  if (e != cudaSuccess) return RQ_ERR_CUDA;
   paged_attn::Params p{};
   p.kv = *kv;
   p.q = q;
@@ -155,17 +261,43 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   p.W = max_blocks;
   p.G = heads / kv->heads;
   p.scale = scale_log2;
-  paged_attn::place(p, l.x, ws);
-  const bool qb = q_dtype == RQ_BF16;
-  for (int i = 0; i < 2; ++i) {
-    p.requests = i == 0 ? map[0] : requests;
-    p.positions = i == 0 ? map[1] : positions;
-    p.out = o[i];
-    p.lse = ls[i];
-    e = kv->dtype == RQ_BF16 ? paged_attn::launch_sums_bf16(p, l.x, qb, s)
-                             : paged_attn::launch_sums_f32(p, l.x, qb, s);
+  paged_attn::place(p, l.x, take(l.x.workspace));
+  auto attend = [&](const int32_t* of, const int32_t* pos, float* o, float* ls) {
+    p.requests = of;
+    p.positions = pos;
+    p.out = o;
+    p.lse = ls;
+    return kv->dtype == RQ_BF16 ? paged_attn::launch_sums_bf16(p, l.x, qb, s)
+                                : paged_attn::launch_sums_f32(p, l.x, qb, s);
+  };
+  if (l.tc) {
+    prefix::Params t{*kv, q, block_table, cu_rows, prefix_requests, prefix_lens, rows, heads, batch, max_blocks,
+                     groups, p.G, std::fabs(scale_log2), scale_log2 < 0.f ? 1u : 0u, o1,
+                     reinterpret_cast<float2*>(lse1)};
+    t.part = reinterpret_cast<float*>(take(l.part));
+    t.part_ml = reinterpret_cast<float2*>(take(l.part_ml));
+    t.group = reinterpret_cast<prefix::Group*>(take(l.group));
+    t.per = reinterpret_cast<long long*>(reinterpret_cast<char*>(t.group) + l.group - 256);
+    cudaError_t e = qb ? prefix::launch_bf16(t, l.ctas, s) : prefix::launch_f32(t, l.ctas, s);
+    if (e == cudaSuccess) e = attend(requests, positions, o2, lse2);
     if (e != cudaSuccess) return RQ_ERR_CUDA;
+    JoinParams j{t, requests, o2, lse2, out, lse};
+    const dim3 grid((unsigned)(((long long)rows * heads + 31) / 32));
+    auto join = [&](auto* kernel) { return launch_dependent(kernel, grid, kJoinWarps * 32, 0, 0, s, j); };
+    switch (kv->head_dim) {
+      case 32: e = qb ? join(join_kernel<uint16_t, 32>) : join(join_kernel<float, 32>); break;
+      case 64: e = qb ? join(join_kernel<uint16_t, 64>) : join(join_kernel<float, 64>); break;
+      default: e = qb ? join(join_kernel<uint16_t, 128>) : join(join_kernel<float, 128>);
+    }
+    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
   }
+  int32_t* const map[2] = {reinterpret_cast<int32_t*>(take(l.map)), reinterpret_cast<int32_t*>(take(l.map))};
+  PrefixParams pp{requests, cu_rows, prefix_requests, prefix_lens, rows, heads, batch, groups, kv->head_dim,
+                  map[0], map[1], o1, o2, lse1, lse2, out, lse};
+  cudaError_t e = launch_dependent(rows_kernel, dim3((unsigned)((rows + 255) / 256)), 256, 0, 0, s, pp);
+  if (e == cudaSuccess) e = attend(map[0], map[1], o1, lse1);
+  if (e == cudaSuccess) e = attend(requests, positions, o2, lse2);
+  if (e != cudaSuccess) return RQ_ERR_CUDA;
   const long long pairs = (long long)rows * heads;
   const int grid = (int)std::min<long long>((pairs + 7) / 8, 8ll * sm_count() + 1);
   e = qb ? launch_dependent(merge_kernel<uint16_t>, dim3((unsigned)grid), 256, 0, 0, s, pp)

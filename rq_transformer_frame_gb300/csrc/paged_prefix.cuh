@@ -1,0 +1,674 @@
+// paged_prefix.cuh -- attention of groups of rows over a prefix that each group shares, on the tcgen05
+// tensor cores: the kernel template (include/rq.h, rq_paged_prefix_attention; launched by
+// paged_prefix.cu, instantiated by paged_prefix_bf16.cu and paged_prefix_f32.cu).
+//
+// The queries that read a K/V head's keys are those of all rows of a group: rows x G of them, one
+// matrix product with the prefix. For a tile of keys
+//   S = Q K^T (f32 in tensor memory), P = 2^(scale S - ref), O += P V, l += sum P,
+// ref a running bound of the maximum: it moves, and O and l are scaled, only when a score passes it. It
+// is set kSlack above the maximum met, so that P stays at most 1 and sums in range.
+//
+// A unit is (group, K/V head, 128 or 256 queries). All units' key tiles form one list, cut into
+// equal runs, a CTA each, one CTA an SM. A unit inside one run leaves its sums in row order; of a unit
+// that is cut each piece leaves (ref, l, O) in its CTA's scratch, and paged_prefix.cu joins them with
+// the rows' own requests.
+//
+// A CTA is 13 warps:
+//   0-3, 4-7  two softmax streams: a thread has one query's row of S. With 256 queries a stream has
+//             128 of them and both read the same keys; with up to 128 the streams take turns by
+//             tiles and are added at the end. While one forms P the tensor cores work for the other.
+//   8-11      the loaders: 16-byte cp.async of K and V rows by the block table into a ring, in the
+//             swizzled layouts that the tensor cores read (K with dimensions inside, V with dimensions
+//             outside: the same rows, read transposed)
+//   12        one thread issues all tcgen05.mma: S_j+2 behind O_j, in order, so that S_j+2 being there
+//             says that O_j is done too
+//
+// bf16 queries enter as they are and P in two bf16 parts (16 bits); f32 queries and their P in three
+// (24 bits, every product exact). Parts are cut, not rounded to nearest (paged_attn.cuh, cut_bf16): all
+// are of the value's sign, so an infinite key or value is met by no zero part. P lies in tensor memory,
+// in the columns of the S it was made of.
+#pragma once
+
+#include "paged_attn.cuh"
+
+namespace rqk {
+namespace prefix {
+
+using paged_attn::cp_async16;
+using paged_attn::cp_async_commit;
+using paged_attn::cp_async_wait;
+using paged_attn::cut_bf16;
+using paged_attn::ex2;
+using paged_attn::finite_or_zero;
+using paged_attn::neg_inf;
+using paged_attn::pack_bf16;
+
+constexpr int kThreads = 416, kLoaders = 128;
+constexpr int kRows = 128;       // queries of a stream
+constexpr int kLag = 2;          // halves that are in flight when an older one is handed over
+constexpr int kUnitCost = 3;     // what a unit's start and end count, in tiles
+constexpr float kSlack = 8.f;
+constexpr int kMasks = 8;        // tiles whose masks are kept
+
+struct alignas(16) Group {  // what the joining kernel needs of a group
+  long long list0;          // its first entry of the list
+  int row0, queries, tiles, unit_rows;
+};
+
+struct Params {
+  rq_paged_kv kv;
+  const void* q;
+  const int32_t *table, *cu_rows, *prefix_requests, *prefix_lens;
+  int rows, heads, batch, W, groups, G;
+  float scale;      // |scale| times log2 e
+  uint32_t flip;    // 1: the scale is negative, queries enter negated
+  float* whole;     // [rows][heads][HD] sums of units of one run
+  float2* whole_ml; // [rows][heads] (ref, l)
+  float* part;      // [ctas][2][unit queries / 128][HD / 4][128][4]
+  float2* part_ml;  // [ctas][2][unit queries]
+  Group* group;     // [groups]
+  long long* per;   // entries of a run
+};
+
+template <typename QT, int HD>
+struct Shape {
+  static constexpr bool kF32 = sizeof(QT) == 4;
+  static constexpr int kQParts = kF32 ? 3 : 1, kPParts = kF32 ? 3 : 2;
+  static constexpr int KT = kF32 ? 64 : 128;           // keys of a tile
+  static constexpr int kTiles = kF32 ? 1 : 2;          // query tiles of a unit
+  static constexpr int kUnit = kTiles * kRows;
+  static constexpr int kHalf = KT * HD * 2;            // bytes of a tile's keys, or values
+  static constexpr int kQ = kQParts * kRows * HD * 2;  // of a query tile
+  static constexpr int kRoom = (224 * 1024 - kTiles * kQ) / kHalf;
+  static constexpr int NH = kRoom < 8 ? kRoom : 8;     // halves of the ring
+  static constexpr int kRing = kTiles * kQ + NH * kHalf;
+  // a row's bytes in shared memory: 64 dimensions, or all 32
+  static constexpr int kPitch = HD < 64 ? 64 : 128;
+  static_assert(NH >= 5, "the loaders run three halves ahead of what they hand over");
+  // where 16-byte piece c of row r of R rows lies
+  template <int R>
+  static __device__ __forceinline__ int at(int r, int c) {
+    if constexpr (HD < 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
+};
+
+struct Small {  // behind the tiles
+  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], done, o_free, drain;
+  uint32_t mask[kMasks][4];
+  float2 ml[2][kRows];
+  long long scan[kThreads / 32], start, start0;
+  int start_group;
+  uint32_t tmem;
+  volatile int abort;
+};
+
+template <typename QT, int HD>
+constexpr size_t smem_bytes = Shape<QT, HD>::kRing + sizeof(Small);
+
+// ---------------------------------------------------------------- tensor memory
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Shared-memory matrix descriptor (tc_common.cuh has the fields) of rows of 128 or 64 bytes in the
+// swizzle of that size: SBO between groups of eight rows, LBO between the 64-dimension
+// halves where dimensions are the outer ones.
+template <int PITCH>
+__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)((lbo >> 4) & 0x3fffu) << 16 |
+         (uint64_t)((8 * PITCH) >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)(PITCH == 128 ? 2u : 4u) << 61;
+}
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- units and pieces
+// A group as the list has it. tiles: key tiles [t0, t0 + tiles) of request b, live positions [lo, end)
+struct View {
+  int row0, queries, b, lo, end, t0, tiles;
+};
+
+template <int KT>
+__device__ __forceinline__ View view_of(const Params& p, int g) {
+  View v{};
+  v.row0 = min(max(p.cu_rows[g], 0), p.rows);
+  const int row1 = min(max(p.cu_rows[g + 1], v.row0), p.rows);
+  v.b = p.prefix_requests[g];
+  v.end = p.prefix_lens[g];
+  if (row1 == v.row0 || v.b < 0 || v.b >= p.batch || v.end < 1) return v;
+  v.queries = (row1 - v.row0) * p.G;
+  const int P = p.kv.block_size, first = (v.end - 1) / P - p.W + 1;
+  v.lo = max(first, 0) * P;
+  v.t0 = v.lo / KT;
+  v.tiles = (v.end - 1) / KT - v.t0 + 1;
+  return v;
+}
+
+// a group's units of one K/V head: the full ones' cost, the last one's, their number
+struct Costs {
+  long long full, last, head;
+  int units, last_weight;
+};
+
+// A tile counts once for each 128 queries.
+template <int UNIT>
+__host__ __device__ __forceinline__ Costs costs_of(int queries, int tiles) {
+  Costs c{};
+  if (tiles == 0) return c;
+  c.units = (queries - 1) / UNIT + 1;
+  c.last_weight = (queries - (c.units - 1) * UNIT - 1) / kRows + 1;
+  c.full = (long long)tiles * (UNIT / kRows) + kUnitCost;
+  c.last = (long long)tiles * c.last_weight + kUnitCost;
+  c.head = (c.units - 1) * c.full + c.last;
+  return c;
+}
+
+struct Piece {
+  View v;
+  int h, unit, t, n;  // K/V head, unit of it, tiles [t, t + n)
+  bool pair, first, last;
+};
+
+// a CTA's walk over its run, the same in every thread
+template <int KT, int UNIT>
+struct Cursor {
+  long long at, stop, list0;
+  int g;
+  __device__ __forceinline__ bool next(const Params& p, Piece& x) {
+    while (at < stop && g < p.groups) {
+      x.v = view_of<KT>(p, g);
+      const Costs c = costs_of<UNIT>(x.v.queries, x.v.tiles);
+      const long long cost = c.head * p.kv.heads;
+      if (at >= list0 + cost) {
+        list0 += cost;
+        ++g;
+        continue;
+      }
+      long long in = at - list0;
+      x.h = (int)(in / c.head);
+      in -= x.h * c.head;
+      x.unit = (int)min(in / c.full, (long long)c.units - 1);
+      in -= x.unit * c.full;
+      const bool tail = x.unit == c.units - 1;
+      const int w = tail ? c.last_weight : UNIT / kRows;
+      const long long begin = at - in;  // the unit's first entry
+      x.t = in <= kUnitCost ? 0 : (int)((in - kUnitCost + w - 1) / w);
+      at = begin + (tail ? c.last : c.full);
+      if (x.t >= x.v.tiles) continue;
+      const long long room = stop - begin - kUnitCost - (long long)x.t * w;
+      if (room <= 0) return false;  // its first tile is the next run's
+      x.n = (int)min((room + w - 1) / w, (long long)(x.v.tiles - x.t));
+      x.pair = w == 2;
+      x.first = x.t == 0;
+      x.last = x.t + x.n == x.v.tiles;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------- the kernel
+template <typename QT, int HD>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
+  using S = Shape<QT, HD>;
+  constexpr int KT = S::KT, NH = S::NH, UNIT = S::kUnit;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Small& s = *reinterpret_cast<Small*>(smem + S::kRing);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the list: each thread a slice of the groups, prefix sums of their costs
+  Cursor<KT, UNIT> cur;
+  {
+    const int slice = (p.groups + kThreads - 1) / kThreads;
+    const int g0 = min(tid * slice, p.groups), g1 = min(g0 + slice, p.groups);
+    auto cost = [&](int g) {
+      const View v = view_of<KT>(p, g);
+      return costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
+    };
+    long long own = 0;
+    for (int g = g0; g < g1; ++g) own += cost(g);
+    long long inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s.scan[warp] = inc;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) inc += s.scan[w];
+      total += s.scan[w];
+    }
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2));
+    const long long begin = blockIdx.x * per;
+    long long at = inc - own;
+    if (blockIdx.x == 0) {
+      for (int g = g0; g < g1; ++g) {
+        const View v = view_of<KT>(p, g);
+        p.group[g] = Group{at, v.row0, v.queries, v.tiles, UNIT};
+        at += costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
+      }
+      if (tid == 0) *p.per = per;
+      at = inc - own;
+    }
+    if (begin >= total) return;
+    if (at <= begin && begin < inc) {
+      for (int g = g0; g < g1; ++g) {
+        const long long c = cost(g);
+        if (begin < at + c) {
+          s.start_group = g;
+          s.start0 = at;
+          break;
+        }
+        at += c;
+      }
+    }
+    cur.at = begin;
+    cur.stop = min(begin + per, total);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NH; ++i) {
+      mbar_init(&s.full[i], kLoaders);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.q_full, kLoaders);
+    mbar_init(&s.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 2);
+      mbar_init(&s.p_full[i], kRows);
+    }
+    mbar_init(&s.done, 1);
+    mbar_init(&s.o_free, 2 * kRows);
+    mbar_init(&s.drain, 1);
+    fence_barrier_init();
+    s.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzles go by the address
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(&s.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s.tmem;
+  cur.g = s.start_group;
+  cur.list0 = s.start0;
+  // a wait that runs out ends the CTA's work: its sums become NaN. wait: of one thread, wait_warp: of a
+  // warp, all of whose lanes go on or none
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (s.abort) return false;
+    if (mbar_wait(bar, parity & 1u)) return true;
+    s.abort = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  Piece x;
+
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ loaders
+    constexpr int RW = KT / 4;          // rows of a warp
+    constexpr int CH = HD / 8;          // 16-byte pieces of a row
+    constexpr int RPI = 32 / CH;        // rows of a warp's copy instruction
+    const int w = warp - 8, P = p.kv.block_size;
+    const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
+    int half = 0, tile = 0, piece = 0;
+    bool ok = true;
+    while (ok && cur.next(p, x)) {
+      const uint16_t* kb = static_cast<const uint16_t*>(p.kv.k) + x.h * p.kv.head_stride;
+      const uint16_t* vb = static_cast<const uint16_t*>(p.kv.v) + x.h * p.kv.head_stride;
+      auto id_of = [&](int t) {
+        const int key = (x.v.t0 + x.t + t) * KT + w * RW + lane % RW, page = key / P;
+        if (t >= x.n || key < x.v.lo || key >= x.v.end) return -1;
+        return p.table[(size_t)x.v.b * p.W + (page < p.W ? page : page % p.W)];
+      };
+      int id_next = id_of(0);
+      for (int t = 0; ok && t < x.n; ++t, ++tile) {
+        const int key = (x.v.t0 + x.t + t) * KT + w * RW + lane % RW, id = id_next;
+        id_next = id_of(t + 1);
+        const bool live = id >= 0 && id < p.kv.n_blocks;
+        const uint32_t mask = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) s.mask[tile % kMasks][w] = RW == 32 ? mask : mask & ((1u << (RW & 31)) - 1u);
+        const long long off = live ? id * p.kv.block_stride + (key % P) * p.kv.row_stride : 0;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const int slot = half % NH;
+          if (half >= NH && !(ok = wait_warp(&s.empty[slot], half / NH - 1))) break;
+          const uint32_t dst = ring + slot * S::kHalf;
+          const uint16_t* base = side == 0 ? kb : vb;
+          const int c = lane % CH;
+#pragma unroll
+          for (int i = 0; i < RW / RPI; ++i) {
+            const int r = i * RPI + lane / CH;
+            const long long e = __shfl_sync(0xffffffffu, off, r);
+            cp_async16(dst + S::template at<KT>(w * RW + r, c), base + e + c * 8, (mask >> r) & 1u);
+          }
+          cp_async_commit();
+          ++half;
+          cp_async_wait<kLag>();
+          if (half > kLag) {
+            fence_proxy_async();
+            mbar_arrive(&s.full[(half - 1 - kLag) % NH]);
+          }
+        }
+        if (ok && t == 0) {
+          // the unit's queries, once the products with the last one's are done
+          if (piece > 0 && !(ok = wait_warp(&s.q_empty, piece - 1))) break;
+          const int i0 = x.unit * UNIT, rows = x.pair ? 2 * kRows : kRows;
+          const uint32_t flip = p.flip ? 0x80008000u : 0u;
+          for (int j = tid - 256; j < rows * CH; j += kLoaders) {
+            const int r = j / CH, c = j % CH, i = i0 + r;
+            const int row = x.v.row0 + i / p.G;
+            const QT* q = static_cast<const QT*>(p.q) +
+                          ((size_t)row * p.heads + (size_t)x.h * p.G + i % p.G) * HD + c * 8;
+            uint8_t* to = smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c);
+            const bool there = i < x.v.queries;
+            if constexpr (S::kF32) {
+              uint4 part[3] = {};
+              if (there) {
+                const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
+                const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                uint32_t* o = reinterpret_cast<uint32_t*>(part);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float lo = fabsf(f[2 * e]), hi = fabsf(f[2 * e + 1]);
+                  const uint32_t sign = ((__float_as_uint(f[2 * e]) >> 16) & 0x8000u) |
+                                        (__float_as_uint(f[2 * e + 1]) & 0x80000000u);
+#pragma unroll
+                  for (int k = 0; k < 3; ++k) {
+                    const uint32_t u = k < 2 ? cut_bf16(lo, hi) : pack_bf16(lo, hi);
+                    o[k * 4 + e] = u ^ sign ^ flip;
+                  }
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(to + k * kRows * HD * 2) = part[k];
+            } else {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (there) v = *reinterpret_cast<const uint4*>(q);
+              v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+              *reinterpret_cast<uint4*>(to) = v;
+            }
+          }
+          fence_proxy_async();
+          mbar_arrive(&s.q_full);
+        }
+      }
+      ++piece;
+    }
+    cp_async_wait<0>();
+    fence_proxy_async();
+    if (ok)
+      for (int i = max(half - kLag, 0); i < half; ++i) mbar_arrive(&s.full[i % NH]);
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ tensor cores
+    if (lane == 0) {
+      const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ;
+      const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
+      const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
+      constexpr int kSub = HD < 64 ? 2 : 4;  // steps of 16 dimensions of a row in shared memory
+      int base = 0, piece = 0, made[2] = {0, 0};
+      bool ok = true;
+      while (ok && cur.next(p, x)) {
+        const int jobs = x.pair ? 2 * x.n : x.n;
+        auto scores = [&](int j) {
+          const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j);
+          if (!wait(&s.full[half % NH], half / NH)) return false;
+          tc::fence_after_sync();
+          const uint32_t q = qs + (x.pair ? st : 0) * S::kQ, k = ring + (half % NH) * S::kHalf;
+#pragma unroll
+          for (int part = 0; part < S::kQParts; ++part)
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i)
+              tc::mma_bf16(tmem + st * 256,
+                           desc<S::kPitch>(q + part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32, 16),
+                           desc<S::kPitch>(k + (i / kSub) * (KT * 128) + (i % kSub) * 32, 16), is, part + i > 0);
+          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
+          tc::commit(&s.s_full[st]);
+          mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
+          if (j == jobs - 1) tc::commit(&s.q_empty);
+          return true;
+        };
+        auto sums = [&](int j) {
+          const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j) + 1;
+          if (!wait(&s.p_full[st], made[st]) || !wait(&s.full[half % NH], half / NH)) return false;
+          ++made[st];
+          if (j == 0 && piece > 0 && !wait(&s.o_free, piece - 1)) return false;
+          tc::fence_after_sync();
+          const uint32_t v = ring + (half % NH) * S::kHalf, a = tmem + st * 256;
+#pragma unroll
+          for (int part = 0; part < S::kPParts; ++part)
+#pragma unroll
+            for (int i = 0; i < KT / 16; ++i)
+              mma_from_tmem(a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
+                            desc<S::kPitch>(v + i * 16 * S::kPitch, KT * 128), io, j > 1 || part + i > 0);
+          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
+          return true;
+        };
+        ok = wait(&s.q_full, piece) && scores(0) && (jobs < 2 || scores(1));
+        for (int j = 0; ok && j < jobs; ++j) {
+          ok = sums(j);
+          if (ok && j + 2 < jobs) ok = scores(j + 2);
+        }
+        if (ok) tc::commit(&s.done);
+        base += 2 * x.n;
+        ++piece;
+      }
+      tc::commit(&s.drain);
+      mbar_wait(&s.drain, 0);  // whatever happened: tensor memory is given back behind it
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int st = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + st * 256 + quarter, to = ts + 128;
+    int jobs = 0, tile = 0, piece = 0;
+    bool ok = true;
+    while (cur.next(p, x)) {
+      float ref = neg_inf(), l = 0.f;
+      bool any = false;
+      for (int t = x.pair ? 0 : st; ok && t < x.n; t += x.pair ? 1 : 2) {
+        if (!(ok = wait_warp(&s.s_full[st], jobs))) break;
+        ++jobs;
+        tc::fence_after_sync();
+        uint32_t mask[KT / 32];
+        bool all = true;
+        {
+          const uint32_t* m = s.mask[(tile + t) % kMasks];
+#pragma unroll
+          for (int c = 0; c < KT / 32; ++c) {
+            mask[c] = KT == 128 ? m[c] : m[2 * c] | m[2 * c + 1] << 16;
+            all &= mask[c] == 0xffffffffu;
+          }
+        }
+        float mx = neg_inf();
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(ts + c * 32, r);
+          tmem_wait_ld();
+          if (all) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (mask[c] >> i) & 1u ? __uint_as_float(r[i]) : neg_inf());
+          }
+        }
+        mx = mx == neg_inf() ? mx : mx * p.scale;
+        const bool over = mx > ref;
+        if (!any) {
+          ref = mx + kSlack;
+        } else if (__any_sync(0xffffffffu, over)) {
+          // the sums so far are of tiles whose products are done (the scores came behind them)
+          const float to_ref = over ? mx + kSlack : ref;
+          const float f = over ? ex2(ref - to_ref) : 1.f;
+          ref = to_ref;
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(to + c * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+            tmem_st32(to + c * 32, r);
+          }
+        }
+        any = true;
+        const float sub = finite_or_zero(ref);
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t r[32], w[32], w3[S::kF32 ? 16 : 1];
+          tmem_ld32(ts + c * 32, r);
+          tmem_wait_ld();
+          float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y = ex2(fmaf(__uint_as_float(r[2 * i]), p.scale, -sub));
+            float z = ex2(fmaf(__uint_as_float(r[2 * i + 1]), p.scale, -sub));
+            if (!all) {
+              if (!((mask[c] >> (2 * i)) & 1u)) y = 0.f;
+              if (!((mask[c] >> (2 * i + 1)) & 1u)) z = 0.f;
+            }
+            a0 += y;
+            a1 += z;
+            w[i] = cut_bf16(y, z);
+            if constexpr (S::kF32) {
+              w[16 + i] = cut_bf16(y, z);
+              w3[i] = pack_bf16(y, z);
+            } else {
+              w[16 + i] = pack_bf16(y, z);
+            }
+          }
+          l += a0 + a1;
+          tmem_st32(ts + c * 32, w);
+          if constexpr (S::kF32) tmem_st16(ts + KT + c * 16, w3);
+        }
+        tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&s.p_full[st]);
+      }
+      tile += x.n;
+      // ---- the piece's sums
+      if (ok) ok = wait_warp(&s.done, piece);
+      tc::fence_after_sync();
+      if (!ok) ref = 0.f, l = __int_as_float(0x7fc00000);
+      const int i0 = x.unit * UNIT + (x.pair ? st * kRows : 0), i = i0 + row;
+      const bool live = i < x.v.queries, cut = !(x.first && x.last);
+      float f[2] = {1.f, 1.f}, m = ref;
+      if (!x.pair) {
+        s.ml[st][row] = make_float2(ref, l);
+        bar_sync(1, 2 * kRows);
+        const float2 a = s.ml[0][row], b = s.ml[1][row];
+        m = fmaxf(a.x, b.x);
+        const float sub = finite_or_zero(m);
+        f[0] = ex2(a.x - sub);
+        f[1] = ex2(b.x - sub);
+        l = a.y * f[0] + b.y * f[1];
+      }
+      const size_t slot = (size_t)blockIdx.x * 2 + (x.first ? 1 : 0);
+      const size_t head = (size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G;
+      float* out = cut ? p.part + (slot * UNIT + (x.pair ? st * kRows : 0)) * HD + row * 4 : p.whole + head * HD;
+      const size_t step = cut ? kRows * 4 : 4;  // floats from four dimensions to the next four
+      if (live && (x.pair || st == 0)) {
+        if (cut) p.part_ml[slot * UNIT + (x.pair ? st * kRows : 0) + row] = make_float2(m, l);
+        else p.whole_ml[head] = make_float2(m, l);
+      }
+      if (ok) {
+        const int c0 = x.pair ? 0 : st * (HD / 2), c1 = x.pair ? HD : c0 + HD / 2;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 16) {
+          float v[16];
+          if (x.pair) {
+            tc::tmem_ld16(to + c, v);
+          } else {
+            tc::tmem_ld16(tmem + quarter + 128 + c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= f[0];
+            if (x.n > 1) {
+              float v1[16];
+              tc::tmem_ld16(tmem + quarter + 256 + 128 + c, v1);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = fmaf(v1[e], f[1], v[e]);
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<float4*>(out + (c / 4 + e) * step) =
+                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        }
+      }
+      tc::fence_before_sync();
+      mbar_arrive(&s.o_free);
+      ++piece;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 12) tc::tmem_dealloc(tmem, 512);
+}
+
+template <typename QT, int HD>
+cudaError_t launch(const Params& p, int ctas, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<QT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem_bytes<QT, HD>);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(prefix_kernel<QT, HD>, dim3((unsigned)ctas), kThreads, smem_bytes<QT, HD>, 0, s, p);
+}
+
+// queries of a unit
+inline int unit_queries(bool q_bf16) { return q_bf16 ? 2 * kRows : kRows; }
+
+cudaError_t launch_bf16(const Params& p, int ctas, cudaStream_t s);  // bf16 queries
+cudaError_t launch_f32(const Params& p, int ctas, cudaStream_t s);   // f32 queries
+
+}  // namespace prefix
+}  // namespace rqk
