@@ -13,14 +13,15 @@
 // that is cut each piece leaves (ref, l, O) in its CTA's scratch, and paged_prefix.cu joins them with
 // the rows' own requests.
 //
-// A CTA is 13 warps:
+// A CTA is 11 warps (168 registers a thread; with 13 it is 128, and spills that miss the little L1
+// beside 227 KB of shared memory):
 //   0-3, 4-7  two softmax streams: a thread has one query's row of S. With 256 queries a stream has
 //             128 of them and both read the same keys; with up to 128 the streams take turns by
 //             tiles and are added at the end. While one forms P the tensor cores work for the other.
-//   8-11      the loaders: 16-byte cp.async of K and V rows by the block table into a ring, in the
+//   8, 9      the loaders: 16-byte cp.async of K and V rows by the block table into a ring, in the
 //             swizzled layouts that the tensor cores read (K with dimensions inside, V with dimensions
 //             outside: the same rows, read transposed)
-//   12        one thread issues all tcgen05.mma: S_j+2 behind O_j, in order, so that S_j+2 being there
+//   10        one thread issues all tcgen05.mma: S_j+2 behind O_j, in order, so that S_j+2 being there
 //             says that O_j is done too
 //
 // bf16 queries enter as they are and P in two bf16 parts (16 bits); f32 queries and their P in three
@@ -43,9 +44,8 @@ using paged_attn::finite_or_zero;
 using paged_attn::neg_inf;
 using paged_attn::pack_bf16;
 
-constexpr int kThreads = 416, kLoaders = 128;
+constexpr int kThreads = 352, kLoaders = 64;
 constexpr int kRows = 128;       // queries of a stream
-constexpr int kLag = 2;          // halves that are in flight when an older one is handed over
 constexpr int kUnitCost = 3;     // what a unit's start and end count, in tiles
 constexpr float kSlack = 8.f;
 constexpr int kMasks = 8;        // tiles whose masks are kept
@@ -84,7 +84,7 @@ struct Shape {
   static constexpr int kRing = kTiles * kQ + NH * kHalf;
   // a row's bytes in shared memory: 64 dimensions, or all 32
   static constexpr int kPitch = HD < 64 ? 64 : 128;
-  static_assert(NH >= 5, "the loaders run three halves ahead of what they hand over");
+  static_assert(NH >= 5, "two tiles and the next one's keys");
   // where 16-byte piece c of row r of R rows lies
   template <int R>
   static __device__ __forceinline__ int at(int r, int c) {
@@ -94,7 +94,7 @@ struct Shape {
 };
 
 struct Small {  // behind the tiles
-  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], p_full[2], done, o_free, drain;
+  uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], done, o_free, drain;
   uint32_t mask[kMasks][4];
   float2 ml[2][kRows];
   long long scan[kThreads / 32], start, start0;
@@ -119,7 +119,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// what was loaded is there; passing the values through keeps their uses behind it
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+      "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+      "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+      "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -140,14 +149,32 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// The issuing warp's instructions, lane by lane: those with `one` set issue.
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(one)
       : "memory");
 }
 // Shared-memory matrix descriptor (tc_common.cuh has the fields) of rows of 128 or 64 bytes in the
@@ -158,8 +185,14 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo) {
   return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)((lbo >> 4) & 0x3fffu) << 16 |
          (uint64_t)((8 * PITCH) >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)(PITCH == 128 ? 2u : 4u) << 61;
 }
+// Between writes that a barrier has passed on and the tensor cores' reads of them. The reader has
+// it: a loader's own would wait for all of its copies in flight.
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// one arrival once this thread's copies so far have landed
+__device__ __forceinline__ void arrive_behind_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------- units and pieces
@@ -247,6 +280,53 @@ struct Cursor {
   }
 };
 
+// A unit's queries into shared memory by the 256 softmax threads, kAhead loads in flight each: in parts, and
+// negated where the scale is negative (the scores then have its size alone). Rows that are not there are 0.
+template <typename QT, int HD>
+__device__ __forceinline__ void load_queries(const Params& p, const Piece& x, uint8_t* smem, int tid) {
+  using S = Shape<QT, HD>;
+  constexpr int CH = HD / 8, STEP = 2 * kRows / CH, kAhead = S::kF32 ? 4 : 8;
+  const int c = tid % CH, rows = x.pair ? 2 * kRows : kRows;
+  const uint32_t flip = p.flip ? 0x80008000u : 0u;
+#pragma unroll 1
+  for (int r0 = tid / CH; r0 < rows; r0 += STEP * kAhead) {
+    uint4 v[kAhead][S::kF32 ? 2 : 1];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = r0 + k * STEP, i = x.unit * S::kUnit + r;
+      const uint4* q = reinterpret_cast<const uint4*>(
+          static_cast<const QT*>(p.q) + ((size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G) * HD + c * 8);
+#pragma unroll
+      for (int e = 0; e < (S::kF32 ? 2 : 1); ++e)
+        v[k][e] = r < rows && i < x.v.queries ? q[e] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = r0 + k * STEP;
+      if (r >= rows) break;
+      uint8_t* to = smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c);
+      if constexpr (S::kF32) {
+        const uint32_t f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+        uint32_t o[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo = __uint_as_float(f[2 * e] & 0x7fffffffu), hi = __uint_as_float(f[2 * e + 1] & 0x7fffffffu);
+          const uint32_t sign = (__byte_perm(f[2 * e], f[2 * e + 1], 0x7632) & 0x80008000u) ^ flip;
+          o[0][e] = cut_bf16(lo, hi) ^ sign;
+          o[1][e] = cut_bf16(lo, hi) ^ sign;
+          o[2][e] = pack_bf16(lo, hi) ^ sign;
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          *reinterpret_cast<uint4*>(to + j * kRows * HD * 2) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      } else {
+        *reinterpret_cast<uint4*>(to) =
+            make_uint4(v[k][0].x ^ flip, v[k][0].y ^ flip, v[k][0].z ^ flip, v[k][0].w ^ flip);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 template <typename QT, int HD>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
@@ -312,11 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   }
   if (tid == 0) {
     for (int i = 0; i < NH; ++i) {
-      mbar_init(&s.full[i], kLoaders);
+      mbar_init(&s.full[i], kLoaders + kLoaders / 32);
       mbar_init(&s.empty[i], 1);
     }
-    mbar_init(&s.q_full, kLoaders);
-    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.q_full, 2 * kRows);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 2);
       mbar_init(&s.p_full[i], kRows);
@@ -327,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     fence_barrier_init();
     s.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzles go by the address
   }
-  if (warp == 12) {
+  if (warp == 10) {
     tc::tmem_alloc(&s.tmem, 512);
     tc::tmem_relinquish();
   }
@@ -348,31 +427,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   Piece x;
 
-  if (warp >= 8 && warp < 12) {
+  if (warp == 8 || warp == 9) {
     // ------------------------------------------------------------ loaders
-    constexpr int RW = KT / 4;          // rows of a warp
+    constexpr int RW = KT / 2;          // rows of a warp
+    constexpr int RL = RW / 32;         // of them a lane looks up
     constexpr int CH = HD / 8;          // 16-byte pieces of a row
     constexpr int RPI = 32 / CH;        // rows of a warp's copy instruction
     const int w = warp - 8, P = p.kv.block_size;
     const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
-    int half = 0, tile = 0, piece = 0;
+    int half = 0, tile = 0;
     bool ok = true;
     while (ok && cur.next(p, x)) {
       const uint16_t* kb = static_cast<const uint16_t*>(p.kv.k) + x.h * p.kv.head_stride;
       const uint16_t* vb = static_cast<const uint16_t*>(p.kv.v) + x.h * p.kv.head_stride;
-      auto id_of = [&](int t) {
-        const int key = (x.v.t0 + x.t + t) * KT + w * RW + lane % RW, page = key / P;
+      auto key_of = [&](int t, int i) { return (x.v.t0 + x.t + t) * KT + w * RW + i * 32 + lane; };
+      auto id_of = [&](int t, int i) {
+        const int key = key_of(t, i), page = key / P;
         if (t >= x.n || key < x.v.lo || key >= x.v.end) return -1;
         return p.table[(size_t)x.v.b * p.W + (page < p.W ? page : page % p.W)];
       };
-      int id_next = id_of(0);
+      int next[RL];
+#pragma unroll
+      for (int i = 0; i < RL; ++i) next[i] = id_of(0, i);
       for (int t = 0; ok && t < x.n; ++t, ++tile) {
-        const int key = (x.v.t0 + x.t + t) * KT + w * RW + lane % RW, id = id_next;
-        id_next = id_of(t + 1);
-        const bool live = id >= 0 && id < p.kv.n_blocks;
-        const uint32_t mask = __ballot_sync(0xffffffffu, live);
-        if (lane == 0) s.mask[tile % kMasks][w] = RW == 32 ? mask : mask & ((1u << (RW & 31)) - 1u);
-        const long long off = live ? id * p.kv.block_stride + (key % P) * p.kv.row_stride : 0;
+        uint32_t mask[RL];
+        long long off[RL];
+#pragma unroll
+        for (int i = 0; i < RL; ++i) {
+          const int id = next[i];
+          next[i] = id_of(t + 1, i);
+          const bool live = id >= 0 && id < p.kv.n_blocks;
+          mask[i] = __ballot_sync(0xffffffffu, live);
+          if (lane == 0) s.mask[tile % kMasks][w * RL + i] = mask[i];
+          off[i] = live ? id * p.kv.block_stride + (key_of(t, i) % P) * p.kv.row_stride : 0;
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           const int slot = half % NH;
@@ -383,123 +471,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < RW / RPI; ++i) {
             const int r = i * RPI + lane / CH;
-            const long long e = __shfl_sync(0xffffffffu, off, r);
-            cp_async16(dst + S::template at<KT>(w * RW + r, c), base + e + c * 8, (mask >> r) & 1u);
+            const long long e = __shfl_sync(0xffffffffu, off[i * RPI / 32], r % 32);
+            cp_async16(dst + S::template at<KT>(w * RW + r, c), base + e + c * 8, (mask[i * RPI / 32] >> (r % 32)) & 1u);
           }
-          cp_async_commit();
           ++half;
-          cp_async_wait<kLag>();
-          if (half > kLag) {
-            fence_proxy_async();
-            mbar_arrive(&s.full[(half - 1 - kLag) % NH]);
-          }
-        }
-        if (ok && t == 0) {
-          // the unit's queries, once the products with the last one's are done
-          if (piece > 0 && !(ok = wait_warp(&s.q_empty, piece - 1))) break;
-          const int i0 = x.unit * UNIT, rows = x.pair ? 2 * kRows : kRows;
-          const uint32_t flip = p.flip ? 0x80008000u : 0u;
-          for (int j = tid - 256; j < rows * CH; j += kLoaders) {
-            const int r = j / CH, c = j % CH, i = i0 + r;
-            const int row = x.v.row0 + i / p.G;
-            const QT* q = static_cast<const QT*>(p.q) +
-                          ((size_t)row * p.heads + (size_t)x.h * p.G + i % p.G) * HD + c * 8;
-            uint8_t* to = smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c);
-            const bool there = i < x.v.queries;
-            if constexpr (S::kF32) {
-              uint4 part[3] = {};
-              if (there) {
-                const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
-                const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                uint32_t* o = reinterpret_cast<uint32_t*>(part);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float lo = fabsf(f[2 * e]), hi = fabsf(f[2 * e + 1]);
-                  const uint32_t sign = ((__float_as_uint(f[2 * e]) >> 16) & 0x8000u) |
-                                        (__float_as_uint(f[2 * e + 1]) & 0x80000000u);
-#pragma unroll
-                  for (int k = 0; k < 3; ++k) {
-                    const uint32_t u = k < 2 ? cut_bf16(lo, hi) : pack_bf16(lo, hi);
-                    o[k * 4 + e] = u ^ sign ^ flip;
-                  }
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(to + k * kRows * HD * 2) = part[k];
-            } else {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (there) v = *reinterpret_cast<const uint4*>(q);
-              v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-              *reinterpret_cast<uint4*>(to) = v;
-            }
-          }
-          fence_proxy_async();
-          mbar_arrive(&s.q_full);
+          arrive_behind_copies(&s.full[slot]);
+          if (lane == 0) mbar_arrive(&s.full[slot]);  // the mask's
         }
       }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ tensor cores
+    // The whole warp walks along, so that addresses stay in uniform registers; lane 0 issues.
+    const uint32_t one = lane == 0;
+    const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ;
+    const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
+    const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
+    constexpr int kSub = HD < 64 ? 2 : 4;  // steps of 16 dimensions of a row in shared memory
+    int base = 0, piece = 0, made[2] = {0, 0};
+    bool ok = true;
+    while (ok && cur.next(p, x)) {
+      const int jobs = x.pair ? 2 * x.n : x.n;
+      auto scores = [&](int j) {
+        const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j);
+        if (!wait_warp(&s.full[half % NH], half / NH)) return false;
+        fence_proxy_async();
+        tc::fence_after_sync();
+        const uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ, 16);
+        const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
+#pragma unroll
+        for (int part = S::kQParts - 1; part >= 0; --part)
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i)
+            mma_ss(one, tmem + st * 256, q + ((part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32) >> 4),
+                   k + (((i / kSub) * (KT * 128) + (i % kSub) * 32) >> 4), is, part < S::kQParts - 1 || i > 0);
+        if (!x.pair || st == 1) commit(one, &s.empty[half % NH]);
+        commit(one, &s.s_full[st]);
+        if (one) mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
+        return true;
+      };
+      auto sums = [&](int j) {
+        const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j) + 1;
+        if (!wait_warp(&s.p_full[st], made[st]) || !wait_warp(&s.full[half % NH], half / NH)) return false;
+        ++made[st];
+        if (j == 0 && piece > 0 && !wait_warp(&s.o_free, piece - 1)) return false;
+        fence_proxy_async();
+        tc::fence_after_sync();
+        const uint32_t a = tmem + st * 256;
+        const uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
+#pragma unroll
+        for (int part = S::kPParts - 1; part >= 0; --part)
+#pragma unroll
+          for (int i = 0; i < KT / 16; ++i)
+            mma_ts(one, a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
+                   v + ((i * 16 * S::kPitch) >> 4), io, j > 1 || part < S::kPParts - 1 || i > 0);
+        if (!x.pair || st == 1) commit(one, &s.empty[half % NH]);
+        return true;
+      };
+      ok = wait_warp(&s.q_full, piece) && scores(0) && (jobs < 2 || scores(1));
+      for (int j = 0; ok && j < jobs; ++j) {
+        ok = sums(j);
+        if (ok && j + 2 < jobs) ok = scores(j + 2);
+      }
+      if (ok) commit(one, &s.done);
+      base += 2 * x.n;
       ++piece;
     }
-    cp_async_wait<0>();
-    fence_proxy_async();
-    if (ok)
-      for (int i = max(half - kLag, 0); i < half; ++i) mbar_arrive(&s.full[i % NH]);
-  } else if (warp == 12) {
-    // ------------------------------------------------------------ tensor cores
-    if (lane == 0) {
-      const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ;
-      const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
-      const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
-      constexpr int kSub = HD < 64 ? 2 : 4;  // steps of 16 dimensions of a row in shared memory
-      int base = 0, piece = 0, made[2] = {0, 0};
-      bool ok = true;
-      while (ok && cur.next(p, x)) {
-        const int jobs = x.pair ? 2 * x.n : x.n;
-        auto scores = [&](int j) {
-          const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j);
-          if (!wait(&s.full[half % NH], half / NH)) return false;
-          tc::fence_after_sync();
-          const uint32_t q = qs + (x.pair ? st : 0) * S::kQ, k = ring + (half % NH) * S::kHalf;
-#pragma unroll
-          for (int part = 0; part < S::kQParts; ++part)
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i)
-              tc::mma_bf16(tmem + st * 256,
-                           desc<S::kPitch>(q + part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32, 16),
-                           desc<S::kPitch>(k + (i / kSub) * (KT * 128) + (i % kSub) * 32, 16), is, part + i > 0);
-          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
-          tc::commit(&s.s_full[st]);
-          mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
-          if (j == jobs - 1) tc::commit(&s.q_empty);
-          return true;
-        };
-        auto sums = [&](int j) {
-          const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j) + 1;
-          if (!wait(&s.p_full[st], made[st]) || !wait(&s.full[half % NH], half / NH)) return false;
-          ++made[st];
-          if (j == 0 && piece > 0 && !wait(&s.o_free, piece - 1)) return false;
-          tc::fence_after_sync();
-          const uint32_t v = ring + (half % NH) * S::kHalf, a = tmem + st * 256;
-#pragma unroll
-          for (int part = 0; part < S::kPParts; ++part)
-#pragma unroll
-            for (int i = 0; i < KT / 16; ++i)
-              mma_from_tmem(a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
-                            desc<S::kPitch>(v + i * 16 * S::kPitch, KT * 128), io, j > 1 || part + i > 0);
-          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
-          return true;
-        };
-        ok = wait(&s.q_full, piece) && scores(0) && (jobs < 2 || scores(1));
-        for (int j = 0; ok && j < jobs; ++j) {
-          ok = sums(j);
-          if (ok && j + 2 < jobs) ok = scores(j + 2);
-        }
-        if (ok) tc::commit(&s.done);
-        base += 2 * x.n;
-        ++piece;
-      }
-      tc::commit(&s.drain);
-      mbar_wait(&s.drain, 0);  // whatever happened: tensor memory is given back behind it
-    }
+    commit(one, &s.drain);
+    mbar_wait(&s.drain, 0);  // whatever happened: tensor memory is given back behind it
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
@@ -509,35 +550,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     int jobs = 0, tile = 0, piece = 0;
     bool ok = true;
     while (cur.next(p, x)) {
+      load_queries<QT, HD>(p, x, smem, tid);  // the last unit's products are done
+      mbar_arrive(&s.q_full);
       float ref = neg_inf(), l = 0.f;
       bool any = false;
       for (int t = x.pair ? 0 : st; ok && t < x.n; t += x.pair ? 1 : 2) {
         if (!(ok = wait_warp(&s.s_full[st], jobs))) break;
         ++jobs;
         tc::fence_after_sync();
-        uint32_t mask[KT / 32];
-        bool all = true;
-        {
-          const uint32_t* m = s.mask[(tile + t) % kMasks];
-#pragma unroll
-          for (int c = 0; c < KT / 32; ++c) {
-            mask[c] = KT == 128 ? m[c] : m[2 * c] | m[2 * c + 1] << 16;
-            all &= mask[c] == 0xffffffffu;
-          }
-        }
+        const uint32_t* mask = s.mask[(tile + t) % kMasks];
         float mx = neg_inf();
-#pragma unroll
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t r[32];
+#pragma unroll 1
+        for (int c = 0; c < KT / 32; c += 2) {
+          uint32_t r[32], r1[32];
           tmem_ld32(ts + c * 32, r);
-          tmem_wait_ld();
-          if (all) {
+          tmem_ld32(ts + c * 32 + 32, r1);
+          tmem_wait_ld(r);
+          tmem_wait_ld(r1);
+          const uint32_t m0 = mask[c], m1 = mask[c + 1];
+          if ((m0 & m1) != 0xffffffffu) {  // scores of no key: -inf, here and for the weights
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (mask[c] >> i) & 1u ? __uint_as_float(r[i]) : neg_inf());
+            for (int i = 0; i < 32; ++i) {
+              if (!((m0 >> i) & 1u)) r[i] = 0xff800000u;
+              if (!((m1 >> i) & 1u)) r1[i] = 0xff800000u;
+            }
+            tmem_st32(ts + c * 32, r);
+            tmem_st32(ts + c * 32 + 32, r1);
+            tmem_wait_st();
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(fmaxf(mx, __uint_as_float(r[i])), __uint_as_float(r1[i]));
         }
         mx = mx == neg_inf() ? mx : mx * p.scale;
         const bool over = mx > ref;
@@ -553,42 +595,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           for (int c = 0; c < HD / 32; ++c) {
             uint32_t r[32];
             tmem_ld32(to + c * 32, r);
-            tmem_wait_ld();
+            tmem_wait_ld(r);
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
             tmem_st32(to + c * 32, r);
           }
         }
         any = true;
-        const float sub = finite_or_zero(ref);
-#pragma unroll
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t r[32], w[32], w3[S::kF32 ? 16 : 1];
-          tmem_ld32(ts + c * 32, r);
-          tmem_wait_ld();
-          float a0 = 0.f, a1 = 0.f;
+        const f32x2 scale2 = pack2(p.scale, p.scale), sub2 = pack2(-finite_or_zero(ref), -finite_or_zero(ref));
+        f32x2 sum2 = pack2(0.f, 0.f);
+        // P of 32 keys: its parts over the scores (a third one behind them)
+        auto weigh = [&](int c, const uint32_t (&r)[32]) {
+          uint32_t w[32], w3[S::kF32 ? 16 : 1];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float y = ex2(fmaf(__uint_as_float(r[2 * i]), p.scale, -sub));
-            float z = ex2(fmaf(__uint_as_float(r[2 * i + 1]), p.scale, -sub));
-            if (!all) {
-              if (!((mask[c] >> (2 * i)) & 1u)) y = 0.f;
-              if (!((mask[c] >> (2 * i + 1)) & 1u)) z = 0.f;
-            }
-            a0 += y;
-            a1 += z;
-            w[i] = cut_bf16(y, z);
+            float2 y = unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale2, sub2));
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum2 = add2(sum2, pack2(y.x, y.y));
+            w[i] = cut_bf16(y.x, y.y);
             if constexpr (S::kF32) {
-              w[16 + i] = cut_bf16(y, z);
-              w3[i] = pack_bf16(y, z);
+              w[16 + i] = cut_bf16(y.x, y.y);
+              w3[i] = pack_bf16(y.x, y.y);
             } else {
-              w[16 + i] = pack_bf16(y, z);
+              w[16 + i] = pack_bf16(y.x, y.y);
             }
           }
-          l += a0 + a1;
           tmem_st32(ts + c * 32, w);
           if constexpr (S::kF32) tmem_st16(ts + KT + c * 16, w3);
+        };
+        uint32_t r0[32], r1[32];
+        tmem_ld32(ts, r0);
+#pragma unroll 1
+        for (int c = 0; c < KT / 32; c += 2) {
+          tmem_wait_ld(r0);
+          tmem_ld32(ts + c * 32 + 32, r1);
+          weigh(c, r0);
+          tmem_wait_ld(r1);
+          if (c + 2 < KT / 32) tmem_ld32(ts + c * 32 + 64, r0);
+          weigh(c + 1, r1);
         }
+        const float2 sum = unpack2(sum2);
+        l += sum.x + sum.y;
         tmem_wait_st();
         tc::fence_before_sync();
         mbar_arrive(&s.p_full[st]);
@@ -653,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 12) tc::tmem_dealloc(tmem, 512);
+  if (warp == 10) tc::tmem_dealloc(tmem, 512);
 }
 
 template <typename QT, int HD>
