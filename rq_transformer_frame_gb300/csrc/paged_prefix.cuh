@@ -18,9 +18,11 @@
 //   0-3, 4-7  two softmax streams: a thread has one query's row of S. With 256 queries a stream has
 //             128 of them and both read the same keys; with up to 128 the streams take turns by
 //             tiles and are added at the end. While one forms P the tensor cores work for the other.
-//   8, 9      the loaders: 16-byte cp.async of K and V rows by the block table into a ring, in the
-//             swizzled layouts that the tensor cores read (K with dimensions inside, V with dimensions
-//             outside: the same rows, read transposed)
+//   8, 9      the loaders: K and V rows by the block table into a ring, in the swizzled layouts that
+//             the tensor cores read (K with dimensions inside, V with dimensions outside: the same
+//             rows, read transposed). Blocks of a multiple of eight positions come by TMA, a lane
+//             a box; rows of other blocks by 16-byte cp.async, which keep the load/store unit busy (the
+//             barriers' waits too: 118 us against XX for 64 rows behind 32768 positions)
 //   10        one thread issues all tcgen05.mma: S_j+2 behind O_j, in order, so that S_j+2 being there
 //             says that O_j is done too
 //
@@ -68,6 +70,8 @@ struct Params {
   float2* part_ml;  // [ctas][2][unit queries]
   Group* group;     // [groups]
   long long* per;   // entries of a run
+  int box;          // rows of a TMA box, 0: copies by threads
+  CUtensorMap kmap, vmap;  // [block][head][row][dimension]
 };
 
 template <typename QT, int HD>
@@ -92,19 +96,6 @@ struct Shape {
     return (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   }
 };
-
-struct Small {  // behind the tiles
-  uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], done, o_free, drain;
-  uint32_t mask[kMasks][4];
-  float2 ml[2][kRows];
-  long long scan[kThreads / 32], start, start0;
-  int start_group;
-  uint32_t tmem;
-  volatile int abort;
-};
-
-template <typename QT, int HD>
-constexpr size_t smem_bytes = Shape<QT, HD>::kRing + sizeof(Small);
 
 // ---------------------------------------------------------------- tensor memory
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
@@ -149,32 +140,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// The issuing warp's instructions, lane by lane: those with `one` set issue.
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// One lane of the warp. With a lane chosen by comparing lane numbers the compiler does not know that it is
+// one alone, and each tensor instruction becomes a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(one)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Shared-memory matrix descriptor (tc_common.cuh has the fields) of rows of 128 or 64 bytes in the
@@ -195,6 +177,17 @@ __device__ __forceinline__ void arrive_behind_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A box of a 4-D tensor map into 16-byte aligned shared memory. x times the element size is a multiple
+// of 16 bytes; what lies past an extent is filled with zeros.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int block,
+                                            uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(block), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- units and pieces
 // A group as the list has it. tiles: key tiles [t0, t0 + tiles) of request b, live positions [lo, end)
 struct View {
@@ -202,7 +195,7 @@ struct View {
 };
 
 template <int KT>
-__device__ __forceinline__ View view_of(const Params& p, int g) {
+__device__ __noinline__ View view_of(const Params& p, int g) {
   View v{};
   v.row0 = min(max(p.cu_rows[g], 0), p.rows);
   const int row1 = min(max(p.cu_rows[g + 1], v.row0), p.rows);
@@ -236,6 +229,19 @@ __host__ __device__ __forceinline__ Costs costs_of(int queries, int tiles) {
   return c;
 }
 
+struct Small {  // behind the tiles
+  uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], done, o_free, drain;
+  uint32_t mask[kMasks][4];
+  float2 ml[2][kRows];
+  long long scan[kThreads / 32], start0;
+  int start_group;
+  uint32_t tmem;
+  volatile int abort;
+};
+
+template <typename QT, int HD>
+constexpr size_t smem_bytes = Shape<QT, HD>::kRing + sizeof(Small);
+
 struct Piece {
   View v;
   int h, unit, t, n;  // K/V head, unit of it, tiles [t, t + n)
@@ -247,7 +253,54 @@ template <int KT, int UNIT>
 struct Cursor {
   long long at, stop, list0;
   int g;
-  __device__ __forceinline__ bool next(const Params& p, Piece& x) {
+  static __device__ __noinline__ long long cost_of(const Params& p, int g) {
+    const View v = view_of<KT>(p, g);
+    return costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
+  }
+  // To the start of the CTA's run: prefix sums of the groups' costs, a slice of the groups a thread. False
+  // where the list ends before.
+  __device__ __noinline__ bool start(const Params& p, Small& s) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int slice = (p.groups + kThreads - 1) / kThreads;
+    const int g0 = min(tid * slice, p.groups), g1 = min(g0 + slice, p.groups);
+    long long own = 0;
+#pragma unroll 1
+    for (int i = g0; i < g1; ++i) own += cost_of(p, i);
+    long long inc = own;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s.scan[warp] = inc;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) inc += s.scan[w];
+      total += s.scan[w];
+    }
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2));
+    at = blockIdx.x * per;
+    stop = min(at + per, total);
+    long long first = inc - own;
+    if (blockIdx.x == 0 && tid == 0) *p.per = per;
+    if (blockIdx.x == 0 || (first <= at && at < inc)) {
+#pragma unroll 1
+      for (int i = g0; i < g1; ++i) {
+        const View v = view_of<KT>(p, i);
+        const long long c = costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
+        if (blockIdx.x == 0) p.group[i] = Group{first, v.row0, v.queries, v.tiles, UNIT};
+        if (first <= at && at < first + c) s.start_group = i, s.start0 = first;
+        first += c;
+      }
+    }
+    __syncthreads();
+    g = s.start_group;
+    list0 = s.start0;
+    return at < total;
+  }
+  __device__ __noinline__ bool next(const Params& p, Piece& x) {
     while (at < stop && g < p.groups) {
       x.v = view_of<KT>(p, g);
       const Costs c = costs_of<UNIT>(x.v.queries, x.v.tiles);
@@ -280,25 +333,39 @@ struct Cursor {
   }
 };
 
+// out of line, as is all that runs once a piece: 140 KB of code took 8 us to arrive at each launch
+static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (*abort) return false;
+  if (mbar_wait(bar, parity)) return true;
+  *abort = 1;
+  return false;
+}
+
 // A unit's queries into shared memory by the 256 softmax threads, kAhead loads in flight each: in parts, and
 // negated where the scale is negative (the scores then have its size alone). Rows that are not there are 0.
 template <typename QT, int HD>
-__device__ __forceinline__ void load_queries(const Params& p, const Piece& x, uint8_t* smem, int tid) {
+__device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8_t* smem, int tid) {
   using S = Shape<QT, HD>;
   constexpr int CH = HD / 8, STEP = 2 * kRows / CH, kAhead = S::kF32 ? 4 : 8;
   const int c = tid % CH, rows = x.pair ? 2 * kRows : kRows;
   const uint32_t flip = p.flip ? 0x80008000u : 0u;
+  // the query's row and head of the group, step by step
+  const int first = x.unit * S::kUnit + tid / CH, rows_step = STEP / p.G, heads_step = STEP % p.G;
+  int row = first / p.G, head = first % p.G;
+  const QT* base = static_cast<const QT*>(p.q) + ((size_t)x.v.row0 * p.heads + (size_t)x.h * p.G) * HD + c * 8;
 #pragma unroll 1
   for (int r0 = tid / CH; r0 < rows; r0 += STEP * kAhead) {
     uint4 v[kAhead][S::kF32 ? 2 : 1];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int r = r0 + k * STEP, i = x.unit * S::kUnit + r;
-      const uint4* q = reinterpret_cast<const uint4*>(
-          static_cast<const QT*>(p.q) + ((size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G) * HD + c * 8);
+      const int r = r0 + k * STEP;
+      const uint4* q = reinterpret_cast<const uint4*>(base + ((size_t)row * p.heads + head) * HD);
+      row += rows_step;
+      head += heads_step;
+      if (head >= p.G) head -= p.G, ++row;
 #pragma unroll
       for (int e = 0; e < (S::kF32 ? 2 : 1); ++e)
-        v[k][e] = r < rows && i < x.v.queries ? q[e] : make_uint4(0, 0, 0, 0);
+        v[k][e] = r < rows && x.unit * S::kUnit + r < x.v.queries ? q[e] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -328,7 +395,8 @@ __device__ __forceinline__ void load_queries(const Params& p, const Piece& x, ui
 }
 
 // ---------------------------------------------------------------- the kernel
-template <typename QT, int HD>
+// BOX: blocks come by TMA
+template <typename QT, int HD, bool BOX>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
   using S = Shape<QT, HD>;
   constexpr int KT = S::KT, NH = S::NH, UNIT = S::kUnit;
@@ -338,61 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   pdl_wait();
   pdl_trigger();
 
-  // ---- the list: each thread a slice of the groups, prefix sums of their costs
   Cursor<KT, UNIT> cur;
-  {
-    const int slice = (p.groups + kThreads - 1) / kThreads;
-    const int g0 = min(tid * slice, p.groups), g1 = min(g0 + slice, p.groups);
-    auto cost = [&](int g) {
-      const View v = view_of<KT>(p, g);
-      return costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
-    };
-    long long own = 0;
-    for (int g = g0; g < g1; ++g) own += cost(g);
-    long long inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) s.scan[warp] = inc;
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) inc += s.scan[w];
-      total += s.scan[w];
-    }
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2));
-    const long long begin = blockIdx.x * per;
-    long long at = inc - own;
-    if (blockIdx.x == 0) {
-      for (int g = g0; g < g1; ++g) {
-        const View v = view_of<KT>(p, g);
-        p.group[g] = Group{at, v.row0, v.queries, v.tiles, UNIT};
-        at += costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
-      }
-      if (tid == 0) *p.per = per;
-      at = inc - own;
-    }
-    if (begin >= total) return;
-    if (at <= begin && begin < inc) {
-      for (int g = g0; g < g1; ++g) {
-        const long long c = cost(g);
-        if (begin < at + c) {
-          s.start_group = g;
-          s.start0 = at;
-          break;
-        }
-        at += c;
-      }
-    }
-    cur.at = begin;
-    cur.stop = min(begin + per, total);
-  }
+  if (!cur.start(p, s)) return;
   if (tid == 0) {
     for (int i = 0; i < NH; ++i) {
-      mbar_init(&s.full[i], kLoaders + kLoaders / 32);
+      mbar_init(&s.full[i], BOX ? 1 : kLoaders + kLoaders / 32);
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.q_full, 2 * kRows);
@@ -414,21 +432,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
-  cur.g = s.start_group;
-  cur.list0 = s.start0;
-  // a wait that runs out ends the CTA's work: its sums become NaN. wait: of one thread, wait_warp: of a
-  // warp, all of whose lanes go on or none
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (s.abort) return false;
-    if (mbar_wait(bar, parity & 1u)) return true;
-    s.abort = 1;
-    return false;
+  // of a warp, all of whose lanes go on or none; a wait that runs out ends the CTA's work: its sums
+  // become NaN
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1u))) return true;
+    return __all_sync(0xffffffffu, slow_wait(bar, parity & 1u, &s.abort)) != 0;
   };
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   Piece x;
 
-  if (warp == 8 || warp == 9) {
-    // ------------------------------------------------------------ loaders
+  if (warp == 8 && BOX) {
+    // ------------------------------------------------------------ loader: TMA
+    // Lane i has box i of a half: rows [g BR, g BR + BR) of the tile, 64 dimensions (or all 32). A box is
+    // of one page; where that has no block it is read past the last one and filled with zeros. What
+    // lies in a box behind the prefix's end must not be read, so that box's rows are copied by the warp.
+    constexpr int kSubs = HD < 64 ? 1 : HD / 64;
+    const int BR = p.box, nb = KT / BR, g = lane % nb, sub = lane / nb, P = p.kv.block_size;
+    const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
+    const uint64_t pol = l2_policy_evict_last();  // other CTAs' queries may read it too
+    int half = 0, tile = 0;
+    bool ok = true;
+    if (lane == 0) {
+      tc::prefetch_tmap(&p.kmap);
+      tc::prefetch_tmap(&p.vmap);
+    }
+    while (ok && cur.next(p, x)) {
+      auto id_of = [&](int t) {
+        const int key = (x.v.t0 + x.t + t) * KT + g * BR, page = key / P;
+        if (t >= x.n || key < x.v.lo || key >= x.v.end) return -1;
+        return p.table[(size_t)x.v.b * p.W + (page < p.W ? page : page % p.W)];
+      };
+      int next = id_of(0);
+      for (int t = 0; ok && t < x.n; ++t, ++tile) {
+        const int key0 = (x.v.t0 + x.t + t) * KT, key = key0 + g * BR, id = next;
+        next = id_of(t + 1);
+        const bool live = id >= 0 && id < p.kv.n_blocks;
+        const uint32_t boxes = __ballot_sync(0xffffffffu, live) & (nb < 32 ? (1u << nb) - 1u : ~0u);
+        const uint32_t torn = __ballot_sync(0xffffffffu, live && x.v.end - key < BR) & boxes;
+        if (lane < KT / 32) {
+          uint32_t m = 0;
+#pragma unroll 1
+          for (int r = 0; r < 32; r += min(BR, 32))
+            if ((boxes >> ((lane * 32 + r) / BR)) & 1u) m |= BR >= 32 ? ~0u : ((1u << BR) - 1u) << r;
+          const int left = x.v.end - key0 - lane * 32;  // keys of the word
+          s.mask[tile % kMasks][lane] = left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
+        }
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const int slot = half % NH;
+          if (half >= NH && !(ok = wait_warp(&s.empty[slot], half / NH - 1))) break;
+          if (torn) {
+            const int b = __ffs(torn) - 1, r0 = key0 + b * BR, rows = x.v.end - r0;
+            const long long at = __shfl_sync(0xffffffffu, id, b) * p.kv.block_stride + x.h * p.kv.head_stride +
+                                 (r0 % P) * p.kv.row_stride;
+            const uint16_t* from = static_cast<const uint16_t*>(side == 0 ? p.kv.k : p.kv.v) + at;
+#pragma unroll 1
+            for (int i = lane; i < BR * (HD / 8); i += 32) {
+              const int r = i / (HD / 8), c = i % (HD / 8);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (r < rows) v = *reinterpret_cast<const uint4*>(from + r * p.kv.row_stride + c * 8);
+              *reinterpret_cast<uint4*>(smem + S::kTiles * S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], (uint32_t)((nb - (torn ? 1 : 0)) * BR * HD * 2));
+          __syncwarp();
+          if (sub < kSubs && !((torn >> g) & 1u))
+            tma_load_4d(ring + slot * S::kHalf + sub * (KT * 128) + g * BR * S::kPitch, side == 0 ? &p.kmap : &p.vmap,
+                        sub * 64, live ? key % P : 0, x.h, live ? id : p.kv.n_blocks, &s.full[slot], pol);
+          ++half;
+        }
+      }
+    }
+    // whatever happened: nothing lands behind the CTA's end
+#pragma unroll 1
+    for (int i = max(half - NH, 0); i < half; ++i) mbar_wait(&s.full[i % NH], (uint32_t)(i / NH) & 1u);
+  } else if ((warp == 8 || warp == 9) && !BOX) {
+    // ------------------------------------------------------------ loaders: copies
     constexpr int RW = KT / 2;          // rows of a warp
     constexpr int RL = RW / 32;         // of them a lane looks up
     constexpr int CH = HD / 8;          // 16-byte pieces of a row
@@ -482,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
     cp_async_commit();
     cp_async_wait<0>();
+  } else if (warp == 8 || warp == 9) {
   } else if (warp == 10) {
     // ------------------------------------------------------------ tensor cores
-    // The whole warp walks along, so that addresses stay in uniform registers; lane 0 issues.
-    const uint32_t one = lane == 0;
+    // The whole warp walks along, so that addresses stay in uniform registers; one lane issues.
     const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ;
     const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
     const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
@@ -499,17 +578,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (!wait_warp(&s.full[half % NH], half / NH)) return false;
         fence_proxy_async();
         tc::fence_after_sync();
-        const uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ, 16);
-        const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
+        if (elect_one()) {
+          const uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ, 16);
+          const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
 #pragma unroll
-        for (int part = S::kQParts - 1; part >= 0; --part)
+          for (int part = S::kQParts - 1; part >= 0; --part)
 #pragma unroll
-          for (int i = 0; i < HD / 16; ++i)
-            mma_ss(one, tmem + st * 256, q + ((part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32) >> 4),
-                   k + (((i / kSub) * (KT * 128) + (i % kSub) * 32) >> 4), is, part < S::kQParts - 1 || i > 0);
-        if (!x.pair || st == 1) commit(one, &s.empty[half % NH]);
-        commit(one, &s.s_full[st]);
-        if (one) mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
+            for (int i = 0; i < HD / 16; ++i)
+              tc::mma_bf16(tmem + st * 256,
+                           q + ((part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32) >> 4),
+                           k + (((i / kSub) * (KT * 128) + (i % kSub) * 32) >> 4), is, part < S::kQParts - 1 || i > 0);
+          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
+          tc::commit(&s.s_full[st]);
+          mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
+        }
+        __syncwarp();
         return true;
       };
       auto sums = [&](int j) {
@@ -519,27 +602,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (j == 0 && piece > 0 && !wait_warp(&s.o_free, piece - 1)) return false;
         fence_proxy_async();
         tc::fence_after_sync();
-        const uint32_t a = tmem + st * 256;
-        const uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
+        if (elect_one()) {
+          const uint32_t a = tmem + st * 256;
+          const uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
 #pragma unroll
-        for (int part = S::kPParts - 1; part >= 0; --part)
+          for (int part = S::kPParts - 1; part >= 0; --part)
 #pragma unroll
-          for (int i = 0; i < KT / 16; ++i)
-            mma_ts(one, a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
-                   v + ((i * 16 * S::kPitch) >> 4), io, j > 1 || part < S::kPParts - 1 || i > 0);
-        if (!x.pair || st == 1) commit(one, &s.empty[half % NH]);
+            for (int i = 0; i < KT / 16; ++i)
+              mma_from_tmem(a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
+                            v + ((i * 16 * S::kPitch) >> 4), io, j > 1 || part < S::kPParts - 1 || i > 0);
+          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
+        }
+        __syncwarp();
         return true;
       };
-      ok = wait_warp(&s.q_full, piece) && scores(0) && (jobs < 2 || scores(1));
-      for (int j = 0; ok && j < jobs; ++j) {
-        ok = sums(j);
+      ok = wait_warp(&s.q_full, piece);
+#pragma unroll 1
+      for (int j = -2; ok && j < jobs; ++j) {
+        if (j >= 0) ok = sums(j);
         if (ok && j + 2 < jobs) ok = scores(j + 2);
       }
-      if (ok) commit(one, &s.done);
+      if (ok && elect_one()) tc::commit(&s.done);
+      __syncwarp();
       base += 2 * x.n;
       ++piece;
     }
-    commit(one, &s.drain);
+    if (elect_one()) tc::commit(&s.drain);
+    __syncwarp();
     mbar_wait(&s.drain, 0);  // whatever happened: tensor memory is given back behind it
     __syncwarp();
   } else {
@@ -561,25 +650,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const uint32_t* mask = s.mask[(tile + t) % kMasks];
         float mx = neg_inf();
 #pragma unroll 1
-        for (int c = 0; c < KT / 32; c += 2) {
-          uint32_t r[32], r1[32];
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t r[32];
           tmem_ld32(ts + c * 32, r);
-          tmem_ld32(ts + c * 32 + 32, r1);
           tmem_wait_ld(r);
-          tmem_wait_ld(r1);
-          const uint32_t m0 = mask[c], m1 = mask[c + 1];
-          if ((m0 & m1) != 0xffffffffu) {  // scores of no key: -inf, here and for the weights
+          const uint32_t m = mask[c];
+          if (m != 0xffffffffu) {  // scores of no key: -inf, here and for the weights
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!((m0 >> i) & 1u)) r[i] = 0xff800000u;
-              if (!((m1 >> i) & 1u)) r1[i] = 0xff800000u;
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!((m >> i) & 1u)) r[i] = 0xff800000u;
             tmem_st32(ts + c * 32, r);
-            tmem_st32(ts + c * 32 + 32, r1);
             tmem_wait_st();
           }
+          float m0 = neg_inf(), m1 = neg_inf();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(fmaxf(mx, __uint_as_float(r[i])), __uint_as_float(r1[i]));
+          for (int i = 0; i < 32; i += 4) {
+            m0 = fmaxf(fmaxf(m0, __uint_as_float(r[i])), __uint_as_float(r[i + 1]));
+            m1 = fmaxf(fmaxf(m1, __uint_as_float(r[i + 2])), __uint_as_float(r[i + 3]));
+          }
+          mx = fmaxf(fmaxf(mx, m0), m1);
         }
         mx = mx == neg_inf() ? mx : mx * p.scale;
         const bool over = mx > ref;
@@ -604,9 +693,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         any = true;
         const f32x2 scale2 = pack2(p.scale, p.scale), sub2 = pack2(-finite_or_zero(ref), -finite_or_zero(ref));
         f32x2 sum2 = pack2(0.f, 0.f);
-        // P of 32 keys: its parts over the scores (a third one behind them)
-        auto weigh = [&](int c, const uint32_t (&r)[32]) {
-          uint32_t w[32], w3[S::kF32 ? 16 : 1];
+#pragma unroll 1
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t r[32], w[32], w3[S::kF32 ? 16 : 1];
+          tmem_ld32(ts + c * 32, r);
+          tmem_wait_ld(r);
+          // P of 32 keys: its parts over the scores (a third one behind them)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 y = unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale2, sub2));
@@ -623,17 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           }
           tmem_st32(ts + c * 32, w);
           if constexpr (S::kF32) tmem_st16(ts + KT + c * 16, w3);
-        };
-        uint32_t r0[32], r1[32];
-        tmem_ld32(ts, r0);
-#pragma unroll 1
-        for (int c = 0; c < KT / 32; c += 2) {
-          tmem_wait_ld(r0);
-          tmem_ld32(ts + c * 32 + 32, r1);
-          weigh(c, r0);
-          tmem_wait_ld(r1);
-          if (c + 2 < KT / 32) tmem_ld32(ts + c * 32 + 64, r0);
-          weigh(c + 1, r1);
         }
         const float2 sum = unpack2(sum2);
         l += sum.x + sum.y;
@@ -704,12 +785,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp == 10) tc::tmem_dealloc(tmem, 512);
 }
 
+// The TMA boxes of a cache: p.box and the maps, or box 0 where there are none for it. Rows of a box: the
+// most of a power of two that divides a block and the tile.
+inline cudaError_t set_maps(Params& p, int tile) {
+  p.box = 0;
+  if (p.kv.block_size % 8 != 0) return cudaSuccess;
+  int box = 8;
+  while (box < tile && p.kv.block_size % (2 * box) == 0) box *= 2;
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+    fn.store(f, std::memory_order_release);
+  }
+  const int hd = p.kv.head_dim;
+  const cuuint64_t extent[4] = {(cuuint64_t)hd, (cuuint64_t)p.kv.block_size, (cuuint64_t)p.kv.heads,
+                                (cuuint64_t)p.kv.n_blocks};
+  // the stride of an extent of one is never used; a map takes none of 0
+  auto bytes = [&](int64_t stride, int64_t n) { return (cuuint64_t)(n > 1 ? stride : hd) * 2; };
+  const cuuint64_t stride[3] = {bytes(p.kv.row_stride, p.kv.block_size), bytes(p.kv.head_stride, p.kv.heads),
+                                bytes(p.kv.block_stride, p.kv.n_blocks)};
+  for (cuuint64_t x : stride)
+    if (x == 0 || x >= 1ull << 40) return cudaSuccess;  // rows that are one, or too far apart: copies
+  const cuuint32_t dims[4] = {(cuuint32_t)(hd < 64 ? hd : 64), (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+  auto encode = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+  for (int i = 0; i < 2; ++i)
+    if (encode(i == 0 ? &p.kmap : &p.vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i == 0 ? p.kv.k : p.kv.v, extent, stride,
+               dims, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               hd < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaSuccess;
+  p.box = box;
+  return cudaSuccess;
+}
+
 template <typename QT, int HD>
-cudaError_t launch(const Params& p, int ctas, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(prefix_kernel<QT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem_bytes<QT, HD>);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(prefix_kernel<QT, HD>, dim3((unsigned)ctas), kThreads, smem_bytes<QT, HD>, 0, s, p);
+cudaError_t launch(Params p, int ctas, cudaStream_t s) {
+  cudaError_t err = set_maps(p, Shape<QT, HD>::KT);
+  if (err != cudaSuccess) return err;
+  auto* kernel = p.box ? prefix_kernel<QT, HD, true> : prefix_kernel<QT, HD, false>;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<QT, HD>);
+  if (err != cudaSuccess) return err;
+  return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, smem_bytes<QT, HD>, 0, s, p);
 }
 
 // queries of a unit
