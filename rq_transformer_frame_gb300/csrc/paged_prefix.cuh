@@ -6,31 +6,37 @@
 // matrix product with the prefix. For a tile of keys
 //   S = Q K^T (f32 in tensor memory), P = 2^(scale S - ref), O += P V, l += sum P,
 // ref a running bound of the maximum: it moves, and O and l are scaled, only when a score passes it. It
-// is set kSlack above the maximum met, so that P stays at most 1 and sums in range.
+// is set kSlack above the maximum met, so that P stays at most 1 and sums in range, and is a whole number, so
+// that what is scaled is scaled exactly.
 //
 // A unit is (group, K/V head, 128 or 256 queries). All units' key tiles form one list, cut into
 // equal runs, a CTA each, one CTA an SM. A unit inside one run leaves its sums in row order; of a unit
 // that is cut each piece leaves (ref, l, O) in its CTA's scratch, and paged_prefix.cu joins them with
 // the rows' own requests.
 //
-// A CTA is 11 warps (168 registers a thread; with 13 it is 128, and spills that miss the little L1
+// A CTA is 12 warps (168 registers a thread; with 13 it is 128, and spills that miss the little L1
 // beside 227 KB of shared memory):
-//   0-3, 4-7  two softmax streams: a thread has one query's row of S. With 256 queries a stream has
-//             128 of them and both read the same keys; with up to 128 the streams take turns by
-//             tiles and are added at the end. While one forms P the tensor cores work for the other.
+//   0-7       softmax. Scores come in two streams, each with its S, P and O in tensor memory: with
+//             256 queries a stream has 128 of them and both read the same keys, with up to 128 the
+//             streams take turns by tiles and are added at the end. All eight warps form one stream's P,
+//             two threads a row, while the tensor cores work for the other. (Four warps a stream came
+//             into step: both at P, then both at their products, 48 us where either alone took 26)
 //   8, 9      the loaders: K and V rows by the block table into a ring, in the swizzled layouts that
 //             the tensor cores read (K with dimensions inside, V with dimensions outside: the same
 //             rows, read transposed). Blocks of a multiple of eight positions come by TMA, a lane
 //             a box; rows of other blocks by 16-byte cp.async, which keep the load/store unit busy (the
 //             barriers' waits too: 118 us against XX for 64 rows behind 32768 positions)
-//   10        one thread issues all tcgen05.mma: S_j+2 behind O_j, in order, so that S_j+2 being there
-//             says that O_j is done too
+//   10, 11    issue the tensor cores' work, a stream each: S of the next tile behind O of this one,
+//             in order, so that S being there says that O is done too. With one warp for both
+//             streams its waits, 300 cycles each, were the kernel's (XX us)
 //
 // bf16 queries enter as they are and P in two bf16 parts (16 bits); f32 queries and their P in three
 // (24 bits, every product exact). Parts are cut, not rounded to nearest (paged_attn.cuh, cut_bf16): all
 // are of the value's sign, so an infinite key or value is met by no zero part. P lies in tensor memory,
 // in the columns of the S it was made of.
 #pragma once
+
+#include <type_traits>
 
 #include "paged_attn.cuh"
 
@@ -46,7 +52,7 @@ using paged_attn::finite_or_zero;
 using paged_attn::neg_inf;
 using paged_attn::pack_bf16;
 
-constexpr int kThreads = 352, kLoaders = 64;
+constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kRows = 128;       // queries of a stream
 constexpr int kUnitCost = 3;     // what a unit's start and end count, in tiles
 constexpr float kSlack = 8.f;
@@ -96,6 +102,18 @@ struct Shape {
     return (c >> 3) * (R * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   }
 };
+
+// A pair of weights' leading bf16 parts, cut towards 0, and in p what is left, and 2^-126 with it: above 0
+// where the weight is, however few bits that has. (cut_bf16 cuts just below the weight instead, by three
+// more instructions of the busiest pipe a pair.)
+__device__ __forceinline__ uint32_t cut_part(f32x2& p) {
+  const float2 x = unpack2(p);
+  uint32_t u;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(x.y), "f"(x.x));
+  const float tiny = 1.17549435e-38f;
+  p = add2(add2(p, pack2(-bf16lo(u), -bf16hi(u))), pack2(tiny, tiny));
+  return u;
+}
 
 // ---------------------------------------------------------------- tensor memory
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
@@ -167,8 +185,8 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo) {
   return (uint64_t)((saddr >> 4) & 0x3fffu) | (uint64_t)((lbo >> 4) & 0x3fffu) << 16 |
          (uint64_t)((8 * PITCH) >> 4) << 32 | (uint64_t)1u << 46 | (uint64_t)(PITCH == 128 ? 2u : 4u) << 61;
 }
-// Between writes that a barrier has passed on and the tensor cores' reads of them. The reader has
-// it: a loader's own would wait for all of its copies in flight.
+// Between threads' writes and the tensor cores' reads of them. Behind copies the reader has it: a
+// loader's own would wait for all of its copies in flight.
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -232,7 +250,7 @@ __host__ __device__ __forceinline__ Costs costs_of(int queries, int tiles) {
 struct Small {  // behind the tiles
   uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], done, o_free, drain;
   uint32_t mask[kMasks][4];
-  float2 ml[2][kRows];
+  float row[2][2][kRows];  // of halves of a row, for its other half: [stream][half], maxima, then sums
   long long scan[kThreads / 32], start0;
   int start_group;
   uint32_t tmem;
@@ -241,6 +259,7 @@ struct Small {  // behind the tiles
 
 template <typename QT, int HD>
 constexpr size_t smem_bytes = Shape<QT, HD>::kRing + sizeof(Small);
+static_assert(smem_bytes<uint16_t, 128> <= 227 * 1024 && smem_bytes<float, 128> <= 227 * 1024, "a CTA's shared memory");
 
 struct Piece {
   View v;
@@ -341,6 +360,27 @@ static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, vo
   return false;
 }
 
+// n columns of O times f. Seldom.
+static __device__ __noinline__ void scale_sums(uint32_t at, int n, float f) {
+#pragma unroll 1
+  for (int i = 0; i < n; i += 16) {
+    float v[16];
+    uint32_t r[16];
+    tc::tmem_ld16(at + i, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e] * f);
+    tmem_st16(at + i, r);
+  }
+  tmem_wait_st();
+}
+
+template <typename T>
+__device__ __forceinline__ void swap(T& a, T& b) {
+  const T c = a;
+  a = b;
+  b = c;
+}
+
 // A unit's queries into shared memory by the 256 softmax threads, kAhead loads in flight each: in parts, and
 // negated where the scale is negative (the scores then have its size alone). Rows that are not there are 0.
 template <typename QT, int HD>
@@ -392,6 +432,7 @@ __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8
       }
     }
   }
+  fence_proxy_async();
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -411,16 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < NH; ++i) {
       mbar_init(&s.full[i], BOX ? 1 : kLoaders + kLoaders / 32);
-      mbar_init(&s.empty[i], 1);
+      mbar_init(&s.empty[i], 2);  // both streams
     }
     mbar_init(&s.q_full, 2 * kRows);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 2);
-      mbar_init(&s.p_full[i], kRows);
+      mbar_init(&s.p_full[i], 2 * kRows);
     }
-    mbar_init(&s.done, 1);
+    mbar_init(&s.done, 2);
     mbar_init(&s.o_free, 2 * kRows);
-    mbar_init(&s.drain, 1);
+    mbar_init(&s.drain, 2);
     fence_barrier_init();
     s.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzles go by the address
   }
@@ -492,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
               if (r < rows) v = *reinterpret_cast<const uint4*>(from + r * p.kv.row_stride + c * 8);
               *reinterpret_cast<uint4*>(smem + S::kTiles * S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
             }
+            fence_proxy_async();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], (uint32_t)((nb - (torn ? 1 : 0)) * BR * HD * 2));
@@ -562,65 +604,79 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == 8 || warp == 9) {
-  } else if (warp == 10) {
+  } else if (warp >= 10) {
     // ------------------------------------------------------------ tensor cores
-    // The whole warp walks along, so that addresses stay in uniform registers; one lane issues.
-    const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ;
+    // The whole warp walks along, so that addresses stay in uniform registers; one lane issues. Loops
+    // that stay loops: unrolled, the instructions came late, once each in 3000 cycles.
+    const int st = warp - 10;
+    const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ, ts = tmem + st * 256;
     const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
     const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
     constexpr int kSub = HD < 64 ? 2 : 4;  // steps of 16 dimensions of a row in shared memory
-    int base = 0, piece = 0, made[2] = {0, 0};
+    int base = 0, piece = 0, made = 0;
     bool ok = true;
+    auto behind = [&] {
+      if (!BOX) fence_proxy_async();
+      tc::fence_after_sync();
+    };
     while (ok && cur.next(p, x)) {
-      const int jobs = x.pair ? 2 * x.n : x.n;
-      auto scores = [&](int j) {
-        const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j);
-        if (!wait_warp(&s.full[half % NH], half / NH)) return false;
-        fence_proxy_async();
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ, 16);
-          const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
-#pragma unroll
-          for (int part = S::kQParts - 1; part >= 0; --part)
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i)
-              tc::mma_bf16(tmem + st * 256,
-                           q + ((part * (kRows * HD * 2) + (i / kSub) * (kRows * 128) + (i % kSub) * 32) >> 4),
-                           k + (((i / kSub) * (KT * 128) + (i % kSub) * 32) >> 4), is, part < S::kQParts - 1 || i > 0);
-          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
-          tc::commit(&s.s_full[st]);
-          mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
-        }
-        __syncwarp();
-        return true;
-      };
-      auto sums = [&](int j) {
-        const int st = j & 1, half = base + 2 * (x.pair ? j >> 1 : j) + 1;
-        if (!wait_warp(&s.p_full[st], made[st]) || !wait_warp(&s.full[half % NH], half / NH)) return false;
-        ++made[st];
-        if (j == 0 && piece > 0 && !wait_warp(&s.o_free, piece - 1)) return false;
-        fence_proxy_async();
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint32_t a = tmem + st * 256;
-          const uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
-#pragma unroll
-          for (int part = S::kPParts - 1; part >= 0; --part)
-#pragma unroll
-            for (int i = 0; i < KT / 16; ++i)
-              mma_from_tmem(a + 128, a + (part < 2 ? 32 * (i / 2) + 16 * part + 8 * (i % 2) : KT + 8 * i),
-                            v + ((i * 16 * S::kPitch) >> 4), io, j > 1 || part < S::kPParts - 1 || i > 0);
-          if (!x.pair || st == 1) tc::commit(&s.empty[half % NH]);
-        }
-        __syncwarp();
-        return true;
+      // this stream's tiles t = first, first + step, ..
+      const int first = x.pair ? 0 : st, step = x.pair ? 1 : 2;
+      auto release = [&](int half) {  // by both streams if both read it
+        tc::commit(&s.empty[half % NH]);
+        if (!x.pair) tc::commit(&s.empty[half % NH]);
       };
       ok = wait_warp(&s.q_full, piece);
 #pragma unroll 1
-      for (int j = -2; ok && j < jobs; ++j) {
-        if (j >= 0) ok = sums(j);
-        if (ok && j + 2 < jobs) ok = scores(j + 2);
+      for (int t = first - step; ok && t < x.n; t += step) {
+        if (t >= first) {  // O of tile t
+          const int half = base + 2 * t + 1;
+          if (t == first && piece > 0 && !(ok = wait_warp(&s.o_free, piece - 1))) break;
+          if (!(ok = wait_warp(&s.full[half % NH], half / NH) && wait_warp(&s.p_full[st], made))) break;
+          ++made;
+          behind();
+          if (elect_one()) {
+            uint32_t acc = t > first;
+#pragma unroll 1
+            for (int part = S::kPParts - 1; part >= 0; --part) {
+              uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
+              uint32_t at = ts + (part < 2 ? 16 * part : KT);
+#pragma unroll 1
+              for (int i = 0; i < KT / 32; ++i) {
+                mma_from_tmem(ts + 128, at, v, io, acc);
+                mma_from_tmem(ts + 128, at + 8, v + ((16 * S::kPitch) >> 4), io, 1);
+                v += (32 * S::kPitch) >> 4;
+                at += part < 2 ? 32 : 16;
+                acc = 1;
+              }
+            }
+            release(half);
+          }
+          __syncwarp();
+        }
+        if (t + step < x.n) {  // S of the next one
+          const int half = base + 2 * (t + step);
+          if (!(ok = wait_warp(&s.full[half % NH], half / NH))) break;
+          behind();
+          if (elect_one()) {
+            uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ + (S::kQParts - 1) * (kRows * HD * 2), 16);
+#pragma unroll 1
+            for (int part = S::kQParts - 1; part >= 0; --part) {
+              const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
+#pragma unroll 1
+              for (int sub = 0; sub < HD / 16 / kSub; ++sub)
+#pragma unroll
+                for (int i = 0; i < kSub; ++i)
+                  tc::mma_bf16(ts, q + ((sub * (kRows * 128) + i * 32) >> 4), k + ((sub * (KT * 128) + i * 32) >> 4), is,
+                               part < S::kQParts - 1 || sub + i > 0);
+              q -= (kRows * HD * 2) >> 4;
+            }
+            release(half);
+            tc::commit(&s.s_full[st]);
+            mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
+          }
+          __syncwarp();
+        }
       }
       if (ok && elect_one()) tc::commit(&s.done);
       __syncwarp();
@@ -633,146 +689,149 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    const int st = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + st * 256 + quarter, to = ts + 128;
-    int jobs = 0, tile = 0, piece = 0;
+    // Warps w and w + 4 share rows (and tensor memory lanes): each has half of a tile's keys, and of O's
+    // dimensions where those are scaled or written.
+    constexpr int C = KT / 64;  // 32 keys at a time
+    const int side = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const f32x2 scale2 = pack2(p.scale, p.scale);
+    uint32_t seen[2] = {0, 0};  // tiles of this stream (the next job's), of the other one
+    int tile = 0, piece = 0;
     bool ok = true;
     while (cur.next(p, x)) {
       load_queries<QT, HD>(p, x, smem, tid);  // the last unit's products are done
       mbar_arrive(&s.q_full);
-      float ref = neg_inf(), l = 0.f;
-      bool any = false;
-      for (int t = x.pair ? 0 : st; ok && t < x.n; t += x.pair ? 1 : 2) {
-        if (!(ok = wait_warp(&s.s_full[st], jobs))) break;
-        ++jobs;
-        tc::fence_after_sync();
-        const uint32_t* mask = s.mask[(tile + t) % kMasks];
-        float mx = neg_inf();
+      const int jobs = x.pair ? 2 * x.n : x.n;
+      float ref[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // as seen
 #pragma unroll 1
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(ts + c * 32, r);
-          tmem_wait_ld(r);
-          const uint32_t m = mask[c];
-          if (m != 0xffffffffu) {  // scores of no key: -inf, here and for the weights
+      for (int j = 0; j < jobs; ++j) {
+        const int st = j & 1;
+        const uint32_t ts = lanes + st * 256;
+        // (a partner warp whose wait ran out is still met at the barrier below)
+        if (ok) ok = wait_warp(&s.s_full[st], seen[0]);
+        ++seen[0];
+        tc::fence_after_sync();
+        uint32_t r[C][32];
+#pragma unroll
+        for (int c = 0; c < C; ++c) tmem_ld32(ts + (side * C + c) * 32, r[c]);
+        float mx = neg_inf();
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          tmem_wait_ld(r[c]);
+          const uint32_t m = s.mask[(tile + (x.pair ? j >> 1 : j)) % kMasks][side * C + c];
+          if (m != 0xffffffffu) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((m >> i) & 1u)) r[i] = 0xff800000u;
-            tmem_st32(ts + c * 32, r);
-            tmem_wait_st();
+              if (!((m >> i) & 1u)) r[c][i] = 0xff800000u;
           }
           float m0 = neg_inf(), m1 = neg_inf();
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            m0 = fmaxf(fmaxf(m0, __uint_as_float(r[i])), __uint_as_float(r[i + 1]));
-            m1 = fmaxf(fmaxf(m1, __uint_as_float(r[i + 2])), __uint_as_float(r[i + 3]));
+            m0 = fmaxf(fmaxf(m0, __uint_as_float(r[c][i])), __uint_as_float(r[c][i + 1]));
+            m1 = fmaxf(fmaxf(m1, __uint_as_float(r[c][i + 2])), __uint_as_float(r[c][i + 3]));
           }
-          mx = fmaxf(fmaxf(mx, m0), m1);
+          mx = fmaxf(mx, fmaxf(m0, m1));
         }
+        s.row[st][side][row] = mx;
+        bar_sync(1 + (warp & 3), 64);
+        mx = fmaxf(mx, s.row[st][side ^ 1][row]);
         mx = mx == neg_inf() ? mx : mx * p.scale;
-        const bool over = mx > ref;
-        if (!any) {
-          ref = mx + kSlack;
-        } else if (__any_sync(0xffffffffu, over)) {
-          // the sums so far are of tiles whose products are done (the scores came behind them)
-          const float to_ref = over ? mx + kSlack : ref;
-          const float f = over ? ex2(ref - to_ref) : 1.f;
-          ref = to_ref;
-          l *= f;
-#pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(to + c * 32, r);
-            tmem_wait_ld(r);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-            tmem_st32(to + c * 32, r);
-          }
+        if (__any_sync(0xffffffffu, mx > ref[0])) {
+          const float was = ref[0];
+          if (mx > was) ref[0] = ceilf(mx) + kSlack;  // whole: sums are scaled exactly
+          const float f = ref[0] > was ? ex2(was - ref[0]) : 1.f;
+          l[0] *= f;
+          // the sums so far are of tiles whose products are done (these scores came behind them)
+          if (j > 1) scale_sums(ts + 128 + side * (HD / 2), HD / 2, f);
         }
-        any = true;
-        const f32x2 scale2 = pack2(p.scale, p.scale), sub2 = pack2(-finite_or_zero(ref), -finite_or_zero(ref));
+        const f32x2 sub2 = pack2(-finite_or_zero(ref[0]), -finite_or_zero(ref[0]));
         f32x2 sum2 = pack2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = 0; c < KT / 32; ++c) {
-          uint32_t r[32], w[32], w3[S::kF32 ? 16 : 1];
-          tmem_ld32(ts + c * 32, r);
-          tmem_wait_ld(r);
-          // P of 32 keys: its parts over the scores (a third one behind them)
+        // P, its parts over the scores (a third one behind them)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          uint32_t w[32], w3[S::kF32 ? 16 : 1];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float2 y = unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale2, sub2));
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            sum2 = add2(sum2, pack2(y.x, y.y));
-            w[i] = cut_bf16(y.x, y.y);
-            if constexpr (S::kF32) {
-              w[16 + i] = cut_bf16(y.x, y.y);
-              w3[i] = pack_bf16(y.x, y.y);
-            } else {
-              w[16 + i] = pack_bf16(y.x, y.y);
-            }
+            float2 y = unpack2(fma2(pack2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), scale2, sub2));
+            f32x2 p2 = pack2(ex2(y.x), ex2(y.y));
+            sum2 = add2(sum2, p2);
+            w[i] = cut_part(p2);
+            if constexpr (S::kF32) w[16 + i] = cut_part(p2);
+            y = unpack2(p2);
+            (S::kF32 ? w3[i] : w[16 + i]) = pack_bf16(y.x, y.y);
           }
-          tmem_st32(ts + c * 32, w);
-          if constexpr (S::kF32) tmem_st16(ts + KT + c * 16, w3);
+          tmem_st32(ts + (side * C + c) * 32, w);
+          if constexpr (S::kF32) tmem_st16(ts + KT + (side * C + c) * 16, w3);
         }
-        const float2 sum = unpack2(sum2);
-        l += sum.x + sum.y;
         tmem_wait_st();
         tc::fence_before_sync();
         mbar_arrive(&s.p_full[st]);
+        const float2 sum = unpack2(sum2);
+        l[0] += sum.x + sum.y;
+        swap(seen[0], seen[1]);
+        swap(ref[0], ref[1]);
+        swap(l[0], l[1]);
+      }
+      if (jobs & 1) {
+        swap(seen[0], seen[1]);
+        swap(ref[0], ref[1]);
+        swap(l[0], l[1]);
       }
       tile += x.n;
       // ---- the piece's sums
+      bar_sync(1 + (warp & 3), 64);  // the last maxima have been read
+      s.row[0][side][row] = l[0];
+      s.row[1][side][row] = l[1];
+      bar_sync(1 + (warp & 3), 64);
+      l[0] += s.row[0][side ^ 1][row];
+      l[1] += s.row[1][side ^ 1][row];
       if (ok) ok = wait_warp(&s.done, piece);
       tc::fence_after_sync();
-      if (!ok) ref = 0.f, l = __int_as_float(0x7fc00000);
-      const int i0 = x.unit * UNIT + (x.pair ? st * kRows : 0), i = i0 + row;
-      const bool live = i < x.v.queries, cut = !(x.first && x.last);
-      float f[2] = {1.f, 1.f}, m = ref;
-      if (!x.pair) {
-        s.ml[st][row] = make_float2(ref, l);
-        bar_sync(1, 2 * kRows);
-        const float2 a = s.ml[0][row], b = s.ml[1][row];
-        m = fmaxf(a.x, b.x);
-        const float sub = finite_or_zero(m);
-        f[0] = ex2(a.x - sub);
-        f[1] = ex2(b.x - sub);
-        l = a.y * f[0] + b.y * f[1];
-      }
+      if (!ok) ref[0] = ref[1] = 0.f, l[0] = l[1] = __int_as_float(0x7fc00000);
+      const bool cut = !(x.first && x.last);
       const size_t slot = (size_t)blockIdx.x * 2 + (x.first ? 1 : 0);
-      const size_t head = (size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G;
-      float* out = cut ? p.part + (slot * UNIT + (x.pair ? st * kRows : 0)) * HD + row * 4 : p.whole + head * HD;
-      const size_t step = cut ? kRows * 4 : 4;  // floats from four dimensions to the next four
-      if (live && (x.pair || st == 0)) {
-        if (cut) p.part_ml[slot * UNIT + (x.pair ? st * kRows : 0) + row] = make_float2(m, l);
-        else p.whole_ml[head] = make_float2(m, l);
+      float f[2] = {1.f, 0.f};
+      if (!x.pair) {  // both streams have the same queries
+        const float m = fmaxf(ref[0], ref[1]), sub = finite_or_zero(m);
+        f[0] = ex2(ref[0] - sub);
+        f[1] = ex2(ref[1] - sub);
+        ref[0] = m;
+        l[0] = l[0] * f[0] + l[1] * f[1];
       }
-      if (ok) {
-        const int c0 = x.pair ? 0 : st * (HD / 2), c1 = x.pair ? HD : c0 + HD / 2;
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 16) {
-          float v[16];
-          if (x.pair) {
-            tc::tmem_ld16(to + c, v);
-          } else {
-            tc::tmem_ld16(tmem + quarter + 128 + c, v);
+      for (int st = 0; st < (x.pair ? 2 : 1); ++st) {
+        const int in = st * kRows + row, i = x.unit * UNIT + in;  // of the unit, of the group
+        const size_t head = (size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G;
+        const bool live = i < x.v.queries;
+        float* out = cut ? p.part + (slot * UNIT + st * kRows) * HD + row * 4 : p.whole + head * HD;
+        const size_t step = cut ? kRows * 4 : 4;  // floats from four dimensions to the next four
+        if (live && side == 0) {
+          if (cut) p.part_ml[slot * UNIT + in] = make_float2(ref[0], l[0]);
+          else p.whole_ml[head] = make_float2(ref[0], l[0]);
+        }
+        if (ok) {
+#pragma unroll 1
+          for (int c = side * (HD / 2); c < (side + 1) * (HD / 2); c += 16) {
+            float v[16];
+            tc::tmem_ld16(lanes + st * 256 + 128 + c, v);
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] *= f[0];
-            if (x.n > 1) {
+            if (!x.pair && x.n > 1) {
               float v1[16];
-              tc::tmem_ld16(tmem + quarter + 256 + 128 + c, v1);
+              tc::tmem_ld16(lanes + 256 + 128 + c, v1);
 #pragma unroll
               for (int e = 0; e < 16; ++e) v[e] = fmaf(v1[e], f[1], v[e]);
             }
-          }
-          if (live) {
+            if (live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<float4*>(out + (c / 4 + e) * step) =
-                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4*>(out + (c / 4 + e) * step) =
+                    make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
           }
         }
+        ref[0] = ref[1];
+        l[0] = l[1];
       }
       tc::fence_before_sync();
       mbar_arrive(&s.o_free);
