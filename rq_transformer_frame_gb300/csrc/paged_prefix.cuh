@@ -198,11 +198,11 @@ __device__ __forceinline__ void arrive_behind_copies(uint64_t* bar) {
 // A box of a 4-D tensor map into 16-byte aligned shared memory. x times the element size is a multiple
 // of 16 bytes; what lies past an extent is filled with zeros.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int block,
-                                            uint64_t* bar, uint64_t policy) {
+                                            uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(block), "r"(smem_u32(bar)), "l"(policy)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -381,38 +381,50 @@ __device__ __forceinline__ void swap(T& a, T& b) {
   b = c;
 }
 
-// A unit's queries into shared memory by the 256 softmax threads, kAhead loads in flight each: in parts, and
-// negated where the scale is negative (the scores then have its size alone). Rows that are not there are 0.
+// A unit's queries into shared memory by the 256 softmax threads, negated where the scale is negative (the
+// scores then have its size alone); rows that are not there are 0. bf16 ones are copied, all copies in
+// flight at once, and are there once the caller has waited for them; f32 ones are cut into parts.
 template <typename QT, int HD>
 __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8_t* smem, int tid) {
   using S = Shape<QT, HD>;
-  constexpr int CH = HD / 8, STEP = 2 * kRows / CH, kAhead = S::kF32 ? 4 : 8;
-  const int c = tid % CH, rows = x.pair ? 2 * kRows : kRows;
-  const uint32_t flip = p.flip ? 0x80008000u : 0u;
+  constexpr int CH = HD / 8, STEP = 2 * kRows / CH, kAhead = 4;
+  const int c = tid % CH, rows = x.pair ? 2 * kRows : kRows, last = x.v.queries - 1 - x.unit * S::kUnit;
   // the query's row and head of the group, step by step
   const int first = x.unit * S::kUnit + tid / CH, rows_step = STEP / p.G, heads_step = STEP % p.G;
   int row = first / p.G, head = first % p.G;
   const QT* base = static_cast<const QT*>(p.q) + ((size_t)x.v.row0 * p.heads + (size_t)x.h * p.G) * HD + c * 8;
-#pragma unroll 1
-  for (int r0 = tid / CH; r0 < rows; r0 += STEP * kAhead) {
-    uint4 v[kAhead][S::kF32 ? 2 : 1];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int r = r0 + k * STEP;
-      const uint4* q = reinterpret_cast<const uint4*>(base + ((size_t)row * p.heads + head) * HD);
-      row += rows_step;
-      head += heads_step;
-      if (head >= p.G) head -= p.G, ++row;
-#pragma unroll
-      for (int e = 0; e < (S::kF32 ? 2 : 1); ++e)
-        v[k][e] = r < rows && x.unit * S::kUnit + r < x.v.queries ? q[e] : make_uint4(0, 0, 0, 0);
+  auto next = [&] {
+    const QT* q = base + ((size_t)row * p.heads + head) * HD;
+    row += rows_step;
+    head += heads_step;
+    if (head >= p.G) head -= p.G, ++row;
+    return q;
+  };
+  if constexpr (!S::kF32) {
+#pragma unroll 2
+    for (int r = tid / CH; r < rows; r += STEP) {
+      const QT* q = next();
+      cp_async16(smem_u32(smem) + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c), r <= last ? q : base,
+                 r <= last);
     }
+    cp_async_commit();
+  } else {
+    const uint32_t flip = p.flip ? 0x80008000u : 0u;
+#pragma unroll 1
+    for (int r0 = tid / CH; r0 < rows; r0 += STEP * kAhead) {
+      uint4 v[kAhead][2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int r = r0 + k * STEP;
-      if (r >= rows) break;
-      uint8_t* to = smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c);
-      if constexpr (S::kF32) {
+      for (int k = 0; k < kAhead; ++k) {
+        const QT* q = next();
+        if (r0 + k * STEP > last) q = base;  // of a row that is there, not used
+        v[k][0] = reinterpret_cast<const uint4*>(q)[0];
+        v[k][1] = reinterpret_cast<const uint4*>(q)[1];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = r0 + k * STEP;
+        if (r >= rows) break;
+        uint8_t* to = smem + S::template at<kRows>(r, c);
         const uint32_t f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
         uint32_t o[3][4];
 #pragma unroll
@@ -425,17 +437,30 @@ __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8
         }
 #pragma unroll
         for (int j = 0; j < 3; ++j)
-          *reinterpret_cast<uint4*>(to + j * kRows * HD * 2) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
-      } else {
-        *reinterpret_cast<uint4*>(to) =
-            make_uint4(v[k][0].x ^ flip, v[k][0].y ^ flip, v[k][0].z ^ flip, v[k][0].w ^ flip);
+          *reinterpret_cast<uint4*>(to + j * kRows * HD * 2) =
+              r <= last ? make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+}
+
+// ... and once they are there
+template <typename QT, int HD>
+__device__ __noinline__ void queries_loaded(const Params& p, const Piece& x, uint8_t* smem, int tid) {
+  using S = Shape<QT, HD>;
+  if constexpr (!S::kF32) {
+    cp_async_wait<0>();
+    if (p.flip) {
+      constexpr int CH = HD / 8;
+      for (int r = tid / CH; r < (x.pair ? 2 * kRows : kRows); r += 2 * kRows / CH) {
+        uint4* v = reinterpret_cast<uint4*>(smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, tid % CH));
+        v->x ^= 0x80008000u, v->y ^= 0x80008000u, v->z ^= 0x80008000u, v->w ^= 0x80008000u;
       }
     }
   }
   fence_proxy_async();
 }
 
-// ---------------------------------------------------------------- the kernel
 // BOX: blocks come by TMA
 template <typename QT, int HD, bool BOX>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
@@ -481,21 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   };
   Piece x;
 
-  if (warp == 8 && BOX) {
-    // ------------------------------------------------------------ loader: TMA
-    // Lane i has box i of a half: rows [g BR, g BR + BR) of the tile, 64 dimensions (or all 32). A box is
+  if ((warp == 8 || warp == 9) && BOX) {
+    // ------------------------------------------------------------ loaders: TMA, one the keys, one the values
+    // Lane i has box i of a half (a copy takes some 60 cycles of its warp, 16 of them are a tile's keys of
+    // blocks of 16 positions): rows [g BR, g BR + BR) of the tile, 64 dimensions (or all 32). A box is
     // of one page; where that has no block it is read past the last one and filled with zeros. What
     // lies in a box behind the prefix's end must not be read, so that box's rows are copied by the warp.
     constexpr int kSubs = HD < 64 ? 1 : HD / 64;
     const int BR = p.box, nb = KT / BR, g = lane % nb, sub = lane / nb, P = p.kv.block_size;
     const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
-    const uint64_t pol = l2_policy_evict_last();  // other CTAs' queries may read it too
-    int half = 0, tile = 0;
+    const int side = warp - 8;
+    const CUtensorMap* const map = side == 0 ? &p.kmap : &p.vmap;
+    int tile = 0;
     bool ok = true;
-    if (lane == 0) {
-      tc::prefetch_tmap(&p.kmap);
-      tc::prefetch_tmap(&p.vmap);
-    }
+    if (lane == 0) tc::prefetch_tmap(map);
     while (ok && cur.next(p, x)) {
       auto id_of = [&](int t) {
         const int key = (x.v.t0 + x.t + t) * KT + g * BR, page = key / P;
@@ -509,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const bool live = id >= 0 && id < p.kv.n_blocks;
         const uint32_t boxes = __ballot_sync(0xffffffffu, live) & (nb < 32 ? (1u << nb) - 1u : ~0u);
         const uint32_t torn = __ballot_sync(0xffffffffu, live && x.v.end - key < BR) & boxes;
-        if (lane < KT / 32) {
+        if (side == 0 && lane < KT / 32) {
           uint32_t m = 0;
 #pragma unroll 1
           for (int r = 0; r < 32; r += min(BR, 32))
@@ -517,37 +541,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           const int left = x.v.end - key0 - lane * 32;  // keys of the word
           s.mask[tile % kMasks][lane] = left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
         }
+        const int half = 2 * tile + side, slot = half % NH;
+        if (half >= NH && !(ok = wait_warp(&s.empty[slot], half / NH - 1))) break;
+        if (torn) {
+          const int b = __ffs(torn) - 1, r0 = key0 + b * BR, rows = x.v.end - r0;
+          const long long at = __shfl_sync(0xffffffffu, id, b) * p.kv.block_stride + x.h * p.kv.head_stride +
+                               (r0 % P) * p.kv.row_stride;
+          const uint16_t* from = static_cast<const uint16_t*>(side == 0 ? p.kv.k : p.kv.v) + at;
 #pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          const int slot = half % NH;
-          if (half >= NH && !(ok = wait_warp(&s.empty[slot], half / NH - 1))) break;
-          if (torn) {
-            const int b = __ffs(torn) - 1, r0 = key0 + b * BR, rows = x.v.end - r0;
-            const long long at = __shfl_sync(0xffffffffu, id, b) * p.kv.block_stride + x.h * p.kv.head_stride +
-                                 (r0 % P) * p.kv.row_stride;
-            const uint16_t* from = static_cast<const uint16_t*>(side == 0 ? p.kv.k : p.kv.v) + at;
-#pragma unroll 1
-            for (int i = lane; i < BR * (HD / 8); i += 32) {
-              const int r = i / (HD / 8), c = i % (HD / 8);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (r < rows) v = *reinterpret_cast<const uint4*>(from + r * p.kv.row_stride + c * 8);
-              *reinterpret_cast<uint4*>(smem + S::kTiles * S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
-            }
-            fence_proxy_async();
+          for (int i = lane; i < BR * (HD / 8); i += 32) {
+            const int r = i / (HD / 8), c = i % (HD / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows) v = *reinterpret_cast<const uint4*>(from + r * p.kv.row_stride + c * 8);
+            *reinterpret_cast<uint4*>(smem + S::kTiles * S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], (uint32_t)((nb - (torn ? 1 : 0)) * BR * HD * 2));
-          __syncwarp();
-          if (sub < kSubs && !((torn >> g) & 1u))
-            tma_load_4d(ring + slot * S::kHalf + sub * (KT * 128) + g * BR * S::kPitch, side == 0 ? &p.kmap : &p.vmap,
-                        sub * 64, live ? key % P : 0, x.h, live ? id : p.kv.n_blocks, &s.full[slot], pol);
-          ++half;
+          fence_proxy_async();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], (uint32_t)((nb - (torn ? 1 : 0)) * BR * HD * 2));
+        __syncwarp();
+        if (sub < kSubs && !((torn >> g) & 1u))
+          tma_load_4d(ring + slot * S::kHalf + sub * (KT * 128) + g * BR * S::kPitch, map, sub * 64, live ? key % P : 0,
+                      x.h, live ? id : p.kv.n_blocks, &s.full[slot]);
       }
     }
     // whatever happened: nothing lands behind the CTA's end
 #pragma unroll 1
-    for (int i = max(half - NH, 0); i < half; ++i) mbar_wait(&s.full[i % NH], (uint32_t)(i / NH) & 1u);
+    for (int i = max(tile - NH / 2 - 1, 0); i < tile; ++i) {
+      const int half = 2 * i + side;
+      if (half >= 2 * tile - NH) mbar_wait(&s.full[half % NH], (uint32_t)(half / NH) & 1u);
+    }
   } else if ((warp == 8 || warp == 9) && !BOX) {
     // ------------------------------------------------------------ loaders: copies
     constexpr int RW = KT / 2;          // rows of a warp
@@ -622,9 +645,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     while (ok && cur.next(p, x)) {
       // this stream's tiles t = first, first + step, ..
       const int first = x.pair ? 0 : st, step = x.pair ? 1 : 2;
-      auto release = [&](int half) {  // by both streams if both read it
-        tc::commit(&s.empty[half % NH]);
-        if (!x.pair) tc::commit(&s.empty[half % NH]);
+      // Each half is passed by both streams, also where only one reads it, in its turn: a barrier's parity
+      // tells two uses of a slot apart, and a stream that went on to the next use while the other's half
+      // were still on its way would take that one's phase for its own.
+      auto pass = [&](int t) {
+#pragma unroll 1
+        for (int half = base + 2 * t; half < base + 2 * t + 2; ++half) {
+          if (!wait_warp(&s.full[half % NH], half / NH)) return false;
+          if (lane == 0) mbar_arrive(&s.empty[half % NH]);
+          __syncwarp();
+        }
+        return true;
       };
       ok = wait_warp(&s.q_full, piece);
 #pragma unroll 1
@@ -632,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (t >= first) {  // O of tile t
           const int half = base + 2 * t + 1;
           if (t == first && piece > 0 && !(ok = wait_warp(&s.o_free, piece - 1))) break;
+          if (!x.pair && t > 0 && !(ok = pass(t - 1))) break;
           if (!(ok = wait_warp(&s.full[half % NH], half / NH) && wait_warp(&s.p_full[st], made))) break;
           ++made;
           behind();
@@ -650,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 acc = 1;
               }
             }
-            release(half);
+            tc::commit(&s.empty[half % NH]);
           }
           __syncwarp();
         }
@@ -671,13 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                                part < S::kQParts - 1 || sub + i > 0);
               q -= (kRows * HD * 2) >> 4;
             }
-            release(half);
+            tc::commit(&s.empty[half % NH]);
             tc::commit(&s.s_full[st]);
             mbar_arrive(&s.s_full[st]);  // passes on what the loaders wrote beside the tile
           }
           __syncwarp();
         }
       }
+      if (ok && !x.pair && ((x.n - 1) & 1) != st) ok = pass(x.n - 1);
       if (ok && elect_one()) tc::commit(&s.done);
       __syncwarp();
       base += 2 * x.n;
@@ -698,8 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     uint32_t seen[2] = {0, 0};  // tiles of this stream (the next job's), of the other one
     int tile = 0, piece = 0;
     bool ok = true;
-    while (cur.next(p, x)) {
-      load_queries<QT, HD>(p, x, smem, tid);  // the last unit's products are done
+    Piece y;
+    bool more = cur.next(p, y);
+    if (more) load_queries<QT, HD>(p, y, smem, tid);
+    while (more) {
+      x = y;
+      queries_loaded<QT, HD>(p, x, smem, tid);
       mbar_arrive(&s.q_full);
       const int jobs = x.pair ? 2 * x.n : x.n;
       float ref[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // as seen
@@ -785,8 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       bar_sync(1 + (warp & 3), 64);
       l[0] += s.row[0][side ^ 1][row];
       l[1] += s.row[1][side ^ 1][row];
+      more = cur.next(p, y);
       if (ok) ok = wait_warp(&s.done, piece);
       tc::fence_after_sync();
+      // the unit's products are done: the next one's queries are under way while its sums are written
+      if (more) load_queries<QT, HD>(p, y, smem, tid);
       if (!ok) ref[0] = ref[1] = 0.f, l[0] = l[1] = __int_as_float(0x7fc00000);
       const bool cut = !(x.first && x.last);
       const size_t slot = (size_t)blockIdx.x * 2 + (x.first ? 1 : 0);
