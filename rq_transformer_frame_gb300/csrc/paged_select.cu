@@ -8,17 +8,20 @@
 //
 // Which pages are taken must not hang on the order of f32 sums, so the second kernel takes only what
 // those decide for sure. An f32 score is off by at most
-//   E = eps (32 + 2 G) sum_d (|u+_d| + |u-_d|) * max |bound|,  eps = 2^-24
-// (sums of 8 terms in a lane and 5 levels of lanes, the G queries' sums before, and half as
-// much again), so with t the k-th largest f32 score, a score above t + 2 E is among the k
-// best and one below t - 2 E is not; what lies between is scored again in f64 and ordered by that.
-// With random keys this is the border page itself and in one row of twenty a second one.
+//   E = eps (16 + G) sum_d (|u+_d| + |u-_d|) * max |bound|,  eps = 2^-24
+// (8 terms one after another in a lane, 5 levels of lanes, and the G queries' sums before), so with t the
+// k-th largest f32 score, a score above t + 2 E is among the k best and one below t - 2 E is not; what
+// lies between is scored again in f64 and ordered by that. With random keys this is the border page
+// itself and in one row of ten a second one.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace rqk {
 namespace {
 
-constexpr int kScoreWarps = 8, kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kScoreWarps = 8;
+constexpr int kChunk = 32;  // pages of a warp
 constexpr uint32_t kNone = 0u, kUnsure = 0xffffffffu;  // keys: no candidate; a score that f32 does not hold
 
 struct SelectParams {
@@ -30,7 +33,7 @@ struct SelectParams {
   unsigned long long* fine;  // the same of the f64 scores, where they are wanted
   float* most;          // [rows][heads][chunks] largest |bound|
   int rows, heads, kv_heads, batch, W, n_blocks, block_size, top, first, last;
-  int stride, chunks, chunk;  // pages of a row's keys, chunks of a row, pages of a chunk
+  int stride, chunks, span;  // pages of a row's keys, chunks of kChunk of a row, those of a warp
 };
 
 struct Live {
@@ -57,6 +60,18 @@ __device__ __forceinline__ int block_of(const SelectParams& p, const Live& x, in
 
 __device__ __forceinline__ float widen(const float* p) { return *p; }
 __device__ __forceinline__ float widen(const uint16_t* p) { return bf16lo(*p); }
+// eight values, or TWICE four
+template <bool TWICE>
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = TWICE ? a : reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <bool TWICE>
+__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
+  const uint2 a = reinterpret_cast<const uint2*>(p)[0], b = TWICE ? a : reinterpret_cast<const uint2*>(p)[1];
+  v[0] = bf16lo(a.x), v[1] = bf16hi(a.x), v[2] = bf16lo(a.y), v[3] = bf16hi(a.y);
+  v[4] = bf16lo(b.x), v[5] = bf16hi(b.x), v[6] = bf16lo(b.y), v[7] = bf16hi(b.y);
+}
 
 // f32 bits in the order of the values
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -73,73 +88,80 @@ __device__ __forceinline__ unsigned long long order_of(double v) {
 }
 
 // ---------------------------------------------------------------- scores
-// A warp takes 32 pages of one K/V head at a time. A page's 2 HD values are HD / 4 lanes' (8 each,
-// 16 bytes of bf16 or twice 16 of f32), so a warp reads 128 / HD pages in a step; the sums of eight
-// steps are reduced together, halving the values with the lanes.
+// A warp takes a few times 32 pages of one K/V head. A page's 2 HD values are HD / 4 lanes' (8 each, 16
+// bytes of bf16 or twice 16 of f32), so a warp reads 128 / HD pages in a step; the sums of eight
+// steps are reduced together, halving the values with the lanes, while the next eight are on their way.
 template <typename T, typename QT, int HD>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int L = HD / 4;             // lanes of a page
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) score_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int L = HD / 4;  // lanes of a page
   constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int N = kF32 ? 2 : 1;  // 16-byte pieces of a lane
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int i = lane % L, sub = lane / L;
-  const int G = p.heads / p.kv_heads, parts = p.chunk / 32;
-  const int page0 = blockIdx.x * p.chunk;
+  const int G = p.heads / p.kv_heads;
+  constexpr int GP = L / 8;  // groups of eight steps of a chunk
   for (int row = blockIdx.y; row < p.rows; row += gridDim.y) {
-  const Live x = live_of(p, row);
-  if (x.n <= p.top || page0 >= x.n) continue;  // up to `top` pages all are taken
-  for (int item = warp; item < p.kv_heads; item += kScoreWarps) {
-    const int h = item;
-    // this lane's 8 values of (u-, u+)
-    float u[8] = {};
-    for (int g = 0; g < G; ++g) {
-      const QT* q = static_cast<const QT*>(p.q) + ((size_t)row * p.heads + (size_t)h * G + g) * HD;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool up = kF32 ? e >= 4 : i >= L / 2;
-        const int d = kF32 ? i * 4 + (e & 3) : (i % (L / 2)) * 8 + e;
-        const float y = widen(q + d);
-        u[e] += up ? fmaxf(y, 0.f) : fminf(y, 0.f);
-      }
-    }
-    float most = 0.f;
-    uint32_t* keys = p.keys + ((size_t)row * p.kv_heads + h) * p.stride;
-    for (int part = 0; part < parts; ++part) {
-      const int first = page0 + part * 32;
-      if (first >= x.n) break;
-      const int mine = first + lane < x.n ? block_of(p, x, x.lo + first + lane) : -1;
-      float score = 0.f;
-#pragma unroll 1
-      for (int g = 0; g < L / 8; ++g) {
-        float s[8];
-        uint4 a[8], b[kF32 ? 8 : 1];
+    const Live x = live_of(p, row);
+    if (x.n <= p.top) continue;  // all of them are taken
+    // the CTA's items: p.span chunks of a K/V head each, K/V heads first
+    const int live = (x.n + kChunk - 1) / kChunk, runs = (live + p.span - 1) / p.span;
+    const long long items = (long long)runs * p.kv_heads;
+    for (long long item = (long long)blockIdx.x * kScoreWarps + warp; item < items; item += (long long)gridDim.x * kScoreWarps) {
+      const int h = (int)(item % p.kv_heads), chunk0 = (int)(item / p.kv_heads) * p.span;
+      const int total = min(p.span, live - chunk0) * GP;
+      auto ids_of = [&](int chunk) {
+        const int at = chunk * kChunk + lane;
+        return at < x.n ? block_of(p, x, x.lo + at) : -1;
+      };
+      int mine = ids_of(chunk0), next = ids_of(chunk0 + 1), chunk = chunk0;
+      const char* const base = static_cast<const char*>(p.bounds) + (size_t)h * 2 * HD * sizeof(T) + i * 16;
+      uint4 a[8][N], b[kF32 ? 1 : 8][N];
+      auto load = [&](int ids, int g, auto& v) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int id = __shfl_sync(0xffffffffu, mine, sub * L + g * 8 + j);
-          const T* at = static_cast<const T*>(p.bounds) + ((size_t)max(id, 0) * p.kv_heads + h) * 2 * HD;
-          a[j] = id >= 0 ? *reinterpret_cast<const uint4*>(at + i * (kF32 ? 4 : 8)) : make_uint4(0, 0, 0, 0);
-          if constexpr (kF32)
-            b[j] = id >= 0 ? *reinterpret_cast<const uint4*>(at + HD + i * 4) : make_uint4(0, 0, 0, 0);
+          const int id = __shfl_sync(0xffffffffu, ids, sub * L + g * 8 + j);
+          const char* at = base + (size_t)max(id, 0) * p.kv_heads * 2 * HD * sizeof(T);
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            v[j][e] = id >= 0 ? *reinterpret_cast<const uint4*>(at + e * HD * sizeof(T)) : make_uint4(0, 0, 0, 0);
         }
+      };
+      load(mine, 0, a);
+      // this lane's 8 values of (u-, u+)
+      float u[8] = {};
+      for (int g = 0; g < G; ++g) {
+        const QT* q = static_cast<const QT*>(p.q) + ((size_t)row * p.heads + (size_t)h * G + g) * HD;
+        float y[8];
+        load8<kF32>(q + (kF32 ? i * 4 : (i % (L / 2)) * 8), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool up = kF32 ? e >= 4 : i >= L / 2;
+          u[e] += up ? fmaxf(y[e], 0.f) : fminf(y[e], 0.f);
+        }
+      }
+      float most = 0.f, score = 0.f;
+      const size_t pair = (size_t)row * p.kv_heads + h;
+      auto reduce = [&](int g, const auto& r) {
+        float s[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float v[8];
           if constexpr (kF32) {
-            v[0] = __uint_as_float(a[j].x), v[1] = __uint_as_float(a[j].y);
-            v[2] = __uint_as_float(a[j].z), v[3] = __uint_as_float(a[j].w);
-            v[4] = __uint_as_float(b[j].x), v[5] = __uint_as_float(b[j].y);
-            v[6] = __uint_as_float(b[j].z), v[7] = __uint_as_float(b[j].w);
+            v[0] = __uint_as_float(r[j][0].x), v[1] = __uint_as_float(r[j][0].y);
+            v[2] = __uint_as_float(r[j][0].z), v[3] = __uint_as_float(r[j][0].w);
+            v[4] = __uint_as_float(r[j][N - 1].x), v[5] = __uint_as_float(r[j][N - 1].y);
+            v[6] = __uint_as_float(r[j][N - 1].z), v[7] = __uint_as_float(r[j][N - 1].w);
           } else {
-            v[0] = bf16lo(a[j].x), v[1] = bf16hi(a[j].x), v[2] = bf16lo(a[j].y), v[3] = bf16hi(a[j].y);
-            v[4] = bf16lo(a[j].z), v[5] = bf16hi(a[j].z), v[6] = bf16lo(a[j].w), v[7] = bf16hi(a[j].w);
+            v[0] = bf16lo(r[j][0].x), v[1] = bf16hi(r[j][0].x), v[2] = bf16lo(r[j][0].y), v[3] = bf16hi(r[j][0].y);
+            v[4] = bf16lo(r[j][0].z), v[5] = bf16hi(r[j][0].z), v[6] = bf16lo(r[j][0].w), v[7] = bf16hi(r[j][0].w);
           }
           s[j] = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             s[j] = fmaf(v[e], u[e], s[j]);
-            const float m = fabsf(v[e]);
-            if (m < 3.4028235e38f) most = fmaxf(most, m);  // pages of others are looked at in f64
+            most = fmaxf(most, fabsf(v[e]));
           }
         }
         // lanes i with i % 8 = j end with step j's sum
@@ -160,86 +182,171 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const __grid_co
 #pragma unroll
         for (int o = 8; o < L; o <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
         if (i / 8 == g) score = s[0];
-      }
-      if (first + lane < x.n) {
-        const bool finite = fabsf(score) <= 3.4028235e38f;
-        keys[first + lane] = mine < 0 ? kNone : finite ? order_of(score) : kUnsure;
+        if (g < GP - 1) return;
+        // the chunk's last: out with it
+        const int at = chunk * kChunk + lane;
+        if (at < x.n) {
+          const bool finite = fabsf(score) <= 3.4028235e38f;
+          p.keys[pair * p.stride + at] = mine < 0 ? kNone : finite ? order_of(score) : kUnsure;
+        }
+        const float largest = warp_max(most);
+        if (lane == 0) p.most[pair * p.chunks + chunk] = largest;
+        ++chunk;
+        mine = next;
+        next = ids_of(chunk + 1);
+        most = 0.f;
+      };
+      // (twice the f32 values do not fit the registers)
+      if constexpr (kF32) {
+#pragma unroll 1
+        for (int k = 0; k < total; ++k) {
+          if (k > 0) load(mine, k % GP, a);
+          reduce(k % GP, a);
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < total; k += 2) {
+          if (k + 1 < total) load(k % GP == GP - 1 ? next : mine, (k + 1) % GP, b);
+          reduce(k % GP, a);
+          if (k + 1 >= total) break;
+          if (k + 2 < total) load((k + 1) % GP == GP - 1 ? next : mine, (k + 2) % GP, a);
+          reduce((k + 1) % GP, b);
+        }
       }
     }
-    most = warp_max(most);
-    if (lane == 0) p.most[((size_t)row * p.kv_heads + h) * p.chunks + blockIdx.x] = most;
-  }
   }
 }
 
 // ---------------------------------------------------------------- the best and the list
+// A CTA of NT threads takes a (row, K/V head); a thread takes a run of its pages. All of it is latency:
+// a pass over the keys for their range, one for a histogram over that, one for the keys of the bin that
+// holds the k-th largest (the f32 scores of random keys leave some dozens there, sorted out among
+// themselves), one that counts what is taken and one that writes it.
+constexpr int kBins = 1024, kFew = 1024;
+
+template <int NT>
 struct SelectShared {
-  int hist[256];
-  int warp_a[kSelectWarps], warp_b[kSelectWarps];
-  float f[kSelectWarps];
-  int digit, left;
+  int hist[kBins];
+  uint32_t few[kFew];       // keys, or pages
+  unsigned long long fine[kFew];
+  int warp_a[NT / 32], warp_b[NT / 32];
+  float warp_f[NT / 32], warp_g[NT / 32];
+  uint32_t warp_u[NT / 32], warp_v[NT / 32];
+  int bin, above, n_few;
+  uint32_t kth;
+  unsigned long long border;
 };
 
-// sums over the CTA of two counts, the same in every thread
-__device__ __forceinline__ int2 block_sum(SelectShared& s, int a, int b) {
+// both sums over the CTA, the same in every thread
+template <int NT>
+__device__ __forceinline__ int2 block_sum(SelectShared<NT>& s, int a, int b) {
   a = __reduce_add_sync(0xffffffffu, a);
   b = __reduce_add_sync(0xffffffffu, b);
   __syncthreads();
   if (threadIdx.x % 32 == 0) s.warp_a[threadIdx.x / 32] = a, s.warp_b[threadIdx.x / 32] = b;
   __syncthreads();
-  int2 r = make_int2(0, 0);
-  for (int w = 0; w < kSelectWarps; ++w) r.x += s.warp_a[w], r.y += s.warp_b[w];
-  return r;
+  const int lane = threadIdx.x % 32;
+  return make_int2(__reduce_add_sync(0xffffffffu, lane < NT / 32 ? s.warp_a[lane] : 0),
+                   __reduce_add_sync(0xffffffffu, lane < NT / 32 ? s.warp_b[lane] : 0));
+}
+// the sum of the threads' counts before this one, and of all
+template <int NT>
+__device__ __forceinline__ int2 block_scan(SelectShared<NT>& s, int a) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int inc = a;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp_a[warp] = inc;
+  __syncthreads();
+  const int w = lane < NT / 32 ? s.warp_a[lane] : 0;
+  return make_int2(inc - a + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0), __reduce_add_sync(0xffffffffu, w));
 }
 
-// The k-th largest of the keys key(0 .. n-1), k >= 1 and at most the number of those above 0 (zeros
-// do not count); `left`: how many of the keys equal to it are among the k. Digits of 8 bits
-// from the top, a histogram each.
-template <typename Key, typename F>
-__device__ Key kth_largest(SelectShared& s, int n, int k, F key, int* left) {
-  Key prefix = 0;
-  for (int shift = (int)sizeof(Key) * 8 - 8; shift >= 0; shift -= 8) {
-    __syncthreads();
-    if (threadIdx.x < 256) s.hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-      const Key x = key(i);
-      if (x != 0 && ((x ^ prefix) >> shift) < 256) atomicAdd(&s.hist[(int)(x >> shift) & 255], 1);
+// The bin of s.hist from the top in which the k-th entry lies, and the number above it, by the first warp.
+template <int NT>
+__device__ __forceinline__ void find_bin(SelectShared<NT>& s, int k) {
+  if (threadIdx.x < 32) {
+    constexpr int B = kBins / 32;  // bins of a lane, from the top
+    const int top = kBins - 1 - threadIdx.x * B;
+    int own = 0;
+#pragma unroll 8
+    for (int j = 0; j < B; ++j) own += s.hist[top - j];
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if ((int)threadIdx.x >= o) inc += y;
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      // bins from the top, 8 a lane
-      int own = 0;
-      for (int j = 0; j < 8; ++j) own += s.hist[255 - (threadIdx.x * 8 + j)];
-      int inc = own;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if ((int)threadIdx.x >= o) inc += y;
-      }
-      int before = inc - own;
-      if (before < k && k <= inc) {
-        for (int j = 0; j < 8; ++j) {
-          const int d = 255 - (threadIdx.x * 8 + j), c = s.hist[d];
-          if (before + c >= k) {
-            s.digit = d;
-            s.left = k - before;
-            break;
-          }
-          before += c;
+    int before = inc - own;
+    if (before < k && k <= inc) {
+      for (int j = 0; j < B; ++j) {
+        const int c = s.hist[top - j];
+        if (before + c >= k) {
+          s.bin = top - j;
+          s.above = before;
+          break;
         }
+        before += c;
       }
     }
+  }
+  __syncthreads();
+}
+
+// The k-th largest of the keys that `each` passes to its argument (twice or more: the same each time),
+// all in [low, low + range]; k at least 1 and at most their number; `left`: how many of those equal to it are
+// among the k.
+template <typename Key, int NT, typename Each>
+__device__ Key kth_largest(SelectShared<NT>& s, Key low, Key range, int k, Each each, int* left) {
+  while (true) {
+    const int bits = range == 0 ? 0 : (int)sizeof(Key) * 8 - (sizeof(Key) == 8 ? __clzll((long long)range) : __clz((int)range));
+    const int shift = max(bits - 10, 0);
     __syncthreads();
-    prefix |= (Key)s.digit << shift;
-    k = s.left;
+    for (int i = threadIdx.x; i < kBins; i += NT) s.hist[i] = 0;
+    if (threadIdx.x == 0) s.n_few = 0;
+    __syncthreads();
+    each([&](Key x) {
+      if (x - low <= range) atomicAdd(&s.hist[(int)((x - low) >> shift)], 1);
+    });
+    __syncthreads();
+    find_bin(s, k);
+    low += (Key)s.bin << shift;
+    k -= s.above;
+    range = ((Key)1 << shift) - 1;
+    if (shift == 0) break;
+    if constexpr (sizeof(Key) == 4) {
+      const int n = s.hist[s.bin];
+      if (n <= kFew) {  // sorted out among themselves
+        each([&](Key x) {
+          if (x - low <= range) s.few[atomicAdd(&s.n_few, 1)] = x;
+        });
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += NT) {
+          const uint32_t x = s.few[i];
+          int more = 0, same = 0;
+          for (int j = 0; j < n; ++j) {
+            more += s.few[j] > x;
+            same += s.few[j] == x;
+          }
+          if (more < k && k <= more + same) s.kth = x, s.above = more;  // of equal ones any
+        }
+        __syncthreads();
+        *left = k - s.above;
+        return s.kth;
+      }
+    }
   }
   *left = k;
-  return prefix;
+  return low;
 }
 
-template <typename T, typename QT>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams p, int HD) {
-  __shared__ SelectShared s;
+template <typename T, typename QT, int NT>
+__global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ SelectParams p, int HD) {
+  __shared__ SelectShared<NT> s;
   pdl_wait();
   pdl_trigger();
   const int pair = blockIdx.x, row = pair / p.kv_heads, h = pair % p.kv_heads;
@@ -250,58 +357,73 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   const int G = p.heads / p.kv_heads, want = p.top - p.first - p.last;
   const uint32_t* keys = p.keys + (size_t)pair * p.stride;
   unsigned long long* fine = p.fine + (size_t)pair * p.stride;
+  const bool all = x.n <= p.top;  // no scores then
   auto always = [&](int i) { return i < p.first || i >= x.n - p.last; };
-  // a page's key among those the score decides about
-  auto key = [&](int i) { return always(i) ? kNone : keys[i]; };
-  // what is taken beside the pages that always are: keys above `sure`; of those in [low, sure]
-  // fine keys above `border`, and the first `left` that equal it
+  // the thread's pages [i0, i1), four at a time
+  const int run = ((x.n + NT - 1) / NT + 3) & ~3;
+  const int i0 = min((long long)tid * run, (long long)x.n), i1 = min(i0 + run, x.n);
+  auto each = [&](auto f) {  // f(page, key among those the score decides about)
+#pragma unroll 2
+    for (int i = i0; i < i1; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < i1 && !always(i + j) && k[j] != kNone) f(i + j, k[j]);
+    }
+  };
+  // taken beside the pages that always are: keys above `sure`, and of those in [low, sure] fine keys above
+  // `border` and the first `left` that equal it; without a border all from `low` on
   uint32_t low = 1, sure = 0;
   unsigned long long border = 0;
   int left = 0;
-  bool all = x.n <= p.top;  // no scores then
-  if (!all) {
+  bool ties = false;
+  if (!all && want > 0) {
+    // range and number of the keys, the largest bound and the sum of the queries' sizes, over the CTA
+    uint32_t least = 0xffffffffu, largest = 0;
     int a = 0, b = 0;
-    for (int i = tid; i < x.n; i += kSelectThreads) {
-      const uint32_t v = key(i);
-      a += v != kNone;
-      b += v == kUnsure;
-    }
+    each([&](int, uint32_t k) {
+      a += 1;
+      b += k == kUnsure;
+      least = min(least, k);
+      largest = max(largest, k);
+    });
+    float most = 0.f, sum = 0.f;
+    for (int i = tid; i < (x.n + kChunk - 1) / kChunk; i += NT)
+      most = fmaxf(most, p.most[(size_t)pair * p.chunks + i]);
+    const QT* q = static_cast<const QT*>(p.q) + ((size_t)row * p.heads + (size_t)h * G) * HD;
+    for (int i = tid * 4; i < G * HD; i += NT * 4)
+      sum += fabsf(widen(q + i)) + fabsf(widen(q + i + 1)) + fabsf(widen(q + i + 2)) + fabsf(widen(q + i + 3));
+    least = __reduce_min_sync(0xffffffffu, least);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    most = warp_max(most);
+    sum = warp_sum(sum);
+    if (lane == 0) s.warp_u[warp] = least, s.warp_v[warp] = largest, s.warp_f[warp] = most, s.warp_g[warp] = sum;
     const int2 n = block_sum(s, a, b);
-    if (n.x > want && want > 0) {
-      // the error of the f32 scores
-      float most = 0.f, sum = 0.f;
-      for (int i = tid; i < (x.n + p.chunk - 1) / p.chunk; i += kSelectThreads)
-        most = fmaxf(most, p.most[(size_t)pair * p.chunks + i]);
-      const QT* q = static_cast<const QT*>(p.q) + ((size_t)row * p.heads + (size_t)h * G) * HD;
-      for (int i = tid; i < G * HD; i += kSelectThreads) sum += fabsf(widen(q + i));
-      most = warp_max(most);
-      sum = warp_sum(sum);
-      __syncthreads();
-      if (lane == 0) s.f[warp] = most, s.warp_a[warp] = __float_as_int(sum);
-      __syncthreads();
-      sum = 0.f;
-      for (int w = 0; w < kSelectWarps; ++w) most = fmaxf(most, s.f[w]), sum += __int_as_float(s.warp_a[w]);
-      const float E = (32.f + 2.f * G) * 5.9604645e-8f * sum * most + 1e-36f;
+    if (n.x > want) {
+      const bool in = lane < NT / 32;
+      least = __reduce_min_sync(0xffffffffu, in ? s.warp_u[lane] : 0xffffffffu);
+      largest = __reduce_max_sync(0xffffffffu, in ? s.warp_v[lane] : 0u);
+      most = warp_max(in ? s.warp_f[lane] : 0.f);
+      sum = warp_sum(in ? s.warp_g[lane] : 0.f);
+      const float E = (16.f + G) * 5.9604645e-8f * sum * most + 1e-36f;
       sure = kUnsure;
       if (n.y == 0 && E < 1e38f) {
         int same;
-        const float t = value_of(kth_largest<uint32_t>(s, x.n, want, key, &same));
+        const float t = value_of(kth_largest<uint32_t, NT>(
+            s, least, largest - least, want, [&](auto f) { each([&](int, uint32_t k) { f(k); }); }, &same));
         low = order_of(t - 2.f * E);
         sure = order_of(t + 2.f * E);
       }
       a = b = 0;
-      for (int i = tid; i < x.n; i += kSelectThreads) {
-        const uint32_t v = key(i);
-        a += v > sure;
-        b += v >= low && v <= sure;
-      }
+      each([&](int, uint32_t k) {
+        a += k > sure;
+        b += k >= low && k <= sure;
+      });
       const int2 m = block_sum(s, a, b);
-      border = 0, left = 0;
       if (m.x + m.y > want) {
-        // the others again in f64, a warp each
-        for (int i = warp; i < x.n; i += kSelectWarps) {
-          const uint32_t v = key(i);
-          if (v < low || v > sure) continue;
+        // those between again in f64, a warp each
+        auto score = [&](int i) {
           const T* at = static_cast<const T*>(p.bounds) +
                         ((size_t)block_of(p, x, x.lo + i) * p.kv_heads + h) * 2 * HD;
           double sum = 0.0;
@@ -316,83 +438,118 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             sum += up * (double)widen(at + HD + d) + down * (double)widen(at + d);
           }
           for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == 0) fine[i] = order_of(sum);
-        }
+          return order_of(sum);
+        };
+        const int wanted = want - m.x;
+        if (tid == 0) s.n_few = 0;
         __syncthreads();
-        border = kth_largest<unsigned long long>(
-            s, x.n, want - m.x,
-            [&](int i) {
-              const uint32_t v = key(i);
-              return v >= low && v <= sure ? fine[i] : 0ull;
-            },
-            &left);
+        if (m.y <= kFew) {
+          each([&](int i, uint32_t k) {
+            if (k >= low && k <= sure) s.few[atomicAdd(&s.n_few, 1)] = i;
+          });
+          __syncthreads();
+          for (int e = warp; e < m.y; e += NT / 32) {
+            const unsigned long long v = score(s.few[e]);
+            if (lane == 0) s.fine[e] = v;
+          }
+          __syncthreads();
+          for (int e = tid; e < m.y; e += NT) {
+            const unsigned long long v = s.fine[e];
+            int more = 0, same = 0;
+            for (int j = 0; j < m.y; ++j) {
+              more += s.fine[j] > v;
+              same += s.fine[j] == v;
+            }
+            fine[s.few[e]] = v;
+            if (more < wanted && wanted <= more + same) s.border = v, s.above = more;  // of equal ones any
+          }
+          __syncthreads();
+          border = s.border;
+          left = wanted - s.above;
+        } else {
+          // many alike
+          for (int i1 = warp * 32; i1 < x.n; i1 += NT) {
+            const uint32_t v = i1 + lane < x.n && !always(i1 + lane) ? keys[i1 + lane] : kNone;
+            uint32_t some = __ballot_sync(0xffffffffu, v != kNone && v >= low && v <= sure);
+            while (some) {
+              const int i = i1 + __ffs(some) - 1;
+              some &= some - 1;
+              const unsigned long long f = score(i);
+              if (lane == 0) fine[i] = f;
+            }
+          }
+          __syncthreads();
+          border = kth_largest<unsigned long long, NT>(
+              s, 0ull, ~0ull, wanted,
+              [&](auto f) {
+                each([&](int i, uint32_t k) {
+                  if (k >= low && k <= sure) f(fine[i]);
+                });
+              },
+              &left);
+        }
+        ties = true;
       } else {
         sure = low - 1;  // all of them
       }
-    } else if (want == 0) {
-      low = sure = kUnsure;
-      border = ~0ull;  // none
     }
   }
-  // ---- the list, page after page
-  int done = 0, ties = 0;  // pages written, equal ones met
-  const bool fine_used = low <= sure;
-  for (int i0 = 0; i0 < x.n; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    int take = 0, tie = 0;
-    if (i < x.n) {
-      if (always(i)) {
-        take = 1;
-      } else if (all) {
-        take = block_of(p, x, x.lo + i) >= 0;
-      } else {
-        const uint32_t v = keys[i];
-        if (v == kNone || want == 0) {
-        } else if (!fine_used || v > sure) {
-          take = v > sure;
-        } else if (v >= low) {
-          const unsigned long long f = fine[i];
-          take = f > border;
-          tie = f == border;
+  // ---- the list: what each thread takes of its run, in order
+  int before = 0;  // equal ones in the runs before
+  if (ties) {
+    int n = 0;
+    each([&](int i, uint32_t k) { n += k >= low && k <= sure && fine[i] == border; });
+    before = block_scan(s, n).x;
+  }
+  auto taken = [&](auto f) {
+    int tie = before;
+    if (all) {
+      for (int i = i0; i < i1; ++i)
+        if (always(i) || block_of(p, x, x.lo + i) >= 0) f(i);
+      return;
+    }
+    for (int i = i0; i < i1; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j >= i1) continue;
+        bool take = always(i + j);
+        if (!take && k[j] != kNone && want > 0) {
+          take = k[j] > sure;
+          if (ties && !take && k[j] >= low) {
+            const unsigned long long f64 = fine[i + j];
+            take = f64 > border || (f64 == border && tie < left);
+            tie += f64 == border;
+          }
         }
+        if (take) f(i + j);
       }
     }
-    // equal ones before this page, then pages before it
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-    __syncthreads();
-    if (lane == 0) s.warp_a[warp] = __popc(tied);
-    __syncthreads();
-    int before = ties + __popc(tied & below);
-    for (int w = 0; w < kSelectWarps; ++w) {
-      if (w < warp) before += s.warp_a[w];
-      ties += s.warp_a[w];
-    }
-    if (tie && before < left) take = 1;
-    const uint32_t taken = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) s.warp_b[warp] = __popc(taken);
-    __syncthreads();
-    int at = done + __popc(taken & below);
-    for (int w = 0; w < kSelectWarps; ++w) {
-      if (w < warp) at += s.warp_b[w];
-      done += s.warp_b[w];
-    }
-    if (take && at < p.top) out[at] = x.lo + i;
-  }
-  for (int i = done + tid; i < p.top; i += kSelectThreads) out[i] = -1;
+  };
+  int n = 0;
+  taken([&](int) { ++n; });
+  const int2 at = block_scan(s, n);
+  int to = at.x;
+  taken([&](int i) {
+    if (to < p.top) out[to] = x.lo + i;
+    ++to;
+  });
+  for (int i = at.y + tid; i < p.top; i += NT) out[i] = -1;
 }
 
 struct Layout {
-  int stride, chunk, chunks;
+  int stride, chunks, span;
   size_t keys, fine, most, bytes;
 };
 
-// chunks: two CTAs an SM at least if the rows are few
 inline Layout layout_of(int rows, int kv_heads, int W) {
   Layout x;
   x.stride = (W + 3) & ~3;
-  x.chunk = 32;
-  x.chunks = (W + x.chunk - 1) / x.chunk;
+  x.chunks = (W + kChunk - 1) / kChunk;
+  // a warp's chunks: more than one where the warps that are resident at once (16 an SM) have had two
+  const long long warps = (long long)rows * kv_heads * x.chunks;
+  x.span = (int)std::min<long long>(std::max<long long>(warps / (32ll * std::max(sm_count(), 1)), 1), 8);
   const size_t n = (size_t)rows * kv_heads;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   x.keys = up(n * x.stride * sizeof(uint32_t));
@@ -404,22 +561,26 @@ inline Layout layout_of(int rows, int kv_heads, int W) {
 
 template <typename T, typename QT>
 cudaError_t launch(const SelectParams& p, int hd, cudaStream_t s) {
-  const dim3 grid((unsigned)p.chunks, (unsigned)(p.rows < 65535 ? p.rows : 65535), 1);
+  const long long items = (long long)((p.chunks + p.span - 1) / p.span) * p.kv_heads;
+  const dim3 grid((unsigned)std::min<long long>((items + kScoreWarps - 1) / kScoreWarps, 1 << 20), (unsigned)(p.rows < 65535 ? p.rows : 65535), 1);
   auto* scores = hd == 32 ? score_kernel<T, QT, 32> : hd == 64 ? score_kernel<T, QT, 64> : score_kernel<T, QT, 128>;
   if (p.W > p.top && p.top > p.first + p.last) {  // some row may have to choose
     const cudaError_t e = launch_dependent(scores, grid, kScoreWarps * 32, 0, 0, s, p);
     if (e != cudaSuccess) return e;
   }
+  // threads: eight keys each, but few CTAs are wide ones
+  const bool wide = p.W > 2048;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.rows * p.kv_heads), 1, 1);
-  cfg.blockDim = dim3(kSelectThreads, 1, 1);
+  cfg.blockDim = dim3(wide ? 1024 : 256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<T, QT>, p, hd);
+  return wide ? cudaLaunchKernelEx(&cfg, select_kernel<T, QT, 1024>, p, hd)
+              : cudaLaunchKernelEx(&cfg, select_kernel<T, QT, 256>, p, hd);
 }
 
 rq_status check(const rq_paged_kv* kv, int32_t rows, int32_t max_blocks) {
@@ -481,7 +642,7 @@ extern "C" rq_status rq_paged_select(const rq_paged_kv* kv, const void* bounds, 
   p.first = first;
   p.last = last;
   p.stride = x.stride;
-  p.chunk = x.chunk;
+  p.span = x.span;
   p.chunks = x.chunks;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool b = kv->dtype == RQ_BF16, qb = q_dtype == RQ_BF16;
