@@ -115,20 +115,27 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) score_kernel(const __grid
         const int at = chunk * kChunk + lane;
         return at < x.n ? block_of(p, x, x.lo + at) : -1;
       };
+      // what is read for a page without a block: another's bounds, so that loads hang on nothing
+      auto there = [&](int ids) {
+        const uint32_t some = __ballot_sync(0xffffffffu, ids >= 0);
+        const int other = __shfl_sync(0xffffffffu, ids, some ? __ffs(some) - 1 : 0);
+        return ids >= 0 ? ids : max(other, 0);
+      };
       int mine = ids_of(chunk0), next = ids_of(chunk0 + 1), chunk = chunk0;
+      int at_mine = there(mine), at_next = there(next);
       const char* const base = static_cast<const char*>(p.bounds) + (size_t)h * 2 * HD * sizeof(T) + i * 16;
+      const uint32_t page_bytes = p.kv_heads * 2 * HD * (uint32_t)sizeof(T);
       uint4 a[8][N], b[kF32 ? 1 : 8][N];
       auto load = [&](int ids, int g, auto& v) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int id = __shfl_sync(0xffffffffu, ids, sub * L + g * 8 + j);
-          const char* at = base + (size_t)max(id, 0) * p.kv_heads * 2 * HD * sizeof(T);
+          const char* at = base + (size_t)id * page_bytes;
 #pragma unroll
-          for (int e = 0; e < N; ++e)
-            v[j][e] = id >= 0 ? *reinterpret_cast<const uint4*>(at + e * HD * sizeof(T)) : make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < N; ++e) v[j][e] = *reinterpret_cast<const uint4*>(at + e * HD * sizeof(T));
         }
       };
-      load(mine, 0, a);
+      load(at_mine, 0, a);
       // this lane's 8 values of (u-, u+)
       float u[8] = {};
       for (int g = 0; g < G; ++g) {
@@ -190,26 +197,29 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) score_kernel(const __grid
           p.keys[pair * p.stride + at] = mine < 0 ? kNone : finite ? order_of(score) : kUnsure;
         }
         const float largest = warp_max(most);
-        if (lane == 0) p.most[pair * p.chunks + chunk] = largest;
+        const bool any = __any_sync(0xffffffffu, mine >= 0);
+        if (lane == 0) p.most[pair * p.chunks + chunk] = any ? largest : 0.f;
         ++chunk;
         mine = next;
+        at_mine = at_next;
         next = ids_of(chunk + 1);
+        at_next = there(next);
         most = 0.f;
       };
       // (twice the f32 values do not fit the registers)
       if constexpr (kF32) {
 #pragma unroll 1
         for (int k = 0; k < total; ++k) {
-          if (k > 0) load(mine, k % GP, a);
+          if (k > 0) load(at_mine, k % GP, a);
           reduce(k % GP, a);
         }
       } else {
 #pragma unroll 1
         for (int k = 0; k < total; k += 2) {
-          if (k + 1 < total) load(k % GP == GP - 1 ? next : mine, (k + 1) % GP, b);
+          if (k + 1 < total) load(k % GP == GP - 1 ? at_next : at_mine, (k + 1) % GP, b);
           reduce(k % GP, a);
           if (k + 1 >= total) break;
-          if (k + 2 < total) load((k + 1) % GP == GP - 1 ? next : mine, (k + 2) % GP, a);
+          if (k + 2 < total) load((k + 1) % GP == GP - 1 ? at_next : at_mine, (k + 2) % GP, a);
           reduce((k + 1) % GP, b);
         }
       }
@@ -226,7 +236,7 @@ constexpr int kBins = 1024, kFew = 1024;
 
 template <int NT>
 struct SelectShared {
-  int hist[kBins];
+  int hist[kBins + kBins / 32];  // bin i at i + i / 32: a lane's bins in a bank of their own
   uint32_t few[kFew];       // keys, or pages
   unsigned long long fine[kFew];
   int warp_a[NT / 32], warp_b[NT / 32];
@@ -236,6 +246,8 @@ struct SelectShared {
   uint32_t kth;
   unsigned long long border;
 };
+
+__device__ __forceinline__ int place(int bin) { return bin + bin / 32; }
 
 // both sums over the CTA, the same in every thread
 template <int NT>
@@ -274,7 +286,7 @@ __device__ __forceinline__ void find_bin(SelectShared<NT>& s, int k) {
     const int top = kBins - 1 - threadIdx.x * B;
     int own = 0;
 #pragma unroll 8
-    for (int j = 0; j < B; ++j) own += s.hist[top - j];
+    for (int j = 0; j < B; ++j) own += s.hist[place(top - j)];
     int inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -284,7 +296,7 @@ __device__ __forceinline__ void find_bin(SelectShared<NT>& s, int k) {
     int before = inc - own;
     if (before < k && k <= inc) {
       for (int j = 0; j < B; ++j) {
-        const int c = s.hist[top - j];
+        const int c = s.hist[place(top - j)];
         if (before + c >= k) {
           s.bin = top - j;
           s.above = before;
@@ -306,11 +318,11 @@ __device__ Key kth_largest(SelectShared<NT>& s, Key low, Key range, int k, Each 
     const int bits = range == 0 ? 0 : (int)sizeof(Key) * 8 - (sizeof(Key) == 8 ? __clzll((long long)range) : __clz((int)range));
     const int shift = max(bits - 10, 0);
     __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += NT) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < kBins + kBins / 32; i += NT) s.hist[i] = 0;
     if (threadIdx.x == 0) s.n_few = 0;
     __syncthreads();
     each([&](Key x) {
-      if (x - low <= range) atomicAdd(&s.hist[(int)((x - low) >> shift)], 1);
+      if (x - low <= range) atomicAdd(&s.hist[place((int)((x - low) >> shift))], 1);
     });
     __syncthreads();
     find_bin(s, k);
@@ -319,7 +331,7 @@ __device__ Key kth_largest(SelectShared<NT>& s, Key low, Key range, int k, Each 
     range = ((Key)1 << shift) - 1;
     if (shift == 0) break;
     if constexpr (sizeof(Key) == 4) {
-      const int n = s.hist[s.bin];
+      const int n = s.hist[place(s.bin)];
       if (n <= kFew) {  // sorted out among themselves
         each([&](Key x) {
           if (x - low <= range) s.few[atomicAdd(&s.n_few, 1)] = x;
@@ -362,10 +374,20 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
   // the thread's pages [i0, i1), four at a time
   const int run = ((x.n + NT - 1) / NT + 3) & ~3;
   const int i0 = min((long long)tid * run, (long long)x.n), i1 = min(i0 + run, x.n);
+  // keys of runs of up to eight stay in registers
+  uint4 held[2] = {};
+  if (!all && want > 0 && run <= 8)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (i0 + 4 * j < i1) held[j] = *reinterpret_cast<const uint4*>(keys + i0 + 4 * j);
+  auto four = [&](int i) {
+    if (run <= 8) return i == i0 ? held[0] : held[1];
+    return *reinterpret_cast<const uint4*>(keys + i);
+  };
   auto each = [&](auto f) {  // f(page, key among those the score decides about)
-#pragma unroll 2
+#pragma unroll 1
     for (int i = i0; i < i1; i += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      const uint4 v = four(i);
       const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -415,6 +437,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         low = order_of(t - 2.f * E);
         sure = order_of(t + 2.f * E);
       }
+      // if from `low` on there are as many as are wanted, it is those
       a = b = 0;
       each([&](int, uint32_t k) {
         a += k > sure;
@@ -427,8 +450,12 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
           const T* at = static_cast<const T*>(p.bounds) +
                         ((size_t)block_of(p, x, x.lo + i) * p.kv_heads + h) * 2 * HD;
           double sum = 0.0;
-          for (int d = lane; d < HD; d += 32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int d = j * 32 + lane;
+            if (d >= HD) break;
             double up = 0.0, down = 0.0;
+#pragma unroll 4
             for (int g = 0; g < G; ++g) {
               const double y = (double)widen(q + (size_t)g * HD + d);
               // a NaN query stays in both
@@ -508,14 +535,15 @@ __global__ void __launch_bounds__(NT) select_kernel(const __grid_constant__ Sele
         if (always(i) || block_of(p, x, x.lo + i) >= 0) f(i);
       return;
     }
+#pragma unroll 1
     for (int i = i0; i < i1; i += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      const uint4 v = want > 0 ? four(i) : make_uint4(0, 0, 0, 0);
       const uint32_t k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (i + j >= i1) continue;
         bool take = always(i + j);
-        if (!take && k[j] != kNone && want > 0) {
+        if (!take && k[j] != kNone) {
           take = k[j] > sure;
           if (ties && !take && k[j] >= low) {
             const unsigned long long f64 = fine[i + j];
@@ -547,9 +575,11 @@ inline Layout layout_of(int rows, int kv_heads, int W) {
   Layout x;
   x.stride = (W + 3) & ~3;
   x.chunks = (W + kChunk - 1) / kChunk;
-  // a warp's chunks: more than one where the warps that are resident at once (16 an SM) have had two
+  // a warp's chunks: more than one where those that are resident at once (16 an SM) would have six; rows
+  // are seldom as long as their tables, and long items leave warps idle at the end (64 rows of 31 to 2031
+  // pages of 2048: 38 us with six chunks an item, XX with two)
   const long long warps = (long long)rows * kv_heads * x.chunks;
-  x.span = (int)std::min<long long>(std::max<long long>(warps / (32ll * std::max(sm_count(), 1)), 1), 8);
+  x.span = (int)std::min<long long>(std::max<long long>(warps / (96ll * std::max(sm_count(), 1)), 1), 4);
   const size_t n = (size_t)rows * kv_heads;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   x.keys = up(n * x.stride * sizeof(uint32_t));
