@@ -50,6 +50,7 @@ struct Params {
   float* lse;
   const int32_t *table, *requests, *positions;
   int rows, heads, batch, W, window;
+  int fold;            // rows from here on have the queries of the rows from 0 on (0: none has)
   int G, GB, HG;       // query heads per K/V head (of all a unit reads), of a unit; units of a K/V head
   int runs;            // runs (warps) of the launch
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
@@ -99,6 +100,8 @@ __device__ __forceinline__ int2 row_words(const Params& p, int r) {
   if (LISTS) r /= p.kv_heads;
   return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
 }
+
+__device__ __forceinline__ int q_row(const Params& p, int r) { return p.fold > 0 && r >= p.fold ? r - p.fold : r; }
 
 template <int kKeys, bool LISTS>
 __device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
@@ -921,7 +924,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (start) {  // the unit's queries will be wanted soon
         const int g0 = hg * Core::kHeads, n = min(Core::kHeads, p.G - g0) * HD * (int)sizeof(QT);
         const char* q = static_cast<const char*>(p.q) +
-                        ((size_t)r * p.heads + (size_t)kvh * p.G + g0) * HD * sizeof(QT);
+                        ((size_t)q_row(p, r) * p.heads + (size_t)kvh * p.G + g0) * HD * sizeof(QT);
         if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
       }
       if (end && !last && first)  // goes on in the runs that follow
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       const size_t head = (size_t)d.x * p.heads + (size_t)d.y * p.G + g0;
       if (d.z & kStart) {
         core.clear();
-        core.load(static_cast<const QT*>(p.q) + head * HD, live, lane, scratch);
+        core.load(static_cast<const QT*>(p.q) + (head - (size_t)(d.x - q_row(p, d.x)) * p.heads) * HD, live, lane, scratch);
       }
       cp_async_wait<NS - 1>();
       __syncwarp();

@@ -1,9 +1,9 @@
 // paged_prefix.cu -- attention over a prefix that a group of rows shares and over each row's own
 // request (include/rq.h, rq_paged_prefix_attention).
 //
-// The rows' own requests are paged_attn.cuh's work, with f32 outputs. The prefixes are paged_prefix.cuh's,
-// all rows of a group at once, where the cache is bf16 and there are queries enough for a matrix
-// product; else paged_attn.cuh's too, a row at a time. Then all parts of a row are joined: with o_i, lse_i
+// Where the cache is bf16 and there is work for it, paged_prefix.cuh multiplies all queries of a group with
+// its prefix at once, and the rows' own requests are paged_attn.cuh's work, with f32 outputs. Else both
+// parts of every row are that, as two rows of one launch. Then all parts of a row are joined: with o_i, lse_i
 // of a part, lse = log sum e^lse_i and o = sum e^(lse_i - lse) o_i. All parts are f32, the output is
 // rounded once.
 #include <algorithm>
@@ -20,14 +20,15 @@ using paged_attn::put;
 
 struct PrefixParams {
   const int32_t *requests, *cu_rows, *prefix_requests, *prefix_lens;
+  const int32_t* positions;
   int rows, heads, batch, groups, hd;
-  int32_t *row_request, *row_position;  // of the prefix, for each row
+  int32_t *row_request, *row_position;  // [2 rows], of the prefixes, then the rows' own
   const float *o1, *o2, *lse1, *lse2;   // prefix, own
   void* out;
   float* lse;
 };
 
-// each row's prefix as a request and the last position read of it
+// each row's prefix as a request and the last position read of it, and its own
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PrefixParams p) {
   pdl_wait();
   pdl_trigger();
@@ -50,6 +51,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Prefi
   }
   p.row_request[r] = request;
   p.row_position[r] = position;
+  p.row_request[p.rows + r] = b;
+  p.row_position[p.rows + r] = p.positions[r];
 }
 
 template <typename OT>
@@ -77,7 +80,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Pref
 }
 
 // The prefix kernel's pieces and the own request's part of each query. A lane has one query -- those of
-// a K/V head one after another, as they lie in the pieces -- and a warp some of its dimensions.
+// a K/V head one after another, as they lie in the pieces -- and four dimensions, eight pieces in flight.
+// (32 dimensions of each query a CTA: 64 CTAs of all 128 took 24 us for 2048 queries of 10 pieces.)
 struct JoinParams {
   prefix::Params t;
   const int32_t* requests;
@@ -90,22 +94,23 @@ constexpr int kJoinWarps = 8;
 
 template <typename OT, int HD>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ JoinParams p) {
-  constexpr int E = HD / 4 / kJoinWarps;  // fours of dimensions of a thread
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const long long of_head = (long long)p.t.rows * p.t.G, all = of_head * p.t.kv.heads;
-  const long long idx = (long long)blockIdx.x * 32 + lane;
-  if (idx >= all) return;
-  const int h = (int)(idx / of_head), in = (int)(idx % of_head), r = in / p.t.G, g = in % p.t.G;
-  const int b = p.requests ? p.requests[r] : r;
-  if (b < 0 || b >= p.t.batch) return;
+  const int lane = threadIdx.x % 32, four = blockIdx.y * kJoinWarps + threadIdx.x / 32;
+  const uint32_t of_head = (uint32_t)p.t.rows * p.t.G, idx = blockIdx.x * 32 + lane;
+  if (idx >= of_head * p.t.kv.heads) return;
+  const int h = idx / of_head, in = idx % of_head, r = in / p.t.G, g = in % p.t.G;
   const size_t head = (size_t)r * p.t.heads + (size_t)h * p.t.G + g;
-  // the query's pieces: none, one in row order, or those of runs [c0, c1]
-  long long c0 = 0, c1 = -1;
-  size_t at = 0;  // in a piece
-  int unit = 0;
-  bool whole = false;
+  const int b = p.requests ? p.requests[r] : r;
+  const float own = p.own_lse[head] * 1.4426950408889634f;
+  const float4 own_o = *reinterpret_cast<const float4*>(p.own + head * HD + four * 4);
+  const long long per = *p.t.per;
+  if (b < 0 || b >= p.t.batch) return;
+  // the query's pieces, `count` of them: the first at ml[0] and part[0], the others one run after another
+  int count = 0;
+  const float2 *ml = nullptr, *ml_rest = nullptr;
+  const float *part = nullptr, *part_rest = nullptr;
+  size_t ml_step = 0, part_step = 0;
   {
     int lo = 0, hi = p.t.groups;  // the last group that starts at the row or before
     while (lo < hi) {
@@ -116,57 +121,55 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (lo > 0 && r < p.t.cu_rows[lo]) {
       const prefix::Group x = p.t.group[lo - 1];
       if (x.tiles > 0) {
-        unit = x.unit_rows;
-        const int i = (r - x.row0) * p.t.G + g, u = i / unit;
+        const int unit = x.unit_rows, i = (r - x.row0) * p.t.G + g, u = i / unit, at = i % unit;
         const prefix::Costs c = unit == 256 ? prefix::costs_of<256>(x.queries, x.tiles)
                                             : prefix::costs_of<128>(x.queries, x.tiles);
-        const long long per = *p.t.per, first = x.list0 + h * c.head + u * c.full + prefix::kUnitCost;
+        const long long first = x.list0 + h * c.head + u * c.full + prefix::kUnitCost;
         const int w = u == c.units - 1 ? c.last_weight : unit / prefix::kRows;
-        c0 = first / per;
-        c1 = (first + (long long)(x.tiles - 1) * w) / per;
-        whole = c0 == c1;
-        at = i % unit;
+        const long long c0 = first / per;
+        count = (int)((first + (long long)(x.tiles - 1) * w) / per - c0) + 1;
+        ml_step = 2 * unit;
+        part_step = ml_step * HD;
+        const size_t slot = (size_t)c0 * 2 * unit;
+        const size_t in_part = (size_t)(at / prefix::kRows * prefix::kRows) * HD + four * (prefix::kRows * 4) +
+                               at % prefix::kRows * 4;
+        if (count == 1) {
+          ml = p.t.whole_ml + head;
+          part = p.t.whole + head * HD + four * 4;
+        } else {
+          ml = p.t.part_ml + slot + unit + at;
+          part = p.t.part + (slot + unit) * HD + in_part;
+        }
+        ml_rest = p.t.part_ml + slot + at;
+        part_rest = p.t.part + slot * HD + in_part;
       }
     }
   }
-  auto slot_of = [&](long long c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * unit; };
-  auto ml_of = [&](long long c) { return whole ? p.t.whole_ml[head] : p.t.part_ml[slot_of(c) + at]; };
-  const float own = p.own_lse[head] * 1.4426950408889634f;
+  auto ml_of = [&](int c) { return c == 0 ? *ml : ml_rest[c * ml_step]; };
   float m = own;
-#pragma unroll 4
-  for (long long c = c0; c <= c1; ++c) m = fmaxf(m, ml_of(c).x);
+#pragma unroll 8
+  for (int c = 0; c < count; ++c) m = fmaxf(m, ml_of(c).x);
   const float ref = finite_or_zero(m);
-  float sum = 0.f, o[E][4] = {};
-  auto add = [&](const float* from, size_t step, float f) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float4 v = *reinterpret_cast<const float4*>(from + (warp * E + e) * step);
-      o[e][0] = fmaf(v.x, f, o[e][0]), o[e][1] = fmaf(v.y, f, o[e][1]);
-      o[e][2] = fmaf(v.z, f, o[e][2]), o[e][3] = fmaf(v.w, f, o[e][3]);
-    }
-  };
-#pragma unroll 4
-  for (long long c = c0; c <= c1; ++c) {
-    const float2 ml = ml_of(c);
-    const float f = exp2f(ml.x - ref);
-    sum = fmaf(ml.y, f, sum);
-    if (whole) add(p.t.whole + head * HD, 4, f);
-    else add(p.t.part + (slot_of(c) + at / prefix::kRows * prefix::kRows) * HD + (at % prefix::kRows) * 4,
-             prefix::kRows * 4, f);
+  float sum = 0.f, o[4] = {};
+#pragma unroll 8
+  for (int c = 0; c < count; ++c) {
+    const float2 x = ml_of(c);
+    const float4 v = *reinterpret_cast<const float4*>(c == 0 ? part : part_rest + c * part_step);
+    const float f = exp2f(x.x - ref);
+    sum = fmaf(x.y, f, sum);
+    o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]), o[2] = fmaf(v.z, f, o[2]), o[3] = fmaf(v.w, f, o[3]);
   }
   if (own != neg_inf()) {
     const float f = exp2f(own - ref);
     sum += f;
-    add(p.own + head * HD, 4, f);
+    o[0] = fmaf(own_o.x, f, o[0]), o[1] = fmaf(own_o.y, f, o[1]);
+    o[2] = fmaf(own_o.z, f, o[2]), o[3] = fmaf(own_o.w, f, o[3]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    OT* out = static_cast<OT*>(p.out) + head * HD + (warp * E + e) * 4;
-    paged_attn::put2(out, o[e][0] * inv, o[e][1] * inv);
-    paged_attn::put2(out + 2, o[e][2] * inv, o[e][3] * inv);
-  }
-  if (p.lse && warp == 0) p.lse[head] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.6931471805599453f;
+  OT* out = static_cast<OT*>(p.out) + head * HD + four * 4;
+  paged_attn::put2(out, o[0] * inv, o[1] * inv);
+  paged_attn::put2(out + 2, o[2] * inv, o[3] * inv);
+  if (p.lse && four == 0) p.lse[head] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
 struct Layout {
@@ -180,17 +183,21 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   using paged_attn::align256;
   Layout l{};
   const size_t hd = kv.head_dim;
-  l.x = paged_attn::choose(kv, rows, heads, max_blocks, 0);
+  // What the tables allow all rows to read for themselves, in bytes: a launch over few short rows is over
+  // before the prefix kernel has its first tile (8 rows of 16 heads, 64 dimensions, 200 positions before 40:
+  // XX us against 25).
+  const double most = 4.0 * rows * kv.heads * hd * max_blocks * kv.block_size;
+  l.tc = groups > 0 && kv.dtype == RQ_BF16 && most > 32e6;
+  l.x = paged_attn::choose(kv, l.tc || groups == 0 ? rows : 2 * rows, heads, max_blocks, 0);
   l.o = align256((size_t)rows * heads * hd * sizeof(float));
   l.lse = align256((size_t)rows * heads * sizeof(float2));
-  l.map = align256((size_t)rows * sizeof(int32_t));
-  l.tc = groups > 0 && kv.dtype == RQ_BF16;
+  l.map = align256((size_t)rows * 2 * sizeof(int32_t));
   l.ctas = std::max(sm_count(), 1);
   l.unit = prefix::unit_queries(q_bf16);
   l.part = align256((size_t)l.ctas * 2 * l.unit * hd * sizeof(float));
   l.part_ml = align256((size_t)l.ctas * 2 * l.unit * sizeof(float2));
   l.group = align256((size_t)groups * sizeof(prefix::Group)) + 256;
-  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : 2 * l.map);
+  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : groups > 0 ? 2 * l.map : 0);
   return l;
 }
 
@@ -198,7 +205,8 @@ rq_status check(const rq_paged_kv* kv, int32_t rows, int32_t heads, int32_t max_
   const rq_status st = paged_kv_check(kv);
   if (st != RQ_OK) return st;
   if (rows < 0 || heads < 1 || heads % kv->heads != 0 || max_blocks < 1 || groups < 0) return RQ_ERR_ARG;
-  if (rows > 1 << 30 || heads > 1 << 23 || (long long)rows * heads > INT_MAX || groups > 1 << 20)
+  // a row is two rows of a launch
+  if (rows > 1 << 29 || heads > 1 << 23 || (long long)rows * heads > 1 << 30 || groups > 1 << 20)
     return RQ_ERR_UNSUPPORTED;
   return RQ_OK;
 }
@@ -246,15 +254,17 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
     ws += n;
     return at;
   };
-  float* const o1 = reinterpret_cast<float*>(take(l.o));
-  float* const o2 = reinterpret_cast<float*>(take(l.o));
-  float* const lse1 = reinterpret_cast<float*>(take(l.lse));
-  float* const lse2 = reinterpret_cast<float*>(take(l.lse));
+  // [2][rows][heads][head_dim] sums and [2][rows][heads] lse: of the prefixes, of the rows' own requests
+  float* const o = reinterpret_cast<float*>(take(2 * l.o));
+  float* const ls = reinterpret_cast<float*>(take(2 * l.lse));
+  float* const own_o = o + (size_t)rows * heads * kv->head_dim;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   paged_attn::Params p{};
   p.kv = *kv;
   p.q = q;
   p.table = block_table;
+  p.requests = requests;
+  p.positions = positions;
   p.rows = rows;
   p.heads = heads;
   p.batch = batch;
@@ -262,45 +272,69 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   p.G = heads / kv->heads;
   p.scale = scale_log2;
   paged_attn::place(p, l.x, take(l.x.workspace));
-  auto attend = [&](const int32_t* of, const int32_t* pos, float* o, float* ls) {
-    p.requests = of;
-    p.positions = pos;
-    p.out = o;
-    p.lse = ls;
-    return kv->dtype == RQ_BF16 ? paged_attn::launch_sums_bf16(p, l.x, qb, s)
-                                : paged_attn::launch_sums_f32(p, l.x, qb, s);
+  const bool bf16 = kv->dtype == RQ_BF16;
+  auto attend = [&] {
+    return bf16 ? paged_attn::launch_sums_bf16(p, l.x, qb, s) : paged_attn::launch_sums_f32(p, l.x, qb, s);
   };
-  if (l.tc) {
-    prefix::Params t{*kv, q, block_table, cu_rows, prefix_requests, prefix_lens, rows, heads, batch, max_blocks,
-                     groups, p.G, std::fabs(scale_log2), scale_log2 < 0.f ? 1u : 0u, o1,
-                     reinterpret_cast<float2*>(lse1)};
+  cudaError_t e;
+  if (groups == 0) {
+    p.out = out;
+    p.lse = lse;
+    e = bf16 ? paged_attn::launch_bf16(p, l.x, qb, s) : paged_attn::launch_f32(p, l.x, qb, s);
+  } else if (l.tc) {
+    float* const own_lse = ls + 2 * (size_t)rows * heads;
+    prefix::Params t{};
+    t.kv = *kv;
+    t.q = q;
+    t.table = block_table;
+    t.cu_rows = cu_rows;
+    t.prefix_requests = prefix_requests;
+    t.prefix_lens = prefix_lens;
+    t.rows = rows;
+    t.heads = heads;
+    t.batch = batch;
+    t.W = max_blocks;
+    t.groups = groups;
+    t.G = p.G;
+    t.scale = std::fabs(scale_log2);
+    t.flip = scale_log2 < 0.f ? 1u : 0u;
+    t.whole = o;
+    t.whole_ml = reinterpret_cast<float2*>(ls);
     t.part = reinterpret_cast<float*>(take(l.part));
     t.part_ml = reinterpret_cast<float2*>(take(l.part_ml));
     t.group = reinterpret_cast<prefix::Group*>(take(l.group));
     t.per = reinterpret_cast<long long*>(reinterpret_cast<char*>(t.group) + l.group - 256);
-    cudaError_t e = qb ? prefix::launch_bf16(t, l.ctas, s) : prefix::launch_f32(t, l.ctas, s);
-    if (e == cudaSuccess) e = attend(requests, positions, o2, lse2);
+    p.out = own_o;
+    p.lse = own_lse;
+    e = qb ? prefix::launch_bf16(t, l.ctas, s) : prefix::launch_f32(t, l.ctas, s);
+    if (e == cudaSuccess) e = attend();
     if (e != cudaSuccess) return RQ_ERR_CUDA;
-    JoinParams j{t, requests, o2, lse2, out, lse};
-    const dim3 grid((unsigned)(((long long)rows * heads + 31) / 32));
+    JoinParams j{t, requests, own_o, own_lse, out, lse};
+    const dim3 grid((unsigned)(((long long)rows * heads + 31) / 32), (unsigned)(kv->head_dim / (4 * kJoinWarps)));
     auto join = [&](auto* kernel) { return launch_dependent(kernel, grid, kJoinWarps * 32, 0, 0, s, j); };
     switch (kv->head_dim) {
       case 32: e = qb ? join(join_kernel<uint16_t, 32>) : join(join_kernel<float, 32>); break;
       case 64: e = qb ? join(join_kernel<uint16_t, 64>) : join(join_kernel<float, 64>); break;
       default: e = qb ? join(join_kernel<uint16_t, 128>) : join(join_kernel<float, 128>);
     }
-    return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+  } else {
+    int32_t* const map = reinterpret_cast<int32_t*>(take(2 * l.map));
+    int32_t* const at = map + 2 * (size_t)rows;
+    const PrefixParams pp{requests, cu_rows, prefix_requests, prefix_lens, positions, rows, heads, batch, groups,
+                          kv->head_dim, map, at, o, own_o, ls, ls + (size_t)rows * heads, out, lse};
+    p.requests = map;
+    p.positions = at;
+    p.rows = 2 * rows;
+    p.fold = rows;
+    p.out = o;
+    p.lse = ls;
+    e = launch_dependent(rows_kernel, dim3((unsigned)((rows + 255) / 256)), 256, 0, 0, s, pp);
+    if (e == cudaSuccess) e = attend();
+    if (e != cudaSuccess) return RQ_ERR_CUDA;
+    const long long pairs = (long long)rows * heads;
+    const int grid = (int)std::min<long long>((pairs + 7) / 8, 8ll * sm_count() + 1);
+    e = qb ? launch_dependent(merge_kernel<uint16_t>, dim3((unsigned)grid), 256, 0, 0, s, pp)
+           : launch_dependent(merge_kernel<float>, dim3((unsigned)grid), 256, 0, 0, s, pp);
   }
-  int32_t* const map[2] = {reinterpret_cast<int32_t*>(take(l.map)), reinterpret_cast<int32_t*>(take(l.map))};
-  PrefixParams pp{requests, cu_rows, prefix_requests, prefix_lens, rows, heads, batch, groups, kv->head_dim,
-                  map[0], map[1], o1, o2, lse1, lse2, out, lse};
-  cudaError_t e = launch_dependent(rows_kernel, dim3((unsigned)((rows + 255) / 256)), 256, 0, 0, s, pp);
-  if (e == cudaSuccess) e = attend(map[0], map[1], o1, lse1);
-  if (e == cudaSuccess) e = attend(requests, positions, o2, lse2);
-  if (e != cudaSuccess) return RQ_ERR_CUDA;
-  const long long pairs = (long long)rows * heads;
-  const int grid = (int)std::min<long long>((pairs + 7) / 8, 8ll * sm_count() + 1);
-  e = qb ? launch_dependent(merge_kernel<uint16_t>, dim3((unsigned)grid), 256, 0, 0, s, pp)
-         : launch_dependent(merge_kernel<float>, dim3((unsigned)grid), 256, 0, 0, s, pp);
   return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }

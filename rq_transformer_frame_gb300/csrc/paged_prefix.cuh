@@ -31,7 +31,9 @@
 //             streams its waits, 300 cycles each, were the kernel's (XX us)
 //
 // bf16 queries enter as they are and P in two bf16 parts (16 bits); f32 queries and their P in three
-// (24 bits, every product exact). Parts are cut, not rounded to nearest (paged_attn.cuh, cut_bf16): all
+// (24 bits, every product exact), smallest first. The tensor cores cut the sum after each product of 16
+// terms, towards 0, so for f32 queries O is a tile's alone and the tiles are added in registers (in one O
+// the cuts of 20 tiles were 2.6e-6 of the result, now XX). Parts are cut, not rounded to nearest (paged_attn.cuh, cut_bf16): all
 // are of the value's sign, so an infinite key or value is met by no zero part. P lies in tensor memory,
 // in the columns of the S it was made of.
 #pragma once
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           ++made;
           behind();
           if (elect_one()) {
-            uint32_t acc = t > first;
+            uint32_t acc = !S::kF32 && t > first;
 #pragma unroll 1
             for (int part = S::kPParts - 1; part >= 0; --part) {
               uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
@@ -740,6 +742,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       mbar_arrive(&s.q_full);
       const int jobs = x.pair ? 2 * x.n : x.n;
       float ref[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // as seen
+      // f32 queries: sums of the tiles so far, by the two streams together
+      constexpr int D = S::kF32 ? HD / 2 : 16;
+      float o[D] = {};
+      auto add_tile = [&](int st, float f) {
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float v[16];
+          tc::tmem_ld16(lanes + st * 256 + 128 + side * (HD / 2) + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[c + e] = fmaf(v[e], f, o[c + e]);
+        }
+      };
 #pragma unroll 1
       for (int j = 0; j < jobs; ++j) {
         const int st = j & 1;
@@ -773,14 +787,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         bar_sync(1 + (warp & 3), 64);
         mx = fmaxf(mx, s.row[st][side ^ 1][row]);
         mx = mx == neg_inf() ? mx : mx * p.scale;
+        // f32 queries have the bound of the tile before, the other stream's, and this stream's tile before is
+        // done (these scores came behind it) and still apart
+        const float mine = ref[0];
+        if (S::kF32) ref[0] = ref[1];
         if (__any_sync(0xffffffffu, mx > ref[0])) {
           const float was = ref[0];
           if (mx > was) ref[0] = ceilf(mx) + kSlack;  // whole: sums are scaled exactly
           const float f = ref[0] > was ? ex2(was - ref[0]) : 1.f;
-          l[0] *= f;
-          // the sums so far are of tiles whose products are done (these scores came behind them)
-          if (j > 1) scale_sums(ts + 128 + side * (HD / 2), HD / 2, f);
+          if constexpr (S::kF32) {
+            l[0] *= f;
+            l[1] *= f;
+#pragma unroll
+            for (int e = 0; e < D; ++e) o[e] *= f;
+          } else {
+            l[0] *= f;
+            // the sums so far are of tiles whose products are done (these scores came behind them)
+            if (j > 1) scale_sums(ts + 128 + side * (HD / 2), HD / 2, f);
+          }
         }
+        if (S::kF32 && j > 1) add_tile(st, mine == neg_inf() ? 0.f : ex2(mine - ref[0]));
         const f32x2 sub2 = pack2(-finite_or_zero(ref[0]), -finite_or_zero(ref[0]));
         f32x2 sum2 = pack2(0.f, 0.f);
         // P, its parts over the scores (a third one behind them)
@@ -836,7 +862,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         f[0] = ex2(ref[0] - sub);
         f[1] = ex2(ref[1] - sub);
         ref[0] = m;
-        l[0] = l[0] * f[0] + l[1] * f[1];
+        // (f32 queries' sums are all relative to the last tile's bound, m)
+        l[0] = S::kF32 ? l[0] + l[1] : l[0] * f[0] + l[1] * f[1];
+        if (S::kF32 && ok) {
+          add_tile(0, f[0]);
+          if (x.n > 1) add_tile(1, f[1]);
+        }
       }
 #pragma unroll 1
       for (int st = 0; st < (x.pair ? 2 : 1); ++st) {
@@ -853,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll 1
           for (int c = side * (HD / 2); c < (side + 1) * (HD / 2); c += 16) {
             float v[16];
+            if constexpr (S::kF32) break;
             tc::tmem_ld16(lanes + st * 256 + 128 + c, v);
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] *= f[0];
@@ -868,6 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 *reinterpret_cast<float4*>(out + (c / 4 + e) * step) =
                     make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
             }
+          }
+          if (S::kF32 && live) {
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e)
+              *reinterpret_cast<float4*>(out + (side * (HD / 8) + e) * step) =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         ref[0] = ref[1];
