@@ -21,9 +21,12 @@
 // Positions outside the live range or in a missing block are filled with zeros by the copy
 // and masked, so nothing that lies there is ever used.
 //
-// Lists. With LISTS a row's positions are not a range but those of the pages that a list names,
+// Lists. In mode kLists a row's positions are not a range but those of the pages that a list names,
 // another list for each K/V head: every (row, K/V head) is then a row of its own, of one K/V head
 // and its queries, and its key j is position j % block_size of the list's entry j / block_size.
+//
+// Prefixes. In mode kPrefixes each row of queries is two rows, one over the prefix that its group
+// shares and one over its own request.
 #pragma once
 
 #include "paged.cuh"
@@ -42,6 +45,7 @@ constexpr int kMaxGrid = 304;              // CTAs of a launch, at most
 constexpr int kMaxRuns = kMaxGrid * kWarps;
 constexpr int kMinRun = 1;                 // tiles of a run, at least
 constexpr int kUnitCost = 1;               // what a unit's start and end count, in tiles
+enum Mode { kRows, kLists, kPrefixes };
 
 struct Params {
   rq_paged_kv kv;
@@ -50,12 +54,13 @@ struct Params {
   float* lse;
   const int32_t *table, *requests, *positions;
   int rows, heads, batch, W, window;
-  int fold;            // rows from here on have the queries of the rows from 0 on (0: none has)
   int G, GB, HG;       // query heads per K/V head (of all a unit reads), of a unit; units of a K/V head
   int runs;            // runs (warps) of the launch
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
-  const int32_t* pages;  // LISTS: [rows][list] pages, -1 in empty entries
-  int list, kv_heads;    // LISTS: entries of a list; rows of one query token
+  const int32_t* pages;  // kLists: [rows][list] pages, -1 in empty entries
+  int list, kv_heads;    // kLists: entries of a list; rows of one query token
+  const int32_t *cu_rows, *prefix_requests, *prefix_lens;  // kPrefixes: rq_paged_prefix_attention's
+  int groups, q_rows;    // rows of queries: over prefixes first, then as many over their own requests
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
   float unit;          // what the sums of values are in (a core's kUnit)
@@ -89,21 +94,42 @@ struct Shape {
 };
 
 struct Row {
-  int r;                   // LISTS: its number
+  int r;                   // kLists: its number
   int b, lo, pos, t0, nt;  // request, live positions [lo, pos], tiles [t0, t0 + nt)
 };
 
+// the group of row r, of groups [cu_rows[g], cu_rows[g + 1]), or -1
+__device__ __forceinline__ int group_of(const int32_t* cu_rows, int groups, int r) {
+  int lo = 0, hi = groups;  // the last one that starts at the row or before
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (cu_rows[mid] <= r) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo > 0 && r < cu_rows[lo] ? lo - 1 : -1;
+}
+
 // row r's request and position as they stand; out of the list: no tiles
-template <bool LISTS>
+template <Mode MODE>
 __device__ __forceinline__ int2 row_words(const Params& p, int r) {
   if ((unsigned)r >= (unsigned)p.rows) return make_int2(-1, -1);
-  if (LISTS) r /= p.kv_heads;
+  if (MODE == kLists) r /= p.kv_heads;
+  if constexpr (MODE == kPrefixes) {
+    const bool own = r >= p.q_rows;
+    if (own) r -= p.q_rows;
+    const int b = p.requests ? p.requests[r] : r;
+    if (own || b < 0 || b >= p.batch) return make_int2(b, p.positions[r]);
+    const int g = group_of(p.cu_rows, p.groups, r);
+    if (g >= 0) {
+      const int x = p.prefix_requests[g];
+      if (x >= 0 && x < p.batch) return make_int2(x, max(p.prefix_lens[g], 0) - 1);
+    }
+    return make_int2(0, -1);  // no prefix: an empty request
+  }
   return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
 }
 
-__device__ __forceinline__ int q_row(const Params& p, int r) { return p.fold > 0 && r >= p.fold ? r - p.fold : r; }
-
-template <int kKeys, bool LISTS>
+template <int kKeys, Mode MODE>
 __device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
   Row x;
   x.r = r;
@@ -111,7 +137,7 @@ __device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
   x.pos = words.y;
   x.lo = x.t0 = x.nt = 0;
   if (x.b < 0 || x.b >= p.batch || x.pos < 0) return x;
-  if constexpr (LISTS) {
+  if constexpr (MODE == kLists) {
     x.nt = (p.list * p.kv.block_size - 1) / kKeys + 1;
     return x;
   }
@@ -733,7 +759,7 @@ enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };
 // 3000 positions in 476 us against 563.
 //
 // OT: the outputs' type, QT but for sums that are joined with others.
-template <typename QT, typename KT, int HD, typename Core, bool SPLIT, bool LISTS, typename OT>
+template <typename QT, typename KT, int HD, typename Core, bool SPLIT, Mode MODE, typename OT>
 __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT ? 1 : 2)
     attend_kernel(const __grid_constant__ Params p) {
   using S = Shape<KT, Core::kLoad>;
@@ -765,8 +791,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     r = blockIdx.y / units;
     kvh = u / p.HG;
     hg = u % p.HG;
-    const int2 words = row_words<LISTS>(p, r);
-    x = row_of<K, LISTS>(p, r, words);
+    const int2 words = row_words<MODE>(p, r);
+    x = row_of<K, MODE>(p, r, words);
     if (x.nt == 0) {  // the whole cluster's
       const int h0 = kvh * p.G + hg * Core::kHeads;
       if (blockIdx.x == 0 && words.x >= 0 && words.x < p.batch)
@@ -785,13 +811,13 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (from < unit_end) {
         r = (int)(from / units);
         int u = (int)(from % units);
-        x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
+        x = row_of<K, MODE>(p, r, row_words<MODE>(p, r));
         while (x.nt == 0 && (long long)(r + 1) * units < unit_end) {
           ++r;
-          x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
+          x = row_of<K, MODE>(p, r, row_words<MODE>(p, r));
           u = 0;
         }
-        next_words = row_words<LISTS>(p, r + 1);
+        next_words = row_words<MODE>(p, r + 1);
         kvh = u / p.HG;
         hg = u % p.HG;
         stop = x.nt ? LLONG_MAX : 0;  // ends by unit_end
@@ -802,7 +828,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       __shared__ int s_row[NW];
       // where each run starts: prefix sums of the rows' costs, a slice of rows per thread
       auto cost = [&](int r) {
-        const int nt = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r)).nt;
+        const int nt = row_of<K, MODE>(p, r, row_words<MODE>(p, r)).nt;
         return nt ? (long long)(nt + kUnitCost) * units : 0ll;
       };
       const int slice = (p.rows + NT - 1) / NT;
@@ -848,8 +874,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       at = stop;
       if (begin < total) {
         r = s_row[warp];
-        x = row_of<K, LISTS>(p, r, row_words<LISTS>(p, r));
-        next_words = row_words<LISTS>(p, r + 1);
+        x = row_of<K, MODE>(p, r, row_words<MODE>(p, r));
+        next_words = row_words<MODE>(p, r + 1);
         const int unit_cost = x.nt + kUnitCost, u = (int)(s_off[warp] / unit_cost);
         const int in = (int)(s_off[warp] % unit_cost);
         kvh = u / p.HG;
@@ -860,7 +886,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     }
     // rows of empty requests
     for (int i = run; i < p.rows; i += p.runs) {
-      const int2 words = row_words<LISTS>(p, i);
+      const int2 words = row_words<MODE>(p, i);
       if (words.x < 0 || words.x >= p.batch || words.y >= 0) continue;
       empty_row(i, 0, p.heads, lane, 32);
     }
@@ -876,7 +902,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     // which holds positions behind the row's, and INT_MIN, the complement of no block, that of none.
     auto ids_from = [&](const Row& y, int first) {
       const int page = first + lane;  // past 2^31: a large unsigned number
-      if constexpr (LISTS) {
+      if constexpr (MODE == kLists) {
         if (y.nt == 0 || (unsigned)page >= (unsigned)p.list) return INT_MIN;
         const int at = p.pages[(size_t)y.r * p.list + page], newest = y.pos / P;
         if (at < 0 || at > newest || at <= newest - p.W) return INT_MIN;
@@ -895,7 +921,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     auto issue = [&]() {
       const int s = issued % NS, key = (x.t0 + t) * K + (K < 32 ? lane % K : lane), page = key / P;
       if (!next_known) {  // its words came with this row's: its first pages
-        const Row y = row_of<K, LISTS>(p, r + 1, next_words);
+        const Row y = row_of<K, MODE>(p, r + 1, next_words);
         ids_next = ids_from(y, y.t0 * K / P);
         next_known = true;
       }
@@ -904,7 +930,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       const int id1 = __shfl_sync(0xffffffffu, ids_after, rel & 31);
       int id = rel < 32 ? id0 : id1;
       bool ok;
-      if constexpr (LISTS) {
+      if constexpr (MODE == kLists) {
         ok = id >= 0 || key - page * P <= x.pos % P;
         if (id < 0) id = ~id;
         ok = ok && id < p.kv.n_blocks && page < p.list;
@@ -913,7 +939,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       }
       const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (K < 32 ? (1u << (K & 31)) - 1u : ~0u);
       const long long off = ok ? id * p.kv.block_stride + (key - page * P) * p.kv.row_stride +
-                                     (LISTS ? r % p.kv_heads : kvh) * p.kv.head_stride
+                                     (MODE == kLists ? r % p.kv_heads : kvh) * p.kv.head_stride
                                : 0;
       if (t == 0) first = true;
       const bool last = t == x.nt - 1, end = last || at + 1 >= stop;
@@ -924,7 +950,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (start) {  // the unit's queries will be wanted soon
         const int g0 = hg * Core::kHeads, n = min(Core::kHeads, p.G - g0) * HD * (int)sizeof(QT);
         const char* q = static_cast<const char*>(p.q) +
-                        ((size_t)q_row(p, r) * p.heads + (size_t)kvh * p.G + g0) * HD * sizeof(QT);
+                        ((size_t)(MODE == kPrefixes && r >= p.q_rows ? r - p.q_rows : r) * p.heads +
+                         (size_t)kvh * p.G + g0) * HD * sizeof(QT);
         if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
       }
       if (end && !last && first)  // goes on in the runs that follow
@@ -958,7 +985,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         t = 0;
         first = false;
         at += kUnitCost;
-        const bool one_window = LISTS ? p.list <= 32 : x.pos / P - x.t0 * K / P < 32;
+        const bool one_window = MODE == kLists ? p.list <= 32 : x.pos / P - x.t0 * K / P < 32;
         if (++hg == p.HG) {
           hg = 0;
           if (++kvh == p.kv.heads) {
@@ -970,19 +997,19 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
               return;
             }
             ++r;
-            x = row_of<K, LISTS>(p, r, next_words);
+            x = row_of<K, MODE>(p, r, next_words);
             ids0 = ids_next;
             // empty rows between, 32 at a time (of a run that is not whole units a row follows)
             while (x.nt == 0 && r < p.rows - 1 && (!p.whole || (long long)(r + 1) * units < unit_end)) {
-              const int2 words = row_words<LISTS>(p, r + 1 + lane);
-              const uint32_t some = __ballot_sync(0xffffffffu, row_of<K, LISTS>(p, 0, words).nt > 0);
+              const int2 words = row_words<MODE>(p, r + 1 + lane);
+              const uint32_t some = __ballot_sync(0xffffffffu, row_of<K, MODE>(p, 0, words).nt > 0);
               const int n = some ? __ffs(some) : min(32, p.rows - 1 - r);
               r += n;
-              x = row_of<K, LISTS>(p, r, make_int2(__shfl_sync(0xffffffffu, words.x, n - 1),
+              x = row_of<K, MODE>(p, r, make_int2(__shfl_sync(0xffffffffu, words.x, n - 1),
                                                    __shfl_sync(0xffffffffu, words.y, n - 1)));
               ids0 = ids_from(x, x.t0 * K / P);
             }
-            next_words = row_words<LISTS>(p, r + 1);
+            next_words = row_words<MODE>(p, r + 1);
             next_known = false;
           }
         }
@@ -1011,7 +1038,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       const size_t head = (size_t)d.x * p.heads + (size_t)d.y * p.G + g0;
       if (d.z & kStart) {
         core.clear();
-        core.load(static_cast<const QT*>(p.q) + (head - (size_t)(d.x - q_row(p, d.x)) * p.heads) * HD, live, lane, scratch);
+        const size_t q_head = MODE == kPrefixes && d.x >= p.q_rows ? head - (size_t)p.q_rows * p.heads : head;
+        core.load(static_cast<const QT*>(p.q) + q_head * HD, live, lane, scratch);
       }
       cp_async_wait<NS - 1>();
       __syncwarp();
@@ -1266,7 +1294,7 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
   return x;
 }
 
-template <typename QT, typename KT, int HD, typename Core, bool LISTS = false, typename OT = QT>
+template <typename QT, typename KT, int HD, typename Core, Mode MODE = kRows, typename OT = QT>
 cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   using S = Shape<KT, Core::kLoad>;
   cudaError_t e;
@@ -1276,7 +1304,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   p.unit = Core::kUnit;
   if constexpr (Core::kLoad == HD) {  // units of one K/V head
     if (x.split) {
-      auto* kernel = attend_kernel<QT, KT, HD, Core, true, LISTS, OT>;
+      auto* kernel = attend_kernel<QT, KT, HD, Core, true, MODE, OT>;
       constexpr size_t ring = (size_t)kSplitWarps *
                               (split_stages<S::kStage, Core::kScratch> * S::kStage + Core::kScratch);
       constexpr size_t sums = (size_t)(kSplitWarps + 1) * Core::kHeads * (HD * 4 + 8);
@@ -1288,7 +1316,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
     }
   }
   // as many CTAs as are resident at once, at most as many as the largest rows could fill
-  auto* kernel = attend_kernel<QT, KT, HD, Core, false, LISTS, OT>;
+  auto* kernel = attend_kernel<QT, KT, HD, Core, false, MODE, OT>;
   constexpr size_t smem = (size_t)kWarps * (kStages * S::kStage + Core::kScratch);
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1321,13 +1349,15 @@ inline void place(Params& p, const Choice& x, void* workspace) {
   p.cut = reinterpret_cast<int4*>(ws + part_bytes(x.unit_heads, p.kv.head_dim) + ml_bytes(x.unit_heads));
 }
 
-// over a bf16 cache, over an f32 cache; with lists; with f32 outputs whatever the queries are
+// over a bf16 cache, over an f32 cache; with lists; with f32 outputs whatever the queries are; and of rows
+// over prefixes too
 cudaError_t launch_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_lists_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_lists_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_sums_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
-cudaError_t launch_sums_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_prefixes_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_prefixes_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 
 }  // namespace paged_attn
 }  // namespace rqk

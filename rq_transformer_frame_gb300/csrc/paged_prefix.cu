@@ -18,45 +18,16 @@ using paged_attn::finite_or_zero;
 using paged_attn::neg_inf;
 using paged_attn::put;
 
-struct PrefixParams {
-  const int32_t *requests, *cu_rows, *prefix_requests, *prefix_lens;
-  const int32_t* positions;
-  int rows, heads, batch, groups, hd;
-  int32_t *row_request, *row_position;  // [2 rows], of the prefixes, then the rows' own
-  const float *o1, *o2, *lse1, *lse2;   // prefix, own
+struct MergeParams {
+  const int32_t* requests;
+  int rows, heads, batch, hd;
+  const float *o1, *o2, *lse1, *lse2;  // prefix, own
   void* out;
   float* lse;
 };
 
-// each row's prefix as a request and the last position read of it, and its own
-__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ PrefixParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= p.rows) return;
-  const int b = p.requests ? p.requests[r] : r;
-  int request = -1, position = -1;
-  if (b >= 0 && b < p.batch) {
-    request = 0;  // without a prefix: an empty request
-    int lo = 0, hi = p.groups;  // the last group that starts at r or before
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (p.cu_rows[mid] <= r) lo = mid + 1;
-      else hi = mid;
-    }
-    if (lo > 0 && r < p.cu_rows[lo]) {
-      const int x = p.prefix_requests[lo - 1], n = p.prefix_lens[lo - 1];
-      if (x >= 0 && x < p.batch && n > 0) request = x, position = n - 1;
-    }
-  }
-  p.row_request[r] = request;
-  p.row_position[r] = position;
-  p.row_request[p.rows + r] = b;
-  p.row_position[p.rows + r] = p.positions[r];
-}
-
 template <typename OT>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeParams p) {
   pdl_wait();
   pdl_trigger();
   const int warps = gridDim.x * 8;
@@ -112,14 +83,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const float *part = nullptr, *part_rest = nullptr;
   size_t ml_step = 0, part_step = 0;
   {
-    int lo = 0, hi = p.t.groups;  // the last group that starts at the row or before
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (p.t.cu_rows[mid] <= r) lo = mid + 1;
-      else hi = mid;
-    }
-    if (lo > 0 && r < p.t.cu_rows[lo]) {
-      const prefix::Group x = p.t.group[lo - 1];
+    const int of = paged_attn::group_of(p.t.cu_rows, p.t.groups, r);
+    if (of >= 0) {
+      const prefix::Group x = p.t.group[of];
       if (x.tiles > 0) {
         const int unit = x.unit_rows, i = (r - x.row0) * p.t.G + g, u = i / unit, at = i % unit;
         const prefix::Costs c = unit == 256 ? prefix::costs_of<256>(x.queries, x.tiles)
@@ -145,25 +111,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       }
     }
   }
-  auto ml_of = [&](int c) { return c == 0 ? *ml : ml_rest[c * ml_step]; };
-  float m = own;
-#pragma unroll 8
-  for (int c = 0; c < count; ++c) m = fmaxf(m, ml_of(c).x);
-  const float ref = finite_or_zero(m);
-  float sum = 0.f, o[4] = {};
-#pragma unroll 8
-  for (int c = 0; c < count; ++c) {
-    const float2 x = ml_of(c);
-    const float4 v = *reinterpret_cast<const float4*>(c == 0 ? part : part_rest + c * part_step);
-    const float f = exp2f(x.x - ref);
-    sum = fmaf(x.y, f, sum);
-    o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]), o[2] = fmaf(v.z, f, o[2]), o[3] = fmaf(v.w, f, o[3]);
-  }
-  if (own != neg_inf()) {
-    const float f = exp2f(own - ref);
-    sum += f;
-    o[0] = fmaf(own_o.x, f, o[0]), o[1] = fmaf(own_o.y, f, o[1]);
-    o[2] = fmaf(own_o.z, f, o[2]), o[3] = fmaf(own_o.w, f, o[3]);
+  // from the own request's part on; four pieces at once, the last one again in place of those behind it
+  float m = own, sum = own == neg_inf() ? 0.f : 1.f;
+  float o[4] = {sum * own_o.x, sum * own_o.y, sum * own_o.z, sum * own_o.w};
+  if (own == neg_inf()) o[0] = o[1] = o[2] = o[3] = 0.f;
+  for (int c0 = 0; c0 < count; c0 += 4) {
+    float2 x[4];
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = min(c0 + j, count - 1);
+      x[j] = *(c == 0 ? ml : ml_rest + c * ml_step);
+      v[j] = *reinterpret_cast<const float4*>(c == 0 ? part : part_rest + c * part_step);
+    }
+    float next = m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) next = fmaxf(next, x[j].x);
+    const float ref = finite_or_zero(next), old = exp2f(m - ref);
+    m = next;
+    sum *= old;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= old;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c0 + j >= count) break;
+      const float f = exp2f(x[j].x - ref);
+      sum = fmaf(x[j].y, f, sum);
+      o[0] = fmaf(v[j].x, f, o[0]), o[1] = fmaf(v[j].y, f, o[1]);
+      o[2] = fmaf(v[j].z, f, o[2]), o[3] = fmaf(v[j].w, f, o[3]);
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   OT* out = static_cast<OT*>(p.out) + head * HD + four * 4;
@@ -176,7 +152,7 @@ struct Layout {
   paged_attn::Choice x;
   bool tc;         // prefixes by matrix products
   int ctas, unit;  // of the prefix kernel
-  size_t o, lse, map, part, part_ml, group, bytes;
+  size_t o, lse, part, part_ml, group, bytes;
 };
 
 Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int groups, bool q_bf16) {
@@ -188,16 +164,24 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   // XX us against 25).
   const double most = 4.0 * rows * kv.heads * hd * max_blocks * kv.block_size;
   l.tc = groups > 0 && kv.dtype == RQ_BF16 && most > 32e6;
-  l.x = paged_attn::choose(kv, l.tc || groups == 0 ? rows : 2 * rows, heads, max_blocks, 0);
+  l.x = paged_attn::choose(kv, rows, heads, max_blocks, 0);
+  if (!l.tc && groups > 0) {
+    // two rows of a query row: where its own alone would be split, both are, over half the CTAs each
+    if (l.x.split) {
+      l.x.split = std::max(l.x.split / 2, 1);
+      l.x.units *= 2;
+    } else {
+      l.x = paged_attn::choose(kv, 2 * rows, heads, max_blocks, 0);
+    }
+  }
   l.o = align256((size_t)rows * heads * hd * sizeof(float));
   l.lse = align256((size_t)rows * heads * sizeof(float2));
-  l.map = align256((size_t)rows * 2 * sizeof(int32_t));
   l.ctas = std::max(sm_count(), 1);
   l.unit = prefix::unit_queries(q_bf16);
   l.part = align256((size_t)l.ctas * 2 * l.unit * hd * sizeof(float));
   l.part_ml = align256((size_t)l.ctas * 2 * l.unit * sizeof(float2));
   l.group = align256((size_t)groups * sizeof(prefix::Group)) + 256;
-  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : groups > 0 ? 2 * l.map : 0);
+  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : 0);
   return l;
 }
 
@@ -273,9 +257,6 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   p.scale = scale_log2;
   paged_attn::place(p, l.x, take(l.x.workspace));
   const bool bf16 = kv->dtype == RQ_BF16;
-  auto attend = [&] {
-    return bf16 ? paged_attn::launch_sums_bf16(p, l.x, qb, s) : paged_attn::launch_sums_f32(p, l.x, qb, s);
-  };
   cudaError_t e;
   if (groups == 0) {
     p.out = out;
@@ -307,7 +288,7 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
     p.out = own_o;
     p.lse = own_lse;
     e = qb ? prefix::launch_bf16(t, l.ctas, s) : prefix::launch_f32(t, l.ctas, s);
-    if (e == cudaSuccess) e = attend();
+    if (e == cudaSuccess) e = paged_attn::launch_sums_bf16(p, l.x, qb, s);
     if (e != cudaSuccess) return RQ_ERR_CUDA;
     JoinParams j{t, requests, own_o, own_lse, out, lse};
     const dim3 grid((unsigned)(((long long)rows * heads + 31) / 32), (unsigned)(kv->head_dim / (4 * kJoinWarps)));
@@ -318,23 +299,21 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
       default: e = qb ? join(join_kernel<uint16_t, 128>) : join(join_kernel<float, 128>);
     }
   } else {
-    int32_t* const map = reinterpret_cast<int32_t*>(take(2 * l.map));
-    int32_t* const at = map + 2 * (size_t)rows;
-    const PrefixParams pp{requests, cu_rows, prefix_requests, prefix_lens, positions, rows, heads, batch, groups,
-                          kv->head_dim, map, at, o, own_o, ls, ls + (size_t)rows * heads, out, lse};
-    p.requests = map;
-    p.positions = at;
+    const MergeParams m{requests, rows, heads, batch, kv->head_dim, o, own_o, ls, ls + (size_t)rows * heads, out, lse};
     p.rows = 2 * rows;
-    p.fold = rows;
+    p.q_rows = rows;
+    p.groups = groups;
+    p.cu_rows = cu_rows;
+    p.prefix_requests = prefix_requests;
+    p.prefix_lens = prefix_lens;
     p.out = o;
     p.lse = ls;
-    e = launch_dependent(rows_kernel, dim3((unsigned)((rows + 255) / 256)), 256, 0, 0, s, pp);
-    if (e == cudaSuccess) e = attend();
+    e = bf16 ? paged_attn::launch_prefixes_bf16(p, l.x, qb, s) : paged_attn::launch_prefixes_f32(p, l.x, qb, s);
     if (e != cudaSuccess) return RQ_ERR_CUDA;
     const long long pairs = (long long)rows * heads;
     const int grid = (int)std::min<long long>((pairs + 7) / 8, 8ll * sm_count() + 1);
-    e = qb ? launch_dependent(merge_kernel<uint16_t>, dim3((unsigned)grid), 256, 0, 0, s, pp)
-           : launch_dependent(merge_kernel<float>, dim3((unsigned)grid), 256, 0, 0, s, pp);
+    e = qb ? launch_dependent(merge_kernel<uint16_t>, dim3((unsigned)grid), 256, 0, 0, s, m)
+           : launch_dependent(merge_kernel<float>, dim3((unsigned)grid), 256, 0, 0, s, m);
   }
   return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
 }

@@ -56,7 +56,7 @@ using paged_attn::pack_bf16;
 
 constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kRows = 128;       // queries of a stream
-constexpr int kUnitCost = 3;     // what a unit's start and end count, in tiles
+constexpr int kUnitCost = 6;     // what a unit's start and end count, in tiles of 128 queries
 constexpr float kSlack = 8.f;
 constexpr int kMasks = 8;        // tiles whose masks are kept
 

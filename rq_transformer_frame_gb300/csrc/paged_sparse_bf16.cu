@@ -7,8 +7,8 @@ namespace paged_attn {
 
 template <typename QT, int HD>
 static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
-  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>, true>(p, x, s)
-                  : launch<QT, uint16_t, HD, WideCore<QT, HD>, true>(p, x, s);
+  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>, kLists>(p, x, s)
+                  : launch<QT, uint16_t, HD, WideCore<QT, HD>, kLists>(p, x, s);
 }
 
 template <typename QT>

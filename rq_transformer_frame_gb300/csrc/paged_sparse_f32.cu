@@ -6,10 +6,10 @@ namespace paged_attn {
 
 template <typename QT, int HD>
 static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
-  if (p.G == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, true>(p, x, s);
-  if (p.G == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, true>(p, x, s);
-  if (p.G <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, true>(p, x, s);
-  return launch<QT, float, HD, FmaCore<QT, HD, 8>, true>(p, x, s);
+  if (p.G == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, kLists>(p, x, s);
+  if (p.G == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, kLists>(p, x, s);
+  if (p.G <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, kLists>(p, x, s);
+  return launch<QT, float, HD, FmaCore<QT, HD, 8>, kLists>(p, x, s);
 }
 
 template <typename QT>
