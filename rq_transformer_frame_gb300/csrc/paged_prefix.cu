@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         const prefix::Costs c = unit == 256 ? prefix::costs_of<256>(x.queries, x.tiles)
                                             : prefix::costs_of<128>(x.queries, x.tiles);
         const long long first = x.list0 + h * c.head + u * c.full + prefix::kUnitCost;
-        const int w = u == c.units - 1 ? c.last_weight : unit / prefix::kRows;
+        const int w = u == c.units - 1 ? c.last_weight : unit / prefix::kRows + prefix::kTileCost;
         const long long c0 = first / per;
         count = (int)((first + (long long)(x.tiles - 1) * w) / per - c0) + 1;
         ml_step = 2 * unit;

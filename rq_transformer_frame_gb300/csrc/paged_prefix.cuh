@@ -56,7 +56,10 @@ using paged_attn::pack_bf16;
 
 constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kRows = 128;       // queries of a stream
-constexpr int kUnitCost = 6;     // what a unit's start and end count, in tiles of 128 queries
+// What a tile of a stream's 128 queries, of two streams' 256, and a unit's start and end count in the list: 1.6,
+// 2.5 and 7 us (250 rows of five groups, 78 GFLOP: 92 us for most CTAs, 122 for those of short units when a
+// tile counted by its queries alone)
+constexpr int kTileCost = 1, kUnitCost = 9;
 constexpr float kSlack = 8.f;
 constexpr int kMasks = 8;        // tiles whose masks are kept
 
@@ -236,14 +239,13 @@ struct Costs {
   int units, last_weight;
 };
 
-// A tile counts once for each 128 queries.
 template <int UNIT>
 __host__ __device__ __forceinline__ Costs costs_of(int queries, int tiles) {
   Costs c{};
   if (tiles == 0) return c;
   c.units = (queries - 1) / UNIT + 1;
-  c.last_weight = (queries - (c.units - 1) * UNIT - 1) / kRows + 1;
-  c.full = (long long)tiles * (UNIT / kRows) + kUnitCost;
+  c.last_weight = (queries - (c.units - 1) * UNIT - 1) / kRows + 1 + kTileCost;
+  c.full = (long long)tiles * (UNIT / kRows + kTileCost) + kUnitCost;
   c.last = (long long)tiles * c.last_weight + kUnitCost;
   c.head = (c.units - 1) * c.full + c.last;
   return c;
@@ -255,6 +257,7 @@ struct Small {  // behind the tiles
   float row[2][2][kRows];  // of halves of a row, for its other half: [stream][half], maxima, then sums
   long long scan[kThreads / 32], start0;
   int start_group;
+  View start_view;
   uint32_t tmem;
   volatile int abort;
 };
@@ -273,11 +276,8 @@ struct Piece {
 template <int KT, int UNIT>
 struct Cursor {
   long long at, stop, list0;
-  int g;
-  static __device__ __noinline__ long long cost_of(const Params& p, int g) {
-    const View v = view_of<KT>(p, g);
-    return costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
-  }
+  int g, of;  // the group, and that of `v`
+  View v;
   // To the start of the CTA's run: prefix sums of the groups' costs, a slice of the groups a thread. False
   // where the list ends before.
   __device__ __noinline__ bool start(const Params& p, Small& s) {
@@ -285,8 +285,12 @@ struct Cursor {
     const int slice = (p.groups + kThreads - 1) / kThreads;
     const int g0 = min(tid * slice, p.groups), g1 = min(g0 + slice, p.groups);
     long long own = 0;
+    View seen{};
 #pragma unroll 1
-    for (int i = g0; i < g1; ++i) own += cost_of(p, i);
+    for (int i = g0; i < g1; ++i) {
+      seen = view_of<KT>(p, i);
+      own += costs_of<UNIT>(seen.queries, seen.tiles).head * p.kv.heads;
+    }
     long long inc = own;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -301,7 +305,7 @@ struct Cursor {
       if (w < warp) inc += s.scan[w];
       total += s.scan[w];
     }
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2));
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2 + kTileCost));
     at = blockIdx.x * per;
     stop = min(at + per, total);
     long long first = inc - own;
@@ -309,21 +313,23 @@ struct Cursor {
     if (blockIdx.x == 0 || (first <= at && at < inc)) {
 #pragma unroll 1
       for (int i = g0; i < g1; ++i) {
-        const View v = view_of<KT>(p, i);
+        const View v = slice == 1 ? seen : view_of<KT>(p, i);
         const long long c = costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
         if (blockIdx.x == 0) p.group[i] = Group{first, v.row0, v.queries, v.tiles, UNIT};
-        if (first <= at && at < first + c) s.start_group = i, s.start0 = first;
+        if (first <= at && at < first + c) s.start_group = i, s.start0 = first, s.start_view = v;
         first += c;
       }
     }
     __syncthreads();
-    g = s.start_group;
+    g = of = s.start_group;
     list0 = s.start0;
+    v = s.start_view;
     return at < total;
   }
   __device__ __noinline__ bool next(const Params& p, Piece& x) {
     while (at < stop && g < p.groups) {
-      x.v = view_of<KT>(p, g);
+      if (of != g) v = view_of<KT>(p, of = g);
+      x.v = v;
       const Costs c = costs_of<UNIT>(x.v.queries, x.v.tiles);
       const long long cost = c.head * p.kv.heads;
       if (at >= list0 + cost) {
@@ -337,7 +343,7 @@ struct Cursor {
       x.unit = (int)min(in / c.full, (long long)c.units - 1);
       in -= x.unit * c.full;
       const bool tail = x.unit == c.units - 1;
-      const int w = tail ? c.last_weight : UNIT / kRows;
+      const int w = tail ? c.last_weight : UNIT / kRows + kTileCost;
       const long long begin = at - in;  // the unit's first entry
       x.t = in <= kUnitCost ? 0 : (int)((in - kUnitCost + w - 1) / w);
       at = begin + (tail ? c.last : c.full);
@@ -345,7 +351,7 @@ struct Cursor {
       const long long room = stop - begin - kUnitCost - (long long)x.t * w;
       if (room <= 0) return false;  // its first tile is the next run's
       x.n = (int)min((room + w - 1) / w, (long long)(x.v.tiles - x.t));
-      x.pair = w == 2;
+      x.pair = w == 2 + kTileCost;
       x.first = x.t == 0;
       x.last = x.t + x.n == x.v.tiles;
       return true;
@@ -735,11 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     bool ok = true;
     Piece y;
     bool more = cur.next(p, y);
-    if (more) load_queries<QT, HD>(p, y, smem, tid);
+    auto queries = [&] {
+      load_queries<QT, HD>(p, y, smem, tid);
+      queries_loaded<QT, HD>(p, y, smem, tid);
+      mbar_arrive(&s.q_full);
+    };
+    if (more) queries();
     while (more) {
       x = y;
-      queries_loaded<QT, HD>(p, x, smem, tid);
-      mbar_arrive(&s.q_full);
       const int jobs = x.pair ? 2 * x.n : x.n;
       float ref[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // as seen
       // f32 queries: sums of the tiles so far, by the two streams together
@@ -851,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       more = cur.next(p, y);
       if (ok) ok = wait_warp(&s.done, piece);
       tc::fence_after_sync();
-      // the unit's products are done: the next one's queries are under way while its sums are written
-      if (more) load_queries<QT, HD>(p, y, smem, tid);
+      // the unit's products are done: the next one's first scores are made while its sums are written
+      if (more) queries();
       if (!ok) ref[0] = ref[1] = 0.f, l[0] = l[1] = __int_as_float(0x7fc00000);
       const bool cut = !(x.first && x.last);
       const size_t slot = (size_t)blockIdx.x * 2 + (x.first ? 1 : 0);
