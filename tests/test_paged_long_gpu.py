@@ -486,52 +486,73 @@ def run_prefix(sizes, prefix, own, heads, hk, hd, io, cache, P, W=None, scale=0.
 
 
 OWN = [1, 0, 2, 15, 16, 17, 40, 3, 0, 64, 65, 5, 0, 9]
+# A table of many columns, most of them never used: rows that may be long meet their prefix on the tensor cores
+# (bf16 caches), short ones each for itself.
+CUT = 60000
+TABLES = pytest.mark.parametrize("W", [None, CUT])
 
 
 @pytest.mark.parametrize("hd", [32, 64, 128])
 @pytest.mark.parametrize("io", [F32, BF16])
 @pytest.mark.parametrize("cache", [F32, BF16])
-def test_prefix_types(hd, io, cache):
+@TABLES
+def test_prefix_types(hd, io, cache, W):
     """Groups of several sizes, an empty one, rows before and behind them, and rows that hold nothing."""
-    run_prefix([5, 0, 1, 4], [300, 40, 129, 17], OWN, 4, 2, hd, io, cache, 16, first=2, pad=3, seed=hd)
+    run_prefix([5, 0, 1, 4], [300, 40, 129, 17], OWN, 4, 2, hd, io, cache, 16, W=W, first=2, pad=3, seed=hd)
 
 
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 63, 64, 65, 127, 128, 129, 255, 256, 257, 385, 1000])
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
-def test_prefix_lengths(n, io, cache):
+@TABLES
+def test_prefix_lengths(n, io, cache, W):
     """Both sides of every tile's edge."""
-    run_prefix([3], [n], [4, 1, 30], 4, 2, 128, io, cache, 16, seed=n)
+    run_prefix([3], [n], [4, 1, 30], 4, 2, 128, io, cache, 16, W=W, seed=n)
 
 
 @pytest.mark.parametrize("heads,hk", [(1, 1), (5, 5), (2, 1), (6, 2), (14, 2), (8, 1), (9, 1), (16, 1), (34, 2),
                                       (40, 1)])
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
-def test_prefix_heads(heads, hk, io, cache):
-    run_prefix([3, 2], [200, 77], [5, 1, 9, 20, 2, 3], heads, hk, 64, io, cache, 8, seed=heads)
+@TABLES
+def test_prefix_heads(heads, hk, io, cache, W):
+    run_prefix([3, 2], [200, 77], [5, 1, 9, 20, 2, 3], heads, hk, 64, io, cache, 8, W=W, seed=heads)
 
 
 @pytest.mark.parametrize("rows,heads,hk", [(31, 4, 1), (32, 4, 1), (33, 4, 1), (64, 2, 1), (70, 12, 4), (127, 1, 1),
                                            (129, 1, 1), (100, 16, 2), (300, 8, 8)])
 @pytest.mark.parametrize("io", [F32, BF16])
-def test_prefix_rows(rows, heads, hk, io):
+@TABLES
+def test_prefix_rows(rows, heads, hk, io, W):
     """Groups around the number of queries that read a tile together."""
     own = [1 + (i * 7) % 23 for i in range(rows)]
-    run_prefix([rows], [333], own, heads, hk, 64, io, BF16, 16, seed=rows)
-    run_prefix([rows // 3, rows // 3], [130, 500], own, heads, hk, 128, io, BF16, 16, seed=rows)
+    run_prefix([rows], [333], own, heads, hk, 64, io, BF16, 16, W=W, seed=rows)
+    run_prefix([rows // 3, rows // 3], [130, 500], own, heads, hk, 128, io, BF16, 16, W=W, seed=rows)
 
 
 @pytest.mark.parametrize("P", [1, 3, 5, 8, 24, 32, 100, 128, 1000])
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
 @pytest.mark.parametrize("hd", [32, 64, 128])
-def test_prefix_block_sizes(P, io, cache, hd):
-    run_prefix([3, 2], [2 * P + 1, 700], [P, 1, 9, P + 1, 2], 4, 2, hd, io, cache, P, seed=P)
+@TABLES
+def test_prefix_block_sizes(P, io, cache, hd, W):
+    run_prefix([3, 2], [2 * P + 1, 700], [P, 1, 9, P + 1, 2], 4, 2, hd, io, cache, P, W=W, seed=P)
 
 
 @pytest.mark.parametrize("layout", ["hnd", "joint"])
-def test_prefix_layouts(layout):
-    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 64, BF16, BF16, 16, seed=1, layout=layout, pad=2)
-    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 128, F32, F32, 16, seed=1, layout=layout, scale=0.3)
-    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 32, F32, BF16, 16, seed=1, layout=layout, scale=-0.2)
+@TABLES
+def test_prefix_layouts(layout, W):
+    kw = dict(W=W, seed=1, layout=layout)
+    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 64, BF16, BF16, 16, pad=2, **kw)
+    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 128, F32, F32, 16, scale=0.3, **kw)
+    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 32, F32, BF16, 16, scale=-0.2, **kw)
+    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 128, BF16, BF16, 16, scale=-0.2, **kw)
+    run_prefix([5, 4], [300, 40], OWN[:10], 6, 3, 64, BF16, BF16, 5, scale=0.3, **kw)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 4.0, -4.0, 60.0])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_prefix_scales(scale, io):
+    """From weights that are all alike to one key's alone: bounds of the scores that rise from tile to tile."""
+    run_prefix([9], [2000], [3] * 9, 4, 2, 64, io, BF16, 16, W=CUT, seed=2, scale=scale)
+    run_prefix([70], [900], [3] * 70, 8, 2, 128, io, BF16, 16, W=CUT, seed=2, scale=scale)
 
 
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32)])
@@ -539,12 +560,16 @@ def test_prefix_long(io, cache):
     """Prefixes that are cut over the card, of one row and of many."""
     run_prefix([1], [20000], [3], 8, 2, 128, io, cache, 16, seed=1)
     run_prefix([40, 2, 30], [9000, 12000, 700], [1 + i % 9 for i in range(72)], 8, 2, 64, io, cache, 32, seed=2)
+    run_prefix([1] * 40, [300 + 7 * i for i in range(40)], [1 + i % 9 for i in range(40)], 4, 2, 64, io, cache, 16, W=CUT,
+               seed=3)
 
 
 def test_prefix_of_a_ring():
     """A prefix longer than its table: the pages that the table still holds."""
     run_prefix([3], [500], [4, 1, 30], 4, 2, 64, BF16, BF16, 16, W=7, seed=3)
     run_prefix([3], [500], [4, 200, 333], 4, 2, 64, F32, F32, 5, W=7, seed=3)
+    run_prefix([3], [7000], [4, 200, 333], 8, 8, 128, BF16, BF16, 16, W=300, seed=3)
+    run_prefix([3], [7000], [4, 200, 333], 8, 8, 128, F32, BF16, 15, W=330, seed=3)
 
 
 def test_prefix_words_out_of_range():
@@ -554,11 +579,12 @@ def test_prefix_words_out_of_range():
         table[preq[0], 2] = -1
         table[preq[0], 5] = 2**31 - 1
         table[0, 0] = -1
-    for io, cache in ((F32, BF16), (BF16, BF16), (F32, F32)):
-        run_prefix([3, 2, 2, 9], [200, 77, 50, 60], [5, 1, 9, 20, 2, 3, 4, 8, 9], 4, 2, 64, io, cache, 8, seed=5,
-                   poke=poke)
-    run_prefix([3], [200], [5, 1, 9], 4, 2, 64, BF16, BF16, 8, seed=5,
-               poke=lambda cu, preq, plen, table: preq.__setitem__(0, 2**31 - 1))
+    for W in (None, CUT):
+        for io, cache in ((F32, BF16), (BF16, BF16), (F32, F32)):
+            run_prefix([3, 2, 2, 9], [200, 77, 50, 60], [5, 1, 9, 20, 2, 3, 4, 8, 9], 4, 2, 64, io, cache, 8, W=W, seed=5,
+                       poke=poke)
+        run_prefix([3], [200], [5, 1, 9], 4, 2, 64, BF16, BF16, 8, W=W, seed=5,
+                   poke=lambda cu, preq, plen, table: preq.__setitem__(0, 2**31 - 1))
 
 
 def test_prefix_shared_by_two_groups_and_own_request():
@@ -566,7 +592,8 @@ def test_prefix_shared_by_two_groups_and_own_request():
     def poke(cu, preq, plen, table):
         preq[1], plen[1] = preq[0], 90
         preq[2], plen[2] = 4, 12
-    run_prefix([2, 2, 2], [200, 200, 77], [5, 1, 9, 20, 30, 3], 4, 2, 64, BF16, BF16, 8, seed=6, poke=poke)
+    for W in (None, CUT):
+        run_prefix([2, 2, 2], [200, 200, 77], [5, 1, 9, 20, 30, 3], 4, 2, 64, BF16, BF16, 8, W=W, seed=6, poke=poke)
 
 
 def test_prefix_no_groups():
@@ -579,14 +606,15 @@ def test_prefix_no_groups():
 
 
 @pytest.mark.parametrize("io,cache", [(F32, BF16), (BF16, BF16), (F32, F32), (BF16, F32)])
-def test_prefix_special_values(io, cache):
+@pytest.mark.parametrize("W", [30, CUT])
+def test_prefix_special_values(io, cache, W):
     """An infinite value at a live position reaches its own dimension of the rows that read it; NaN keys
     make those rows NaN and no others."""
     g = torch.Generator().manual_seed(1)
     P, hk, hd, heads = 8, 2, 64, 4
     k, v = make_cache(60, P, hk, hd, cache, g)
-    table = torch.full((5, 30), -1, dtype=torch.int32)
-    table[3], table[4, :20] = torch.arange(30), torch.arange(30, 50)
+    table = torch.full((5, W), -1, dtype=torch.int32)
+    table[3, :30], table[4, :20] = torch.arange(30), torch.arange(30, 50)
     for r in range(3):
         table[r, 0] = 50 + r
     v[4, 3, 0, 5], v[33, 1, 1, 7] = INF, -INF
@@ -675,10 +703,10 @@ def test_shared_prompt_of_a_server(dtype, io):
         assert torch.allclose(lse, bl, rtol=1e-5)
 
 
-def _calls(seed, io=BF16):
+def _calls(seed, io=BF16, scratch=None):
     """The four calls on one set of inputs, as closures on tensors that stay."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    R, H, hk, hd, P, W = 9, 8, 2, 64, 8, 40
+    R, H, hk, hd, P, W = 9, 8, 2, 128, 8, 500
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(io)  # noqa: E731
     N = (R + 1) * W
     k, v = rnd(N, P, hk, hd), rnd(N, P, hk, hd)
@@ -692,6 +720,8 @@ def _calls(seed, io=BF16):
     cu, preq, plen = ints([0, 5, 9]), ints([R, 3]), ints([W * P - 3, 50])
     ws = [paged.paged_select_workspace(q, bounds, table, P), paged.paged_sparse_attention_workspace(q, k, pages),
           paged.paged_prefix_attention_workspace(q, k, table, plen)]
+    if scratch is not None:
+        ws = scratch + ws[len(scratch):]
 
     def run(stream=None):
         paged.paged_bounds(k, bounds, every, slots, stream=stream)
@@ -699,6 +729,7 @@ def _calls(seed, io=BF16):
         paged.paged_sparse_attention(q, k, v, table, pos, pages, out=out[0], lse=lse[0], workspace=ws[1], stream=stream)
         paged.paged_prefix_attention(q, k, v, table, pos, cu, preq, plen, out=out[1], lse=lse[1], workspace=ws[2],
                                      stream=stream)
+    run.scratch = ws
     return run, [bounds, pages, out, lse], [k, v, q, pos]
 
 
@@ -727,7 +758,7 @@ def test_calls_in_a_graph_and_twice():
 def test_two_graphs_one_after_the_other():
     """Two captured graphs that share scratch, replayed in turn on one stream."""
     run1, outs1, _ = _calls(3)
-    run2, outs2, _ = _calls(4)
+    run2, outs2, _ = _calls(4, scratch=run1.scratch)
     run1(), run2()
     first = [[x.clone() for x in o] for o in (outs1, outs2)]
     graphs = []
