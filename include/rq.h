@@ -518,7 +518,7 @@ rq_status rq_paged_sparse_attention(const rq_paged_kv *kv, int32_t rows, int32_t
  * were appended once); the rows' own requests hold what follows, at positions of their own
  * from 0.  (Rotations are rq_paged_append's: its positions count from the prefix's start.)
  *   rows, heads  rows at most 2^29, rows * heads at most 2^30 (RQ_ERR_UNSUPPORTED above)
- *   groups      G >= 0, at most 2^20 (RQ_ERR_UNSUPPORTED above)
+ *   groups      G >= 0, at most 2^16 (RQ_ERR_UNSUPPORTED above)
  *   cu_rows     device [G + 1] int32, rising: rows cu_rows[g] .. cu_rows[g+1]-1 are group g's; rows
  *               outside all groups attend to their own request alone.  Entries outside [0, R]
  *               count as its ends

@@ -577,7 +577,7 @@ inline Layout layout_of(int rows, int kv_heads, int W) {
   x.chunks = (W + kChunk - 1) / kChunk;
   // a warp's chunks: more than one where those that are resident at once (16 an SM) would have six; rows
   // are seldom as long as their tables, and long items leave warps idle at the end (64 rows of 31 to 2031
-  // pages of 2048: 38 us with six chunks an item, XX with two)
+  // pages of 2048: 38 us with six chunks an item, 32 with two)
   const long long warps = (long long)rows * kv_heads * x.chunks;
   x.span = (int)std::min<long long>(std::max<long long>(warps / (96ll * std::max(sm_count(), 1)), 1), 4);
   const size_t n = (size_t)rows * kv_heads;
