@@ -316,13 +316,19 @@ def _geometry(bounds, block_size):
     return _KV.pack(at, at, 0, 0, 0, _TYPE[dtype], h, hd, block_size, n), h, hd, dev
 
 
+@lru_cache(maxsize=1024)
+def _select_workspace_size(dev, dtype, rows, kv_heads, head_dim, block_size, max_blocks):
+    kv = _KV.pack(16, 16, 0, 0, 0, dtype, kv_heads, head_dim, block_size, 1)
+    return load().rq_paged_select_workspace_size(kv, rows, max_blocks)
+
+
 def paged_select_workspace(q, bounds, block_table, block_size):
     """Scratch for paged_select with these shapes."""
-    kv, _, _, _ = _geometry(bounds, block_size)
+    _, hk, hd, dev = _geometry(bounds, block_size)
     if (q.shape[0] | block_table.shape[1]) >> 31:
         _past_int32(q.shape[0], block_table.shape[1])
     with _on(bounds.device, None):
-        size = load().rq_paged_select_workspace_size(kv, q.shape[0], block_table.shape[1])
+        size = _select_workspace_size(dev, _TYPE[bounds.dtype], q.shape[0], hk, hd, block_size, block_table.shape[1])
     return torch.empty(size, dtype=torch.uint8, device=bounds.device)
 
 
@@ -360,15 +366,16 @@ def paged_select(q, bounds, block_table, positions, block_size, top, first=1, la
             not pages.is_contiguous():
         _bad_rows("pages", (R, hk, top), _I32, dev)
     if workspace is None:
-        workspace = torch.empty(load().rq_paged_select_workspace_size(kv, R, W), dtype=torch.uint8,
-                                device=bounds.device)
+        nbytes = _select_workspace_size(dev, _TYPE[bounds.dtype], R, hk, hd, block_size, W)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=bounds.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     rc = load().rq_paged_select(
         kv, bounds.data_ptr(), R, heads, B, W, block_table.data_ptr(),
         None if requests is None else requests.data_ptr(), positions.data_ptr(), top, first, last,
-        _TYPE[dtype], q.data_ptr(), pages.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _current_stream(dev))
+        _TYPE[dtype], q.data_ptr(), pages.data_ptr(), workspace.data_ptr(), nbytes, _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_select", rc)
     return pages
@@ -439,15 +446,6 @@ def _rows(q, k, hd, dev, block_table, positions, requests, out, lse, scale):
     return R, heads, B, W, out, lse
 
 
-def _scratch(workspace, nbytes, k, dev):
-    """(workspace, its bytes), allocated where the caller passed none."""
-    if workspace is None:
-        return (torch.empty(nbytes, dtype=torch.uint8, device=k.device) if nbytes else None), nbytes
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 def paged_sparse_attention(q, k, v, block_table, positions, pages, requests=None, scale=0.0, out=None,
                            lse=None, workspace=None, stream=None):
     """rq_paged_sparse_attention: paged_attention in which row r's queries of K/V head h read the
@@ -464,8 +462,14 @@ def paged_sparse_attention(q, k, v, block_table, positions, pages, requests=None
     n = pages.shape[2]
     if n >> 31:
         _past_int32(n)
-    workspace, nbytes = _scratch(workspace, 0 if workspace is not None else _sparse_workspace_size(
-        dev, _TYPE[k.dtype], R, heads, hk, hd, k.shape[1], n), k, dev)
+    if workspace is None:
+        nbytes = _sparse_workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.shape[1], n)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     rc = load().rq_paged_sparse_attention(
         kv, R, heads, B, W, block_table.data_ptr(), None if requests is None else requests.data_ptr(),
         positions.data_ptr(), n, pages.data_ptr(), scale, _TYPE[q.dtype], q.data_ptr(), out.data_ptr(),
@@ -491,17 +495,26 @@ def paged_prefix_attention(q, k, v, block_table, positions, cu_rows, prefix_requ
     G = prefix_lens.numel()
     if G >> 31:
         _past_int32(G)
-    for name, t, n in (("cu_rows", cu_rows, G + 1), ("prefix_requests", prefix_requests, G),
-                       ("prefix_lens", prefix_lens, G)):
-        if t.dtype is not _I32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
-            _bad_ints(name, n, dev)
-    workspace, nbytes = _scratch(workspace, 0 if workspace is not None else _prefix_workspace_size(
-        dev, _TYPE[k.dtype], R, heads, hk, hd, k.stride(2), k.shape[1], W, G), k, dev)
+    if cu_rows.dtype is not _I32 or cu_rows.get_device() != dev or cu_rows.numel() <= G or \
+            not cu_rows.is_contiguous():
+        _bad_ints("cu_rows", G + 1, dev)
+    if prefix_requests.dtype is not _I32 or prefix_requests.get_device() != dev or \
+            prefix_requests.numel() < G or not prefix_requests.is_contiguous():
+        _bad_ints("prefix_requests", G, dev)
+    if prefix_lens.dtype is not _I32 or prefix_lens.get_device() != dev or not prefix_lens.is_contiguous():
+        _bad_ints("prefix_lens", G, dev)
+    if workspace is None:
+        nbytes = _prefix_workspace_size(dev, _TYPE[k.dtype], R, heads, hk, hd, k.stride(2), k.shape[1], W, G)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=k.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on cuda:%d" % dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     rc = load().rq_paged_prefix_attention(
         kv, R, heads, B, W, block_table.data_ptr(), None if requests is None else requests.data_ptr(),
         positions.data_ptr(), G, cu_rows.data_ptr(), prefix_requests.data_ptr(), prefix_lens.data_ptr(),
         scale, _TYPE[q.dtype], q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), nbytes, _current_stream(dev))
+        workspace.data_ptr(), nbytes, _current_stream(dev))
     if rc != RQ_OK:
         _fail("rq_paged_prefix_attention", rc)
     return out, lse
