@@ -26,8 +26,11 @@
 // and its queries, and its key j is position j % block_size of the list's entry j / block_size.
 //
 // Prefixes. In mode kPrefixes each row of queries is two rows, one over the prefix that its group
-// shares and one over its own request.
+// shares and one over its own request. Of the first kind `bundle` rows of a group are one, their queries
+// a unit's like those of one row are; the others of the bundle have nothing to do.
 #pragma once
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "tc_common.cuh"
@@ -61,6 +64,8 @@ struct Params {
   int list, kv_heads;    // kLists: entries of a list; rows of one query token
   const int32_t *cu_rows, *prefix_requests, *prefix_lens;  // kPrefixes: rq_paged_prefix_attention's
   int groups, q_rows;    // rows of queries: over prefixes first, then as many over their own requests
+  int bundle;            // rows over a prefix that are one
+  int row_heads, row_skip;  // queries of a row in a unit, and the heads to the next row's first behind them
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
   float unit;          // what the sums of values are in (a core's kUnit)
@@ -115,19 +120,36 @@ __device__ __forceinline__ int2 row_words(const Params& p, int r) {
   if ((unsigned)r >= (unsigned)p.rows) return make_int2(-1, -1);
   if (MODE == kLists) r /= p.kv_heads;
   if constexpr (MODE == kPrefixes) {
-    const bool own = r >= p.q_rows;
-    if (own) r -= p.q_rows;
-    const int b = p.requests ? p.requests[r] : r;
-    if (own || b < 0 || b >= p.batch) return make_int2(b, p.positions[r]);
+    if (r >= p.q_rows) {
+      r -= p.q_rows;
+      return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
+    }
     const int g = group_of(p.cu_rows, p.groups, r);
     if (g >= 0) {
-      const int x = p.prefix_requests[g];
-      if (x >= 0 && x < p.batch) return make_int2(x, max(p.prefix_lens[g], 0) - 1);
+      const int x = p.prefix_requests[g], n = p.prefix_lens[g];
+      if (x >= 0 && x < p.batch && n > 0)
+        return (r - max(p.cu_rows[g], 0)) % p.bundle == 0 ? make_int2(x, n - 1) : make_int2(-1, -1);
     }
     return make_int2(0, -1);  // no prefix: an empty request
   }
   return make_int2(p.requests ? p.requests[r] : r, p.positions[r]);
 }
+
+// rows of a unit of row r
+template <Mode MODE>
+__device__ __forceinline__ int bundle_of(const Params& p, int r) {
+  if (MODE != kPrefixes || p.bundle == 1 || r >= p.q_rows) return 1;
+  const int g = group_of(p.cu_rows, p.groups, r);
+  return g < 0 ? 1 : min(p.bundle, min(p.cu_rows[g + 1], p.q_rows) - r);
+}
+// where query g of a unit is, in heads from its first
+struct Next {
+  __device__ __forceinline__ size_t operator()(int g) const { return g; }
+};
+struct Bundled {
+  int row_heads, row_skip;
+  __device__ __forceinline__ size_t operator()(int g) const { return g + (size_t)(g / row_heads) * row_skip; }
+};
 
 template <int kKeys, Mode MODE>
 __device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
@@ -271,7 +293,8 @@ struct MmaCore {
     m = neg_inf();
     l = 0.f;
   }
-  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
+  template <typename At>
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*, At at) {
     const int g = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
@@ -280,12 +303,12 @@ struct MmaCore {
         const int d = k * 16 + c + i * 8;
         if constexpr (kF32) {
           float2 x = make_float2(0.f, 0.f);
-          if (g < live) x = *reinterpret_cast<const float2*>(qrow + (size_t)g * HD + d);
+          if (g < live) x = *reinterpret_cast<const float2*>(qrow + at(g) * HD + d);
           q[0][k][i] = split_bf16(x.x, x.y);
           q[1][k][i] = split_bf16(x.x, x.y);
           q[2][k][i] = pack_bf16(x.x, x.y);
         } else {
-          q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)g * HD + d) : 0u;
+          q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + at(g) * HD + d) : 0u;
         }
       }
   }
@@ -384,8 +407,8 @@ struct MmaCore {
   }
 
   // the unit's outputs, or with PARTIAL its (m, l) and sums
-  template <bool PARTIAL, typename OT>
-  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+  template <bool PARTIAL, typename OT, typename At>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane, At at) {
     float t = l + __shfl_xor_sync(0xffffffffu, l, 1);
     t += __shfl_xor_sync(0xffffffffu, t, 2);
     const int g = lane >> 2, c = (lane & 3) * 2;
@@ -394,11 +417,11 @@ struct MmaCore {
 #pragma unroll
     for (int i = 0; i < HD / 8; ++i) {
       const float2 x = unpack2(acc[i]);
-      put2(out + (size_t)g * HD + i * 8 + c, x.x * inv, x.y * inv);
+      put2(out + at(g) * HD + i * 8 + c, x.x * inv, x.y * inv);
     }
     if ((lane & 3) != 0) return;
     if (PARTIAL) ml[g] = make_float2(m, t);
-    else if (lse) lse[g] = log_sum(m, t);
+    else if (lse) lse[at(g)] = log_sum(m, t);
   }
 };
 
@@ -429,7 +452,8 @@ struct WideCore {
     m[0] = m[1] = neg_inf();
     l[0] = l[1] = 0.f;
   }
-  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
+  template <typename At>
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*, At at) {
     const int c = (lane & 3) * 2;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
@@ -438,11 +462,11 @@ struct WideCore {
         const int g = (lane >> 2) + (i & 1) * 8, d = k * 16 + c + (i >> 1) * 8;
         if constexpr (kF32) {
           float2 x = make_float2(0.f, 0.f);
-          if (g < live) x = *reinterpret_cast<const float2*>(qrow + (size_t)g * HD + d);
+          if (g < live) x = *reinterpret_cast<const float2*>(qrow + at(g) * HD + d);
 #pragma unroll
           for (int j = 0; j < QP; ++j) q[j][k][i] = split_bf16(x.x, x.y);
         } else {
-          q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + (size_t)g * HD + d) : 0u;
+          q[0][k][i] = g < live ? *reinterpret_cast<const uint32_t*>(qrow + at(g) * HD + d) : 0u;
         }
       }
   }
@@ -529,8 +553,8 @@ struct WideCore {
     }
   }
 
-  template <bool PARTIAL, typename OT>
-  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+  template <bool PARTIAL, typename OT, typename At>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane, At at) {
     const int c = (lane & 3) * 2;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -541,10 +565,10 @@ struct WideCore {
       const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : 1.f / t;
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i)
-        put2(out + (size_t)g * HD + i * 8 + c, acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
+        put2(out + at(g) * HD + i * 8 + c, acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
       if ((lane & 3) != 0) continue;
       if (PARTIAL) ml[g] = make_float2(m[h], t);
-      else if (lse) lse[g] = log_sum(m[h], t);
+      else if (lse) lse[at(g)] = log_sum(m[h], t);
     }
   }
 };
@@ -568,22 +592,23 @@ struct SideCore {
 #pragma unroll
     for (int i = 0; i < N; ++i) core[i].clear();
   }
-  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*) {
+  template <typename At>
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float*, At at) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) core[i].load(qrow + (size_t)i * (live / N) * HD, live / N, lane, nullptr);
+    for (int i = 0; i < N; ++i) core[i].load(qrow + (size_t)i * (live / N) * HD, live / N, lane, nullptr, at);
   }
   template <int I = 0>
   __device__ __forceinline__ void tile(float scale_log2, uint32_t ks, uint32_t mask, int lane, float*) {
     core[I].template tile<I * HD / 8>(scale_log2, ks, mask, lane, nullptr);
     if constexpr (I + 1 < N) tile<I + 1>(scale_log2, ks, mask, lane, nullptr);
   }
-  template <bool PARTIAL, typename OT>
-  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+  template <bool PARTIAL, typename OT, typename At>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane, At at) {
     const int g = live / N;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       core[i].template end<PARTIAL>(out + (size_t)i * g * HD, lse ? lse + i * g : nullptr,
-                                    ml ? ml + i * g : nullptr, g, lane);
+                                    ml ? ml + i * g : nullptr, g, lane, at);
   }
 };
 
@@ -628,13 +653,14 @@ struct FmaCore {
       l[h] = 0.f;
     }
   }
-  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float* scratch) {
+  template <typename At>
+  __device__ __forceinline__ void load(const QT* qrow, int live, int lane, float* scratch, At at) {
 #pragma unroll
     for (int h = 0; h < GP; ++h)
 #pragma unroll
       for (int sl = 0; sl < SL; ++sl)
         scratch[(h * SL + sl) * kQPitch + lane] =
-            h < live ? one(qrow + (size_t)h * HD + sl * 32 + lane) : 0.f;
+            h < live ? one(qrow + at(h) * HD + sl * 32 + lane) : 0.f;
     __syncwarp();
   }
 
@@ -717,8 +743,8 @@ struct FmaCore {
     __syncwarp();
   }
 
-  template <bool PARTIAL, typename OT>
-  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane) {
+  template <bool PARTIAL, typename OT, typename At>
+  __device__ __forceinline__ void end(OT* out, float* lse, float2* ml, int live, int lane, At at) {
 #pragma unroll
     for (int h = 0; h < GP; ++h) {
       float t = l[h];
@@ -735,12 +761,12 @@ struct FmaCore {
       if (h >= live) continue;
       const float inv = PARTIAL ? 1.f : t == 0.f ? 0.f : kUnit / t;
       if (lane < HD / 4) {
-        put2(out + (size_t)h * HD + lane * 4, a.x * inv, a.y * inv);
-        put2(out + (size_t)h * HD + lane * 4 + 2, b.x * inv, b.y * inv);
+        put2(out + at(h) * HD + lane * 4, a.x * inv, a.y * inv);
+        put2(out + at(h) * HD + lane * 4 + 2, b.x * inv, b.y * inv);
       }
       if (lane != 0) continue;
       if (PARTIAL) ml[h] = make_float2(m[h], t);
-      else if (lse) lse[h] = log_sum(m[h], t);
+      else if (lse) lse[at(h)] = log_sum(m[h], t);
     }
   }
 };
@@ -893,6 +919,9 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   }
   Core core;
   core.clear();
+  using At = std::conditional_t<MODE == kPrefixes, Bundled, Next>;
+  At place{};
+  if constexpr (MODE == kPrefixes) place = Bundled{p.row_heads, p.row_skip};
   if (at < stop) {
     // ---- the cursor over the tiles. Table entries are read 32 pages at a time, a lane each,
     // well ahead of their use: ids of pages [base, base + 32), then the 32 that follow, the
@@ -915,7 +944,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     int base = (x.t0 + t) * K / P, ids = ids_from(x, base), ids_after = ids_from(x, base + 32);
     int ids0 = SPLIT || t == 0 ? ids : ids_from(x, x.t0 * K / P), ids_next = -1;
     bool next_known = SPLIT, more = true, start = true, first = false;
-    int issued = 0;
+    int issued = 0, n = 0;  // kPrefixes: rows of the unit
     const uint32_t ring = smem_u32(smem) + warp * NS * S::kStage;
     float* const scratch = reinterpret_cast<float*>(smem + NW * NS * S::kStage + warp * Core::kScratch);
     auto issue = [&]() {
@@ -943,8 +972,9 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
                                : 0;
       if (t == 0) first = true;
       const bool last = t == x.nt - 1, end = last || at + 1 >= stop;
+      if (MODE == kPrefixes && start) n = bundle_of<MODE>(p, r);
       if (lane == 0)
-        s_desc[warp][s] = make_int4(r, kvh, hg * 16 + ((start ? kStart : 0) | (end ? kEnd : 0) |
+        s_desc[warp][s] = make_int4(r, kvh | n << 24, hg * 16 + ((start ? kStart : 0) | (end ? kEnd : 0) |
                                                        (first ? kFirst : 0) | (last ? kLast : 0)),
                                     (int)mask);
       if (start) {  // the unit's queries will be wanted soon
@@ -955,7 +985,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
       }
       if (end && !last && first)  // goes on in the runs that follow
-        cut = make_int4(r, kvh * p.G + hg * Core::kHeads, min(Core::kHeads, p.G - hg * Core::kHeads),
+        cut = make_int4(r, kvh * p.G + hg * Core::kHeads,
+                        n > 1 ? n * p.G : min(Core::kHeads, p.G - hg * Core::kHeads),
                         (int)((at + (x.nt - t) - 1) / per - run) + 1);
       if (mask) {
         constexpr int CH = S::kPitch / 16;        // 16-byte pieces of a row
@@ -1034,12 +1065,13 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       cp_async_commit();
       __syncwarp();
       const int4 d = s_desc[warp][i % NS];
-      const int g0 = (d.z >> 4) * Core::kHeads, live = min(Core::kHeads, p.G - g0);
-      const size_t head = (size_t)d.x * p.heads + (size_t)d.y * p.G + g0;
+      const int g0 = (d.z >> 4) * Core::kHeads, n = d.y >> 24;
+      const int live = n > 1 ? n * p.G : min(Core::kHeads, p.G - g0);
+      const size_t head = (size_t)d.x * p.heads + (size_t)(d.y & 0xffffff) * p.G + g0;
       if (d.z & kStart) {
         core.clear();
         const size_t q_head = MODE == kPrefixes && d.x >= p.q_rows ? head - (size_t)p.q_rows * p.heads : head;
-        core.load(static_cast<const QT*>(p.q) + q_head * HD, live, lane, scratch);
+        core.load(static_cast<const QT*>(p.q) + q_head * HD, live, lane, scratch, place);
       }
       cp_async_wait<NS - 1>();
       __syncwarp();
@@ -1048,10 +1080,10 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (SPLIT || !(d.z & kEnd)) continue;
       if ((d.z & kFirst) && (d.z & kLast)) {
         core.template end<false>(static_cast<OT*>(p.out) + head * HD, p.lse ? p.lse + head : nullptr,
-                                 nullptr, live, lane);
+                                 nullptr, live, lane, place);
       } else {
         const size_t slot = ((size_t)run * 2 + ((d.z & kFirst) ? 1 : 0)) * p.GB;
-        core.template end<true>(p.part + slot * HD, nullptr, p.part_ml + slot, live, lane);
+        core.template end<true>(p.part + slot * HD, nullptr, p.part_ml + slot, live, lane, Next());
       }
     }
   }
@@ -1060,13 +1092,14 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   } else {
     // ---- join: the warps' sums in this CTA's shared memory (its ring is free), then each CTA
     // of the cluster finishes a share of the outputs from every CTA's sums
-    const int live = min(Core::kHeads, p.G - hg * Core::kHeads), n = live * HD;
+    const int rows = bundle_of<MODE>(p, r);
+    const int live = rows > 1 ? rows * p.G : min(Core::kHeads, p.G - hg * Core::kHeads), n = live * HD;
     float* const s_sum = reinterpret_cast<float*>(smem);              // [NW][kHeads][HD]
     float* const s_cta = s_sum + NW * Core::kHeads * HD;              // [kHeads][HD]
     float2* const s_ml = reinterpret_cast<float2*>(s_cta + Core::kHeads * HD);  // [NW][kHeads]
     float2* const s_cta_ml = s_ml + NW * Core::kHeads;                // [kHeads]
     __syncthreads();
-    core.template end<true>(s_sum + warp * Core::kHeads * HD, nullptr, s_ml + warp * Core::kHeads, live, lane);
+    core.template end<true>(s_sum + warp * Core::kHeads * HD, nullptr, s_ml + warp * Core::kHeads, live, lane, Next());
     __syncthreads();
     const size_t head = (size_t)r * p.heads + (size_t)kvh * p.G + hg * Core::kHeads;
     const int ctas = gridDim.x;
@@ -1086,8 +1119,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         s_cta[i] = a;
         if (i % HD == 0) s_cta_ml[g] = make_float2(m, l);
       } else {
-        put(static_cast<OT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
-        if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
+        put(static_cast<OT*>(p.out) + (head + place(g)) * HD + i % HD, l == 0.f ? 0.f : a / l * Core::kUnit);
+        if (p.lse && i % HD == 0) p.lse[head + place(g)] = log_sum(m, l);
       }
     }
     if (ctas == 1) return;
@@ -1104,8 +1137,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         l += tc::ld_cluster(tc::mapa(mls + g * 8 + 4, c)) * f;
         a = fmaf(tc::ld_cluster(tc::mapa(sums + i * 4, c)), f, a);
       }
-      put(static_cast<OT*>(p.out) + head * HD + i, l == 0.f ? 0.f : a / l * Core::kUnit);
-      if (p.lse && i % HD == 0) p.lse[head + g] = log_sum(m, l);
+      put(static_cast<OT*>(p.out) + (head + place(g)) * HD + i % HD, l == 0.f ? 0.f : a / l * Core::kUnit);
+      if (p.lse && i % HD == 0) p.lse[head + place(g)] = log_sum(m, l);
     }
     tc::cluster_sync();  // no CTA leaves while another reads its sums
   }
@@ -1174,7 +1207,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
   auto write = [&](const int4& cut, float m, float l, const float (&a)[E]) {
-    const size_t head = (size_t)cut.x * p.heads + cut.y + g;
+    const size_t head = (size_t)cut.x * p.heads + cut.y + Bundled{p.row_heads, p.row_skip}(g);
     const float inv = l == 0.f ? 0.f : p.unit / l;
 #pragma unroll
     for (int e = 0; e < E; ++e) put(static_cast<OT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
@@ -1263,7 +1296,8 @@ inline int split_ctas(long long units, long long tiles, int rows, bool bf16, int
   return most <= (rows > 1 ? 8 : full ? 128 : bf16 ? 24 : 8) ? c : 0;
 }
 
-inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int window) {
+// bundle: rows whose queries are one unit's (g * bundle at most eight)
+inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int window, int bundle = 1) {
   Choice x{};
   const int g = heads / kv.heads;
   const bool bf16 = kv.dtype == RQ_BF16;
@@ -1273,7 +1307,7 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
   if (window > 0 && window < keys) keys = window;
   const int row_bytes = kv.head_dim * (bf16 ? 2 : 4), tile = 4096 / row_bytes < 32 ? 4096 / row_bytes : 32;
   x.side = 1;
-  x.unit_heads = g < most ? g : most;
+  x.unit_heads = g < most ? g * bundle : most;
   x.units_of_kv = (g + most - 1) / most;
   x.units = (long long)rows * kv.heads * x.units_of_kv;
   x.tiles = keys / tile + 2;
@@ -1284,7 +1318,7 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
   x.workspace = 0;
   if (x.split || x.whole) return x;
   // runs that the memory bounds: two heads at a time where they lie side by side
-  if (bf16 && kv.head_dim < 128 && g <= 8 && kv.head_stride == kv.head_dim && kv.heads % 2 == 0) {
+  if (bf16 && bundle == 1 && kv.head_dim < 128 && g <= 8 && kv.head_stride == kv.head_dim && kv.heads % 2 == 0) {
     x.side = 2;
     x.unit_heads = 2 * g;
     x.units /= 2;
@@ -1301,6 +1335,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   if (x.unit_heads > Core::kHeads) return cudaErrorInvalidValue;
   p.HG = x.units_of_kv;
   p.GB = x.unit_heads;
+  if (MODE != kPrefixes) p.row_heads = INT_MAX;
   p.unit = Core::kUnit;
   if constexpr (Core::kLoad == HD) {  // units of one K/V head
     if (x.split) {

@@ -152,6 +152,7 @@ struct Layout {
   paged_attn::Choice x;
   bool tc;         // prefixes by matrix products
   int ctas, unit;  // of the prefix kernel
+  int bundle;      // else: rows of a group whose queries are a unit's
   size_t o, lse, part, part_ml, group, bytes;
 };
 
@@ -164,15 +165,14 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   // 19 us against 25).
   const double most = 4.0 * rows * kv.heads * hd * max_blocks * kv.block_size;
   l.tc = groups > 0 && kv.dtype == RQ_BF16 && most > 32e6;
-  l.x = paged_attn::choose(kv, rows, heads, max_blocks, 0);
-  if (!l.tc && groups > 0) {
-    // two rows of a query row: where its own alone would be split, both are, over half the CTAs each
-    if (l.x.split) {
-      l.x.split = std::max(l.x.split / 2, 1);
-      l.x.units *= 2;
-    } else {
-      l.x = paged_attn::choose(kv, 2 * rows, heads, max_blocks, 0);
-    }
+  if (l.tc || groups == 0) {
+    l.x = paged_attn::choose(kv, rows, heads, max_blocks, 0);
+  } else {
+    // the rows' own, and a bundle of them each over a prefix: that is the work, but all are rows of the launch
+    const int g = heads / kv.heads;
+    l.bundle = std::min(g <= 8 ? 8 / g : 1, rows);
+    l.x = paged_attn::choose(kv, rows + (rows + l.bundle - 1) / l.bundle, heads, max_blocks, 0, l.bundle);
+    l.x.units = 2ll * rows * kv.heads * l.x.units_of_kv;
   }
   l.o = align256((size_t)rows * heads * hd * sizeof(float));
   l.lse = align256((size_t)rows * heads * sizeof(float2));
@@ -302,6 +302,9 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
     const MergeParams m{requests, rows, heads, batch, kv->head_dim, o, own_o, ls, ls + (size_t)rows * heads, out, lse};
     p.rows = 2 * rows;
     p.q_rows = rows;
+    p.bundle = l.bundle;
+    p.row_heads = p.G;
+    p.row_skip = heads - p.G;
     p.groups = groups;
     p.cu_rows = cu_rows;
     p.prefix_requests = prefix_requests;

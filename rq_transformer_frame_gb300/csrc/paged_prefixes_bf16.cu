@@ -14,9 +14,10 @@ static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
       side.kv.heads /= N;
       side.kv.head_stride *= N;
       side.G *= N;
+      side.row_heads = side.G;
       return launch<QT, uint16_t, HD, SideCore<QT, HD, N>, kPrefixes, float>(side, x, s);
     }
-  return p.G <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>, kPrefixes, float>(p, x, s)
+  return x.unit_heads <= 8 ? launch<QT, uint16_t, HD, MmaCore<QT, HD>, kPrefixes, float>(p, x, s)
                   : launch<QT, uint16_t, HD, WideCore<QT, HD>, kPrefixes, float>(p, x, s);
 }
 

@@ -7,9 +7,9 @@ namespace paged_attn {
 
 template <typename QT, int HD>
 static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
-  if (p.G == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, kPrefixes, float>(p, x, s);
-  if (p.G == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, kPrefixes, float>(p, x, s);
-  if (p.G <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, kPrefixes, float>(p, x, s);
+  if (x.unit_heads == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, kPrefixes, float>(p, x, s);
+  if (x.unit_heads == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, kPrefixes, float>(p, x, s);
+  if (x.unit_heads <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, kPrefixes, float>(p, x, s);
   return launch<QT, float, HD, FmaCore<QT, HD, 8>, kPrefixes, float>(p, x, s);
 }
 
