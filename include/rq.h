@@ -446,7 +446,7 @@ rq_status rq_paged_attention(const rq_paged_kv *kv, int32_t rows, int32_t heads,
 /* ---- Long contexts over the paged cache.  Beside rq_paged_attention, which reads all of a
  * row's positions, two ways of reading less: pages that a cheap score selects for each row
  * (rq_paged_bounds, rq_paged_select, rq_paged_sparse_attention), and a prefix that many rows
- * share, read once for all of them (rq_paged_prefix_attention).  Rows, requests, positions,
+ * share, read once for all of them over a bf16 cache (rq_paged_prefix_attention).  Rows, requests, positions,
  * block tables (rings too) and types are as there, and so are padding rows (a request outside
  * [0, batch): outputs left as they were) and empty ones (a negative position). */
 

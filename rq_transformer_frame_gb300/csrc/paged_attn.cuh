@@ -60,18 +60,24 @@ struct Params {
   int G, GB, HG;       // query heads per K/V head (of all a unit reads), of a unit; units of a K/V head
   int runs;            // runs (warps) of the launch
   int whole;           // units of a run that takes whole ones, 0: runs are cut anywhere
-  const int32_t* pages;  // kLists: [rows][list] pages, -1 in empty entries
-  int list, kv_heads;    // kLists: entries of a list; rows of one query token
-  const int32_t *cu_rows, *prefix_requests, *prefix_lens;  // kPrefixes: rq_paged_prefix_attention's
-  int groups, q_rows;    // rows of queries: over prefixes first, then as many over their own requests
-  int bundle;            // rows over a prefix that are one
-  int row_heads, row_skip;  // queries of a row in a unit, and the heads to the next row's first behind them
   float scale;         // times log2 e
   float* part;         // [runs][2][GB][HD] partial sums
   float unit;          // what the sums of values are in (a core's kUnit)
   float2* part_ml;     // [runs][2][GB] (m, l)
   int4* cut;           // [runs] (row, first head, heads, parts) of the unit that starts there and goes on
 };
+
+// what the other modes have besides (a launch's time goes by the size of its parameters too)
+struct MoreParams : Params {
+  const int32_t* pages;  // kLists: [rows][list] pages, -1 in empty entries
+  int list, kv_heads;    // kLists: entries of a list; rows of one query token
+  const int32_t *cu_rows, *prefix_requests, *prefix_lens;  // kPrefixes: rq_paged_prefix_attention's
+  int groups, q_rows;    // rows of queries: over prefixes first, then as many over their own requests
+  int bundle;            // rows over a prefix that are one
+  int row_heads, row_skip;  // queries of a row in a unit, and the heads to the next row's first behind them
+};
+template <Mode MODE>
+using ParamsOf = std::conditional_t<MODE == kRows, Params, MoreParams>;
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline size_t part_bytes(int gb, int hd) {
@@ -116,9 +122,9 @@ __device__ __forceinline__ int group_of(const int32_t* cu_rows, int groups, int 
 
 // row r's request and position as they stand; out of the list: no tiles
 template <Mode MODE>
-__device__ __forceinline__ int2 row_words(const Params& p, int r) {
+__device__ __forceinline__ int2 row_words(const ParamsOf<MODE>& p, int r) {
   if ((unsigned)r >= (unsigned)p.rows) return make_int2(-1, -1);
-  if (MODE == kLists) r /= p.kv_heads;
+  if constexpr (MODE == kLists) r /= p.kv_heads;
   if constexpr (MODE == kPrefixes) {
     if (r >= p.q_rows) {
       r -= p.q_rows;
@@ -137,8 +143,9 @@ __device__ __forceinline__ int2 row_words(const Params& p, int r) {
 
 // rows of a unit of row r
 template <Mode MODE>
-__device__ __forceinline__ int bundle_of(const Params& p, int r) {
-  if (MODE != kPrefixes || p.bundle == 1 || r >= p.q_rows) return 1;
+__device__ __forceinline__ int bundle_of(const ParamsOf<MODE>& p, int r) {
+  static_assert(MODE == kPrefixes, "rows of the other modes are one each");
+  if (p.bundle == 1 || r >= p.q_rows) return 1;
   const int g = group_of(p.cu_rows, p.groups, r);
   return g < 0 ? 1 : min(p.bundle, min(p.cu_rows[g + 1], p.q_rows) - r);
 }
@@ -152,7 +159,7 @@ struct Bundled {
 };
 
 template <int kKeys, Mode MODE>
-__device__ __forceinline__ Row row_of(const Params& p, int r, int2 words) {
+__device__ __forceinline__ Row row_of(const ParamsOf<MODE>& p, int r, int2 words) {
   Row x;
   x.r = r;
   x.b = words.x;
@@ -787,7 +794,7 @@ enum : int { kStart = 1, kEnd = 2, kFirst = 4, kLast = 8 };
 // OT: the outputs' type, QT but for sums that are joined with others.
 template <typename QT, typename KT, int HD, typename Core, bool SPLIT, Mode MODE, typename OT>
 __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT ? 1 : 2)
-    attend_kernel(const __grid_constant__ Params p) {
+    attend_kernel(const __grid_constant__ ParamsOf<MODE> p) {
   using S = Shape<KT, Core::kLoad>;
   constexpr int NW = SPLIT ? kSplitWarps : kWarps, NT = NW * 32;
   constexpr int NS = SPLIT ? split_stages<S::kStage, Core::kScratch> : kStages, K = S::kKeys;
@@ -922,6 +929,10 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   using At = std::conditional_t<MODE == kPrefixes, Bundled, Next>;
   At place{};
   if constexpr (MODE == kPrefixes) place = Bundled{p.row_heads, p.row_skip};
+  auto behind = [&](int r) {  // rows from that of the queries to this one
+    if constexpr (MODE == kPrefixes) return r >= p.q_rows ? p.q_rows : 0;
+    else return 0;
+  };
   if (at < stop) {
     // ---- the cursor over the tiles. Table entries are read 32 pages at a time, a lane each,
     // well ahead of their use: ids of pages [base, base + 32), then the 32 that follow, the
@@ -957,22 +968,24 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       const int rel = page - base;
       const int id0 = __shfl_sync(0xffffffffu, ids, rel & 31);
       const int id1 = __shfl_sync(0xffffffffu, ids_after, rel & 31);
-      int id = rel < 32 ? id0 : id1;
+      int id = rel < 32 ? id0 : id1, kv_head = kvh;
       bool ok;
       if constexpr (MODE == kLists) {
         ok = id >= 0 || key - page * P <= x.pos % P;
         if (id < 0) id = ~id;
         ok = ok && id < p.kv.n_blocks && page < p.list;
+        kv_head = r % p.kv_heads;
       } else {
         ok = key >= x.lo && key <= x.pos && id >= 0 && id < p.kv.n_blocks;
       }
       const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (K < 32 ? (1u << (K & 31)) - 1u : ~0u);
       const long long off = ok ? id * p.kv.block_stride + (key - page * P) * p.kv.row_stride +
-                                     (MODE == kLists ? r % p.kv_heads : kvh) * p.kv.head_stride
+                                     kv_head * p.kv.head_stride
                                : 0;
       if (t == 0) first = true;
       const bool last = t == x.nt - 1, end = last || at + 1 >= stop;
-      if (MODE == kPrefixes && start) n = bundle_of<MODE>(p, r);
+      if constexpr (MODE == kPrefixes)
+        if (start) n = bundle_of<MODE>(p, r);
       if (lane == 0)
         s_desc[warp][s] = make_int4(r, kvh | n << 24, hg * 16 + ((start ? kStart : 0) | (end ? kEnd : 0) |
                                                        (first ? kFirst : 0) | (last ? kLast : 0)),
@@ -980,8 +993,7 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       if (start) {  // the unit's queries will be wanted soon
         const int g0 = hg * Core::kHeads, n = min(Core::kHeads, p.G - g0) * HD * (int)sizeof(QT);
         const char* q = static_cast<const char*>(p.q) +
-                        ((size_t)(MODE == kPrefixes && r >= p.q_rows ? r - p.q_rows : r) * p.heads +
-                         (size_t)kvh * p.G + g0) * HD * sizeof(QT);
+                        ((size_t)(r - behind(r)) * p.heads + (size_t)kvh * p.G + g0) * HD * sizeof(QT);
         if (lane * 128 < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
       }
       if (end && !last && first)  // goes on in the runs that follow
@@ -1016,7 +1028,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         t = 0;
         first = false;
         at += kUnitCost;
-        const bool one_window = MODE == kLists ? p.list <= 32 : x.pos / P - x.t0 * K / P < 32;
+        bool one_window = x.pos / P - x.t0 * K / P < 32;
+        if constexpr (MODE == kLists) one_window = p.list <= 32;
         if (++hg == p.HG) {
           hg = 0;
           if (++kvh == p.kv.heads) {
@@ -1065,12 +1078,12 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
       cp_async_commit();
       __syncwarp();
       const int4 d = s_desc[warp][i % NS];
-      const int g0 = (d.z >> 4) * Core::kHeads, n = d.y >> 24;
+      const int g0 = (d.z >> 4) * Core::kHeads, n = MODE == kPrefixes ? d.y >> 24 : 0;
       const int live = n > 1 ? n * p.G : min(Core::kHeads, p.G - g0);
-      const size_t head = (size_t)d.x * p.heads + (size_t)(d.y & 0xffffff) * p.G + g0;
+      const size_t head = (size_t)d.x * p.heads + (size_t)(MODE == kPrefixes ? d.y & 0xffffff : d.y) * p.G + g0;
       if (d.z & kStart) {
         core.clear();
-        const size_t q_head = MODE == kPrefixes && d.x >= p.q_rows ? head - (size_t)p.q_rows * p.heads : head;
+        const size_t q_head = head - (size_t)behind(d.x) * p.heads;
         core.load(static_cast<const QT*>(p.q) + q_head * HD, live, lane, scratch, place);
       }
       cp_async_wait<NS - 1>();
@@ -1092,7 +1105,8 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
   } else {
     // ---- join: the warps' sums in this CTA's shared memory (its ring is free), then each CTA
     // of the cluster finishes a share of the outputs from every CTA's sums
-    const int rows = bundle_of<MODE>(p, r);
+    int rows = 1;
+    if constexpr (MODE == kPrefixes) rows = bundle_of<MODE>(p, r);
     const int live = rows > 1 ? rows * p.G : min(Core::kHeads, p.G - hg * Core::kHeads), n = live * HD;
     float* const s_sum = reinterpret_cast<float*>(smem);              // [NW][kHeads][HD]
     float* const s_cta = s_sum + NW * Core::kHeads * HD;              // [kHeads][HD]
@@ -1102,6 +1116,14 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
     core.template end<true>(s_sum + warp * Core::kHeads * HD, nullptr, s_ml + warp * Core::kHeads, live, lane, Next());
     __syncthreads();
     const size_t head = (size_t)r * p.heads + (size_t)kvh * p.G + hg * Core::kHeads;
+    auto at_out = [&](int i, int g) {  // element i, of query g, behind the first head
+      if constexpr (MODE == kPrefixes) return place(g) * HD + i % HD;
+      else return i;
+    };
+    auto at_lse = [&](int g) {
+      if constexpr (MODE == kPrefixes) return place(g);
+      else return g;
+    };
     const int ctas = gridDim.x;
     for (int i = tid; i < n; i += NT) {
       const int g = i / HD;
@@ -1119,8 +1141,9 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         s_cta[i] = a;
         if (i % HD == 0) s_cta_ml[g] = make_float2(m, l);
       } else {
-        put(static_cast<OT*>(p.out) + (head + place(g)) * HD + i % HD, l == 0.f ? 0.f : a / l * Core::kUnit);
-        if (p.lse && i % HD == 0) p.lse[head + place(g)] = log_sum(m, l);
+        put(static_cast<OT*>(p.out) + head * HD + at_out(i, g),
+            l == 0.f ? 0.f : a / l * Core::kUnit);
+        if (p.lse && i % HD == 0) p.lse[head + at_lse(g)] = log_sum(m, l);
       }
     }
     if (ctas == 1) return;
@@ -1137,8 +1160,9 @@ __global__ void __launch_bounds__(SPLIT ? kSplitWarps * 32 : kWarps * 32, SPLIT 
         l += tc::ld_cluster(tc::mapa(mls + g * 8 + 4, c)) * f;
         a = fmaf(tc::ld_cluster(tc::mapa(sums + i * 4, c)), f, a);
       }
-      put(static_cast<OT*>(p.out) + (head + place(g)) * HD + i % HD, l == 0.f ? 0.f : a / l * Core::kUnit);
-      if (p.lse && i % HD == 0) p.lse[head + place(g)] = log_sum(m, l);
+      put(static_cast<OT*>(p.out) + head * HD + at_out(i, g),
+          l == 0.f ? 0.f : a / l * Core::kUnit);
+      if (p.lse && i % HD == 0) p.lse[head + at_lse(g)] = log_sum(m, l);
     }
     tc::cluster_sync();  // no CTA leaves while another reads its sums
   }
@@ -1197,8 +1221,8 @@ __device__ __forceinline__ void join_parts(const Params& p, int i0, int i1, Slot
   }
 }
 
-template <typename OT, int HD>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_constant__ Params p) {
+template <typename OT, int HD, Mode MODE>
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_constant__ ParamsOf<MODE> p) {
   constexpr int E = HD / 32;
   __shared__ int4 s_cut[kJoinWarps];
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][HD];
@@ -1207,7 +1231,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) join_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
   auto write = [&](const int4& cut, float m, float l, const float (&a)[E]) {
-    const size_t head = (size_t)cut.x * p.heads + cut.y + Bundled{p.row_heads, p.row_skip}(g);
+    size_t head = (size_t)cut.x * p.heads + cut.y + g;
+    if constexpr (MODE == kPrefixes) head += Bundled{p.row_heads, p.row_skip}(g) - g;
     const float inv = l == 0.f ? 0.f : p.unit / l;
 #pragma unroll
     for (int e = 0; e < E; ++e) put(static_cast<OT*>(p.out) + head * HD + lane * E + e, a[e] * inv);
@@ -1329,13 +1354,12 @@ inline Choice choose(const rq_paged_kv& kv, int rows, int heads, int max_blocks,
 }
 
 template <typename QT, typename KT, int HD, typename Core, Mode MODE = kRows, typename OT = QT>
-cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
+cudaError_t launch(ParamsOf<MODE> p, const Choice& x, cudaStream_t s) {
   using S = Shape<KT, Core::kLoad>;
   cudaError_t e;
   if (x.unit_heads > Core::kHeads) return cudaErrorInvalidValue;
   p.HG = x.units_of_kv;
   p.GB = x.unit_heads;
-  if (MODE != kPrefixes) p.row_heads = INT_MAX;
   p.unit = Core::kUnit;
   if constexpr (Core::kLoad == HD) {  // units of one K/V head
     if (x.split) {
@@ -1373,7 +1397,7 @@ cudaError_t launch(Params p, const Choice& x, cudaStream_t s) {
   p.runs = grid * kWarps;
   if ((e = launch_dependent(kernel, dim3((unsigned)grid), kWarps * 32, smem, 0, s, p)) != cudaSuccess) return e;
   const dim3 joins((unsigned)((p.runs + kJoinWarps - 1) / kJoinWarps), (unsigned)p.GB, 1);
-  return launch_dependent(join_kernel<OT, HD>, joins, kJoinWarps * 32, 0, 0, s, p);
+  return launch_dependent(join_kernel<OT, HD, MODE>, joins, kJoinWarps * 32, 0, 0, s, p);
 }
 
 // a launch's scratch in its workspace
@@ -1388,11 +1412,11 @@ inline void place(Params& p, const Choice& x, void* workspace) {
 // over prefixes too
 cudaError_t launch_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
-cudaError_t launch_lists_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
-cudaError_t launch_lists_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_lists_bf16(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_lists_f32(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s);
 cudaError_t launch_sums_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
-cudaError_t launch_prefixes_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
-cudaError_t launch_prefixes_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_prefixes_bf16(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s);
+cudaError_t launch_prefixes_f32(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s);
 
 }  // namespace paged_attn
 }  // namespace rqk

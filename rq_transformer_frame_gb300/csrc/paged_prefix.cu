@@ -243,7 +243,7 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   float* const ls = reinterpret_cast<float*>(take(2 * l.lse));
   float* const own_o = o + (size_t)rows * heads * kv->head_dim;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  paged_attn::Params p{};
+  paged_attn::MoreParams p{};
   p.kv = *kv;
   p.q = q;
   p.table = block_table;

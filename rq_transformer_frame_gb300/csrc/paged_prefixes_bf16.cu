@@ -6,11 +6,11 @@ namespace rqk {
 namespace paged_attn {
 
 template <typename QT, int HD>
-static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_heads(const MoreParams& p, const Choice& x, cudaStream_t s) {
   if constexpr (HD < 128)
     if (x.side > 1) {
       constexpr int N = 2;
-      Params side = p;
+      MoreParams side = p;
       side.kv.heads /= N;
       side.kv.head_stride *= N;
       side.G *= N;
@@ -22,7 +22,7 @@ static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
 }
 
 template <typename QT>
-static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_head_dim(const MoreParams& p, const Choice& x, cudaStream_t s) {
   switch (p.kv.head_dim) {
     case 32: return by_heads<QT, 32>(p, x, s);
     case 64: return by_heads<QT, 64>(p, x, s);
@@ -30,7 +30,7 @@ static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s)
   }
 }
 
-cudaError_t launch_prefixes_bf16(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s) {
+cudaError_t launch_prefixes_bf16(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s) {
   return q_bf16 ? by_head_dim<uint16_t>(p, x, s) : by_head_dim<float>(p, x, s);
 }
 

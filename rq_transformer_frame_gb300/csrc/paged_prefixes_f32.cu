@@ -6,7 +6,7 @@ namespace rqk {
 namespace paged_attn {
 
 template <typename QT, int HD>
-static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_heads(const MoreParams& p, const Choice& x, cudaStream_t s) {
   if (x.unit_heads == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, kPrefixes, float>(p, x, s);
   if (x.unit_heads == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, kPrefixes, float>(p, x, s);
   if (x.unit_heads <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, kPrefixes, float>(p, x, s);
@@ -14,7 +14,7 @@ static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
 }
 
 template <typename QT>
-static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_head_dim(const MoreParams& p, const Choice& x, cudaStream_t s) {
   switch (p.kv.head_dim) {
     case 32: return by_heads<QT, 32>(p, x, s);
     case 64: return by_heads<QT, 64>(p, x, s);
@@ -22,7 +22,7 @@ static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s)
   }
 }
 
-cudaError_t launch_prefixes_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s) {
+cudaError_t launch_prefixes_f32(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s) {
   return q_bf16 ? by_head_dim<uint16_t>(p, x, s) : by_head_dim<float>(p, x, s);
 }
 

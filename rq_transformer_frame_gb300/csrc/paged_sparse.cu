@@ -60,7 +60,7 @@ extern "C" rq_status rq_paged_sparse_attention(const rq_paged_kv* kv, int32_t ro
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
   const paged_attn::Choice x = paged_attn::choose_lists(*kv, rows, heads, list);
   if (workspace_bytes < x.workspace || (x.workspace && !workspace)) return RQ_ERR_ARG;
-  paged_attn::Params p{};
+  paged_attn::MoreParams p{};
   p.kv = *kv;
   p.kv.heads = 1;
   p.kv_heads = kv->heads;

@@ -5,7 +5,7 @@ namespace rqk {
 namespace paged_attn {
 
 template <typename QT, int HD>
-static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_heads(const MoreParams& p, const Choice& x, cudaStream_t s) {
   if (p.G == 1) return launch<QT, float, HD, FmaCore<QT, HD, 1>, kLists>(p, x, s);
   if (p.G == 2) return launch<QT, float, HD, FmaCore<QT, HD, 2>, kLists>(p, x, s);
   if (p.G <= 4) return launch<QT, float, HD, FmaCore<QT, HD, 4>, kLists>(p, x, s);
@@ -13,7 +13,7 @@ static cudaError_t by_heads(const Params& p, const Choice& x, cudaStream_t s) {
 }
 
 template <typename QT>
-static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s) {
+static cudaError_t by_head_dim(const MoreParams& p, const Choice& x, cudaStream_t s) {
   switch (p.kv.head_dim) {
     case 32: return by_heads<QT, 32>(p, x, s);
     case 64: return by_heads<QT, 64>(p, x, s);
@@ -21,7 +21,7 @@ static cudaError_t by_head_dim(const Params& p, const Choice& x, cudaStream_t s)
   }
 }
 
-cudaError_t launch_lists_f32(const Params& p, const Choice& x, bool q_bf16, cudaStream_t s) {
+cudaError_t launch_lists_f32(const MoreParams& p, const Choice& x, bool q_bf16, cudaStream_t s) {
   return q_bf16 ? by_head_dim<uint16_t>(p, x, s) : by_head_dim<float>(p, x, s);
 }
 
