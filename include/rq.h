@@ -483,8 +483,8 @@ rq_status rq_paged_bounds(const rq_paged_kv *kv, void *bounds, int32_t tokens,
  *   workspace   device scratch of at least rq_paged_select_workspace_size bytes, 16-byte aligned,
  *               needing no initialisation; calls that may overlap need their own
  * rows, heads and rows * heads as rq_paged_attention; rows * kv->heads * max_blocks at most 2^40,
- * max_blocks at most 2^30 (RQ_ERR_UNSUPPORTED above).  Pages are compared by scores in f64
- * wherever f32 could order them wrongly. */
+ * max_blocks and top at most 2^30, a block's bounds below 4 GiB (RQ_ERR_UNSUPPORTED above).  Pages
+ * are compared by scores in f64 wherever f32 could order them wrongly. */
 size_t rq_paged_select_workspace_size(const rq_paged_kv *kv, int32_t rows, int32_t max_blocks);
 rq_status rq_paged_select(const rq_paged_kv *kv, const void *bounds, int32_t rows, int32_t heads,
                           int32_t batch, int32_t max_blocks, const int32_t *block_table,

@@ -14,6 +14,7 @@
 // lies between is scored again in f64 and ordered by that. With random keys this is the border page
 // itself and in one row of ten a second one.
 #include <algorithm>
+#include <climits>
 
 #include "paged.cuh"
 
@@ -619,6 +620,8 @@ rq_status check(const rq_paged_kv* kv, int32_t rows, int32_t max_blocks) {
   if (rows < 0 || max_blocks < 1) return RQ_ERR_ARG;
   if (max_blocks > 1 << 30 || kv->heads > 1 << 23 || (long long)rows * kv->heads > INT_MAX) return RQ_ERR_UNSUPPORTED;
   if ((double)rows * kv->heads * max_blocks > 1099511627776.0) return RQ_ERR_UNSUPPORTED;
+  // a block's bounds are counted in 32 bits of bytes
+  if ((long long)kv->heads * 2 * kv->head_dim * (kv->dtype == RQ_BF16 ? 2 : 4) > UINT_MAX) return RQ_ERR_UNSUPPORTED;
   return RQ_OK;
 }
 
@@ -643,7 +646,7 @@ extern "C" rq_status rq_paged_select(const rq_paged_kv* kv, const void* bounds, 
       (long long)first + last > top)
     return RQ_ERR_ARG;
   if (q_dtype != RQ_F32 && q_dtype != RQ_BF16) return RQ_ERR_ARG;
-  if (rows > 1 << 30 || heads > 1 << 23 || (long long)rows * heads > INT_MAX) return RQ_ERR_UNSUPPORTED;
+  if (rows > 1 << 30 || heads > 1 << 23 || (long long)rows * heads > INT_MAX || top > 1 << 30) return RQ_ERR_UNSUPPORTED;
   if (rows == 0) return RQ_OK;
   if (!requests && rows > batch) return RQ_ERR_ARG;
   if (!bounds || !block_table || !positions || !q || !pages || !workspace) return RQ_ERR_ARG;

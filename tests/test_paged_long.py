@@ -90,7 +90,8 @@ ROWS = [(dict(rows=-1), 1), (dict(heads=0), 1), (dict(heads=6), 1), (dict(batch=
 @pytest.mark.parametrize("kw,status", ROWS + [
     (dict(bounds=None), 1), (dict(bounds=C_ + 8), 1), (dict(pages=None), 1), (dict(ws=None), 1), (dict(top=0), 1),
     (dict(first=-1), 1), (dict(last=0), 1), (dict(last=9), 1), (dict(first=2**31 - 1, last=2**31 - 1), 1),
-    (dict(W=2**30 + 1), 6), (dict(rows=2**20, req=A, W=2**30), 6)])
+    (dict(W=2**30 + 1), 6), (dict(rows=2**20, req=A, W=2**30), 6), (dict(top=2**30 + 1), 6),
+    (dict(kv=_kv(dtype=0, heads=2**22, bs=2**33), rows=1, heads=2**22), 6)])
 def test_select_refusals(lib, kw, status):
     assert _select(lib, **kw) == status
 
