@@ -817,3 +817,51 @@ def test_past_32_bits():
     for x, xl in ((a, al), (b, bl)):
         assert (x.double() - want.double()).abs().max() <= 4 * 2.0 ** -8 * want.double().abs().max()
         assert torch.allclose(xl, lse, rtol=1e-5)
+
+
+def test_binding_refusals():
+    """Tensors of the wrong type, shape, order or size, before anything runs."""
+    k, v = (torch.zeros(6, 8, 2, 64, device="cuda") for _ in range(2))
+    q, table, pos = torch.zeros(3, 4 * 64, device="cuda"), ints([[0, 1]] * 4), ints([9, 3, 15])
+    bounds, pages = torch.zeros(6, 2, 2, 64, device="cuda"), torch.zeros(3, 2, 5, dtype=torch.int32, device="cuda")
+    slots, cu, one = ints([0, 1, 2], torch.int64), ints([0, 3]), ints([3])
+    small = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    wide = torch.zeros(6, 2, 2, 128, device="cuda")
+    for call in (
+            lambda: paged.paged_bounds(k, bounds.to(BF16), pos, slots),
+            lambda: paged.paged_bounds(k, wide[..., ::2], pos, slots),
+            lambda: paged.paged_bounds(k, bounds[:5], pos, slots),
+            lambda: paged.paged_bounds(k, bounds, pos, slots[:2]),
+            lambda: paged.paged_bounds(k, bounds, pos, pos),
+            lambda: paged.paged_select(q, wide[..., ::2], table, pos, 8, 5),
+            lambda: paged.paged_select(q, bounds[:, :, 0], table, pos, 8, 5),
+            lambda: paged.paged_select(q[:, :100], bounds, table, pos, 8, 5),
+            lambda: paged.paged_select(q, bounds, table.long(), pos, 8, 5),
+            lambda: paged.paged_select(q, bounds, table, pos[:2], 8, 5),
+            lambda: paged.paged_select(q, bounds, table, pos, 8, 5, pages=pages[:, :, :4]),
+            lambda: paged.paged_select(q, bounds, table, pos, 8, -1),
+            lambda: paged.paged_select(q, bounds, table, pos, 2**32 + 8, 5),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages[:2]),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages[:, :1]),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages.long()),
+            lambda: paged.paged_sparse_attention(q, k, v.to(BF16), table, pos, pages),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages, out=q.to(BF16)),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages, scale=1e-40),
+            lambda: paged.paged_prefix_attention(q, k, v, table, pos, one, one, one),
+            lambda: paged.paged_prefix_attention(q, k, v, table, pos, cu, cu[:0], one),
+            lambda: paged.paged_prefix_attention(q, k, v, table, pos, cu, one, one.float()),
+            lambda: paged.paged_prefix_attention(q, k, v, table, pos, cu, one, one, requests=pos.long()),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    for call in (
+            lambda: paged.paged_select(q, bounds, table, pos, 8, 0),
+            lambda: paged.paged_select(q, bounds, table, pos, 8, 5, first=4, last=2),
+            lambda: paged.paged_select(q, bounds, table, pos, 8, 5, workspace=small),
+            lambda: paged.paged_sparse_attention(q, k, v, table, pos, pages[:, :, :0].contiguous()),
+            lambda: paged.paged_sparse_attention(q, k, v, table[:2], pos, pages),
+            lambda: paged.paged_prefix_attention(q, k, v, table, pos, cu, one, one, workspace=small),
+            lambda: paged.paged_prefix_attention(q, k, v, table[:2], pos, cu, one, one),
+    ):
+        with pytest.raises(binding.RQError):
+            call()
