@@ -87,24 +87,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (of >= 0) {
       const prefix::Group x = p.t.group[of];
       if (x.tiles > 0) {
-        const int unit = x.unit_rows, i = (r - x.row0) * p.t.G + g, u = i / unit, at = i % unit;
-        const prefix::Costs c = unit == 256 ? prefix::costs_of<256>(x.queries, x.tiles)
-                                            : prefix::costs_of<128>(x.queries, x.tiles);
-        const long long first = x.list0 + h * c.head + u * c.full + prefix::kUnitCost;
-        const int w = u == c.units - 1 ? c.last_weight : unit / prefix::kRows + prefix::kTileCost;
+        const int i = (r - x.row0) * p.t.G + g, u = i / prefix::kRows, at = i % prefix::kRows;
+        const prefix::Costs c = prefix::costs_of(x.queries, x.tiles);
+        const long long first = x.list0 + h * c.head + u * c.unit + prefix::kUnitCost;
         const long long c0 = first / per;
-        count = (int)((first + (long long)(x.tiles - 1) * w) / per - c0) + 1;
-        ml_step = 2 * unit;
+        count = (int)((first + (long long)(x.tiles - 1) * prefix::kTileCost) / per - c0) + 1;
+        ml_step = 2 * prefix::kRows;
         part_step = ml_step * HD;
-        const size_t slot = (size_t)c0 * 2 * unit;
-        const size_t in_part = (size_t)(at / prefix::kRows * prefix::kRows) * HD + four * (prefix::kRows * 4) +
-                               at % prefix::kRows * 4;
+        const size_t slot = (size_t)c0 * 2 * prefix::kRows;
+        const size_t in_part = (size_t)four * (prefix::kRows * 4) + at * 4;
         if (count == 1) {
           ml = p.t.whole_ml + head;
           part = p.t.whole + head * HD + four * 4;
         } else {
-          ml = p.t.part_ml + slot + unit + at;
-          part = p.t.part + (slot + unit) * HD + in_part;
+          ml = p.t.part_ml + slot + prefix::kRows + at;
+          part = p.t.part + (slot + prefix::kRows) * HD + in_part;
         }
         ml_rest = p.t.part_ml + slot + at;
         part_rest = p.t.part + slot * HD + in_part;
@@ -151,12 +148,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 struct Layout {
   paged_attn::Choice x;
   bool tc;         // prefixes by matrix products
-  int ctas, unit;  // of the prefix kernel
+  int ctas;        // of the prefix kernel
   int bundle;      // else: rows of a group whose queries are a unit's
   size_t o, lse, part, part_ml, group, bytes;
 };
 
-Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int groups, bool q_bf16) {
+Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int groups) {
   using paged_attn::align256;
   Layout l{};
   const size_t hd = kv.head_dim;
@@ -177,9 +174,8 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   l.o = align256((size_t)rows * heads * hd * sizeof(float));
   l.lse = align256((size_t)rows * heads * sizeof(float2));
   l.ctas = std::max(sm_count(), 1);
-  l.unit = prefix::unit_queries(q_bf16);
-  l.part = align256((size_t)l.ctas * 2 * l.unit * hd * sizeof(float));
-  l.part_ml = align256((size_t)l.ctas * 2 * l.unit * sizeof(float2));
+  l.part = align256((size_t)l.ctas * 2 * prefix::kRows * hd * sizeof(float));
+  l.part_ml = align256((size_t)l.ctas * 2 * prefix::kRows * sizeof(float2));
   l.group = align256((size_t)groups * sizeof(prefix::Group)) + 256;
   l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : 0);
   return l;
@@ -203,8 +199,7 @@ extern "C" size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv* kv
                                                            int32_t groups) {
   using namespace rqk;
   if (check(kv, rows, heads, max_blocks, groups) != RQ_OK || rows < 1) return 0;
-  return std::max(layout_of(*kv, rows, heads, max_blocks, groups, true).bytes,
-                  layout_of(*kv, rows, heads, max_blocks, groups, false).bytes);
+  return layout_of(*kv, rows, heads, max_blocks, groups).bytes;
 }
 
 extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t rows, int32_t heads,
@@ -230,7 +225,7 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   if (groups > 0 && (!cu_rows || !prefix_requests || !prefix_lens)) return RQ_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return RQ_ERR_ARG;
   const bool qb = q_dtype == RQ_BF16;
-  const Layout l = layout_of(*kv, rows, heads, max_blocks, groups, qb);
+  const Layout l = layout_of(*kv, rows, heads, max_blocks, groups);
   if (workspace_bytes < l.bytes) return RQ_ERR_ARG;
   char* ws = static_cast<char*>(workspace);
   auto take = [&](size_t n) {

@@ -9,37 +9,38 @@
 // is set kSlack above the maximum met, so that P stays at most 1 and sums in range, and is a whole number, so
 // that what is scaled is scaled exactly.
 //
-// A unit is (group, K/V head, 128 or 256 queries). All units' key tiles form one list, cut into
-// equal runs, a CTA each, one CTA an SM. A unit inside one run leaves its sums in row order; of a unit
+// A unit is (group, K/V head, 128 queries). All units' tiles, of 128 keys for bf16 queries and 64 for f32
+// ones, form one list, cut into equal runs, a CTA each, one CTA an SM. A unit inside one run leaves its sums in row order; of a unit
 // that is cut each piece leaves (ref, l, O) in its CTA's scratch, and paged_prefix.cu joins them with
 // the rows' own requests.
 //
 // A CTA is 12 warps (168 registers a thread; with 13 it is 128, and spills that miss the little L1
 // beside 227 KB of shared memory):
-//   0-7       softmax. Scores come in two streams, each with its S, P and O in tensor memory: with
-//             256 queries a stream has 128 of them and both read the same keys, with up to 128 the
-//             streams take turns by tiles and are added at the end. All eight warps form one stream's P,
-//             two threads a row, while the tensor cores work for the other. (Four warps a stream came
-//             into step: both at P, then both at their products, 48 us where either alone took 26)
+//   0-7       softmax. Scores come in two streams, each with its S and P in tensor memory, that take
+//             turns by tiles. All eight warps form one stream's P, two threads a row, while the tensor
+//             cores work for the other, and add the other's O before they hand P over. (Four warps a stream
+//             came into step: both at P, then both at their products, 48 us where either alone took 26)
 //   8, 9      the loaders: K and V rows by the block table into a ring, in the swizzled layouts that
 //             the tensor cores read (K with dimensions inside, V with dimensions outside: the same
 //             rows, read transposed). Blocks of a multiple of eight positions come by TMA, a lane
 //             a box; rows of other blocks by 16-byte cp.async
 //   10, 11    issue the tensor cores' work, a stream each: S of the next tile behind O of this one,
-//             in order, so that S being there says that O is done too. (One warp for both
-//             streams: 2800 cycles a tile of 128 queries, 900 of them its waits)
+//             in order: it takes the place of the P that O is made of. (One warp for both streams:
+//             2800 cycles a tile, 900 of them its waits)
 //
-// bf16 queries enter as they are and P in two bf16 parts (16 bits); f32 queries and their P in three
-// (24 bits, every product exact), smallest first. The tensor cores cut the sum after each product of 16
-// terms, towards 0, so for f32 queries O is a tile's alone and the tiles are added in registers (in one O
-// the cuts of 20 tiles were 2.6e-6 of the result, now it is within 3.3e-7). Parts are cut, not rounded to
-// nearest: all are of the value's sign, so an infinite key or value is met by no zero part. P lies in
-// tensor memory, in the columns of the S it was made of.
+// bf16 queries enter as they are, f32 queries and all P in three bf16 parts (24 bits, every product exact),
+// smallest first. The tensor cores cut the sum after each product of 16 terms, towards 0: a bias that
+// grows with the sum's length, so O is a tile's alone and the tiles are added in registers, rounded to
+// nearest (in one O the cuts of 20 tiles were 2.6e-6 of the result, now it is within 3.3e-7 whatever the
+// length). The first two parts are cut, not rounded to nearest, so that all three are of the value's sign
+// and an infinite key or value is met by no zero part. P lies in tensor memory, in the columns of the S it
+// was made of.
 //
-// What bounds it: a tile of 128 queries and 128 keys is 24 products of 64 to 100 cycles (two parts of P: half of
-// them), 0.86 us, and as long in the softmax (its 1024 exponentials and 5600 other instructions an SM quarter);
-// together 1.15 us. 64 rows of 32 heads behind 32768 positions: 33 us of tiles a CTA, 10 before the first
-// scores and 3 behind the last ones.
+// What bounds it: a tile of 128 queries and 128 keys is 32 products of 64 cycles (24 of them P's three parts),
+// 1.1 us, beside the softmax, some 3000 cycles or 1.5 us: 410 for scores and maxima, 130 for the exchange of
+// these, 1850 for exponentials (1024 of the unit that makes them) and parts, 420 for sums, the rest waits. A
+// loader is busy for 2600 of them with blocks of 16 positions. One O for all tiles of a piece, two parts of P and
+// 256 queries a unit took 1.15 us a tile; its outputs were off by 1e-4 behind 50000 positions.
 #pragma once
 
 #include <type_traits>
@@ -59,17 +60,17 @@ using paged_attn::neg_inf;
 using paged_attn::pack_bf16;
 
 constexpr int kThreads = 384, kLoaders = 64;
-constexpr int kRows = 128;       // queries of a stream
-// What a tile of a stream's 128 queries, of two streams' 256, and a unit's start and end count in the list: 1.6,
-// 2.5 and 7 us (250 rows of five groups, 78 GFLOP: 92 us for most CTAs, 122 for those of short units when a
-// tile counted by its queries alone)
-constexpr int kTileCost = 1, kUnitCost = 9;
+constexpr int kRows = 128;       // queries of a unit
+// What a tile, and a unit's start and end count in the list: 1.6 and 7 us
+constexpr int kTileCost = 2, kUnitCost = 9;
 constexpr float kSlack = 8.f;
 constexpr int kMasks = 8;        // tiles whose masks are kept
+// columns of tensor memory: the two streams' scores, and P's first two parts, at 0 and 128; O; P's third parts
+constexpr int kSumsAt = 256, kThirdAt = 384;
 
 struct alignas(16) Group {  // what the joining kernel needs of a group
   long long list0;          // its first entry of the list
-  int row0, queries, tiles, unit_rows;
+  int row0, queries, tiles;
 };
 
 struct Params {
@@ -81,8 +82,8 @@ struct Params {
   uint32_t flip;    // 1: the scale is negative, queries enter negated
   float* whole;     // [rows][heads][HD] sums of units of one run
   float2* whole_ml; // [rows][heads] (ref, l)
-  float* part;      // [ctas][2][unit queries / 128][HD / 4][128][4]
-  float2* part_ml;  // [ctas][2][unit queries]
+  float* part;      // [ctas][2][HD / 4][kRows][4]
+  float2* part_ml;  // [ctas][2][kRows]
   Group* group;     // [groups]
   long long* per;   // entries of a run
   int box;          // rows of a TMA box, 0: copies by threads
@@ -92,15 +93,13 @@ struct Params {
 template <typename QT, int HD>
 struct Shape {
   static constexpr bool kF32 = sizeof(QT) == 4;
-  static constexpr int kQParts = kF32 ? 3 : 1, kPParts = kF32 ? 3 : 2;
+  static constexpr int kQParts = kF32 ? 3 : 1, kPParts = 3;
   static constexpr int KT = kF32 ? 64 : 128;           // keys of a tile
-  static constexpr int kTiles = kF32 ? 1 : 2;          // query tiles of a unit
-  static constexpr int kUnit = kTiles * kRows;
   static constexpr int kHalf = KT * HD * 2;            // bytes of a tile's keys, or values
-  static constexpr int kQ = kQParts * kRows * HD * 2;  // of a query tile
-  static constexpr int kRoom = (224 * 1024 - kTiles * kQ) / kHalf;
+  static constexpr int kQ = kQParts * kRows * HD * 2;  // of the queries
+  static constexpr int kRoom = (224 * 1024 - kQ) / kHalf;
   static constexpr int NH = kRoom < 8 ? kRoom : 8;     // halves of the ring
-  static constexpr int kRing = kTiles * kQ + NH * kHalf;
+  static constexpr int kRing = kQ + NH * kHalf;
   // a row's bytes in shared memory: 64 dimensions, or all 32
   static constexpr int kPitch = HD < 64 ? 64 : 128;
   static_assert(NH >= 5, "two tiles and the next one's keys");
@@ -237,26 +236,19 @@ __device__ __noinline__ View view_of(const Params& p, int g) {
   return v;
 }
 
-// a group's units of one K/V head: the full ones' cost, the last one's, their number
+// what a group's units of a K/V head count in the list
 struct Costs {
-  long long full, last, head;
-  int units, last_weight;
+  long long unit, head;
 };
 
-template <int UNIT>
 __host__ __device__ __forceinline__ Costs costs_of(int queries, int tiles) {
-  Costs c{};
-  if (tiles == 0) return c;
-  c.units = (queries - 1) / UNIT + 1;
-  c.last_weight = (queries - (c.units - 1) * UNIT - 1) / kRows + 1 + kTileCost;
-  c.full = (long long)tiles * (UNIT / kRows + kTileCost) + kUnitCost;
-  c.last = (long long)tiles * c.last_weight + kUnitCost;
-  c.head = (c.units - 1) * c.full + c.last;
-  return c;
+  if (tiles == 0) return Costs{0, 0};
+  const long long unit = (long long)tiles * kTileCost + kUnitCost;
+  return Costs{unit, ((queries - 1) / kRows + 1) * unit};
 }
 
 struct Small {  // behind the tiles
-  uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], done, o_free, drain;
+  uint64_t full[8], empty[8], q_full, s_full[2], p_full[2], o_full, drain;
   uint32_t mask[kMasks][4];
   float row[2][2][kRows];  // of halves of a row, for its other half: [stream][half], maxima, then sums
   long long scan[kThreads / 32], start0;
@@ -273,11 +265,11 @@ static_assert(smem_bytes<uint16_t, 128> <= 227 * 1024 && smem_bytes<float, 128> 
 struct Piece {
   View v;
   int h, unit, t, n;  // K/V head, unit of it, tiles [t, t + n)
-  bool pair, first, last;
+  bool first, last;
 };
 
 // a CTA's walk over its run, the same in every thread
-template <int KT, int UNIT>
+template <int KT>
 struct Cursor {
   long long at, stop, list0;
   int g, of;  // the group, and that of `v`
@@ -293,7 +285,7 @@ struct Cursor {
 #pragma unroll 1
     for (int i = g0; i < g1; ++i) {
       seen = view_of<KT>(p, i);
-      own += costs_of<UNIT>(seen.queries, seen.tiles).head * p.kv.heads;
+      own += costs_of(seen.queries, seen.tiles).head * p.kv.heads;
     }
     long long inc = own;
 #pragma unroll 1
@@ -309,7 +301,7 @@ struct Cursor {
       if (w < warp) inc += s.scan[w];
       total += s.scan[w];
     }
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + 2 + kTileCost));
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)(kUnitCost + kTileCost));
     at = blockIdx.x * per;
     stop = min(at + per, total);
     long long first = inc - own;
@@ -318,8 +310,8 @@ struct Cursor {
 #pragma unroll 1
       for (int i = g0; i < g1; ++i) {
         const View v = slice == 1 ? seen : view_of<KT>(p, i);
-        const long long c = costs_of<UNIT>(v.queries, v.tiles).head * p.kv.heads;
-        if (blockIdx.x == 0) p.group[i] = Group{first, v.row0, v.queries, v.tiles, UNIT};
+        const long long c = costs_of(v.queries, v.tiles).head * p.kv.heads;
+        if (blockIdx.x == 0) p.group[i] = Group{first, v.row0, v.queries, v.tiles};
         if (first <= at && at < first + c) s.start_group = i, s.start0 = first, s.start_view = v;
         first += c;
       }
@@ -334,7 +326,7 @@ struct Cursor {
     while (at < stop && g < p.groups) {
       if (of != g) v = view_of<KT>(p, of = g);
       x.v = v;
-      const Costs c = costs_of<UNIT>(x.v.queries, x.v.tiles);
+      const Costs c = costs_of(x.v.queries, x.v.tiles);
       const long long cost = c.head * p.kv.heads;
       if (at >= list0 + cost) {
         list0 += cost;
@@ -344,18 +336,15 @@ struct Cursor {
       long long in = at - list0;
       x.h = (int)(in / c.head);
       in -= x.h * c.head;
-      x.unit = (int)min(in / c.full, (long long)c.units - 1);
-      in -= x.unit * c.full;
-      const bool tail = x.unit == c.units - 1;
-      const int w = tail ? c.last_weight : UNIT / kRows + kTileCost;
+      x.unit = (int)(in / c.unit);
+      in -= x.unit * c.unit;
       const long long begin = at - in;  // the unit's first entry
-      x.t = in <= kUnitCost ? 0 : (int)((in - kUnitCost + w - 1) / w);
-      at = begin + (tail ? c.last : c.full);
+      x.t = in <= kUnitCost ? 0 : (int)((in - kUnitCost + kTileCost - 1) / kTileCost);
+      at = begin + c.unit;
       if (x.t >= x.v.tiles) continue;
-      const long long room = stop - begin - kUnitCost - (long long)x.t * w;
+      const long long room = stop - begin - kUnitCost - (long long)x.t * kTileCost;
       if (room <= 0) return false;  // its first tile is the next run's
-      x.n = (int)min((room + w - 1) / w, (long long)(x.v.tiles - x.t));
-      x.pair = w == 2 + kTileCost;
+      x.n = (int)min((room + kTileCost - 1) / kTileCost, (long long)(x.v.tiles - x.t));
       x.first = x.t == 0;
       x.last = x.t + x.n == x.v.tiles;
       return true;
@@ -372,27 +361,6 @@ static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, vo
   return false;
 }
 
-// n columns of O times f. Seldom.
-static __device__ __noinline__ void scale_sums(uint32_t at, int n, float f) {
-#pragma unroll 1
-  for (int i = 0; i < n; i += 16) {
-    float v[16];
-    uint32_t r[16];
-    tc::tmem_ld16(at + i, v);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e] * f);
-    tmem_st16(at + i, r);
-  }
-  tmem_wait_st();
-}
-
-template <typename T>
-__device__ __forceinline__ void swap(T& a, T& b) {
-  const T c = a;
-  a = b;
-  b = c;
-}
-
 // A unit's queries into shared memory by the 256 softmax threads, negated where the scale is negative (the
 // scores then have its size alone); rows that are not there are 0. bf16 ones are copied, all copies in
 // flight at once, and are there once the caller has waited for them; f32 ones are cut into parts.
@@ -400,9 +368,9 @@ template <typename QT, int HD>
 __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8_t* smem, int tid) {
   using S = Shape<QT, HD>;
   constexpr int CH = HD / 8, STEP = 2 * kRows / CH, kAhead = 4;
-  const int c = tid % CH, rows = x.pair ? 2 * kRows : kRows, last = x.v.queries - 1 - x.unit * S::kUnit;
+  const int c = tid % CH, last = x.v.queries - 1 - x.unit * kRows;
   // the query's row and head of the group, step by step
-  const int first = x.unit * S::kUnit + tid / CH, rows_step = STEP / p.G, heads_step = STEP % p.G;
+  const int first = x.unit * kRows + tid / CH, rows_step = STEP / p.G, heads_step = STEP % p.G;
   int row = first / p.G, head = first % p.G;
   const QT* base = static_cast<const QT*>(p.q) + ((size_t)x.v.row0 * p.heads + (size_t)x.h * p.G) * HD + c * 8;
   auto next = [&] {
@@ -414,16 +382,15 @@ __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8
   };
   if constexpr (!S::kF32) {
 #pragma unroll 2
-    for (int r = tid / CH; r < rows; r += STEP) {
+    for (int r = tid / CH; r < kRows; r += STEP) {
       const QT* q = next();
-      cp_async16(smem_u32(smem) + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, c), r <= last ? q : base,
-                 r <= last);
+      cp_async16(smem_u32(smem) + S::template at<kRows>(r, c), r <= last ? q : base, r <= last);
     }
     cp_async_commit();
   } else {
     const uint32_t flip = p.flip ? 0x80008000u : 0u;
 #pragma unroll 1
-    for (int r0 = tid / CH; r0 < rows; r0 += STEP * kAhead) {
+    for (int r0 = tid / CH; r0 < kRows; r0 += STEP * kAhead) {
       uint4 v[kAhead][2];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
@@ -435,7 +402,7 @@ __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int r = r0 + k * STEP;
-        if (r >= rows) break;
+        if (r >= kRows) break;
         uint8_t* to = smem + S::template at<kRows>(r, c);
         const uint32_t f[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
         uint32_t o[3][4];
@@ -458,14 +425,14 @@ __device__ __noinline__ void load_queries(const Params& p, const Piece& x, uint8
 
 // ... and once they are there
 template <typename QT, int HD>
-__device__ __noinline__ void queries_loaded(const Params& p, const Piece& x, uint8_t* smem, int tid) {
+__device__ __noinline__ void queries_loaded(const Params& p, uint8_t* smem, int tid) {
   using S = Shape<QT, HD>;
   if constexpr (!S::kF32) {
     cp_async_wait<0>();
     if (p.flip) {
       constexpr int CH = HD / 8;
-      for (int r = tid / CH; r < (x.pair ? 2 * kRows : kRows); r += 2 * kRows / CH) {
-        uint4* v = reinterpret_cast<uint4*>(smem + (r / kRows) * S::kQ + S::template at<kRows>(r % kRows, tid % CH));
+      for (int r = tid / CH; r < kRows; r += 2 * kRows / CH) {
+        uint4* v = reinterpret_cast<uint4*>(smem + S::template at<kRows>(r, tid % CH));
         v->x ^= 0x80008000u, v->y ^= 0x80008000u, v->z ^= 0x80008000u, v->w ^= 0x80008000u;
       }
     }
@@ -477,14 +444,14 @@ __device__ __noinline__ void queries_loaded(const Params& p, const Piece& x, uin
 template <typename QT, int HD, bool BOX>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Params p) {
   using S = Shape<QT, HD>;
-  constexpr int KT = S::KT, NH = S::NH, UNIT = S::kUnit;
+  constexpr int KT = S::KT, NH = S::NH;
   extern __shared__ __align__(1024) uint8_t smem[];
   Small& s = *reinterpret_cast<Small*>(smem + S::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
 
-  Cursor<KT, UNIT> cur;
+  Cursor<KT> cur;
   if (!cur.start(p, s)) return;
   if (tid == 0) {
     for (int i = 0; i < NH; ++i) {
@@ -496,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       mbar_init(&s.s_full[i], 2);
       mbar_init(&s.p_full[i], 2 * kRows);
     }
-    mbar_init(&s.done, 2);
-    mbar_init(&s.o_free, 2 * kRows);
+    mbar_init(&s.o_full, 1);
     mbar_init(&s.drain, 2);
     fence_barrier_init();
     s.abort = (smem_u32(smem) & 1023u) != 0;  // the swizzles go by the address
@@ -520,36 +486,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
   if ((warp == 8 || warp == 9) && BOX) {
     // ------------------------------------------------------------ loaders: TMA, one the keys, one the values
-    // Lane i has box i of a half (a copy takes some 60 cycles of its warp, 16 of them are a tile's keys of
+    // Lane i has box i of a half (a copy takes some 110 cycles of its warp, 16 of them are a tile's keys of
     // blocks of 16 positions): rows [g BR, g BR + BR) of the tile, 64 dimensions (or all 32). A box is
     // of one page; where that has no block it is read past the last one and filled with zeros. What
     // lies in a box behind the prefix's end must not be read, so that box's rows are copied by the warp.
     constexpr int kSubs = HD < 64 ? 1 : HD / 64;
-    const int BR = p.box, nb = KT / BR, g = lane % nb, sub = lane / nb, P = p.kv.block_size;
-    const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
+    const int BR = p.box, box_log = __ffs(BR) - 1, nb = KT >> box_log, g = lane & (nb - 1), sub = lane / nb;
+    const int P = p.kv.block_size, step_pages = KT / P % p.W, step_rows = KT % P;
+    const uint32_t ring = smem_u32(smem) + S::kQ;
     const int side = warp - 8;
     const CUtensorMap* const map = side == 0 ? &p.kmap : &p.vmap;
     int tile = 0;
     bool ok = true;
     if (lane == 0) tc::prefetch_tmap(map);
     while (ok && cur.next(p, x)) {
-      auto id_of = [&](int t) {
-        const int key = (x.v.t0 + x.t + t) * KT + g * BR, page = key / P;
-        if (t >= x.n || key < x.v.lo || key >= x.v.end) return -1;
-        return p.table[(size_t)x.v.b * p.W + (page < p.W ? page : page % p.W)];
-      };
+      // the lane's box's first key, column of the table and row of the block, a tile ahead. Divided once a piece:
+      // with divisions every tile a loader, which has 16 copies of 110 cycles to make for one, took 3200 cycles
+      const int32_t* const table = p.table + (size_t)x.v.b * p.W;
+      int ahead = (x.v.t0 + x.t) * KT + g * BR, column = ahead / P % p.W, in_block = ahead % P;
+      auto id_of = [&](int t) { return t >= x.n || ahead < x.v.lo || ahead >= x.v.end ? -1 : table[column]; };
       int next = id_of(0);
       for (int t = 0; ok && t < x.n; ++t, ++tile) {
-        const int key0 = (x.v.t0 + x.t + t) * KT, key = key0 + g * BR, id = next;
+        const int key0 = (x.v.t0 + x.t + t) * KT, key = key0 + g * BR, id = next, at_row = in_block;
+        ahead += KT;
+        in_block += step_rows;
+        column += step_pages;
+        if (in_block >= P) in_block -= P, ++column;
+        if (column >= p.W) column -= p.W;
         next = id_of(t + 1);
         const bool live = id >= 0 && id < p.kv.n_blocks;
         const uint32_t boxes = __ballot_sync(0xffffffffu, live) & (nb < 32 ? (1u << nb) - 1u : ~0u);
         const uint32_t torn = __ballot_sync(0xffffffffu, live && x.v.end - key < BR) & boxes;
         if (side == 0 && lane < KT / 32) {
-          uint32_t m = 0;
+          uint32_t m = BR >= 32 && ((boxes >> (lane * 32 >> box_log)) & 1u) ? ~0u : 0u;
 #pragma unroll 1
-          for (int r = 0; r < 32; r += min(BR, 32))
-            if ((boxes >> ((lane * 32 + r) / BR)) & 1u) m |= BR >= 32 ? ~0u : ((1u << BR) - 1u) << r;
+          for (int r = 0; BR < 32 && r < 32; r += BR)
+            if ((boxes >> ((lane * 32 + r) >> box_log)) & 1u) m |= ((1u << BR) - 1u) << r;
           const int left = x.v.end - key0 - lane * 32;  // keys of the word
           s.mask[tile % kMasks][lane] = left >= 32 ? m : left <= 0 ? 0u : m & ((1u << left) - 1u);
         }
@@ -565,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             const int r = i / (HD / 8), c = i % (HD / 8);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < rows) v = *reinterpret_cast<const uint4*>(from + r * p.kv.row_stride + c * 8);
-            *reinterpret_cast<uint4*>(smem + S::kTiles * S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
+            *reinterpret_cast<uint4*>(smem + S::kQ + slot * S::kHalf + S::template at<KT>(b * BR + r, c)) = v;
           }
           fence_proxy_async();
         }
@@ -573,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], (uint32_t)((nb - (torn ? 1 : 0)) * BR * HD * 2));
         __syncwarp();
         if (sub < kSubs && !((torn >> g) & 1u))
-          tma_load_4d(ring + slot * S::kHalf + sub * (KT * 128) + g * BR * S::kPitch, map, sub * 64, live ? key % P : 0,
+          tma_load_4d(ring + slot * S::kHalf + sub * (KT * 128) + g * BR * S::kPitch, map, sub * 64, live ? at_row : 0,
                       x.h, live ? id : p.kv.n_blocks, &s.full[slot]);
       }
     }
@@ -590,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     constexpr int CH = HD / 8;          // 16-byte pieces of a row
     constexpr int RPI = 32 / CH;        // rows of a warp's copy instruction
     const int w = warp - 8, P = p.kv.block_size;
-    const uint32_t ring = smem_u32(smem) + S::kTiles * S::kQ;
+    const uint32_t ring = smem_u32(smem) + S::kQ;
     int half = 0, tile = 0;
     bool ok = true;
     while (ok && cur.next(p, x)) {
@@ -644,19 +616,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     // The whole warp walks along, so that addresses stay in uniform registers; one lane issues. Loops
     // that stay loops: unrolled, the instructions came late, once each in 3000 cycles.
     const int st = warp - 10;
-    const uint32_t qs = smem_u32(smem), ring = qs + S::kTiles * S::kQ, ts = tmem + st * 256;
+    const uint32_t qs = smem_u32(smem), ring = qs + S::kQ, ts = tmem + st * 128, to = tmem + kSumsAt;
     const uint32_t is = tc::idesc_bf16_f32(kRows, KT);
     const uint32_t io = tc::idesc_bf16_f32(kRows, HD) | 1u << 16;  // B: dimensions outside
     constexpr int kSub = HD < 64 ? 2 : 4;  // steps of 16 dimensions of a row in shared memory
-    int base = 0, piece = 0, made = 0;
+    int base = 0, made = 0, piece = 0;
     bool ok = true;
     auto behind = [&] {
       if (!BOX) fence_proxy_async();
       tc::fence_after_sync();
     };
     while (ok && cur.next(p, x)) {
-      // this stream's tiles t = first, first + step, ..
-      const int first = x.pair ? 0 : st, step = x.pair ? 1 : 2;
       // Each half is passed by both streams, also where only one reads it, in its turn: a barrier's parity
       // tells two uses of a slot apart, and a stream that went on to the next use while the other's half
       // were still on its way would take that one's phase for its own.
@@ -671,39 +641,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       };
       ok = wait_warp(&s.q_full, piece);
 #pragma unroll 1
-      for (int t = first - step; ok && t < x.n; t += step) {
-        if (t >= first) {  // O of tile t
+      for (int t = st - 2; ok && t < x.n; t += 2) {
+        if (t >= 0) {  // O of tile t
           const int half = base + 2 * t + 1;
-          if (t == first && piece > 0 && !(ok = wait_warp(&s.o_free, piece - 1))) break;
-          if (!x.pair && t > 0 && !(ok = pass(t - 1))) break;
+          if (t > 0 && !(ok = pass(t - 1))) break;
           if (!(ok = wait_warp(&s.full[half % NH], half / NH) && wait_warp(&s.p_full[st], made))) break;
           ++made;
           behind();
           if (elect_one()) {
-            uint32_t acc = !S::kF32 && t > first;
+            uint32_t acc = 0;
 #pragma unroll 1
             for (int part = S::kPParts - 1; part >= 0; --part) {
               uint64_t v = desc<S::kPitch>(ring + (half % NH) * S::kHalf, KT * 128);
-              uint32_t at = ts + (part < 2 ? 16 * part : KT);
+              uint32_t at = part < 2 ? ts + 16 * part : tmem + kThirdAt + st * 64;
 #pragma unroll 1
               for (int i = 0; i < KT / 32; ++i) {
-                mma_from_tmem(ts + 128, at, v, io, acc);
-                mma_from_tmem(ts + 128, at + 8, v + ((16 * S::kPitch) >> 4), io, 1);
+                mma_from_tmem(to, at, v, io, acc);
+                mma_from_tmem(to, at + 8, v + ((16 * S::kPitch) >> 4), io, 1);
                 v += (32 * S::kPitch) >> 4;
                 at += part < 2 ? 32 : 16;
                 acc = 1;
               }
             }
             tc::commit(&s.empty[half % NH]);
+            tc::commit(&s.o_full);
           }
           __syncwarp();
         }
-        if (t + step < x.n) {  // S of the next one
-          const int half = base + 2 * (t + step);
+        if (t + 2 < x.n) {  // S of this stream's next one
+          const int half = base + 2 * (t + 2);
           if (!(ok = wait_warp(&s.full[half % NH], half / NH))) break;
           behind();
           if (elect_one()) {
-            uint64_t q = desc<S::kPitch>(qs + (x.pair ? st : 0) * S::kQ + (S::kQParts - 1) * (kRows * HD * 2), 16);
+            uint64_t q = desc<S::kPitch>(qs + (S::kQParts - 1) * (kRows * HD * 2), 16);
 #pragma unroll 1
             for (int part = S::kQParts - 1; part >= 0; --part) {
               const uint64_t k = desc<S::kPitch>(ring + (half % NH) * S::kHalf, 16);
@@ -722,9 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           __syncwarp();
         }
       }
-      if (ok && !x.pair && ((x.n - 1) & 1) != st) ok = pass(x.n - 1);
-      if (ok && elect_one()) tc::commit(&s.done);
-      __syncwarp();
+      if (ok && ((x.n - 1) & 1) != st) ok = pass(x.n - 1);
       base += 2 * x.n;
       ++piece;
     }
@@ -735,64 +703,72 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax
     // Warps w and w + 4 share rows (and tensor memory lanes): each has half of a tile's keys, and of O's
-    // dimensions where those are scaled or written.
+    // dimensions.
     constexpr int C = KT / 64;  // 32 keys at a time
     const int side = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), to = lanes + kSumsAt + side * (HD / 2);
     const f32x2 scale2 = pack2(p.scale, p.scale);
-    uint32_t seen[2] = {0, 0};  // tiles of this stream (the next job's), of the other one
-    int tile = 0, piece = 0;
+    uint32_t seen[2] = {0, 0};  // tiles of a stream
+    int tile = 0;
     bool ok = true;
     Piece y;
     bool more = cur.next(p, y);
     auto queries = [&] {
       load_queries<QT, HD>(p, y, smem, tid);
-      queries_loaded<QT, HD>(p, y, smem, tid);
+      queries_loaded<QT, HD>(p, smem, tid);
       mbar_arrive(&s.q_full);
     };
     if (more) queries();
     while (more) {
       x = y;
-      const int jobs = x.pair ? 2 * x.n : x.n;
-      float ref[2] = {neg_inf(), neg_inf()}, l[2] = {0.f, 0.f};  // as seen
-      // f32 queries: sums of the tiles so far, by the two streams together
-      constexpr int D = S::kF32 ? HD / 2 : 16;
-      float o[D] = {};
-      auto add_tile = [&](int st, float f) {
+      float ref = neg_inf(), l = 0.f;
+      constexpr int D = HD / 2;
+      float o[D] = {};  // sums of the tiles so far
+      uint32_t r[32];
+      // the sums of the tile before, times f
+      auto add_tile = [&](float f) {
+        if (ok) ok = wait_warp(&s.o_full, tile - 1);
+        tc::fence_after_sync();
+        if constexpr (D >= 32) {
 #pragma unroll
-        for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D; c += 32) {
+            tmem_ld32(to + c, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[c + e] = fmaf(__uint_as_float(r[e]), f, o[c + e]);
+          }
+        } else {
           float v[16];
-          tc::tmem_ld16(lanes + st * 256 + 128 + side * (HD / 2) + c, v);
+          tc::tmem_ld16(to, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[c + e] = fmaf(v[e], f, o[c + e]);
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(v[e], f, o[e]);
         }
       };
 #pragma unroll 1
-      for (int j = 0; j < jobs; ++j) {
+      for (int j = 0; j < x.n; ++j, ++tile) {
         const int st = j & 1;
-        const uint32_t ts = lanes + st * 256;
+        const uint32_t ts = lanes + st * 128;
         // (a partner warp whose wait ran out is still met at the barrier below)
-        if (ok) ok = wait_warp(&s.s_full[st], seen[0]);
-        ++seen[0];
+        if (ok) ok = wait_warp(&s.s_full[st], st ? seen[1]++ : seen[0]++);
         tc::fence_after_sync();
-        uint32_t r[C][32];
+        auto scores = [&](int c) {
+          tmem_ld32(ts + (side * C + c) * 32, r);
+          tmem_wait_ld(r);
+          const uint32_t m = s.mask[tile % kMasks][side * C + c];
+          if (m == 0xffffffffu) return;
 #pragma unroll
-        for (int c = 0; c < C; ++c) tmem_ld32(ts + (side * C + c) * 32, r[c]);
+          for (int i = 0; i < 32; ++i)
+            if (!((m >> i) & 1u)) r[i] = 0xff800000u;
+        };
         float mx = neg_inf();
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          tmem_wait_ld(r[c]);
-          const uint32_t m = s.mask[(tile + (x.pair ? j >> 1 : j)) % kMasks][side * C + c];
-          if (m != 0xffffffffu) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((m >> i) & 1u)) r[c][i] = 0xff800000u;
-          }
+          scores(c);
           float m0 = neg_inf(), m1 = neg_inf();
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            m0 = fmaxf(fmaxf(m0, __uint_as_float(r[c][i])), __uint_as_float(r[c][i + 1]));
-            m1 = fmaxf(fmaxf(m1, __uint_as_float(r[c][i + 2])), __uint_as_float(r[c][i + 3]));
+            m0 = fmaxf(fmaxf(m0, __uint_as_float(r[i])), __uint_as_float(r[i + 1]));
+            m1 = fmaxf(fmaxf(m1, __uint_as_float(r[i + 2])), __uint_as_float(r[i + 3]));
           }
           mx = fmaxf(mx, fmaxf(m0, m1));
         }
@@ -800,133 +776,66 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         bar_sync(1 + (warp & 3), 64);
         mx = fmaxf(mx, s.row[st][side ^ 1][row]);
         mx = mx == neg_inf() ? mx : mx * p.scale;
-        // f32 queries have the bound of the tile before, the other stream's, and this stream's tile before is
-        // done (these scores came behind it) and still apart
-        const float mine = ref[0];
-        if (S::kF32) ref[0] = ref[1];
-        if (__any_sync(0xffffffffu, mx > ref[0])) {
-          const float was = ref[0];
-          if (mx > was) ref[0] = ceilf(mx) + kSlack;  // whole: sums are scaled exactly
-          const float f = ref[0] > was ? ex2(was - ref[0]) : 1.f;
-          if constexpr (S::kF32) {
-            l[0] *= f;
-            l[1] *= f;
+        float f = 1.f;
+        if (__any_sync(0xffffffffu, mx > ref)) {
+          const float was = ref;
+          if (mx > was) ref = ceilf(mx) + kSlack;  // whole: sums are scaled exactly
+          if (ref > was) f = ex2(was - ref);
+          l *= f;
 #pragma unroll
-            for (int e = 0; e < D; ++e) o[e] *= f;
-          } else {
-            l[0] *= f;
-            // the sums so far are of tiles whose products are done (these scores came behind them)
-            if (j > 1) scale_sums(ts + 128 + side * (HD / 2), HD / 2, f);
-          }
+          for (int e = 0; e < D; ++e) o[e] *= f;
         }
-        if (S::kF32 && j > 1) add_tile(st, mine == neg_inf() ? 0.f : ex2(mine - ref[0]));
-        const f32x2 sub2 = pack2(-finite_or_zero(ref[0]), -finite_or_zero(ref[0]));
+        const f32x2 sub2 = pack2(-finite_or_zero(ref), -finite_or_zero(ref));
         f32x2 sum2 = pack2(0.f, 0.f);
-        // P, its parts over the scores (a third one behind them)
+        // P, two parts over the scores, the third one behind them; the scores read last are still there
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          uint32_t w[32], w3[S::kF32 ? 16 : 1];
+        for (int c = C - 1; c >= 0; --c) {
+          if (c < C - 1) scores(c);
+          uint32_t w[32], w3[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float2 y = unpack2(fma2(pack2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), scale2, sub2));
+            float2 y = unpack2(fma2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale2, sub2));
             f32x2 p2 = pack2(ex2(y.x), ex2(y.y));
             sum2 = add2(sum2, p2);
             w[i] = cut_part(p2);
-            if constexpr (S::kF32) w[16 + i] = cut_part(p2);
+            w[16 + i] = cut_part(p2);
             y = unpack2(p2);
-            (S::kF32 ? w3[i] : w[16 + i]) = pack_bf16(y.x, y.y);
+            w3[i] = pack_bf16(y.x, y.y);
           }
           tmem_st32(ts + (side * C + c) * 32, w);
-          if constexpr (S::kF32) tmem_st16(ts + KT + (side * C + c) * 16, w3);
+          tmem_st16(lanes + kThirdAt + st * 64 + (side * C + c) * 16, w3);
         }
+        const float2 sum = unpack2(sum2);
+        l += sum.x + sum.y;
+        // the products of this tile go where those of the one before are
+        if (j > 0) add_tile(f);
         tmem_wait_st();
         tc::fence_before_sync();
         mbar_arrive(&s.p_full[st]);
-        const float2 sum = unpack2(sum2);
-        l[0] += sum.x + sum.y;
-        swap(seen[0], seen[1]);
-        swap(ref[0], ref[1]);
-        swap(l[0], l[1]);
       }
-      if (jobs & 1) {
-        swap(seen[0], seen[1]);
-        swap(ref[0], ref[1]);
-        swap(l[0], l[1]);
-      }
-      tile += x.n;
       // ---- the piece's sums
       bar_sync(1 + (warp & 3), 64);  // the last maxima have been read
-      s.row[0][side][row] = l[0];
-      s.row[1][side][row] = l[1];
+      s.row[0][side][row] = l;
       bar_sync(1 + (warp & 3), 64);
-      l[0] += s.row[0][side ^ 1][row];
-      l[1] += s.row[1][side ^ 1][row];
+      l += s.row[0][side ^ 1][row];
       more = cur.next(p, y);
-      if (ok) ok = wait_warp(&s.done, piece);
-      tc::fence_after_sync();
+      add_tile(1.f);
       // the unit's products are done: the next one's first scores are made while its sums are written
       if (more) queries();
-      if (!ok) ref[0] = ref[1] = 0.f, l[0] = l[1] = __int_as_float(0x7fc00000);
+      if (!ok) ref = 0.f, l = __int_as_float(0x7fc00000);
       const bool cut = !(x.first && x.last);
       const size_t slot = (size_t)blockIdx.x * 2 + (x.first ? 1 : 0);
-      float f[2] = {1.f, 0.f};
-      if (!x.pair) {  // both streams have the same queries
-        const float m = fmaxf(ref[0], ref[1]), sub = finite_or_zero(m);
-        f[0] = ex2(ref[0] - sub);
-        f[1] = ex2(ref[1] - sub);
-        ref[0] = m;
-        // (f32 queries' sums are all relative to the last tile's bound, m)
-        l[0] = S::kF32 ? l[0] + l[1] : l[0] * f[0] + l[1] * f[1];
-        if (S::kF32 && ok) {
-          add_tile(0, f[0]);
-          if (x.n > 1) add_tile(1, f[1]);
-        }
-      }
-#pragma unroll 1
-      for (int st = 0; st < (x.pair ? 2 : 1); ++st) {
-        const int in = st * kRows + row, i = x.unit * UNIT + in;  // of the unit, of the group
+      const int i = x.unit * kRows + row;  // of the group
+      if (i < x.v.queries) {
         const size_t head = (size_t)(x.v.row0 + i / p.G) * p.heads + (size_t)x.h * p.G + i % p.G;
-        const bool live = i < x.v.queries;
-        float* out = cut ? p.part + (slot * UNIT + st * kRows) * HD + row * 4 : p.whole + head * HD;
+        float* out = cut ? p.part + slot * kRows * HD + row * 4 : p.whole + head * HD;
         const size_t step = cut ? kRows * 4 : 4;  // floats from four dimensions to the next four
-        if (live && side == 0) {
-          if (cut) p.part_ml[slot * UNIT + in] = make_float2(ref[0], l[0]);
-          else p.whole_ml[head] = make_float2(ref[0], l[0]);
-        }
-        if (ok) {
-#pragma unroll 1
-          for (int c = side * (HD / 2); c < (side + 1) * (HD / 2); c += 16) {
-            float v[16];
-            if constexpr (S::kF32) break;
-            tc::tmem_ld16(lanes + st * 256 + 128 + c, v);
+        if (side == 0) *(cut ? p.part_ml + slot * kRows + row : p.whole_ml + head) = make_float2(ref, l);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= f[0];
-            if (!x.pair && x.n > 1) {
-              float v1[16];
-              tc::tmem_ld16(lanes + 256 + 128 + c, v1);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = fmaf(v1[e], f[1], v[e]);
-            }
-            if (live) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<float4*>(out + (c / 4 + e) * step) =
-                    make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            }
-          }
-          if (S::kF32 && live) {
-#pragma unroll
-            for (int e = 0; e < D / 4; ++e)
-              *reinterpret_cast<float4*>(out + (side * (HD / 8) + e) * step) =
-                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-        }
-        ref[0] = ref[1];
-        l[0] = l[1];
+        for (int e = 0; e < D / 4; ++e)
+          *reinterpret_cast<float4*>(out + (side * (HD / 8) + e) * step) =
+              make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
-      tc::fence_before_sync();
-      mbar_arrive(&s.o_free);
-      ++piece;
     }
   }
   tc::fence_before_sync();
@@ -980,9 +889,6 @@ cudaError_t launch(Params p, int ctas, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   return launch_dependent(kernel, dim3((unsigned)ctas), kThreads, smem_bytes<QT, HD>, 0, s, p);
 }
-
-// queries of a unit
-inline int unit_queries(bool q_bf16) { return q_bf16 ? 2 * kRows : kRows; }
 
 cudaError_t launch_bf16(const Params& p, int ctas, cudaStream_t s);  // bf16 queries
 cudaError_t launch_f32(const Params& p, int ctas, cudaStream_t s);   // f32 queries
