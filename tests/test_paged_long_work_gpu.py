@@ -150,3 +150,100 @@ def test_long_sums_are_those_of_f32(hd, sign):
             assert err <= 2.0 ** -19
         exact_lse = torch.stack([want[r][2] for r in range(256)])
         assert ((lse.double() - exact_lse).abs() <= 2.0 ** -19 + 2 * U * exact_lse.abs()).all()
+
+
+# ---------------------------------------------------------------- many tiles, many units
+def check(c, out, lse, rows):
+    """Against the exact rows, with the tolerances of test_paged_long_gpu.py (scores at most norm)."""
+    e, part = torch.finfo(out.dtype).eps / 2, 2.0 ** -16 if out.dtype is BF16 else 0.0
+    out, lse = out.double().view(c.R, c.heads, c.hd), lse.double()
+    for r, (o, mass, exact_lse, norm) in c.exact(rows).items():
+        n = c.own[r] + (c.prefix[c.group[r]] if c.group[r] >= 0 else 0)
+        ds = U * (8 * math.sqrt(c.hd) + 8) * norm
+        sums = U * (4 * math.sqrt(n) + 16)
+        join = 2 * (ds + sums + 4 * U * (exact_lse.abs() + norm))
+        tol = (2 * ds + sums + part + join)[:, None] * mass * (1 + e) + e * o.abs() + 1e-30
+        err = (out[r] - o).abs()
+        assert (err <= tol).all(), (r, float((err / tol).max()))
+        assert ((lse[r] - exact_lse).abs() <= ds + sums + join / 2 + 4 * U * exact_lse.abs()).all(), r
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("P", [5, 16, 128])
+def test_many_tiles(hd, io, P):
+    """More tiles a CTA than its ring and its masks hold, in pieces that are cut: blocks by TMA and by copies."""
+    c = Prefixes([64], [27000], [1 + r % 40 for r in range(64)], 32, 8, hd, io, P=P, seed=hd + P)
+    assert c.of_a_cta()[0] > 20
+    check(c, *c.run(), range(64))
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128])
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("P", [5, 16])
+def test_many_units(hd, io, P):
+    """More than twenty units a CTA: 420 groups of one row behind one to four tiles (more groups than a CTA has
+    threads), two of 30 rows behind a hundred, and rows behind none."""
+    sizes = [1] * 200 + [30] + [1] * 220 + [30]
+    prefix = [1 + i * 53 % 250 for i in range(200)] + [9000] + [1 + i * 91 % 250 for i in range(220)] + [7777]
+    own = [i * 7 % 23 for i in range(sum(sizes) + 3)]
+    c = Prefixes(sizes, prefix, own, 16, 8, hd, io, P=P, seed=hd + P)
+    assert c.of_a_cta()[1] > 20 and len(sizes) > 384
+    rows = [0, 1, 199] + list(range(200, 230, 7)) + list(range(230, 450, 13)) + [449, 450, 479, 480, 481, 482]
+    check(c, *c.run(), [r for r in rows if own[r] or c.group[r] >= 0])
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("rising", [True, False])
+def test_scores_that_rise(io, rising):
+    """Scores that grow along the prefix, so that the bound moves and sums are scaled again and again, or that
+    shrink, so that the first tiles' stays."""
+    n = 27000
+    grow = lambda pos: 0.1 + 3 * (pos if rising else n - pos) / n  # noqa: E731
+    c = Prefixes([40, 24], [n, n], [3] * 64, 32, 8, 64, io, seed=5, keys=lambda pos, k: (k.float() * grow(pos)).to(BF16))
+    assert c.of_a_cta()[0] > 20
+    check(c, *c.run(), range(0, 64, 3))
+
+
+@pytest.mark.parametrize("P", [5, 8])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_prefix_past_32_bits(P, io):
+    """Blocks past 2^32 elements in the tensor cores' kernel: whole boxes and the rows of one that is torn by the
+    prefix's end (blocks of 8), and copies (blocks of 5)."""
+    hd, W, stride = 32, 40000, 2**31 + 64
+    big_k, big_v = (torch.zeros(2 * stride + P * hd, dtype=BF16, device="cuda") for _ in range(2))
+    k, v = (x.as_strided((3, P, 1, hd), (stride, hd, hd, 1)) for x in (big_k, big_v))
+    for x in (k, v):
+        x[1:] = torch.randn(2, P, 1, hd, device="cuda").to(BF16)
+    n = 2 * P - 3
+    k[2, P - 3:], v[2, P - 3:] = NAN, INF
+    table = torch.full((3, W), -1, dtype=torch.int32, device="cuda")
+    table[2, :2] = ints([1, 2])
+    assert 4 * 2 * hd * W * P > 32e6
+    q = torch.randn(2, 4 * hd, device="cuda").to(io)
+    got, got_lse = paged.paged_prefix_attention(q, k, v, table, ints([-1, -1]), ints([0, 2]), ints([2]), ints([n]), lse=True)
+    kk, vv = (torch.cat([x[1, :, 0], x[2, :P - 3, 0]]).double() for x in (k, v))
+    s = q.double().view(2, 4, hd) @ kk.T * hd ** -0.5
+    want = (torch.softmax(s, -1) @ vv).view(2, -1)
+    mass, e = (torch.softmax(s, -1) @ vv.abs()).view(2, -1), torch.finfo(io).eps / 2
+    # scores at most norm: their f32 sums, weights and their sum, the store, as in check
+    norm = q.double().view(2, 4, hd).norm(dim=-1).max() * kk.norm(dim=-1).max() * hd ** -0.5
+    tol = U * (4 * (8 * math.sqrt(hd) + 8) * norm + 100)
+    assert ((got.double() - want).abs() <= tol * mass * (1 + e) + e * want.abs()).all()
+    assert ((got_lse.double() - torch.logsumexp(s, -1)).abs() <= tol).all()
+
+
+def test_select_of_many_rows():
+    """More rows than one launch has in y: three pages, of which the last is taken and one of the others."""
+    R, hd, P = 66000, 32, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mid = torch.randn(50, 1, 1, hd, generator=g, device="cuda")
+    bounds = torch.cat([mid - 1, mid + 1], 2)
+    table = torch.randint(0, 50, (R, 3), generator=g, device="cuda").to(torch.int32)
+    q = torch.randn(R, hd, generator=g, device="cuda")
+    pages = paged.paged_select(q, bounds, table, ints([3 * P - 1]).repeat(R), P, 2, first=0, last=1)
+    b, x = bounds.double()[:, 0], q.double()
+    score = ((x.clamp(min=0)[:, None] * b[table[:, :2].long(), 1]).sum(-1) +
+             (x.clamp(max=0)[:, None] * b[table[:, :2].long(), 0]).sum(-1))
+    best = (score[:, 1] > score[:, 0]).to(torch.int32)
+    assert torch.equal(pages[:, 0], torch.stack([best, torch.full_like(best, 2)], 1))
