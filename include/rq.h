@@ -329,7 +329,8 @@ typedef struct {
 enum {
   RQ_PAGED_BAD_INPUT = 1, /* a length or the pool's own words out of range */
   RQ_PAGED_NO_TOKENS = 2, /* the new tokens exceed max_tokens */
-  RQ_PAGED_NO_BLOCKS = 4  /* the new pages exceed the free blocks */
+  RQ_PAGED_NO_BLOCKS = 4, /* the new pages exceed the free blocks */
+  RQ_PAGED_TIMEOUT = 8    /* a wait on the device ran out (rq_paged_prefix_attention) */
 };
 
 /* The pool's free blocks: device pool [4] int32 {head, count, status, taken} and device
@@ -527,7 +528,11 @@ rq_status rq_paged_sparse_attention(const rq_paged_kv *kv, int32_t rows, int32_t
  *               max_blocks pages are read, as of a row's own request
  *   positions   device [R] int32, the row's position in its own request; negative: it holds
  *               nothing there, the prefix alone is read
- * The rest, results and workspace too, as rq_paged_attention (no window). */
+ *   workspace   as there, but never NULL.  Once the call has run its first int32 is 0, or
+ *               RQ_PAGED_TIMEOUT: a wait inside the kernel, each bounded to 2 s, ran out (the
+ *               GPU was taken away, or a fault of the library); rows whose prefix was concerned are
+ *               then NaN
+ * The rest, results too, as rq_paged_attention (no window). */
 size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv *kv, int32_t rows,
                                                 int32_t heads, int32_t max_blocks,
                                                 int32_t groups);
@@ -539,6 +544,11 @@ rq_status rq_paged_prefix_attention(const rq_paged_kv *kv, int32_t rows, int32_t
                                     const int32_t *prefix_lens, float scale, int32_t q_dtype,
                                     const void *q, void *out, float *lse, void *workspace,
                                     size_t workspace_bytes, void *cuda_stream);
+
+/* Test hook of that failure path, for the calls that the process enqueues from now on: the limit of
+ * a wait in nanoseconds (0: 2 s), and a thread block (stall >= 0) that never gets its prefix, so
+ * that its waits run out; -1: none.  Nothing traps and no wait is unbounded. */
+rq_status rq_paged_set_wait_limit(uint64_t limit_ns, int32_t stall);
 
 /* Token picks ("moshi_lm.rs", `Sampling`, `MoshiLm::set_sampling`, `pick`): every frame
  * picks the text token (temp_text, top_k_text) and then codebooks 0..7 (temp, top_k),

@@ -36,7 +36,7 @@ _CFG_INT_FIELDS = ["batch", "dim", "layers", "heads", "head_dim", "hidden", "con
 
 RQ_SCHEDULE_AUTO, RQ_SCHEDULE_GRAPH, RQ_SCHEDULE_PERSISTENT, RQ_SCHEDULE_TENSOR = 0, 1, 2, 3
 RQ_ROPE_INTERLEAVED, RQ_ROPE_HALVES = 0, 1
-RQ_PAGED_BAD_INPUT, RQ_PAGED_NO_TOKENS, RQ_PAGED_NO_BLOCKS = 1, 2, 4
+RQ_PAGED_BAD_INPUT, RQ_PAGED_NO_TOKENS, RQ_PAGED_NO_BLOCKS, RQ_PAGED_TIMEOUT = 1, 2, 4, 8
 RQ_PICK_GREEDY, RQ_PICK_TOPK, RQ_PICK_GUMBEL = 0, 1, 2
 RQ_F32, RQ_BF16, RQ_Q8, RQ_Q4 = 0, 1, 2, 3
 # stacked weight matrices (the weight bands quantize these; tables and alphas stay)
@@ -133,6 +133,8 @@ def load() -> C.CDLL:
     L.rq_paged_prefix_attention_workspace_size.argtypes = [C.c_char_p, I32, I32, I32, I32]
     L.rq_paged_prefix_attention.argtypes = [C.c_char_p, I32, I32, I32, I32, P, P, P, I32, P, P, P,
                                             F32, I32, P, P, P, P, C.c_size_t, P]
+    L.rq_paged_set_wait_limit.argtypes = [C.c_uint64, I32]
+    L.rq_paged_set_wait_limit.restype = C.c_int
     for f in ("rq_paged_select", "rq_paged_sparse_attention", "rq_paged_prefix_attention"):
         getattr(L, f + "_workspace_size").restype = C.c_size_t
     for f in ("rq_paged_pool_init", "rq_paged_plan", "rq_paged_append", "rq_paged_attention",

@@ -5,8 +5,9 @@
 // its prefix at once, and the rows' own requests are paged_attn.cuh's work, with f32 outputs. Else both
 // parts of every row are that, as two rows of one launch. Then all parts of a row are joined: with o_i, lse_i
 // of a part, lse = log sum e^lse_i and o = sum e^(lse_i - lse) o_i. All parts are f32, the output is
-// rounded once.
+// rounded once. The last launch of a call leaves its status in the workspace's first word.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "paged_prefix.cuh"
@@ -24,12 +25,14 @@ struct MergeParams {
   const float *o1, *o2, *lse1, *lse2;  // prefix, own
   void* out;
   float* lse;
+  int32_t* status;
 };
 
 template <typename OT>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeParams p) {
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;  // nothing waits in this form
   const int warps = gridDim.x * 8;
   for (long long i = (long long)blockIdx.x * 8 + threadIdx.x / 32; i < (long long)p.rows * p.heads; i += warps) {
     const int r = (int)(i / p.heads), lane = threadIdx.x % 32;
@@ -59,6 +62,8 @@ struct JoinParams {
   const float *own, *own_lse;
   void* out;
   float* lse;
+  int32_t* status;
+  int ctas;
 };
 
 constexpr int kJoinWarps = 8;
@@ -68,6 +73,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 32, four = blockIdx.y * kJoinWarps + threadIdx.x / 32;
+  if (blockIdx.x == 0 && four == 0) {
+    uint32_t gave_up = 0;
+    for (int i = lane; i < p.ctas; i += 32) gave_up |= p.t.gave_up[i];
+    gave_up = __any_sync(0xffffffffu, gave_up != 0);
+    if (lane == 0) *p.status = gave_up ? RQ_PAGED_TIMEOUT : 0;
+  }
   const uint32_t of_head = (uint32_t)p.t.rows * p.t.G, idx = blockIdx.x * 32 + lane;
   if (idx >= of_head * p.t.kv.heads) return;
   const int h = idx / of_head, in = idx % of_head, r = in / p.t.G, g = in % p.t.G;
@@ -145,12 +156,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   if (p.lse && four == 0) p.lse[head] = sum == 0.f ? neg_inf() : (m + log2f(sum)) * 0.6931471805599453f;
 }
 
+constexpr size_t kHead = 256;  // bytes of the workspace for the status, in front
+// what rq_paged_set_wait_limit set
+std::atomic<unsigned long long> g_wait_ns{0};
+std::atomic<int> g_stall{-1};
+
 struct Layout {
   paged_attn::Choice x;
   bool tc;         // prefixes by matrix products
   int ctas;        // of the prefix kernel
   int bundle;      // else: rows of a group whose queries are a unit's
-  size_t o, lse, part, part_ml, group, bytes;
+  size_t o, lse, part, part_ml, group, gave_up, bytes;
 };
 
 Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int groups) {
@@ -177,7 +193,8 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   l.part = align256((size_t)l.ctas * 2 * prefix::kRows * hd * sizeof(float));
   l.part_ml = align256((size_t)l.ctas * 2 * prefix::kRows * sizeof(float2));
   l.group = align256((size_t)groups * sizeof(prefix::Group)) + 256;
-  l.bytes = 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group : 0);
+  l.gave_up = align256((size_t)l.ctas * sizeof(uint32_t));
+  l.bytes = kHead + 2 * (l.o + l.lse) + l.x.workspace + (l.tc ? l.part + l.part_ml + l.group + l.gave_up : 0);
   return l;
 }
 
@@ -193,6 +210,13 @@ rq_status check(const rq_paged_kv* kv, int32_t rows, int32_t heads, int32_t max_
 
 }  // namespace
 }  // namespace rqk
+
+extern "C" rq_status rq_paged_set_wait_limit(uint64_t limit_ns, int32_t stall) {
+  if (stall < -1) return RQ_ERR_ARG;
+  rqk::g_wait_ns.store(limit_ns, std::memory_order_relaxed);
+  rqk::g_stall.store(stall, std::memory_order_relaxed);
+  return RQ_OK;
+}
 
 extern "C" size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv* kv, int32_t rows,
                                                            int32_t heads, int32_t max_blocks,
@@ -233,6 +257,7 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
     ws += n;
     return at;
   };
+  int32_t* const status = reinterpret_cast<int32_t*>(take(kHead));
   // [2][rows][heads][head_dim] sums and [2][rows][heads] lse: of the prefixes, of the rows' own requests
   float* const o = reinterpret_cast<float*>(take(2 * l.o));
   float* const ls = reinterpret_cast<float*>(take(2 * l.lse));
@@ -256,6 +281,8 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
   if (groups == 0) {
     p.out = out;
     p.lse = lse;
+    e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
+    if (e != cudaSuccess) return RQ_ERR_CUDA;
     e = bf16 ? paged_attn::launch_bf16(p, l.x, qb, s) : paged_attn::launch_f32(p, l.x, qb, s);
   } else if (l.tc) {
     float* const own_lse = ls + 2 * (size_t)rows * heads;
@@ -280,12 +307,16 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
     t.part_ml = reinterpret_cast<float2*>(take(l.part_ml));
     t.group = reinterpret_cast<prefix::Group*>(take(l.group));
     t.per = reinterpret_cast<long long*>(reinterpret_cast<char*>(t.group) + l.group - 256);
+    t.gave_up = reinterpret_cast<uint32_t*>(take(l.gave_up));
+    const unsigned long long wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    t.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
+    t.stall = g_stall.load(std::memory_order_relaxed);
     p.out = own_o;
     p.lse = own_lse;
     e = qb ? prefix::launch_bf16(t, l.ctas, s) : prefix::launch_f32(t, l.ctas, s);
     if (e == cudaSuccess) e = paged_attn::launch_sums_bf16(p, l.x, qb, s);
     if (e != cudaSuccess) return RQ_ERR_CUDA;
-    JoinParams j{t, requests, own_o, own_lse, out, lse};
+    JoinParams j{t, requests, own_o, own_lse, out, lse, status, l.ctas};
     const dim3 grid((unsigned)(((long long)rows * heads + 31) / 32), (unsigned)(kv->head_dim / (4 * kJoinWarps)));
     auto join = [&](auto* kernel) { return launch_dependent(kernel, grid, kJoinWarps * 32, 0, 0, s, j); };
     switch (kv->head_dim) {
@@ -294,7 +325,7 @@ extern "C" rq_status rq_paged_prefix_attention(const rq_paged_kv* kv, int32_t ro
       default: e = qb ? join(join_kernel<uint16_t, 128>) : join(join_kernel<float, 128>);
     }
   } else {
-    const MergeParams m{requests, rows, heads, batch, kv->head_dim, o, own_o, ls, ls + (size_t)rows * heads, out, lse};
+    const MergeParams m{requests, rows, heads, batch, kv->head_dim, o, own_o, ls, ls + (size_t)rows * heads, out, lse, status};
     p.rows = 2 * rows;
     p.q_rows = rows;
     p.bundle = l.bundle;

@@ -86,6 +86,9 @@ struct Params {
   float2* part_ml;  // [ctas][2][kRows]
   Group* group;     // [groups]
   long long* per;   // entries of a run
+  uint32_t* gave_up;  // [ctas] 1: a wait of the CTA ran out, 0: none did
+  unsigned long long wait_ns;  // after which one does
+  int stall;        // a test's: the CTA whose loaders load nothing, or -1
   int box;          // rows of a TMA box, 0: copies by threads
   CUtensorMap kmap, vmap;  // [block][head][row][dimension]
 };
@@ -354,9 +357,9 @@ struct Cursor {
 };
 
 // out of line, as is all that runs once a piece: 140 KB of code took 8 us to arrive at each launch
-static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+static __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (*abort) return false;
-  if (mbar_wait(bar, parity)) return true;
+  if (mbar_wait_for(bar, parity, limit_ns)) return true;
   *abort = 1;
   return false;
 }
@@ -452,7 +455,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   pdl_trigger();
 
   Cursor<KT> cur;
-  if (!cur.start(p, s)) return;
+  if (!cur.start(p, s)) {
+    if (tid == 0) p.gave_up[blockIdx.x] = 0;
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < NH; ++i) {
       mbar_init(&s.full[i], BOX ? 1 : kLoaders + kLoaders / 32);
@@ -477,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
   // of a warp, all of whose lanes go on or none; a wait that runs out ends the CTA's work: its sums
-  // become NaN
+  // become NaN, and it says so
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity & 1u))) return true;
-    return __all_sync(0xffffffffu, slow_wait(bar, parity & 1u, &s.abort)) != 0;
+    return __all_sync(0xffffffffu, slow_wait(bar, parity & 1u, &s.abort, p.wait_ns)) != 0;
   };
   Piece x;
 
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int side = warp - 8;
     const CUtensorMap* const map = side == 0 ? &p.kmap : &p.vmap;
     int tile = 0;
-    bool ok = true;
+    bool ok = (int)blockIdx.x != p.stall;
     if (lane == 0) tc::prefetch_tmap(map);
     while (ok && cur.next(p, x)) {
       // the lane's box's first key, column of the table and row of the block, a tile ahead. Divided once a piece:
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int w = warp - 8, P = p.kv.block_size;
     const uint32_t ring = smem_u32(smem) + S::kQ;
     int half = 0, tile = 0;
-    bool ok = true;
+    bool ok = (int)blockIdx.x != p.stall;
     while (ok && cur.next(p, x)) {
       const uint16_t* kb = static_cast<const uint16_t*>(p.kv.k) + x.h * p.kv.head_stride;
       const uint16_t* vb = static_cast<const uint16_t*>(p.kv.v) + x.h * p.kv.head_stride;
@@ -698,7 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
     if (elect_one()) tc::commit(&s.drain);
     __syncwarp();
-    mbar_wait(&s.drain, 0);  // whatever happened: tensor memory is given back behind it
+    // whatever happened: tensor memory is given back behind it
+    if (!mbar_wait(&s.drain, 0)) s.abort = 1;
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
@@ -842,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 10) tc::tmem_dealloc(tmem, 512);
+  if (tid == 0) p.gave_up[blockIdx.x] = s.abort != 0;
 }
 
 // The TMA boxes of a cache: p.box and the maps, or box 0 where there are none for it. Rows of a box: the

@@ -13,7 +13,7 @@ rq_paged_* calls; argument marshalling only, like `binding`).
 
 A layer's cache is a pair of tensors k, v [n_blocks][block_size][kv_heads][head_dim] (f32
 or bf16, of any strides that keep head_dim contiguous and every row 16-byte aligned).
-Nothing here synchronizes except PagedCache.status(), so a step can be captured into a CUDA
+Nothing here synchronizes except PagedCache.status() and paged_prefix_attention_status(), so a step can be captured into a CUDA
 graph; a captured step keeps its tensors' addresses, so pass `out`, `lse` and `workspace` (the
 paged_*_workspace functions).
 Every call runs on `stream` (a torch.cuda.Stream; default: the current one of the
@@ -404,12 +404,19 @@ def _prefix_workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, head_str
 
 
 def paged_prefix_attention_workspace(q, k, block_table, prefix_lens):
-    """Scratch for paged_prefix_attention with these shapes."""
+    """Scratch for paged_prefix_attention with these shapes (paged_prefix_attention_status reads from it how a
+    call ended)."""
     n, p, hk, hd = k.shape
     with _on(k.device, None):
         size = _prefix_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
                                       k.stride(2), p, block_table.shape[1], prefix_lens.numel())
     return torch.empty(size, dtype=torch.uint8, device=k.device)
+
+
+def paged_prefix_attention_status(workspace):
+    """0, or RQ_PAGED_TIMEOUT: a wait of the last paged_prefix_attention with this workspace ran out on the GPU,
+    and rows of it are NaN. Synchronizes."""
+    return int(workspace.view(-1).view(torch.uint8)[:4].view(_I32).item())
 
 
 def _rows(q, k, hd, dev, block_table, positions, requests, out, lse, scale):

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from rq_transformer_frame_gb300 import paged
+from rq_transformer_frame_gb300 import binding, paged
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -247,3 +247,44 @@ def test_select_of_many_rows():
              (x.clamp(max=0)[:, None] * b[table[:, :2].long(), 0]).sum(-1))
     best = (score[:, 1] > score[:, 0]).to(torch.int32)
     assert torch.equal(pages[:, 0], torch.stack([best, torch.full_like(best, 2)], 1))
+
+
+# ---------------------------------------------------------------- a wait that runs out
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("P", [5, 16])
+def test_a_wait_that_runs_out_is_reported(io, P):
+    """One thread block never gets its prefix: after 20 ms its waits run out, the call says so, the rows that hang on
+    it are NaN and no others; the calls before and behind it are as ever."""
+    c = Prefixes([64], [9000], [1 + r % 9 for r in range(64)], 16, 8, 64, io, P=P, seed=P)
+    L = binding.load()
+    ws = paged.paged_prefix_attention_workspace(c.q, c.k, c.table, c.words[3])
+    ws.fill_(0xff)
+    out, lse = c.run(workspace=ws)
+    assert paged.paged_prefix_attention_status(ws) == 0 and out.isfinite().all()
+    try:
+        assert L.rq_paged_set_wait_limit(20_000_000, -2) == binding.RQ_ERR_ARG
+        assert L.rq_paged_set_wait_limit(20_000_000, 0) == binding.RQ_OK
+        bad, bad_lse = c.run(workspace=ws)
+        assert paged.paged_prefix_attention_status(ws) == binding.RQ_PAGED_TIMEOUT
+    finally:
+        L.rq_paged_set_wait_limit(0, -1)
+    # the first thread block has tiles of the first K/V head's queries alone: two heads of all rows
+    gone = torch.zeros(64, 16, dtype=torch.bool, device="cuda")
+    gone[:, :2] = True
+    assert torch.equal(bad_lse.isnan(), gone) and torch.equal(bad_lse[~gone], lse[~gone])
+    bad, out = bad.view(64, 16, 64), out.view(64, 16, 64)
+    assert bad[gone].isnan().all() and torch.equal(bad[~gone], out[~gone])
+    again, again_lse = c.run(workspace=ws)
+    assert paged.paged_prefix_attention_status(ws) == 0
+    assert torch.equal(again.view(64, 16, 64), out) and torch.equal(again_lse, lse)
+
+
+def test_status_of_the_other_forms():
+    """Rows each for itself, and no groups at all: nothing there waits, and the status says so."""
+    k, v = (torch.randn(6, 8, 2, 64, device="cuda") for _ in range(2))
+    q, table, pos, one = torch.randn(2, 4 * 64, device="cuda"), ints([[0, 1], [2, 3], [4, 5]]), ints([9, 15]), ints([2])
+    for cu, group, n in ((ints([0, 2]), one, ints([11])), (ints([0]), ints([]), ints([]))):
+        ws = paged.paged_prefix_attention_workspace(q, k, table, n)
+        ws.fill_(0xff)
+        paged.paged_prefix_attention(q, k, v, table, pos, cu, group, n, workspace=ws)
+        assert paged.paged_prefix_attention_status(ws) == 0
