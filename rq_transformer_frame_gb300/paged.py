@@ -561,10 +561,12 @@ class PagedCache:
         return paged_plan(new_lens, m.lens, m.pool, self.free_ids, self.block_table,
                           self.block_size, self.max_tokens, out=m, stream=stream)
 
-    def append(self, layer, qkv, **kw):
-        """The step's rows qkv [T][...], T <= max_tokens, into layer `layer` -> queries."""
+    def append(self, layer, qkv, positions=None, **kw):
+        """The step's rows qkv [T][...], T <= max_tokens, into layer `layer` -> queries. positions: int32 [T]
+        that the rows are rotated by, where they are not the plan's: a request behind a shared prefix has its
+        own positions from 0, and its rows stand at these plus the prefix's length."""
         T = qkv.shape[0]
-        return paged_append(qkv, self.k[layer], self.v[layer], self.maps.positions[:T],
+        return paged_append(qkv, self.k[layer], self.v[layer], self.maps.positions[:T] if positions is None else positions,
                             self.maps.slots[:T], **kw)
 
     def attend(self, layer, q, **kw):

@@ -288,3 +288,39 @@ def test_status_of_the_other_forms():
         ws.fill_(0xff)
         paged.paged_prefix_attention(q, k, v, table, pos, cu, group, n, workspace=ws)
         assert paged.paged_prefix_attention_status(ws) == 0
+
+
+# ---------------------------------------------------------------- behind a shared prompt
+@pytest.mark.parametrize("rope", ["interleaved", "halves"])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_rotations_behind_a_shared_prompt(rope, io):
+    """Two prompts appended once, then steps of requests behind them, through PagedCache alone: the queries, keys and
+    results of requests that hold all of it themselves."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    B, P, hk, H, hd = 5, 8, 2, 4, 64
+    plen = [37, 90]
+    of = [0, 0, 0, 1, 1]  # each request's prompt
+    c = paged.PagedCache(B + 2, 400, P, 60, 512, hk, hd, layers=2, dtype=io)
+    whole = paged.PagedCache(B, 400, P, 60, 512, hk, hd, layers=2, dtype=io)
+    prompts = [torch.randn(n, (H + 2 * hk) * hd, generator=g, device="cuda").to(io) for n in plen]
+    c.plan(ints([0] * B + plen))
+    whole.plan(ints([plen[i] for i in of]))
+    for layer in range(2):
+        c.append(layer, torch.cat(prompts), rope=rope)
+        whole.append(layer, torch.cat([prompts[i] for i in of]), rope=rope)
+    behind = ints([plen[i] for i in of] + [0, 0])
+    for new in ([3, 1, 9, 2, 5], [1] * B, [1, 2, 1, 1, 4]):
+        T, n = sum(new), sum(new[:3])
+        qkv = torch.randn(T, (H + 2 * hk) * hd, generator=g, device="cuda").to(io)
+        c.plan(ints(new + [0, 0]))
+        whole.plan(ints(new))
+        at = c.maps.positions[:T] + behind[c.maps.requests[:T]]
+        for layer in range(2):
+            q = c.append(layer, qkv, positions=at, rope=rope)
+            q2 = whole.append(layer, qkv, rope=rope)
+            assert torch.equal(q, q2)
+            out, lse = c.attend_prefix(layer, q, ints([0, n, T]), ints([B, B + 1]), ints(plen), lse=True)
+            want, want_lse = whole.attend(layer, q2, lse=True)
+            assert (out.double() - want.double()).abs().max() <= 4 * torch.finfo(io).eps * want.double().abs().max() + \
+                1e-5 * (io is F32)
+            assert torch.allclose(lse, want_lse, rtol=1e-5)
