@@ -113,8 +113,8 @@ def paged_attention_workspace(q, k, block_table, window=0):
     """Scratch for paged_attention with these shapes, for calls whose addresses must stay (a
     captured graph), or None where the call needs none."""
     n, p, hk, hd = k.shape
-    if (window | block_table.shape[1]) >> 31:
-        _past_int32(window, block_table.shape[1])
+    if (window | block_table.shape[1] | q.shape[0] | p) >> 31:
+        _past_int32(window, block_table.shape[1], q.shape[0], p)
     with _on(k.device, None):
         size = _workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
                                k.stride(2), p, block_table.shape[1], window)
@@ -389,10 +389,12 @@ def _sparse_workspace_size(dev, dtype, rows, heads, kv_heads, head_dim, block_si
 
 def paged_sparse_attention_workspace(q, k, pages):
     """Scratch for paged_sparse_attention with these shapes, or None where the call needs none."""
-    hk, hd = k.shape[2:]
+    n, p, hk, hd = k.shape
+    if (q.shape[0] | p | pages.shape[2]) >> 31:
+        _past_int32(q.shape[0], p, pages.shape[2])
     with _on(k.device, None):
-        size = _sparse_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
-                                      k.shape[1], pages.shape[2])
+        size = _sparse_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd, p,
+                                      pages.shape[2])
     return torch.empty(size, dtype=torch.uint8, device=k.device) if size else None
 
 
@@ -407,6 +409,8 @@ def paged_prefix_attention_workspace(q, k, block_table, prefix_lens):
     """Scratch for paged_prefix_attention with these shapes (paged_prefix_attention_status reads from it how a
     call ended)."""
     n, p, hk, hd = k.shape
+    if (q.shape[0] | p | block_table.shape[1] | prefix_lens.numel()) >> 31:
+        _past_int32(q.shape[0], p, block_table.shape[1], prefix_lens.numel())
     with _on(k.device, None):
         size = _prefix_workspace_size(k.get_device(), _TYPE[k.dtype], q.shape[0], q.shape[1] // hd, hk, hd,
                                       k.stride(2), p, block_table.shape[1], prefix_lens.numel())

@@ -151,6 +151,23 @@ def test_binding_refuses_host_tensors(lib):
         paged.paged_prefix_attention(q, k, k, i(4, 4), i(3), i(2), i(1), i(1))
 
 
+
+BIG = 2**32 + 5
+
+
+@pytest.mark.parametrize("rows,p,W,n", [(BIG, 16, 4, 2), (3, BIG, 4, 2), (3, 16, BIG, 2), (3, 16, 4, BIG)])
+def test_workspaces_of_sizes_past_32_bits(lib, rows, p, W, n):
+    """A size that ctypes would take modulo 2^32 is refused (tensors that are shapes alone)."""
+    e = lambda *s, dtype=torch.int32: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    q, k, table = e(rows, 256, dtype=torch.bfloat16), e(4, p, 2, 64, dtype=torch.bfloat16), e(3, W)
+    calls = [lambda: paged.paged_prefix_attention_workspace(q, k, table, e(n))]
+    if W < BIG:
+        calls.append(lambda: paged.paged_sparse_attention_workspace(q, k, e(rows, 2, n)))
+    calls.append(lambda: paged.paged_attention_workspace(q, k, table, window=n))
+    for call in calls:
+        with pytest.raises(ValueError, match="does not fit 32 bits"):
+            call()
+
 @pytest.mark.parametrize("seed", range(4))
 def test_plain_attention_over_all_pages_is_attention(seed):
     """Every live page listed, or the positions cut into a prefix and the rest: paged_ref's attention."""
