@@ -581,15 +581,20 @@ class PagedCache:
         return paged_attention(q, self.k[layer], self.v[layer], self.block_table,
                                self.maps.positions[:T], requests=self.maps.requests[:T], **kw)
 
+    def _bounds(self, layer):
+        if self.bounds is None:
+            raise ValueError("a PagedCache made with bounds=True is wanted")
+        return self.bounds[layer]
+
     def bound(self, layer, T, **kw):
         """The bounds of the blocks that the step's first T tokens lie in, once they are appended
         (a cache made with bounds=True)."""
-        return paged_bounds(self.k[layer], self.bounds[layer], self.maps.positions[:T], self.maps.slots[:T], **kw)
+        return paged_bounds(self.k[layer], self._bounds(layer), self.maps.positions[:T], self.maps.slots[:T], **kw)
 
     def select(self, layer, q, top, **kw):
         """`top` pages of its own request for each of the step's tokens and K/V heads."""
         T = q.shape[0]
-        return paged_select(q, self.bounds[layer], self.block_table, self.maps.positions[:T],
+        return paged_select(q, self._bounds(layer), self.block_table, self.maps.positions[:T],
                             self.block_size, top, requests=self.maps.requests[:T], **kw)
 
     def attend_pages(self, layer, q, pages, **kw):

@@ -168,6 +168,16 @@ def test_workspaces_of_sizes_past_32_bits(lib, rows, p, W, n):
         with pytest.raises(ValueError, match="does not fit 32 bits"):
             call()
 
+
+def test_a_cache_without_bounds_says_so():
+    c = paged.PagedCache.__new__(paged.PagedCache)  # the host's side of one: its buffers are on a GPU
+    c.bounds, c.k, c.block_size = None, torch.zeros(1, 4, 16, 2, 64), 16
+    c.block_table = torch.zeros(3, 4, dtype=torch.int32)
+    c.maps = paged.PagedPlan(*[torch.zeros(3, dtype=torch.int32)] * 6)
+    for call in (lambda: c.bound(0, 3), lambda: c.select(0, torch.zeros(3, 256), 2)):
+        with pytest.raises(ValueError, match="bounds=True"):
+            call()
+
 @pytest.mark.parametrize("seed", range(4))
 def test_plain_attention_over_all_pages_is_attention(seed):
     """Every live page listed, or the positions cut into a prefix and the rest: paged_ref's attention."""
