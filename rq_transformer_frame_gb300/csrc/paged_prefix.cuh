@@ -61,8 +61,10 @@ using paged_attn::pack_bf16;
 
 constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kRows = 128;       // queries of a unit
-// What a tile, and a unit's start and end count in the list: 1.6 and 7 us
-constexpr int kTileCost = 2, kUnitCost = 9;
+// What a tile, and a unit's start and end count in the list: between what is best for bf16 and for f32 queries (250
+// rows of five groups with bf16 ones, 64 rows behind 2500 positions with f32 ones: 192 and 57.7 us where a unit
+// counts 9, 185 and 57.5 with 12, 180 and 58.9 with 16, 177 and 59.6 with 20)
+constexpr int kTileCost = 2, kUnitCost = 14;
 constexpr float kSlack = 8.f;
 constexpr int kMasks = 8;        // tiles whose masks are kept
 // columns of tensor memory: the two streams' scores, and P's first two parts, at 0 and 128; O; P's third parts
