@@ -473,7 +473,7 @@ rq_status rq_paged_bounds(const rq_paged_kv *kv, void *bounds, int32_t tokens,
  *   - of the others whose block lies in [0, n_blocks) the top - first - last best (or all) by
  *     score = sum over dimensions d of max_d sum_h max(q_hd, 0) + min_d sum_h min(q_hd, 0),
  *     h over the K/V head's queries: no sum of their scores with a key of the page is larger.
- *     Of equal scores the lowest page is taken; a NaN score is lower than all others.
+ *     Of equal scores the lowest page is taken; a NaN score counts as minus infinity.
  *   kv          the cache's sizes and type (its addresses and strides are not used)
  *   bounds      rq_paged_bounds of the layer; the live blocks' must be there
  *   top, first, last  pages; last >= 1 (the row's own page is always taken), first >= 0,
@@ -528,11 +528,12 @@ rq_status rq_paged_sparse_attention(const rq_paged_kv *kv, int32_t rows, int32_t
  *               max_blocks pages are read, as of a row's own request
  *   positions   device [R] int32, the row's position in its own request; negative: it holds
  *               nothing there, the prefix alone is read
- *   workspace   as there, but never NULL.  Once the call has run its first int32 is 0, or
+ *   workspace   as there, but never NULL.  Once the call has run (R > 0) its first int32 is 0, or
  *               RQ_PAGED_TIMEOUT: a wait inside the kernel, each bounded to 2 s, ran out (the
  *               GPU was taken away, or a fault of the library); rows whose prefix was concerned are
  *               then NaN
- * The rest, results too, as rq_paged_attention (no window). */
+ * The rest, results too, as rq_paged_attention (no window); over a bf16 cache long prefixes' weights keep 24 bits
+ * with bf16 queries too, and errors do not grow with a prefix's length beyond those of f32 sums. */
 size_t rq_paged_prefix_attention_workspace_size(const rq_paged_kv *kv, int32_t rows,
                                                 int32_t heads, int32_t max_blocks,
                                                 int32_t groups);

@@ -420,6 +420,8 @@ def paged_prefix_attention_workspace(q, k, block_table, prefix_lens):
 def paged_prefix_attention_status(workspace):
     """0, or RQ_PAGED_TIMEOUT: a wait of the last paged_prefix_attention with this workspace ran out on the GPU,
     and rows of it are NaN. Synchronizes."""
+    if workspace.numel() == 0:  # for no rows, of which nothing runs
+        return 0
     return int(workspace.view(-1).view(torch.uint8)[:4].view(_I32).item())
 
 

@@ -286,8 +286,18 @@ def test_status_of_the_other_forms():
     for cu, group, n in ((ints([0, 2]), one, ints([11])), (ints([0]), ints([]), ints([]))):
         ws = paged.paged_prefix_attention_workspace(q, k, table, n)
         ws.fill_(0xff)
-        paged.paged_prefix_attention(q, k, v, table, pos, cu, group, n, workspace=ws)
+        out, _ = paged.paged_prefix_attention(q, k, v, table, pos, cu, group, n, workspace=ws)
         assert paged.paged_prefix_attention_status(ws) == 0
+        captured = torch.zeros_like(out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            paged.paged_prefix_attention(q, k, v, table, pos, cu, group, n, out=captured, workspace=ws)
+        ws.fill_(0xff)
+        graph.replay()
+        assert paged.paged_prefix_attention_status(ws) == 0 and torch.equal(captured, out)
+    none = paged.paged_prefix_attention_workspace(q[:0], k, table, one)
+    paged.paged_prefix_attention(q[:0], k, v, table, pos, ints([0, 0]), one, one, workspace=none)
+    assert paged.paged_prefix_attention_status(none) == 0
 
 
 # ---------------------------------------------------------------- behind a shared prompt
