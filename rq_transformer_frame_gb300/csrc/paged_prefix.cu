@@ -175,7 +175,7 @@ Layout layout_of(const rq_paged_kv& kv, int rows, int heads, int max_blocks, int
   const size_t hd = kv.head_dim;
   // What the tables allow all rows to read for themselves, in bytes: a launch over few short rows is over
   // before the prefix kernel has its first tile (8 rows of 16 heads, 64 dimensions, 200 positions before 40:
-  // 19 us against 25).
+  // 20 us against 22).
   const double most = 4.0 * rows * kv.heads * hd * max_blocks * kv.block_size;
   l.tc = groups > 0 && kv.dtype == RQ_BF16 && most > 32e6;
   if (l.tc || groups == 0) {

@@ -14,8 +14,8 @@
 // that is cut each piece leaves (ref, l, O) in its CTA's scratch, and paged_prefix.cu joins them with
 // the rows' own requests.
 //
-// A CTA is 12 warps (168 registers a thread; with 13 it is 128, and spills that miss the little L1
-// beside 227 KB of shared memory):
+// A CTA is 12 warps (168 registers a thread, of which the bf16-query kernels spill 4 to 24 bytes; with 13 it is
+// 128, and spills that miss the little L1 beside 227 KB of shared memory):
 //   0-7       softmax. Scores come in two streams, each with its S and P in tensor memory, that take
 //             turns by tiles. All eight warps form one stream's P, two threads a row, while the tensor
 //             cores work for the other, and add the other's O before they hand P over. (Four warps a stream
@@ -39,8 +39,10 @@
 // What bounds it: a tile of 128 queries and 128 keys is 32 products of 64 cycles (24 of them P's three parts),
 // 1.1 us, beside the softmax, some 3000 cycles or 1.5 us: 410 for scores and maxima, 130 for the exchange of
 // these, 1850 for exponentials (1024 of the unit that makes them) and parts, 420 for sums, the rest waits. A
-// loader is busy for 2600 of them with blocks of 16 positions. One O for all tiles of a piece, two parts of P and
-// 256 queries a unit took 1.15 us a tile; its outputs were off by 1e-4 behind 50000 positions.
+// loader is busy for 2600 of them with blocks of 16 positions. 64 rows of 32 heads over 8 K/V heads behind
+// 32768 positions, two units a head: 58 us, 27 tiles a CTA, tensor pipe 53% of the time; the second unit's
+// keys come from HBM again (243 MB of 134). One O for all tiles of a piece, two parts of P and 256 queries a unit
+// took 1.15 us a tile, 47 us in all, and was off by 1e-4 behind 50000 positions.
 #pragma once
 
 #include <type_traits>

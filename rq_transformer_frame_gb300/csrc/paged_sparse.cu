@@ -1,9 +1,9 @@
 // paged_sparse.cu -- rq_paged_sparse_attention (include/rq.h): checks, workspace and launch of the
 // kernels in paged_attn.cuh with lists of pages.
 //
-// Each (row, K/V head) is a row of one K/V head, with a list of its own. All have the same number
-// of entries, so a launch's longest unit is as long as the others and few units are split as one row
-// is.
+// Each (row, K/V head) is a row of one K/V head, with a list of its own, and launches are chosen as for
+// such rows: few units are split up to 8 tiles a warp where there are several lists, as one request with
+// several K/V heads has, and further for one list alone (paged_attn.cuh, split_ctas).
 #include <cmath>
 
 #include "paged_attn.cuh"
